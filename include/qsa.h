@@ -334,6 +334,100 @@ QSA_API int qsa_select_noalloc(const uint16_t* q, const int8_t* kq, const uint16
                                int pos0, int32_t* ids, const qsa_params* params, void* stream);
 
 /*
+ * Drafted tokens (speculative decoding) and continuous batching.  The pages have no counterpart of the
+ * four operators below; the layer, the cache layouts, the pool and the seqs table are those above.
+ * A step of a server that drafts: qsa_prep_batched writes the drafted tokens' cache cells,
+ * qsa_tree_attention attends for all of them at once, and when the model's answers have settled which
+ * path is accepted, qsa_cache_commit moves that path's cells to the front.
+ *
+ * qsa_prep_batched - qsa_prep for n_tok tokens of any sequences: token t has its own position and its
+ * own pool cell, and the raw rows may be slices of a fused projection.
+ *   q_raw, k_raw, v_raw  rows of token t at q_raw + t * q_stride (24 x 256 fp16 in a row), k_raw + t *
+ *         k_stride and v_raw + t * v_stride (2 x 256 each); strides in elements, multiples of 8, at
+ *         least the row's width
+ *   pos   [n_tok][axes] int32 (DEVICE), axes 1 (plain) or 3 (mrope, sections as in qsa_prep); any
+ *         32-bit position: the angle is formed as a 64-bit fixed-point fraction of a turn
+ *   cells [n_tok] int32 (DEVICE): the pool cell that receives token t's K and V; -1 marks a padding
+ *         token, for which nothing is written.  A cell given twice in one call is left with
+ *         unspecified contents.
+ *   qcur [n_tok][24][256], kcur [n_tok][2][256] or NULL: as in qsa_prep
+ * Norm, rotation, roundings and the quantiser are qsa_prep's; angles may differ from its in the last
+ * bits.  A cell outside [0, n_pool) other than -1 is skipped like padding and flagged in the status
+ * word (QSA_ERR_DEVICE).  n_tok 0 does nothing.
+ */
+QSA_API int qsa_prep_batched(const uint16_t* q_raw, const uint16_t* k_raw, const uint16_t* v_raw, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float* q_gamma, const float* k_gamma,
+                             const int32_t* pos, int axes, const int32_t* cells, const qsa_rope* rope, int n_tok,
+                             int64_t n_pool, uint16_t* qcur, uint16_t* kcur, int8_t* kq, uint16_t* ksc, int8_t* vq,
+                             uint16_t* vsc, void* stream);
+
+/*
+ * qsa_cache_read - cells of the pool back as fp16 rows, k16[i] = fp16(kq * ksc) of cell cells[i] and
+ * v16[i] likewise (one rounding: the values the prefill kernels attend to).
+ *   cells [n] int32 (DEVICE), in any order, repeats allowed; -1: rows i are left as they are.  Any
+ *         other index outside [0, n_pool) is skipped and flagged in the status word (QSA_ERR_DEVICE).
+ *   k16, v16 [n][2][256] fp16 (written); either may be NULL, and then its codes and scales may be too
+ */
+QSA_API int qsa_cache_read(const int8_t* kq, const uint16_t* ksc, const int8_t* vq, const uint16_t* vsc, int64_t n_pool,
+                           const int32_t* cells, int64_t n, uint16_t* k16, uint16_t* v16, void* stream);
+
+/*
+ * Bytes of device workspace qsa_tree_attention needs (0 when it needs none or for invalid arguments).
+ */
+QSA_API size_t qsa_tree_attention_workspace_bytes(int n_seq, int n_tok, int max_n_kv, const qsa_params* params);
+
+/*
+ * qsa_tree_attention - attention of drafted token trees over the cache, for many sequences in one
+ * call.  Pool and seqs table as in qsa_flash_prefill_batched: drafted token i of sequence s is row
+ * seqs[s][3] + i of q / tree / ids / out, its K/V are already in the sequence's cell pos0 + i (pos0 =
+ * seqs[s][2] cells are committed), and it sees the committed cells 0 .. pos0 - 1 and the drafted cells
+ * pos0 + j, j < the sequence's token count, with bit j % 32 of tree[row][j / 32] set.  The mask is the
+ * caller's: ancestors and the token itself for a tree, any other pattern as well (a token that should
+ * see itself needs its own bit).  n_kv of a token is the number of cells it sees; it attends to all of
+ * them while n_kv <= identity_max, else to the topk of them with the largest selection score (the
+ * exact ranking of qsa_select, equal scores going to the lower cell):
+ *   out[t,h,:] = fp16( sum_{c in set(t,g)} softmax_c(sm_scale * q[t,h,:] . k^[c,g,:]) * v^[c,g,:]
+ *                      * (gate ? 1 / (1 + exp(-gate[t,h,:])) : 1) )
+ * so a token whose ancestors end up accepted gets what decoding them one by one gives.  A token that
+ * sees no cell gets zeros.  Cells that no token sees may hold anything, infinities and NaN included.
+ *   seqs  DEVICE [n_seq][4] int32 {first pool cell, n_cells, pos0, first token row}, first token rows
+ *         non-decreasing from 0, the last sequence running to n_tok; a sequence with n_cells 0 is
+ *         padding: its rows are left as they are
+ *   tree  DEVICE [n_tok][tree_words] uint32, tree_words 1 .. 8: up to 32 * tree_words drafted tokens
+ *         per sequence; bits past the sequence's token count are ignored
+ *   max_n_kv  an upper bound on every sequence's pos0 + token count, at most qsa_decode_layer's limit
+ *   ids   [n_tok][2][topk] int32, or NULL: the cells of selected tokens within the sequence, ascending
+ *         (rows of other tokens are not written)
+ *   gate  [n_tok][24][256] fp16, or NULL
+ *   out   [n_tok][24][256] fp16 (written)
+ *   ws    qsa_tree_attention_workspace_bytes(n_seq, n_tok, max_n_kv, params) bytes, 16-byte aligned,
+ *         clobbered; may be NULL when that is 0.  Calls that overlap on the GPU (two streams, two
+ *         captured graphs) need a workspace each.
+ * A sequence whose entry breaks the cache contract, exceeds max_n_kv or has more tokens than its mask
+ * has bits is skipped (its rows are not written) and flagged in the status word (QSA_ERR_DEVICE).
+ * n_tok and n_seq at most 65535; n_tok or n_seq 0 does nothing.
+ */
+QSA_API int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, const uint16_t* ksc,
+                               const uint16_t* vsc, int64_t n_pool, const int32_t* seqs, int n_seq, int n_tok,
+                               const uint32_t* tree, int tree_words, int max_n_kv, int32_t* ids, const uint16_t* gate,
+                               uint16_t* out, void* ws, size_t ws_bytes, const qsa_params* params, void* stream);
+
+/*
+ * qsa_cache_commit - the accepted path of each sequence moved to the front of its drafted cells: for
+ * i < n_path[s], cell pos0 + path[s][i] of sequence s (codes and scales of K and V) is copied to its
+ * cell pos0 + i.  In place, any number of sequences in one launch; cells behind the path keep what
+ * they held.  (pos0 in the table is then advanced by the caller.)
+ *   seqs   as in qsa_tree_attention; first token rows are not read, padding sequences are left alone
+ *   path   DEVICE [n_seq][path_cap] int32: drafted token indices, strictly ascending; entries from
+ *          n_path[s] on are not read
+ *   n_path DEVICE [n_seq] int32, 0 .. path_cap
+ * A sequence whose entry or path breaks these rules (or names a cell past n_cells) is left as it is
+ * and flagged in the status word (QSA_ERR_DEVICE).  n_seq 0 does nothing.
+ */
+QSA_API int qsa_cache_commit(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64_t n_pool, const int32_t* seqs,
+                             int n_seq, const int32_t* path, const int32_t* n_path, int path_cap, void* stream);
+
+/*
  * qsa_debug_wait_probe - a test hook for the failure path of the bounded device waits; the
  * pages have no counterpart.  Launches one CTA whose bounded mbarrier wait (the wait every
  * pipeline of this library uses) is given budget_ns (1 us .. 2 s) on a barrier that nothing

@@ -108,6 +108,23 @@ int check_layer(const uint16_t* q, const int8_t* kq, const uint16_t* ksc, int n_
   return QSA_OK;
 }
 
+// The rope parameters of a prep call (defaults for NULL); sections are checked only where three
+// position axes use them.
+int check_rope(const qsa_rope* in, bool use_sections, qsa_rope* out) {
+  qsa_rope r{10000.f, 256, 1e-6f, {32, 48, 48}};
+  if (in) r = *in;
+  const int rd = r.rotary_dim;
+  if (rd < 16 || rd > 256 || (rd & (rd - 1)))
+    return fail(QSA_ERR_UNSUPPORTED, "rotary_dim must be a power of two in [16, 256] (got %d)", rd);
+  if (!(r.base > 1.f) || !(r.base < 3.0e38f)) return fail(QSA_ERR_INVALID_ARG, "rope base must be > 1 and finite");
+  if (!(r.eps > 0.f) || !(r.eps < 1.f)) return fail(QSA_ERR_INVALID_ARG, "eps must be in (0, 1)");
+  if (use_sections && (r.sections[0] < 0 || r.sections[1] < 0 || r.sections[2] < 0 ||
+                       (long long)r.sections[0] + r.sections[1] + r.sections[2] != rd / 2))
+    return fail(QSA_ERR_INVALID_ARG, "mrope sections must be >= 0 and sum to rotary_dim / 2 = %d", rd / 2);
+  *out = r;
+  return QSA_OK;
+}
+
 // Largest n_kv the fused decode takes on this device (cells per CTA x the largest cluster).
 int decode_layer_limit(int* rc) {
   int c = 0;
@@ -161,8 +178,6 @@ int qsa_prep_quantize(const uint16_t* x, int64_t n_rows, int8_t* xq, uint16_t* x
 int qsa_prep(const uint16_t* q_raw, const uint16_t* k_raw, const uint16_t* v_raw, const float* q_gamma,
              const float* k_gamma, const int32_t* pos3, const qsa_rope* rope, int T, int pos0, int n_cells,
              uint16_t* qcur, uint16_t* kcur, int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, void* stream) {
-  qsa_rope r{10000.f, 256, 1e-6f, {32, 48, 48}};
-  if (rope) r = *rope;
   CHECK_PTR(q_raw, "q_raw");
   CHECK_PTR(k_raw, "k_raw");
   CHECK_PTR(v_raw, "v_raw");
@@ -179,17 +194,12 @@ int qsa_prep(const uint16_t* q_raw, const uint16_t* k_raw, const uint16_t* v_raw
   if (pos0 < 0) return fail(QSA_ERR_INVALID_ARG, "pos0 must be >= 0 (got %d)", pos0);
   if ((long long)pos0 + T > (long long)n_cells)
     return fail(QSA_ERR_INVALID_ARG, "cache too small: pos0 + T = %lld > n_cells = %d", (long long)pos0 + T, n_cells);
-  const int rd = r.rotary_dim;
-  if (rd < 16 || rd > 256 || (rd & (rd - 1)))
-    return fail(QSA_ERR_UNSUPPORTED, "rotary_dim must be a power of two in [16, 256] (got %d)", rd);
-  if (!(r.base > 1.f) || !(r.base < 3.0e38f)) return fail(QSA_ERR_INVALID_ARG, "rope base must be > 1 and finite");
-  if (!(r.eps > 0.f) || !(r.eps < 1.f)) return fail(QSA_ERR_INVALID_ARG, "eps must be in (0, 1)");
-  if (pos3 && (r.sections[0] < 0 || r.sections[1] < 0 || r.sections[2] < 0 ||
-               r.sections[0] + r.sections[1] + r.sections[2] != rd / 2))
-    return fail(QSA_ERR_INVALID_ARG, "mrope sections must be >= 0 and sum to rotary_dim / 2 = %d", rd / 2);
+  qsa_rope r;
+  int rc = check_rope(rope, pos3 != nullptr, &r);
+  if (rc) return rc;
   cudaError_t e = qsa::launch_prep(
       reinterpret_cast<const __half*>(q_raw), reinterpret_cast<const __half*>(k_raw),
-      reinterpret_cast<const __half*>(v_raw), q_gamma, k_gamma, pos3, T, pos0, (double)r.base, rd, r.eps, r.sections,
+      reinterpret_cast<const __half*>(v_raw), q_gamma, k_gamma, pos3, T, pos0, (double)r.base, r.rotary_dim, r.eps, r.sections,
       reinterpret_cast<__half*>(qcur), reinterpret_cast<__half*>(kcur), kq, reinterpret_cast<__half*>(ksc), vq,
       reinterpret_cast<__half*>(vsc), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "qsa_prep launch");
@@ -473,6 +483,155 @@ int qsa_flash_prefill_batched(const uint16_t* q, const int8_t* kq, const int8_t*
                                  reinterpret_cast<__half*>(out), true);
     if (e != cudaSuccess) return cuda_fail(e, "qsa_flash_prefill_batched (selected tokens) launch");
   }
+  return ok();
+}
+
+int qsa_prep_batched(const uint16_t* q_raw, const uint16_t* k_raw, const uint16_t* v_raw, int64_t q_stride,
+                     int64_t k_stride, int64_t v_stride, const float* q_gamma, const float* k_gamma, const int32_t* pos,
+                     int axes, const int32_t* cells, const qsa_rope* rope, int n_tok, int64_t n_pool, uint16_t* qcur,
+                     uint16_t* kcur, int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, void* stream) {
+  if (n_tok < 0) return fail(QSA_ERR_INVALID_ARG, "n_tok must be >= 0 (got %d)", n_tok);
+  if (axes != 1 && axes != 3) return fail(QSA_ERR_INVALID_ARG, "axes must be 1 or 3 (got %d)", axes);
+  qsa_rope r;
+  int rc = check_rope(rope, axes == 3, &r);
+  if (rc) return rc;
+  if (n_pool <= 0 || n_pool > 0x7fffffffLL)
+    return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
+  if (n_tok == 0) return ok();
+  CHECK_PTR(q_raw, "q_raw");
+  CHECK_PTR(k_raw, "k_raw");
+  CHECK_PTR(v_raw, "v_raw");
+  CHECK_PTR(q_gamma, "q_gamma");
+  CHECK_PTR(k_gamma, "k_gamma");
+  CHECK_PTR(pos, "pos");
+  CHECK_PTR(cells, "cells");
+  CHECK_PTR(qcur, "qcur");
+  CHECK_PTR(kq, "kq");
+  CHECK_PTR(ksc, "ksc");
+  CHECK_PTR(vq, "vq");
+  CHECK_PTR(vsc, "vsc");
+  if (kcur && !aligned16(kcur)) return fail(QSA_ERR_INVALID_ARG, "kcur is not 16-byte aligned");
+  const int64_t stride[3] = {q_stride, k_stride, v_stride};
+  const int width[3] = {QSA_N_HEADS * QSA_HEAD_DIM, QSA_N_GROUPS * QSA_HEAD_DIM, QSA_N_GROUPS * QSA_HEAD_DIM};
+  for (int i = 0; i < 3; ++i)
+    if (stride[i] < width[i] || stride[i] % 8)
+      return fail(QSA_ERR_INVALID_ARG, "%c_stride must be a multiple of 8 and at least %d (got %lld)", "qkv"[i], width[i],
+                  (long long)stride[i]);
+  int* st = status_ptr(&rc);
+  if (!st) return rc;
+  cudaError_t e = qsa::launch_prep_batched(
+      reinterpret_cast<const __half*>(q_raw), reinterpret_cast<const __half*>(k_raw),
+      reinterpret_cast<const __half*>(v_raw), q_stride, k_stride, v_stride, q_gamma, k_gamma, pos, axes, cells, n_tok,
+      n_pool, (double)r.base, r.rotary_dim, r.eps, r.sections, reinterpret_cast<__half*>(qcur),
+      reinterpret_cast<__half*>(kcur), kq, reinterpret_cast<__half*>(ksc), vq, reinterpret_cast<__half*>(vsc), st,
+      static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_prep_batched launch");
+  return ok();
+}
+
+int qsa_cache_read(const int8_t* kq, const uint16_t* ksc, const int8_t* vq, const uint16_t* vsc, int64_t n_pool,
+                   const int32_t* cells, int64_t n, uint16_t* k16, uint16_t* v16, void* stream) {
+  if (n < 0) return fail(QSA_ERR_INVALID_ARG, "n must be >= 0");
+  if (n_pool <= 0 || n_pool > 0x7fffffffLL)
+    return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
+  if (!k16 && !v16) return fail(QSA_ERR_INVALID_ARG, "k16 and v16 are both NULL");
+  if (n == 0) return ok();
+  CHECK_PTR(cells, "cells");
+  if (k16) {
+    CHECK_PTR(k16, "k16");
+    CHECK_PTR(kq, "kq");
+    CHECK_PTR(ksc, "ksc");
+  }
+  if (v16) {
+    CHECK_PTR(v16, "v16");
+    CHECK_PTR(vq, "vq");
+    CHECK_PTR(vsc, "vsc");
+  }
+  int rc = 0;
+  int* st = status_ptr(&rc);
+  if (!st) return rc;
+  cudaError_t e = qsa::launch_cache_read(kq, reinterpret_cast<const __half*>(ksc), vq,
+                                         reinterpret_cast<const __half*>(vsc), n_pool, cells, n,
+                                         reinterpret_cast<__half*>(k16), reinterpret_cast<__half*>(v16), st,
+                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_cache_read launch");
+  return ok();
+}
+
+size_t qsa_tree_attention_workspace_bytes(int n_seq, int n_tok, int max_n_kv, const qsa_params* params) {
+  qsa::Params p{};
+  if (n_seq < 1 || n_tok < 1 || max_n_kv < 1 || resolve_params(params, &p) != QSA_OK) return 0;
+  return 0;
+}
+
+int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, const uint16_t* ksc, const uint16_t* vsc,
+                       int64_t n_pool, const int32_t* seqs, int n_seq, int n_tok, const uint32_t* tree, int tree_words,
+                       int max_n_kv, int32_t* ids, const uint16_t* gate, uint16_t* out, void* ws, size_t ws_bytes,
+                       const qsa_params* params, void* stream) {
+  qsa::Params p;
+  int rc = resolve_params(params, &p);
+  if (rc) return rc;
+  if (n_seq < 0 || n_tok < 0)
+    return fail(QSA_ERR_INVALID_ARG, "n_seq and n_tok must be >= 0 (got %d, %d)", n_seq, n_tok);
+  if (n_tok > 65535 || n_seq > 65535)
+    return fail(QSA_ERR_UNSUPPORTED, "n_tok and n_seq must be at most 65535 (got %d, %d)", n_tok, n_seq);
+  if (tree_words < 1 || tree_words > qsa::kTreeWords)
+    return fail(QSA_ERR_UNSUPPORTED, "tree_words must be in [1, %d] (got %d)", qsa::kTreeWords, tree_words);
+  if (n_pool <= 0 || n_pool > 0x7fffffffLL)
+    return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
+  if (n_tok == 0 || n_seq == 0) return ok();
+  CHECK_PTR(q, "q");
+  CHECK_PTR(kq, "kq");
+  CHECK_PTR(vq, "vq");
+  CHECK_PTR(ksc, "ksc");
+  CHECK_PTR(vsc, "vsc");
+  CHECK_PTR(seqs, "seqs");
+  CHECK_PTR(tree, "tree");
+  CHECK_PTR(out, "out");
+  if (ids && !aligned16(ids)) return fail(QSA_ERR_INVALID_ARG, "ids is not 16-byte aligned");
+  if (gate && !aligned16(gate)) return fail(QSA_ERR_INVALID_ARG, "gate is not 16-byte aligned");
+  if (ws && !aligned16(ws)) return fail(QSA_ERR_INVALID_ARG, "ws is not 16-byte aligned");
+  if (max_n_kv < 1) return fail(QSA_ERR_INVALID_ARG, "max_n_kv must be positive (got %d)", max_n_kv);
+  const size_t need = qsa_tree_attention_workspace_bytes(n_seq, n_tok, max_n_kv, params);
+  if (need && (!ws || ws_bytes < need))
+    return fail(QSA_ERR_WORKSPACE, "tree attention workspace of %zu bytes given, %zu needed", ws ? ws_bytes : (size_t)0,
+                need);
+  const int limit = decode_layer_limit(&rc);
+  if (!limit) return rc;
+  if (max_n_kv > limit)
+    return fail(QSA_ERR_UNSUPPORTED, "max_n_kv must be in [1, %d] (got %d)", limit, max_n_kv);
+  int* st = status_ptr(&rc);
+  if (!st) return rc;
+  cudaError_t e = qsa::launch_decode_layer(
+      reinterpret_cast<const __half*>(q), kq, vq, reinterpret_cast<const __half*>(ksc),
+      reinterpret_cast<const __half*>(vsc), reinterpret_cast<const int4*>(seqs), n_seq, (long long)n_pool, 0, 0, n_tok,
+      max_n_kv, ids, reinterpret_cast<const __half*>(gate), nullptr, p, st, static_cast<cudaStream_t>(stream),
+      reinterpret_cast<__half*>(out), false, false, tree, tree_words);
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention launch");
+  return ok();
+}
+
+int qsa_cache_commit(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64_t n_pool, const int32_t* seqs, int n_seq,
+                     const int32_t* path, const int32_t* n_path, int path_cap, void* stream) {
+  if (n_seq < 0) return fail(QSA_ERR_INVALID_ARG, "n_seq must be >= 0 (got %d)", n_seq);
+  if (path_cap < 1) return fail(QSA_ERR_INVALID_ARG, "path_cap must be positive (got %d)", path_cap);
+  if (n_pool <= 0 || n_pool > 0x7fffffffLL)
+    return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
+  if (n_seq == 0) return ok();
+  CHECK_PTR(kq, "kq");
+  CHECK_PTR(ksc, "ksc");
+  CHECK_PTR(vq, "vq");
+  CHECK_PTR(vsc, "vsc");
+  CHECK_PTR(seqs, "seqs");
+  CHECK_PTR(path, "path");
+  CHECK_PTR(n_path, "n_path");
+  int rc = 0;
+  int* st = status_ptr(&rc);
+  if (!st) return rc;
+  cudaError_t e = qsa::launch_cache_commit(kq, reinterpret_cast<__half*>(ksc), vq, reinterpret_cast<__half*>(vsc), n_pool,
+                                           reinterpret_cast<const int4*>(seqs), n_seq, path, n_path, path_cap, st,
+                                           static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_cache_commit launch");
   return ok();
 }
 

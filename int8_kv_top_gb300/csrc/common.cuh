@@ -41,6 +41,7 @@ constexpr int kNB = kD / kBlk;     // scales per row
 constexpr int kChunk = 64;         // decode split size
 constexpr int kPartStride = 258;   // o[256], m, l
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTreeWords = 8;      // 32-bit words of a drafted token's mask row at most (256 drafted tokens)
 
 struct Params {
   int topk;
@@ -126,14 +127,15 @@ cudaError_t launch_decode_partial(const __half* q, const int8_t* kq, const int8_
 
 // Fused decode layer (decode_fused.cu): selection, attention and merge in one launch, one
 // cluster per (token, group).  seqs (device, may be null) lists {first pool cell, n_cells, pos0,
-// first token} per sequence; with null the call is one sequence of n_cells cells at pos0.
+// first token} per sequence; with null the call is one sequence of n_cells cells at pos0.  With
+// `tree` (seqs given) the tokens are drafted ones that see each other by their mask rows.
 int decode_layer_cells_per_cta();
 cudaError_t decode_layer_max_cluster(int* c);
 cudaError_t launch_decode_layer(const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                                 const __half* vsc, const int4* seqs, int n_seq, long long n_pool, int n_cells, int pos0,
                                 int n_tok, int max_n_kv, int32_t* ids, const __half* gate, float* xp, Params p,
                                 int* status, cudaStream_t stream, __half* out16 = nullptr, bool selected_only = false,
-                                bool ids_only = false);
+                                bool ids_only = false, const uint32_t* tree = nullptr, int tree_words = 0);
 
 // Output gate: the elementwise logistic function of the gate input, in fp32, 1 / (1 + e^-x).  The
 // exponential takes the special-function unit; the reciprocal of d = 1 + e^-x (d >= 1, and finite
@@ -163,6 +165,24 @@ cudaError_t launch_prep(const __half* q_raw, const __half* k_raw, const __half* 
                         const float* k_gamma, const int32_t* pos3, int T, int pos0, double base, int rotary_dim,
                         float eps, const int* sections, __half* qcur, __half* kcur, int8_t* kq, __half* ksc,
                         int8_t* vq, __half* vsc, cudaStream_t stream);
+
+// Batched prep (prep.cu): launch_prep's work for tokens of any sequences, each with its own position
+// (pos [n_tok][axes], axes 1 or 3) and its own pool cell (-1: padding, nothing written); rows of
+// token t start at q_raw + t * q_stride and so on.
+cudaError_t launch_prep_batched(const __half* q_raw, const __half* k_raw, const __half* v_raw, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, const float* q_gamma, const float* k_gamma,
+                                const int32_t* pos, int axes, const int32_t* cells, int n_tok, int64_t n_pool,
+                                double base, int rotary_dim, float eps, const int* sections, __half* qcur, __half* kcur,
+                                int8_t* kq, __half* ksc, int8_t* vq, __half* vsc, int* status, cudaStream_t stream);
+
+// Cells of the pool read back as fp16 rows, and the accepted path of each sequence moved to the
+// front of its drafted cells (cache.cu).
+cudaError_t launch_cache_read(const int8_t* kq, const __half* ksc, const int8_t* vq, const __half* vsc, int64_t n_pool,
+                              const int32_t* cells, int64_t n, __half* k16, __half* v16, int* status,
+                              cudaStream_t stream);
+cudaError_t launch_cache_commit(int8_t* kq, __half* ksc, int8_t* vq, __half* vsc, int64_t n_pool, const int4* seqs,
+                                int n_seq, const int32_t* path, const int32_t* n_path, int path_cap, int* status,
+                                cudaStream_t stream);
 
 // The score-GEMM and top-k selection holds caches of up to select_max_cells() cells; longer
 // caches are selected by the single-launch decode layer's cluster kernel (ids only).

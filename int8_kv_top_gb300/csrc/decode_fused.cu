@@ -123,6 +123,10 @@ struct FusedArgs {
   __half* out16;     // [n_tok][24][256] fp16 output instead of xp (a prefill), or null
   int selected_only; // tokens at or under the identity threshold are left to another kernel
   int ids_only;      // the selection alone: ids of selected tokens, no attention (V not read)
+  // drafted-token trees (the kTree kernels, seqs given): token i of a sequence sits at cell pos0 + i
+  // and sees the cells before pos0 and the drafted cells pos0 + j with bit j of its mask row set
+  const uint32_t* tree;  // [n_tok][tree_words]
+  int tree_words, max_n_kv;
 };
 
 // ---------------------------------------------------------------- small helpers
@@ -225,12 +229,15 @@ __device__ __forceinline__ int block_scan(int v, int* s_red, int* total) {
 
 struct Seq {
   long long cell0;  // first pool cell of the sequence
-  int n_kv, tl;     // causal cells of this token, token index within its sequence
+  int n_kv, tl;     // visible cells of this token, token index within its sequence
   bool ok;
+  // trees: committed cells, drafted tokens of the sequence, and a sequence of no cells (padding)
+  int pos0, n_draft;
+  bool padding;
 };
 
 __device__ __forceinline__ Seq resolve_seq(const FusedArgs& a, int t) {
-  Seq s{0, 0, t, true};
+  Seq s{0, 0, t, true, 0, 0, false};
   if (a.seqs == nullptr) {
     s.n_kv = a.pos0 + t + 1;
     return s;
@@ -249,10 +256,23 @@ __device__ __forceinline__ Seq resolve_seq(const FusedArgs& a, int t) {
   // the sequence must hold its tokens' cells inside the pool
   s.ok = e.x >= 0 && e.y >= 1 && e.z >= 0 && e.w <= t && t < next && (long long)e.z + (next - e.w) <= e.y &&
          (long long)e.x + e.y <= a.n_pool;
+  s.pos0 = e.z;
+  s.n_draft = next - e.w;
+  s.padding = e.y == 0;
   return s;
 }
 
-template <int C>
+// Word w of token t's tree mask, with the bits past the sequence's drafted tokens cleared.
+__device__ __forceinline__ uint32_t tree_word(const FusedArgs& a, int t, int w, int n_draft) {
+  const int left = n_draft - 32 * w;
+  if (w >= a.tree_words || left <= 0) return 0u;
+  const uint32_t m = __ldg(a.tree + (size_t)t * a.tree_words + w);
+  return left >= 32 ? m : m & ((1u << left) - 1u);
+}
+
+// kTree: the token's cells are scanned up to the sequence's last drafted cell, and those its mask
+// leaves out are skipped everywhere: not scored, not counted, no candidates, never gathered.
+template <int C, bool kTree>
 __global__ void __launch_bounds__(kFThreads, 1)
     decode_fused_kernel(const FusedArgs a, const __grid_constant__ CUtensorMap tm_codes,
                         const __grid_constant__ CUtensorMap tm_scales) {
@@ -273,16 +293,33 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const int g = blockIdx.y, t = blockIdx.z;
   const Params p = a.p;
   const Seq sq = resolve_seq(a, t);
-  const int n_kv = sq.n_kv;
-  if (!sq.ok || n_kv > C * kMaxW) {  // uniform over the cluster: nobody touches another CTA
+  int n_kv = sq.n_kv, n_scan = sq.n_kv;  // visible cells; cells the cluster divides among its CTAs
+  __shared__ uint32_t s_tree[kTree ? kTreeWords : 1];
+  if constexpr (kTree) {
+    if (sq.padding) return;
+    n_scan = sq.pos0 + sq.n_draft;
+    n_kv = sq.pos0;
+    for (int w = 0; w < kTreeWords; ++w) {
+      const uint32_t m = sq.ok ? tree_word(a, t, w, sq.n_draft) : 0u;
+      n_kv += __popc(m);
+      if (tid == w) s_tree[w] = m;
+    }
+  }
+  // cell c of the sequence is visible to this token
+  auto visible = [&](int c) -> bool {
+    if constexpr (!kTree) return true;
+    const int dj = c - sq.pos0;
+    return dj < 0 || ((s_tree[dj >> 5] >> (dj & 31)) & 1u) != 0u;
+  };
+  if (!sq.ok || n_scan > C * kMaxW || (kTree && (sq.n_draft > 32 * a.tree_words || n_scan > a.max_n_kv))) {  // uniform over the cluster: nobody touches another CTA
     if (tid == 0 && r == 0) set_dev_status(a.status, QSA_DEV_BAD_ID);
     return;
   }
   const bool selected = n_kv > p.identity_max;
   if (!selected && (a.selected_only || a.ids_only)) return;  // uniform over the cluster, before any cluster barrier
   const int K = p.topk;
-  const int W = (n_kv + C - 1) / C;
-  const int c_lo = r * W, c_hi = min(n_kv, c_lo + W), nloc = max(0, c_hi - c_lo);
+  const int W = (n_scan + C - 1) / C;
+  const int c_lo = r * W, c_hi = min(n_scan, c_lo + W), nloc = max(0, c_hi - c_lo);
   const int8_t* kq = a.kq + sq.cell0 * (kGroups * kD);
   const int8_t* vq = a.vq + sq.cell0 * (kGroups * kD);
   const __half* ksc = a.ksc + sq.cell0 * (kGroups * kNB);
@@ -339,6 +376,30 @@ __global__ void __launch_bounds__(kFThreads, 1)
   }
 
   int n_sel = nloc;  // identity: every owned cell
+  // ascending list (s_list) of the owned cells whose status byte is 1
+  auto list_kept = [&]() {
+    constexpr int kPerT = kMaxW / kFThreads;  // 16 consecutive cells per thread
+    static_assert(kPerT == 16, "one 16-byte status read per thread");
+    const int i0 = tid * kPerT;
+    uint32_t keep = 0;  // bit u: cell i0 + u is kept
+    if (i0 < nloc) {
+      const uint4 w = *reinterpret_cast<const uint4*>(s_stat + i0);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int u = 0; u < kPerT; ++u)
+        if (i0 + u < nloc && ((ww[u >> 2] >> (8 * (u & 3))) & 0xFFu) == 1u) keep |= 1u << u;
+    }
+    int total;
+    int off = block_scan(__popc(keep), s_red, &total);
+    while (keep) {
+      const int u = __ffs(keep) - 1;
+      keep &= keep - 1;
+      s_list[off++] = (uint16_t)(i0 + u);
+    }
+    if (tid == 0) s_nlist = total;
+    __syncthreads();
+    n_sel = s_nlist;
+  };
   if (selected) {
     long long* s_qsum = reinterpret_cast<long long*>(sm + kOffQsum);
     __half* s_hl = reinterpret_cast<__half*>(sm + kOffHL);
@@ -426,7 +487,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll
           for (int hr = 0; hr < 2; ++hr) {
             const int lc = cell0 + r8 + 8 * hr;  // local cell
-            if (lc < nloc) {
+            if (lc < nloc && visible(c_lo + lc)) {
               const uint2 sw = *reinterpret_cast<const uint2*>(base + 2 * kBoxB + (16 * warp + r8 + 8 * hr) * 16 + 8 * g);
               const float s0 = __half2float(__ushort_as_half((unsigned short)(sw.x & 0xFFFFu)));
               const float s1 = __half2float(__ushort_as_half((unsigned short)(sw.x >> 16)));
@@ -537,9 +598,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
         const int i = base + tid;
         int st = 0;
         if (i < nloc) {
-          const float f = s_score[i];
-          const float Lf = f - ea - eb * fabsf(f), Uf = f + ea + eb * fabsf(f);
-          st = Lf > Uhi ? 1 : (Uf < Llo ? 0 : 2);
+          if (visible(c_lo + i)) {
+            const float f = s_score[i];
+            const float Lf = f - ea - eb * fabsf(f), Uf = f + ea + eb * fabsf(f);
+            st = Lf > Uhi ? 1 : (Uf < Llo ? 0 : 2);
+          }
           s_stat[i] = (uint8_t)st;
           n_in += st == 1;
           // the V rows of the cells that may be kept go to L2 now, for the attention phase
@@ -721,30 +784,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       cluster_wait();
     }
     __syncthreads();
-    // ---- ascending list of the kept owned cells
-    {
-      constexpr int kPerT = kMaxW / kFThreads;  // 16 consecutive cells per thread
-      static_assert(kPerT == 16, "one 16-byte status read per thread");
-      const int i0 = tid * kPerT;
-      uint32_t keep = 0;  // bit u: cell i0 + u is kept
-      if (i0 < nloc) {
-        const uint4 w = *reinterpret_cast<const uint4*>(s_stat + i0);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int u = 0; u < kPerT; ++u)
-          if (i0 + u < nloc && ((ww[u >> 2] >> (8 * (u & 3))) & 0xFFu) == 1u) keep |= 1u << u;
-      }
-      int total;
-      int off = block_scan(__popc(keep), s_red, &total);
-      while (keep) {
-        const int u = __ffs(keep) - 1;
-        keep &= keep - 1;
-        s_list[off++] = (uint16_t)(i0 + u);
-      }
-      if (tid == 0) s_nlist = total;
-      __syncthreads();
-      n_sel = s_nlist;
-    }
+    list_kept();
     if (a.ids_only) {  // uniform: the kept counts to every CTA, then the ids; no attention
       if (tid < C) st_cluster_u32(mapa_shared(smem_u32(&s_nsel_all[r]), tid), (uint32_t)n_sel);
       cluster_arrive();
@@ -755,7 +795,14 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
   } else {
     // identity: the V rows to L2 while the first batch is set up
-    for (int i = tid; i < nloc; i += kFThreads) prefetch_l2_256(vq + ((size_t)(c_lo + i) * kGroups + g) * kD);
+    for (int i = tid; i < nloc; i += kFThreads) {
+      prefetch_l2_256(vq + ((size_t)(c_lo + i) * kGroups + g) * kD);
+      if constexpr (kTree) s_stat[i] = visible(c_lo + i) ? 1 : 0;
+    }
+    if constexpr (kTree) {
+      __syncthreads();
+      list_kept();
+    }
   }
 
   // ---- 4. attention over the kept owned cells, batches of 64 (bulk copies, two stages)
@@ -769,7 +816,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const int nb = (n_sel + kBatch - 1) / kBatch;
     __half* s_vh = reinterpret_cast<__half*>(sm + kOffVh);
     __half* s_p = reinterpret_cast<__half*>(sm + kOffP);
-    auto cell_of = [&](int i) -> int { return c_lo + (selected ? (int)s_list[i] : i); };
+    auto cell_of = [&](int i) -> int { return c_lo + (selected || kTree ? (int)s_list[i] : i); };
     // cp.async of the batch's K and V rows (16 bytes a piece, 16 pieces a row) and scale lines
     auto issue = [&](int bi) {
       if (bi < nb) {
@@ -980,7 +1027,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       L = fmaf(r_l[qq * 12 + h], w, L);
       O = fmaf(r_o[qq * kPerCta + e], w, O);
     }
-    float v = O / L;
+    float v = kTree && L == 0.f ? 0.f : O / L;  // a mask may leave a token no cell at all
     if (a.gate) v *= gate_sigmoid(__half2float(a.gate[((size_t)t * kHeads + g * kHPG + h) * kD + d]));
     const size_t o = ((size_t)t * kHeads + g * kHPG + h) * kD + d;
     if (a.out16) a.out16[o] = __float2half_rn(v);
@@ -1019,9 +1066,9 @@ int g_dev_of_setup() {
   return dev >= 0 && dev < 64 ? dev : 0;
 }
 
-template <int C>
+template <int C, bool kTree>
 cudaError_t set_attrs() {
-  auto kern = decode_fused_kernel<C>;
+  auto kern = decode_fused_kernel<C, kTree>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
@@ -1034,18 +1081,18 @@ cudaError_t device_setup(int* state) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int s = g_setup[dev].load(std::memory_order_acquire);
   if (s == 0) {
-    if ((e = set_attrs<2>()) != cudaSuccess) return e;
-    if ((e = set_attrs<4>()) != cudaSuccess) return e;
-    if ((e = set_attrs<8>()) != cudaSuccess) return e;
-    if ((e = set_attrs<16>()) != cudaSuccess) return e;
+    if ((e = set_attrs<2, false>()) != cudaSuccess || (e = set_attrs<2, true>()) != cudaSuccess) return e;
+    if ((e = set_attrs<4, false>()) != cudaSuccess || (e = set_attrs<4, true>()) != cudaSuccess) return e;
+    if ((e = set_attrs<8, false>()) != cudaSuccess || (e = set_attrs<8, true>()) != cudaSuccess) return e;
+    if ((e = set_attrs<16, false>()) != cudaSuccess || (e = set_attrs<16, true>()) != cudaSuccess) return e;
     int nmax[4] = {0, 0, 0, 0};
     for (int i = 0; i < 4; ++i) {
       cudaLaunchAttribute attr[2];
       cudaLaunchConfig_t cfg = launch_config(kClusterSizes[i], 1, nullptr, attr);
-      e = i == 0   ? cudaOccupancyMaxActiveClusters(&nmax[i], decode_fused_kernel<2>, &cfg)
-          : i == 1 ? cudaOccupancyMaxActiveClusters(&nmax[i], decode_fused_kernel<4>, &cfg)
-          : i == 2 ? cudaOccupancyMaxActiveClusters(&nmax[i], decode_fused_kernel<8>, &cfg)
-                   : cudaOccupancyMaxActiveClusters(&nmax[i], decode_fused_kernel<16>, &cfg);
+      e = i == 0   ? cudaOccupancyMaxActiveClusters(&nmax[i], decode_fused_kernel<2, false>, &cfg)
+          : i == 1 ? cudaOccupancyMaxActiveClusters(&nmax[i], decode_fused_kernel<4, false>, &cfg)
+          : i == 2 ? cudaOccupancyMaxActiveClusters(&nmax[i], decode_fused_kernel<8, false>, &cfg)
+                   : cudaOccupancyMaxActiveClusters(&nmax[i], decode_fused_kernel<16, false>, &cfg);
       if (e != cudaSuccess) return e;
     }
     if (nmax[2] <= 0) return cudaErrorInvalidConfiguration;  // clusters of 8 are portable
@@ -1060,7 +1107,7 @@ cudaError_t device_setup(int* state) {
 template <int C>
 cudaError_t launch_c(const FusedArgs& a, int n_tok, const CUtensorMap& tmc, const CUtensorMap& tms,
                      cudaStream_t stream) {
-  auto kern = decode_fused_kernel<C>;
+  auto kern = a.tree ? decode_fused_kernel<C, true> : decode_fused_kernel<C, false>;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = launch_config(C, n_tok, stream, attr);
   return cudaLaunchKernelEx(&cfg, kern, a, tmc, tms);
@@ -1103,9 +1150,9 @@ cudaError_t launch_decode_layer(const __half* q, const int8_t* kq, const int8_t*
                                 const __half* vsc, const int4* seqs, int n_seq, long long n_pool, int n_cells, int pos0,
                                 int n_tok, int max_n_kv, int32_t* ids, const __half* gate, float* xp, Params p,
                                 int* status, cudaStream_t stream, __half* out16, bool selected_only,
-                                bool ids_only) {
+                                bool ids_only, const uint32_t* tree, int tree_words) {
   FusedArgs a{q, kq, vq, ksc, vsc, seqs, n_seq, n_pool, n_cells, pos0, ids, gate, xp, p, status, out16,
-              selected_only ? 1 : 0, ids_only ? 1 : 0};
+              selected_only ? 1 : 0, ids_only ? 1 : 0, tree, tree_words, max_n_kv};
   int state = 0;
   cudaError_t e = device_setup(&state);
   if (e != cudaSuccess) return e;

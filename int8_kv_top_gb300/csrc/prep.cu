@@ -19,6 +19,8 @@
 // lanes l >= R hold 8 consecutive unrotated dims rd + 8 (l - R) ..; so every lane holds 8 values in
 // two 4-dim runs at dims (a, b), the rotation needs no exchange between lanes, and the row's
 // sum of squares and the quantiser's four 64-element block maxima are warp reductions.
+#include <cmath>
+
 #include "common.cuh"
 
 namespace qsa {
@@ -213,6 +215,103 @@ __global__ void __launch_bounds__(256, 5) prep_kernel(const __half* __restrict__
   }
 }
 
+// ---------------------------------------------------------------- batched form
+// qsa_prep_batched: the same rows for tokens of any sequences.  Token t has its own position(s) and
+// its own pool cell, and its rows start at t times a stride (slices of a fused projection).
+struct BatchedCfg {
+  uint64_t turns[kD / 2];  // base^(-2i / rd) / (2 pi) as a 0.64 fixed-point fraction of a turn
+  int rotary_dim, sec0, sec1, axes;
+  float eps;
+};
+
+// (cos, sin) of p * base^(-2i / rd) for any 32-bit position: the product of the integer position and
+// the fixed-point frequency wraps at whole turns by itself, so its top 32 bits are the angle as a
+// signed fraction of a turn, within |p| 2^-54 turns (the frequency is a double) and 2^-32 turns of the
+// exact one.
+__device__ __forceinline__ float2 rope_cos_sin(int p, uint64_t turns) {
+  const int64_t prod = (int64_t)((uint64_t)(int64_t)p * turns);
+  float sn, cs;
+  sincospif((float)(int)(prod >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31: half turns
+  return make_float2(cs, sn);
+}
+
+__global__ void __launch_bounds__(256, 5)
+    prep_batched_kernel(const __half* __restrict__ q_raw, const __half* __restrict__ k_raw,
+                        const __half* __restrict__ v_raw, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                        const float* __restrict__ q_gamma, const float* __restrict__ k_gamma,
+                        const int32_t* __restrict__ pos, const int32_t* __restrict__ cells, int64_t n_pool,
+                        const __grid_constant__ BatchedCfg cfg, __half* __restrict__ qcur, __half* __restrict__ kcur,
+                        int8_t* __restrict__ kq, __half* __restrict__ ksc, int8_t* __restrict__ vq,
+                        __half* __restrict__ vsc, int* status) {
+  __shared__ float2 s_cs[kD / 2];
+  pdl_begin();
+  const int t = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cell = __ldg(cells + t);
+  if (cell < 0 || cell >= n_pool) {  // uniform
+    if (cell != -1 && tid == 0) set_dev_status(status, QSA_DEV_BAD_ID);
+    return;
+  }
+  const int rd = cfg.rotary_dim, h2 = rd / 2;
+  const bool rot_lane = lane < (rd >> 3);
+  int da, db;
+  lane_dims(lane, rd, da, db);
+  if (tid < h2) {
+    const int axis = tid < cfg.sec0 ? 0 : (tid < cfg.sec0 + cfg.sec1 ? 1 : 2);
+    s_cs[tid] = rope_cos_sin(__ldg(pos + (int64_t)t * cfg.axes + (cfg.axes == 3 ? axis : 0)), cfg.turns[tid]);
+  }
+  __syncthreads();
+  float2 cs4[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) cs4[u] = rot_lane ? s_cs[da + u] : make_float2(1.f, 0.f);
+  for (int r = warp; r < kPrepRows; r += 8) {
+    const bool is_v = r >= kHeads + kGroups, is_k = !is_v && r >= kHeads;
+    const int g = is_v ? r - kHeads - kGroups : r - kHeads;
+    const __half* src = is_v ? v_raw + t * v_stride + g * kD : is_k ? k_raw + t * k_stride + g * kD : q_raw + t * q_stride + r * kD;
+    float x[8];
+    unpack4(__ldg(reinterpret_cast<const uint2*>(src + da)), x);
+    unpack4(__ldg(reinterpret_cast<const uint2*>(src + db)), x + 4);
+    if (!is_v) {
+      float ss = 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) ss = fmaf(x[u], x[u], ss);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float rs = 1.f / sqrtf(ss * (1.f / kD) + cfg.eps);
+      const float* gam = is_k ? k_gamma : q_gamma;
+      const float4 ga = __ldg(reinterpret_cast<const float4*>(gam + da));
+      const float4 gb = __ldg(reinterpret_cast<const float4*>(gam + db));
+      const float gw[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = x[u] * rs * gw[u];
+      if (rot_lane) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float lo = x[u], hi = x[4 + u];
+          x[u] = lo * cs4[u].x - hi * cs4[u].y;
+          x[4 + u] = hi * cs4[u].x + lo * cs4[u].y;
+        }
+      }
+      uint32_t ow[4];  // the fp16 rounding of the row: what attends, and for k what the cache holds quantised
+#pragma unroll
+      for (int u = 0; u < 4; ++u) ow[u] = pack_half2(x[2 * u], x[2 * u + 1]);
+      __half* dst = is_k ? (kcur ? kcur + ((size_t)t * kGroups + g) * kD : nullptr) : qcur + ((size_t)t * kHeads + r) * kD;
+      if (dst) {
+        *reinterpret_cast<uint2*>(dst + da) = make_uint2(ow[0], ow[1]);
+        *reinterpret_cast<uint2*>(dst + db) = make_uint2(ow[2], ow[3]);
+      }
+      if (!is_k) continue;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ow[u]));
+        x[2 * u] = f.x;
+        x[2 * u + 1] = f.y;
+      }
+    }
+    quantize_row(x, da, db, (is_k ? kq : vq) + ((size_t)cell * kGroups + g) * kD,
+                 (is_k ? ksc : vsc) + ((size_t)cell * kGroups + g) * kNB, lane);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_prep(const __half* q_raw, const __half* k_raw, const __half* v_raw, const float* q_gamma,
@@ -231,6 +330,23 @@ cudaError_t launch_prep(const __half* q_raw, const __half* k_raw, const __half* 
   cfg.eps = eps;
   return launch_pdl(prep_kernel, dim3(T), dim3(256), 0, stream, q_raw, k_raw, v_raw, q_gamma, k_gamma, pos3, pos0, cfg,
                     qcur, kcur, kq, ksc, vq, vsc);
+}
+
+cudaError_t launch_prep_batched(const __half* q_raw, const __half* k_raw, const __half* v_raw, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, const float* q_gamma, const float* k_gamma,
+                                const int32_t* pos, int axes, const int32_t* cells, int n_tok, int64_t n_pool,
+                                double base, int rotary_dim, float eps, const int* sections, __half* qcur, __half* kcur,
+                                int8_t* kq, __half* ksc, int8_t* vq, __half* vsc, int* status, cudaStream_t stream) {
+  BatchedCfg cfg{};
+  for (int i = 0; i < rotary_dim / 2; ++i)
+    cfg.turns[i] = (uint64_t)llround(ldexp(pow(base, -2.0 * i / rotary_dim) / 6.283185307179586, 64));
+  cfg.rotary_dim = rotary_dim;
+  cfg.sec0 = sections[0];
+  cfg.sec1 = sections[1];
+  cfg.axes = axes;
+  cfg.eps = eps;
+  return launch_pdl(prep_batched_kernel, dim3(n_tok), dim3(256), 0, stream, q_raw, k_raw, v_raw, q_stride, k_stride,
+                    v_stride, q_gamma, k_gamma, pos, cells, n_pool, cfg, qcur, kcur, kq, ksc, vq, vsc, status);
 }
 
 }  // namespace qsa

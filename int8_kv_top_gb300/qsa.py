@@ -31,7 +31,8 @@ EXPORTS = ("qsa_last_error", "qsa_prep_quantize", "qsa_prep", "qsa_select_worksp
            "qsa_flash_prefill_workspace_bytes", "qsa_flash_prefill",
            "qsa_flash_prefill_gated", "qsa_decode_partial", "qsa_merge", "qsa_merge_gated", "qsa_decode_layer",
            "qsa_decode_layer_batched", "qsa_flash_prefill_batched_workspace_bytes", "qsa_flash_prefill_batched",
-           "qsa_check_device_status", "qsa_select_noalloc", "qsa_debug_wait_probe")
+           "qsa_check_device_status", "qsa_select_noalloc", "qsa_debug_wait_probe", "qsa_prep_batched", "qsa_cache_read",
+           "qsa_tree_attention_workspace_bytes", "qsa_tree_attention", "qsa_cache_commit")
 
 
 class QSAError(RuntimeError):
@@ -81,12 +82,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qsa_flash_prefill_batched_workspace_bytes.argtypes = [I, I, I, PP]
     lib.qsa_flash_prefill_batched_workspace_bytes.restype = SZ
     lib.qsa_flash_prefill_batched.argtypes = [P, P, P, P, P, I64, P, I, I, I, P, P, P, P, SZ, PP, P]
+    lib.qsa_prep_batched.argtypes = [P, P, P, I64, I64, I64, P, P, P, I, P, ctypes.POINTER(qsa_rope), I, I64, P, P, P, P,
+                                     P, P, P]
+    lib.qsa_cache_read.argtypes = [P, P, P, P, I64, P, I64, P, P, P]
+    lib.qsa_tree_attention_workspace_bytes.argtypes = [I, I, I, PP]
+    lib.qsa_tree_attention_workspace_bytes.restype = SZ
+    lib.qsa_tree_attention.argtypes = [P, P, P, P, P, I64, P, I, I, P, I, I, P, P, P, P, SZ, PP, P]
+    lib.qsa_cache_commit.argtypes = [P, P, P, P, I64, P, I, P, P, I, P]
     lib.qsa_check_device_status.argtypes = [P]
     lib.qsa_debug_wait_probe.argtypes = [ctypes.c_uint64, P]
     lib.qsa_select_noalloc.argtypes = [P, P, P, I, I, I, P, PP, P]
     for name in EXPORTS:
         if name not in ("qsa_last_error", "qsa_select_workspace_bytes", "qsa_flash_prefill_workspace_bytes",
-                        "qsa_flash_prefill_batched_workspace_bytes"):
+                        "qsa_flash_prefill_batched_workspace_bytes", "qsa_tree_attention_workspace_bytes"):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -115,6 +123,13 @@ def _params(params):
     return ctypes.byref(qsa_params(int(topk), int(identity_max), float(sm_scale)))
 
 
+def _rope(rope):
+    if rope is None:
+        return None
+    base, rd, eps, sec = rope
+    return qsa_rope(float(base), int(rd), float(eps), (ctypes.c_int * 3)(*sec))
+
+
 def _check(rc: int):
     if rc != QSA_OK:
         raise QSAError(rc, load().qsa_last_error().decode(errors="replace"))
@@ -133,11 +148,7 @@ def qsa_prep(q_raw, k_raw, v_raw, q_gamma, k_gamma, T: int, pos0: int, n_cells: 
              pos3=None, rope=None, stream=None):
     """Fused prep: norm + rotary of q and k, qcur / kcur and the new tokens' int8 cache rows.
     rope: None or (base, rotary_dim, eps, (s0, s1, s2))."""
-    r = None
-    if rope is not None:
-        base, rd, eps, sec = rope
-        r = ctypes.byref(qsa_rope(float(base), int(rd), float(eps), (ctypes.c_int * 3)(*sec)))
-    _check(load().qsa_prep(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(q_gamma), _ptr(k_gamma), _ptr(pos3), r, T,
+    _check(load().qsa_prep(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(q_gamma), _ptr(k_gamma), _ptr(pos3), _rope(rope), T,
                            pos0, n_cells, _ptr(qcur), _ptr(kcur), _ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc),
                            _stream(stream)))
 
@@ -217,6 +228,49 @@ def qsa_flash_prefill_batched(q, kq, vq, ksc, vsc, n_pool: int, seqs, n_seq: int
     _check(load().qsa_flash_prefill_batched(_ptr(q), _ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), n_pool, _ptr(seqs),
                                             n_seq, n_tok, max_n_kv, _ptr(ids), _ptr(gate), _ptr(out), _ptr(ws),
                                             ws_bytes, _params(params), _stream(stream)))
+
+
+def _row_stride(t, width: int) -> int:
+    """Elements between two tokens' rows of a raw projection [n_tok, ...] (a slice of a wider one, say); the
+    elements of a token's own row lie side by side."""
+    return width if t.shape[0] <= 1 else t.stride(0)
+
+
+def qsa_prep_batched(q_raw, k_raw, v_raw, q_gamma, k_gamma, pos, cells, n_tok: int, n_pool: int, qcur, kcur, kq, ksc, vq,
+                     vsc, rope=None, stream=None):
+    """qsa_prep for tokens of any sequences: pos int32 [n_tok] or [n_tok, 1 or 3], cells int32 [n_tok] (-1: padding).
+    q_raw, k_raw and v_raw may be slices along a token's row of a fused projection; kcur may be None."""
+    axes = pos.shape[1] if pos.dim() > 1 else 1
+    kv = N_GROUPS * HEAD_DIM
+    _check(load().qsa_prep_batched(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _row_stride(q_raw, N_HEADS * HEAD_DIM),
+                                   _row_stride(k_raw, kv), _row_stride(v_raw, kv), _ptr(q_gamma), _ptr(k_gamma), _ptr(pos),
+                                   axes, _ptr(cells), _rope(rope), n_tok, n_pool, _ptr(qcur), _ptr(kcur), _ptr(kq),
+                                   _ptr(ksc), _ptr(vq), _ptr(vsc), _stream(stream)))
+
+
+def qsa_cache_read(kq, ksc, vq, vsc, n_pool: int, cells, n: int, k16, v16, stream=None):
+    """Cells of the pool as fp16 rows; k16 or v16 may be None."""
+    _check(load().qsa_cache_read(_ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), n_pool, _ptr(cells), n, _ptr(k16), _ptr(v16),
+                                 _stream(stream)))
+
+
+def qsa_tree_attention_workspace_bytes(n_seq: int, n_tok: int, max_n_kv: int, params=None) -> int:
+    return int(load().qsa_tree_attention_workspace_bytes(n_seq, n_tok, max_n_kv, _params(params)))
+
+
+def qsa_tree_attention(q, kq, vq, ksc, vsc, n_pool: int, seqs, n_seq: int, n_tok: int, tree, max_n_kv: int, ids, out,
+                       ws=None, params=None, stream=None, gate=None):
+    """Attention of drafted token trees; tree is an int32 or uint32 tensor [n_tok, words] of mask bits."""
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(load().qsa_tree_attention(_ptr(q), _ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), n_pool, _ptr(seqs), n_seq, n_tok,
+                                     _ptr(tree), tree.shape[1], max_n_kv, _ptr(ids), _ptr(gate), _ptr(out), _ptr(ws),
+                                     ws_bytes, _params(params), _stream(stream)))
+
+
+def qsa_cache_commit(kq, ksc, vq, vsc, n_pool: int, seqs, n_seq: int, path, n_path, stream=None):
+    """The accepted paths (path int32 [n_seq, cap], n_path int32 [n_seq]) moved to the front of the drafted cells."""
+    _check(load().qsa_cache_commit(_ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), n_pool, _ptr(seqs), n_seq, _ptr(path),
+                                   _ptr(n_path), path.shape[1], _stream(stream)))
 
 
 def qsa_debug_wait_probe(budget_ns: int, stream=None):
