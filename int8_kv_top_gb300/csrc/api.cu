@@ -602,12 +602,19 @@ int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, co
     return fail(QSA_ERR_UNSUPPORTED, "max_n_kv must be in [1, %d] (got %d)", limit, max_n_kv);
   int* st = status_ptr(&rc);
   if (!st) return rc;
-  cudaError_t e = qsa::launch_decode_layer(
-      reinterpret_cast<const __half*>(q), kq, vq, reinterpret_cast<const __half*>(ksc),
-      reinterpret_cast<const __half*>(vsc), reinterpret_cast<const int4*>(seqs), n_seq, (long long)n_pool, 0, 0, n_tok,
-      max_n_kv, ids, reinterpret_cast<const __half*>(gate), nullptr, p, st, static_cast<cudaStream_t>(stream),
-      reinterpret_cast<__half*>(out), false, false, tree, tree_words);
-  if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention launch");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int4* sq = reinterpret_cast<const int4*>(seqs);
+  const __half *hq = reinterpret_cast<const __half*>(q), *hg = reinterpret_cast<const __half*>(gate);
+  const __half *hksc = reinterpret_cast<const __half*>(ksc), *hvsc = reinterpret_cast<const __half*>(vsc);
+  __half* hout = reinterpret_cast<__half*>(out);
+  cudaError_t e = qsa::launch_tree_dense(hq, kq, vq, hksc, hvsc, (long long)n_pool, sq, n_seq, n_tok, tree, tree_words,
+                                         max_n_kv, hg, hout, p, st, s);
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention (identity tokens) launch");
+  if (max_n_kv > p.identity_max) {
+    e = qsa::launch_decode_layer(hq, kq, vq, hksc, hvsc, sq, n_seq, (long long)n_pool, 0, 0, n_tok, max_n_kv, ids, hg,
+                                 nullptr, p, st, s, hout, true, false, tree, tree_words);
+    if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention (selected tokens) launch");
+  }
   return ok();
 }
 

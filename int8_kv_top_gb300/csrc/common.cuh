@@ -137,6 +137,13 @@ cudaError_t launch_decode_layer(const __half* q, const int8_t* kq, const int8_t*
                                 int* status, cudaStream_t stream, __half* out16 = nullptr, bool selected_only = false,
                                 bool ids_only = false, const uint32_t* tree = nullptr, int tree_words = 0);
 
+// Drafted-token trees, identity tokens (tree.cu): every visible cell, on the tensor cores; tokens above the
+// threshold are left to launch_decode_layer.
+cudaError_t launch_tree_dense(const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc, const __half* vsc,
+                              long long n_pool, const int4* seqs, int n_seq, int n_tok, const uint32_t* tree,
+                              int tree_words, int max_n_kv, const __half* gate, __half* out, Params p, int* status,
+                              cudaStream_t stream);
+
 // Output gate: the elementwise logistic function of the gate input, in fp32, 1 / (1 + e^-x).  The
 // exponential takes the special-function unit; the reciprocal of d = 1 + e^-x (d >= 1, and finite
 // for |x| <= 80, past which the result is 0 or 1 in every output format) is formed on the FMA
