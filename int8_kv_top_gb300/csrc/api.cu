@@ -7,7 +7,7 @@
 #include <mutex>
 
 #include "../../include/qsa.h"
-#include "common.cuh"
+#include "tree_common.cuh"
 
 namespace qsa {
 
@@ -134,6 +134,12 @@ int decode_layer_limit(int* rc) {
     return 0;
   }
   return c * qsa::decode_layer_cells_per_cta();
+}
+
+// Whether a tree call selects for its tokens together (tree_select.cu, then one tensor-core attention for all)
+// or gives each selected (token, group) a cluster of its own.
+bool tree_selects_together(int n_seq, int n_tok, int max_n_kv, const qsa::Params& p) {
+  return max_n_kv > p.identity_max && max_n_kv <= qsa::select_max_cells() && n_tok >= 2LL * n_seq;
 }
 
 // Selection over a cache longer than the score-GEMM path holds: the single-launch decode layer's
@@ -561,7 +567,7 @@ int qsa_cache_read(const int8_t* kq, const uint16_t* ksc, const int8_t* vq, cons
 size_t qsa_tree_attention_workspace_bytes(int n_seq, int n_tok, int max_n_kv, const qsa_params* params) {
   qsa::Params p{};
   if (n_seq < 1 || n_tok < 1 || max_n_kv < 1 || resolve_params(params, &p) != QSA_OK) return 0;
-  return 0;
+  return tree_selects_together(n_seq, n_tok, max_n_kv, p) ? qsa::tree_select_layout(n_seq, n_tok, max_n_kv, nullptr, nullptr) : 0;
 }
 
 int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, const uint16_t* ksc, const uint16_t* vsc,
@@ -607,10 +613,18 @@ int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, co
   const __half *hq = reinterpret_cast<const __half*>(q), *hg = reinterpret_cast<const __half*>(gate);
   const __half *hksc = reinterpret_cast<const __half*>(ksc), *hvsc = reinterpret_cast<const __half*>(vsc);
   __half* hout = reinterpret_cast<__half*>(out);
-  cudaError_t e = qsa::launch_tree_dense(hq, kq, vq, hksc, hvsc, (long long)n_pool, sq, n_seq, n_tok, tree, tree_words,
-                                         max_n_kv, hg, hout, p, st, s);
-  if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention (identity tokens) launch");
-  if (max_n_kv > p.identity_max) {
+  const qsa::TreeBatch b{sq, (long long)n_pool, n_seq, n_tok, tree, tree_words, max_n_kv, p.identity_max};
+  const bool together = tree_selects_together(n_seq, n_tok, max_n_kv, p);
+  qsa::TreeSelect w{};
+  cudaError_t e;
+  if (together) {
+    qsa::tree_select_layout(n_seq, n_tok, max_n_kv, ws, &w);
+    e = qsa::launch_tree_select(b, w, hq, kq, hksc, ids, p, st, s);
+    if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention (selection) launch");
+  }
+  e = qsa::launch_tree_dense(b, hq, kq, vq, hksc, hvsc, w.bits, w.pitch / 32, hg, hout, p.sm_scale, st, s);
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention launch");
+  if (max_n_kv > p.identity_max && !together) {
     e = qsa::launch_decode_layer(hq, kq, vq, hksc, hvsc, sq, n_seq, (long long)n_pool, 0, 0, n_tok, max_n_kv, ids, hg,
                                  nullptr, p, st, s, hout, true, false, tree, tree_words);
     if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention (selected tokens) launch");

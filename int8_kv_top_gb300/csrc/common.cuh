@@ -137,12 +137,20 @@ cudaError_t launch_decode_layer(const __half* q, const int8_t* kq, const int8_t*
                                 int* status, cudaStream_t stream, __half* out16 = nullptr, bool selected_only = false,
                                 bool ids_only = false, const uint32_t* tree = nullptr, int tree_words = 0);
 
-// Drafted-token trees, identity tokens (tree.cu): every visible cell, on the tensor cores; tokens above the
-// threshold are left to launch_decode_layer.
-cudaError_t launch_tree_dense(const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc, const __half* vsc,
-                              long long n_pool, const int4* seqs, int n_seq, int n_tok, const uint32_t* tree,
-                              int tree_words, int max_n_kv, const __half* gate, __half* out, Params p, int* status,
-                              cudaStream_t stream);
+// Drafted-token trees (tree.cu, tree_select.cu, tree_common.cuh).  launch_tree_dense attends on the tensor
+// cores: identity tokens over every visible cell and, where `bits` gives them, selected tokens over their
+// selected cells (without it they are left to launch_decode_layer).  launch_tree_select makes those bits, and
+// the ids where asked, for every selected token of a call of at most select_max_cells() cells.
+struct TreeBatch;
+struct TreeSelect;
+size_t tree_select_layout(int n_seq, int n_tok, int max_n_kv, void* ws, TreeSelect* out);
+cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __half* q, const int8_t* kq,
+                               const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream);
+cudaError_t launch_tree_topk(const TreeBatch& b, const TreeSelect& w, const __half* q, const int8_t* kq,
+                             const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream);
+cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
+                              const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
+                              float sm_scale, int* status, cudaStream_t stream);
 
 // Output gate: the elementwise logistic function of the gate input, in fp32, 1 / (1 + e^-x).  The
 // exponential takes the special-function unit; the reciprocal of d = 1 + e^-x (d >= 1, and finite

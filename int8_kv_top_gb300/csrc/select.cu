@@ -33,6 +33,7 @@
 //              select over recomputed keys.  Ids are emitted in ascending order.
 #include "common.cuh"
 #include "select_math.cuh"
+#include "tree_common.cuh"
 
 namespace qsa {
 namespace {
@@ -718,12 +719,15 @@ __device__ uint32_t first_key_warp(P pred) {
 // One 512-thread CTA per (token, group).  Thread tid owns cells [tid*V, tid*V + V) of the
 // row in registers (fp16 pairs); every pass over the row is a packed fp16 compare against a
 // threshold, because the error-band tests are monotone in the stored score.
-template <int V>
+//
+// kTree: rows are the drafted tokens of a tree batch (row, group); the scores of cells that a token does not
+// see are -inf, its selected cells go to a bitmap as well, and `ids` may be null.
+template <int V, bool kTree>
 __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     topk_kernel(const __half* __restrict__ scores, const __half* __restrict__ q, const int8_t* __restrict__ kq,
                 const __half* __restrict__ ksc, const float* __restrict__ eh, const float* __restrict__ kmax,
                 const unsigned* __restrict__ hist1, int32_t* __restrict__ ids, int t_sel, int T_sel, int n_pad,
-                int pos0, int K, float sm_scale, int* status) {
+                int pos0, int K, float sm_scale, int* status, const TreeBatch tb, const TreeSelect ts) {
   pdl_begin();
   extern __shared__ __align__(16) uint8_t topk_smem[];
   unsigned* s_hist = reinterpret_cast<unsigned*>(topk_smem);                   // [2][256]
@@ -747,8 +751,32 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int nwarps = kTkThreads / 32;
   const int t = t_sel + r;
-  const int n_kv = pos0 + t + 1;
+  int n_kv = pos0 + t + 1;  // cells of the row
   const __half* row = scores + ((size_t)g * T_sel + r) * n_pad;
+  float row_scale = 1.f;    // of the stored scores
+  float km[kNB];
+  if constexpr (kTree) {
+    const int s = warp_find_seq(tb.n_seq, t, [&](int i) { return (long long)__ldg(&tb.seqs[i].w); });
+    int4 e;
+    const int T = tree_seq_tokens(tb, s, &e);
+    if (T <= 0 || t < e.w || t >= e.w + T) return;  // uniform, as all that follows
+    int seen = e.z;
+    for (int w = 0; w < tb.tree_words; ++w) seen += __popc(tree_mask_word(tb, t, w, T));
+    if (seen <= tb.identity_max) return;
+    n_kv = e.z + T;
+    kq += (size_t)e.x * (kGroups * kD);
+    ksc += (size_t)e.x * (kGroups * kNB);
+    const float* kc = kmax + (size_t)s * ts.chunks * (kGroups * kNB) + g * kNB;
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) km[b] = 0.f;
+    for (int c = 0; c * kTreeChunk < n_kv; ++c)
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) km[b] = fmaxf(km[b], __ldg(kc + c * (kGroups * kNB) + b));
+    row_scale = tree_row_scale(eh + ((size_t)g * T_sel + r) * 8, km, sm_scale);
+  } else {
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) km[b] = kmax[g * kNB + b];
+  }
   // few-row calls: the row's high-byte histogram, loaded now so its latency overlaps the row's
   const unsigned h1_pre = (hist1 != nullptr && tid < 256) ? __ldg(hist1 + ((size_t)g * T_sel + r) * 256 + tid) : 0u;
 
@@ -768,8 +796,8 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     // fp16 rounding of the stored score.  Both doubled for margin.
     const float* e = eh + ((size_t)g * T_sel + r) * 8;
     float acc = 0.f;
-    for (int b = 0; b < kNB; ++b) acc += kmax[g * kNB + b] * (e[b] + e[kNB + b] * (1.5258789e-05f + 4.7683716e-07f));
-    s_bound.a = 2.f * (sm_scale * 128.f * acc + 1.2e-7f);
+    for (int b = 0; b < kNB; ++b) acc += km[b] * (e[b] + e[kNB + b] * (1.5258789e-05f + 4.7683716e-07f));
+    s_bound.a = 2.f * (sm_scale * row_scale * 128.f * acc + 1.2e-7f);
     s_bound.b = 2.f * 4.8852e-04f;
     s_cnt[0] = 0;
     s_cnt[1] = 0;
@@ -1124,6 +1152,13 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
   int total;
   int pos = block_excl_scan(n_keep, s_red, &total);
   if (total != K && tid == 0) set_dev_status(status, QSA_DEV_BAND_OVERFLOW);
+  if constexpr (kTree) {
+    uint8_t* brow = reinterpret_cast<uint8_t*>(ts.bits + (size_t)(g * tb.n_tok + t) * (ts.pitch / 32));
+#pragma unroll
+    for (int m = 0; m < V / 8; m += 2)  // 16 cells; the pitch is a multiple of 256
+      if (c0 + 8 * m < n_pad) *reinterpret_cast<uint16_t*>(brow + (c0 >> 3) + m) = (uint16_t)(keep[m] | (keep[m + 1] << 8));
+    if (ids == nullptr) return;
+  }
   int32_t* dst = ids + ((size_t)t * kGroups + g) * K;
 #pragma unroll
   for (int m = 0; m < V / 8; ++m) {
@@ -1255,12 +1290,27 @@ cudaError_t launch_select(const __half* q, const int8_t* kq, const __half* ksc, 
     if (err != cudaSuccess) return err;
     const unsigned* h1 = L.T_sel <= kSmallRows ? hist1 : nullptr;
     return launch_pdl(kern, grid, dim3(kTkThreads), kTopkSmem, stream, sc, q, kq, ksc, eh, kmax, h1, ids, L.t_sel,
-                      L.T_sel, L.n_pad, pos0, p.topk, p.sm_scale, status);
+                      L.T_sel, L.n_pad, pos0, p.topk, p.sm_scale, status, TreeBatch{}, TreeSelect{});
   };
-  if (L.n_max <= 16 * kTkThreads) return run(topk_kernel<16>);
-  if (L.n_max <= 32 * kTkThreads) return run(topk_kernel<32>);
-  if (L.n_max <= 64 * kTkThreads) return run(topk_kernel<64>);
-  return run(topk_kernel<128>);
+  if (L.n_max <= 16 * kTkThreads) return run(topk_kernel<16, false>);
+  if (L.n_max <= 32 * kTkThreads) return run(topk_kernel<32, false>);
+  if (L.n_max <= 64 * kTkThreads) return run(topk_kernel<64, false>);
+  return run(topk_kernel<128, false>);
+}
+
+cudaError_t launch_tree_topk(const TreeBatch& b, const TreeSelect& w, const __half* q, const int8_t* kq,
+                             const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream) {
+  auto run = [&](auto kern) -> cudaError_t {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopkSmem);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kern, dim3(b.n_tok, kGroups), dim3(kTkThreads), kTopkSmem, stream, w.scores, q, kq, ksc, w.eh,
+                      w.kmax, static_cast<const unsigned*>(nullptr), ids, 0, b.n_tok, w.pitch, 0, p.topk, p.sm_scale,
+                      status, b, w);
+  };
+  if (b.max_n_kv <= 16 * kTkThreads) return run(topk_kernel<16, true>);
+  if (b.max_n_kv <= 32 * kTkThreads) return run(topk_kernel<32, true>);
+  if (b.max_n_kv <= 64 * kTkThreads) return run(topk_kernel<64, true>);
+  return run(topk_kernel<128, true>);
 }
 
 }  // namespace qsa

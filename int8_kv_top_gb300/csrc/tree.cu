@@ -33,21 +33,17 @@
 #include <algorithm>
 #include <atomic>
 
-#include "common.cuh"
+#include "tree_common.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kRows = 128;                  // (token, head) rows of a block (UMMA M)
-constexpr int kCells = 128;                 // cells per tile (UMMA N of QK^T)
-constexpr int kParts = 4;                   // ring stages per tile and operand
-constexpr int kStages = 4;                  // ring depth
-constexpr int kStageBytes = 16 * 1024;
+constexpr int kRows = 128;                  // (token, head) rows of a block (UMMA M); 128-cell tiles are N of QK^T
 constexpr int kMaxTok = (kRows + kHPG - 2) / kHPG + 1;  // tokens a block's rows may touch
 constexpr int kThreads = 17 * 32;
 constexpr int kMaxC = 16;
 constexpr int kNS = 2;
-constexpr int kOffK = 0, kOffV = kStages * kStageBytes, kOffQ = 2 * kStages * kStageBytes;
+constexpr int kOffK = 0, kOffV = kTileStages * kTileStageBytes, kOffQ = 2 * kTileStages * kTileStageBytes;
 constexpr int kOffML = kOffQ + kRows * kD * 2;          // float2 (m, l) [kMaxC][kRows], pushed by every CTA
 constexpr int kSmem = kOffML + kMaxC * kRows * 8 + 1024;  // + alignment slack
 constexpr int kOStride = kD + 4;            // floats per merged row: 16 bytes of padding spread the banks
@@ -57,16 +53,14 @@ constexpr uint32_t kColO = 0, kColS = 256;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
 struct DenseTreeArgs {
+  TreeBatch b;
   const __half* q;
   const int8_t* kq;
   const int8_t* vq;
   const __half* ksc;
   const __half* vsc;
-  const int4* seqs;
-  long long n_pool;
-  int n_seq, n_tok;
-  const uint32_t* tree;
-  int tree_words, max_n_kv, identity_max;
+  const uint32_t* bits;  // selected cells [2][n_tok][bits_pitch words], or null: selected tokens are not ours
+  int bits_pitch;
   float scale_log2;
   const __half* gate;
   __half* out;
@@ -74,23 +68,10 @@ struct DenseTreeArgs {
 };
 
 struct __align__(8) TreeBars {
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
   uint64_t s_full[kNS], p_full[kNS], pv_done[kNS];
   uint64_t q_full, drain;
 };
-
-// Sequence s's token count, or -1 when its entry breaks the contract; a padding sequence has none.
-__device__ __forceinline__ int tree_seq_tokens(const DenseTreeArgs& a, int s, int4* e_out) {
-  const int4 e = __ldg(&a.seqs[s]);
-  const int next = s + 1 < a.n_seq ? __ldg(&a.seqs[s + 1].w) : a.n_tok;
-  *e_out = e;
-  const bool rows_ok = (s == 0 ? e.w == 0 : e.w >= 0) && next >= e.w && next <= a.n_tok;
-  if (rows_ok && e.y == 0) return 0;
-  const long long T = (long long)next - e.w, end = (long long)e.z + T;
-  const bool ok = rows_ok && e.x >= 0 && e.y >= 1 && e.z >= 0 && end <= e.y && (long long)e.x + e.y <= a.n_pool &&
-                  end <= a.max_n_kv && T <= 32 * a.tree_words;
-  return ok ? (int)T : -1;
-}
 
 // Index of a sequence's first block in the grid: block k of sequence s has index first_block(s) + k.
 // The sequences' ranges never meet, since floor((a + b) / 128) + 1 >= floor(a / 128) + ceil(b / 128), so
@@ -108,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   __shared__ volatile int s_abort;
   __shared__ int s_blk[8];                       // active, first pool cell, pos0, T, first token row, first row
   __shared__ uint32_t s_mask[kMaxTok][kTreeWords];
-  __shared__ uint32_t s_union[kTreeWords];       // drafted cells that some identity token of the block sees
-  __shared__ int s_ident;                        // bit i: token i of the block is an identity token
+  __shared__ uint32_t s_union[kTreeWords];       // drafted cells that some token of ours sees
+  __shared__ int s_ours, s_sel;                  // bit i: token i of the block is computed here; is a selected one
   __shared__ float s_xm[2][kRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -117,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   const int blk = blockIdx.x / nC;
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kTileStages; ++i) {
       mbar_init(&bars.k_full[i], 4);
       mbar_init(&bars.k_empty[i], 1);
       mbar_init(&bars.v_full[i], 4);
@@ -134,24 +115,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
   pdl_begin();
   if (blk == 0 && rank == 0 && g == 0) {  // one CTA looks over the whole table and flags bad entries
-    for (int s = tid; s < a.n_seq; s += kThreads) {
+    for (int s = tid; s < a.b.n_seq; s += kThreads) {
       int4 e;
-      if (tree_seq_tokens(a, s, &e) < 0) set_dev_status(a.status, QSA_DEV_BAD_ID);
+      if (tree_seq_tokens(a.b, s, &e) < 0) set_dev_status(a.status, QSA_DEV_BAD_ID);
     }
   }
   if (warp == 0) {
-    // the sequence of this block: the last one whose first block is not behind blk (32 probes a step)
-    int lo = 0, n = a.n_seq;
-    while (n > 1) {
-      const int step = (n + 31) / 32, at = lo + lane * step;
-      const bool le = lane * step < n && first_block(__ldg(&a.seqs[at].w), at) <= blk;
-      const int c = max(__popc(__ballot_sync(0xffffffffu, le)), 1);
-      n = min(step, n - (c - 1) * step);
-      lo += (c - 1) * step;
-    }
+    const int sq = warp_find_seq(a.b.n_seq, blk, [&](int s) { return first_block(__ldg(&a.b.seqs[s].w), s); });
     int4 e;
-    const int T = tree_seq_tokens(a, lo, &e);
-    const long long k = blk - first_block(e.w, lo);
+    const int T = tree_seq_tokens(a.b, sq, &e);
+    const long long k = blk - first_block(e.w, sq);
     const bool here = T > 0 && k >= 0 && k * kRows < (long long)T * kHPG;
     const int row0 = here ? (int)k * kRows : 0;
     const int tok = row0 / kHPG + lane;  // lane = token of the block
@@ -160,25 +133,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     uint32_t m[kTreeWords];
 #pragma unroll
     for (int w = 0; w < kTreeWords; ++w) {
-      const int left = T - 32 * w;
-      m[w] = 0u;
-      if (live && w < a.tree_words && left > 0) {
-        m[w] = __ldg(a.tree + (size_t)(e.w + tok) * a.tree_words + w);
-        if (left < 32) m[w] &= (1u << left) - 1u;
-      }
+      m[w] = live ? tree_mask_word(a.b, e.w + tok, w, T) : 0u;
       n_kv += __popc(m[w]);
     }
-    const bool ident = live && n_kv <= a.identity_max;
-    const unsigned idents = __ballot_sync(0xffffffffu, ident);
+    const bool sel = live && n_kv > a.b.identity_max, ours = live && (!sel || a.bits != nullptr);
+    const unsigned all_ours = __ballot_sync(0xffffffffu, ours), all_sel = __ballot_sync(0xffffffffu, sel);
 #pragma unroll
     for (int w = 0; w < kTreeWords; ++w) {
-      const uint32_t u = __reduce_or_sync(0xffffffffu, ident ? m[w] : 0u);
+      const uint32_t u = __reduce_or_sync(0xffffffffu, ours ? m[w] : 0u);
       if (lane < kMaxTok) s_mask[lane][w] = m[w];
       if (lane == 0) s_union[w] = u;
     }
     if (lane == 0) {
-      s_ident = (int)idents;
-      s_blk[0] = idents != 0u;
+      s_ours = (int)all_ours;
+      s_sel = (int)all_sel;
+      s_blk[0] = all_ours != 0u;
       s_blk[1] = e.x;
       s_blk[2] = e.z;
       s_blk[3] = T;
@@ -187,11 +156,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     }
   }
   __syncthreads();
-  if (!s_blk[0]) return;  // the same in every CTA of the cluster: an unused index, or no identity token
+  if (!s_blk[0]) return;  // the same in every CTA of the cluster: an unused index, or no token of ours
   const long long cell0 = s_blk[1];
   const int pos0 = s_blk[2], T = s_blk[3], first = s_blk[4], row0 = s_blk[5];
   const int n_scan = pos0 + T;
-  const int n_tiles = (n_scan + kCells - 1) / kCells;
+  const int n_tiles = (n_scan + kTileCells - 1) / kTileCells;
   const int j_begin = n_tiles * rank / nC, J = n_tiles * (rank + 1) / nC - j_begin;
   if (warp == 16) {
     tmem_alloc(&s_tmem, 512);
@@ -206,85 +175,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   bool ok = true;
 
   if (warp < 8) {
-    // ------------------------------------------------------------ producers
-    // Four lanes take 64 codes of a cell (one scale block), eight cells a load; K warps share the cells of a
-    // stage, V warps its dim blocks.  Two stages are in flight in registers while a third is converted.
-    const bool is_v = warp >= 4;
-    const int w4 = warp & 3, sub = lane >> 2, piece = lane & 3;
-    const int8_t* codes = is_v ? a.vq : a.kq;
-    const __half* scales = is_v ? a.vsc : a.ksc;
-    uint64_t* full = is_v ? bars.v_full : bars.k_full;
-    uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
-    uint8_t* ring = smem + (is_v ? kOffV : kOffK);
-    const int n_st = J * kParts;
-    auto load = [&](int s, uint4 (&w)[4], __half (&sc)[4]) {
-      const int c0 = (j_begin + (s >> 2)) * kCells, part = s & 3;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int cell = c0 + (is_v ? part * 32 + i * 8 : i * 32 + w4 * 8) + sub;
-        const int blk64 = is_v ? w4 : part;
-        const int dj = cell - pos0;
-        // cells past the sequence, and drafted ones that nobody here sees, are zeros: they may hold anything
-        const bool use = dj < 0 || (dj < T && ((s_union[dj >> 5] >> (dj & 31)) & 1u));
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        sc[i] = __ushort_as_half(0);
-        if (use) {
-          const size_t row = (size_t)(cell0 + cell) * kGroups + g;
-          w[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * kD + blk64 * kBlk) + piece);
-          sc[i] = scales[row * kNB + blk64];
-        }
-      }
-    };
-    auto store = [&](int s, const uint4 (&w)[4], const __half (&sc)[4]) -> bool {
-      const int slot = s % kStages;
-      if (s >= kStages && !mbar_wait_warp(&empty[slot], ((s / kStages) & 1) ^ 1, a.status, &s_abort)) return false;
-      uint8_t* stage = ring + slot * kStageBytes + (is_v ? w4 * 4096 : 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = (is_v ? i * 8 : i * 32 + w4 * 8) + sub;
-        uint32_t lo[4], hi[4];
-        const __half2 s2 = __half2half2(sc[i]);
-        dequant8(w[i].x, w[i].y, s2, lo);
-        dequant8(w[i].z, w[i].w, s2, hi);
-        uint8_t* row = stage + r * 128;
-        *reinterpret_cast<uint4*>(row + (((2 * piece) ^ (r & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(row + (((2 * piece + 1) ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[slot]);
-      return true;
-    };
-    uint4 wa[4], wb[4];
-    __half sa[4], sb[4];
-    if (n_st > 0) {
-      load(0, wa, sa);
-      load(1, wb, sb);
-    }
-    for (int s = 0; s < n_st; s += 2) {  // n_st is a multiple of kParts
-      if (!store(s, wa, sa)) break;
-      if (s + 2 < n_st) load(s + 2, wa, sa);
-      if (!store(s + 1, wb, sb)) break;
-      if (s + 3 < n_st) load(s + 3, wb, sb);
-    }
+    const TileRun t{cell0, pos0, T, j_begin, J, g, s_union, &s_abort, a.status};
+    if (warp < 4)
+      produce_tiles<false, false>(t, a.kq, a.ksc, smem_u32(smem + kOffK), bars.k_full, bars.k_empty, warp, lane);
+    else
+      produce_tiles<true, false>(t, a.vq, a.vsc, smem_u32(smem + kOffV), bars.v_full, bars.v_empty, warp - 4, lane);
   } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issue
     if (lane == 0 && J > 0) {
-      const uint32_t idesc_qk = idesc_f16_f32(kRows, kCells, 0, 0);
+      const uint32_t idesc_qk = idesc_f16_f32(kRows, kTileCells, 0, 0);
       const uint32_t idesc_pv = idesc_f16_f32(kRows, kD, 0, 1);
       const uint32_t k0 = smem_u32(smem + kOffK), v0 = smem_u32(smem + kOffV);
       const uint64_t qdesc = sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024);
       auto issue_qk = [&](int j) -> bool {
         const int b = j % kNS;
         if (j >= kNS && !mbar_wait_poll<false>(&bars.pv_done[b], ((j / kNS) - 1) & 1, a.status, &s_abort)) return false;
-        for (int d = 0; d < kParts; ++d) {
-          const int s = j * kParts + d, slot = s % kStages;
-          if (!mbar_wait_poll<false>(&bars.k_full[slot], (s / kStages) & 1, a.status, &s_abort)) return false;
+        for (int d = 0; d < kTileParts; ++d) {
+          const int s = j * kTileParts + d, slot = s % kTileStages;
+          if (!mbar_wait_poll<false>(&bars.k_full[slot], (s / kTileStages) & 1, a.status, &s_abort)) return false;
           tc_fence_after();
-          const uint64_t kdesc = sdesc_sw128(k0 + slot * kStageBytes, 16, 1024);
+          const uint64_t kdesc = sdesc_sw128(k0 + slot * kTileStageBytes, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ss(tmem + kColS + b * kCells, qdesc + (uint64_t)((d * (kRows * 128) + kk * 32) >> 4),
+            umma_ss(tmem + kColS + b * kTileCells, qdesc + (uint64_t)((d * (kRows * 128) + kk * 32) >> 4),
                     kdesc + (uint64_t)((kk * 32) >> 4), idesc_qk, (d > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&bars.k_empty[slot]);
         }
@@ -294,14 +207,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       auto issue_pv = [&](int j) -> bool {
         const int b = j % kNS;
         if (!mbar_wait_poll<false>(&bars.p_full[b], (j / kNS) & 1, a.status, &s_abort)) return false;
-        for (int c = 0; c < kParts; ++c) {
-          const int s = j * kParts + c, slot = s % kStages;
-          if (!mbar_wait_poll<false>(&bars.v_full[slot], (s / kStages) & 1, a.status, &s_abort)) return false;
+        for (int c = 0; c < kTileParts; ++c) {
+          const int s = j * kTileParts + c, slot = s % kTileStages;
+          if (!mbar_wait_poll<false>(&bars.v_full[slot], (s / kTileStages) & 1, a.status, &s_abort)) return false;
           tc_fence_after();
-          const uint64_t vdesc = sdesc_sw128(v0 + slot * kStageBytes, 4096, 1024);
+          const uint64_t vdesc = sdesc_sw128(v0 + slot * kTileStageBytes, 4096, 1024);
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
-            umma_ts(tmem + kColO, tmem + kColS + b * kCells + (2 * c + kk) * 8, vdesc + (uint64_t)((kk * 2048) >> 4),
+            umma_ts(tmem + kColO, tmem + kColS + b * kTileCells + (2 * c + kk) * 8, vdesc + (uint64_t)((kk * 2048) >> 4),
                     idesc_pv, (j > 0 || c > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&bars.v_empty[slot]);
         }
@@ -347,7 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const int R = row0 + r;
     const int ti = R / kHPG - row0 / kHPG;  // token of the block
-    const bool active = R < T * kHPG && ((s_ident >> ti) & 1);
+    const bool active = R < T * kHPG && ((s_ours >> ti) & 1), chosen = active && ((s_sel >> ti) & 1);
+    const uint2* sel_bits = reinterpret_cast<const uint2*>(
+        chosen ? a.bits + (size_t)(g * a.b.n_tok + first + R / kHPG) * a.bits_pitch : nullptr);
+    uint2 m_next = make_uint2(0u, 0u);  // a selected row's bits, loaded a tile ahead
+    if (chosen && J > 0) m_next = __ldg(sel_bits + 2 * j_begin + wg);
     // 32 visibility bits from drafted cell x on: cells before the drafted ones are seen, those past the mask not
     auto bits32 = [&](int x) -> uint32_t {
       const int w = x >> 5;  // floor
@@ -362,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       float s[64];
       {
         uint32_t sa[32], sb[32];
-        tmem_ld32(lane_base + kColS + b * kCells + wg * 64, sa);
-        tmem_ld32(lane_base + kColS + b * kCells + wg * 64 + 32, sb);
+        tmem_ld32(lane_base + kColS + b * kTileCells + wg * 64, sa);
+        tmem_ld32(lane_base + kColS + b * kTileCells + wg * 64 + 32, sb);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -371,9 +288,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
           s[32 + i] = __uint_as_float(sb[i]);
         }
       }
-      const int x0 = (j_begin + j) * kCells + wg * 64 - pos0;  // drafted index of this half's first cell
-      if (x0 + 64 > 0 || !active) {  // a tile of committed cells only needs no mask
-        const uint32_t m0 = active ? bits32(x0) : 0u, m1 = active ? bits32(x0 + 32) : 0u;
+      const int x0 = (j_begin + j) * kTileCells + wg * 64 - pos0;  // drafted index of this half's first cell
+      const uint2 m_sel = m_next;
+      if (chosen && j + 1 < J) m_next = __ldg(sel_bits + 2 * (j_begin + j + 1) + wg);
+      if (x0 + 64 > 0 || !active || chosen) {  // an identity row needs no mask over committed cells
+        const uint32_t m0 = !active ? 0u : chosen ? m_sel.x : bits32(x0);
+        const uint32_t m1 = !active ? 0u : chosen ? m_sel.y : bits32(x0 + 32);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           s[i] = (m0 >> i) & 1u ? s[i] : -INFINITY;
@@ -438,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
           lsum += p0 + p1;
           p[i] = pack_half2(p0, p1);
         }
-        tmem_st16(lane_base + kColS + b * kCells + wg * 32 + 16 * hf, p);
+        tmem_st16(lane_base + kColS + b * kTileCells + wg * 32 + 16 * hf, p);
       }
       l_run += lsum;
       tmem_wait_st();
@@ -510,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     for (int x = tid; x < per * 32; x += 512) {
       const int rr = x >> 5, d8 = x & 31, r = rank * per + rr, R = row0 + r;
       const int ti = R / kHPG - row0 / kHPG;
-      if (R >= T * kHPG || !((s_ident >> ti) & 1)) continue;
+      if (R >= T * kHPG || !((s_ours >> ti) & 1)) continue;
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       for (int c = 0; c < nC; ++c) {
         if (ml[c * kRows + r].x == -INFINITY) continue;  // nothing pushed for this row
@@ -590,32 +510,31 @@ cudaError_t tree_setup(int (&n_max)[5]) {
 
 }  // namespace
 
-cudaError_t launch_tree_dense(const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc, const __half* vsc,
-                              long long n_pool, const int4* seqs, int n_seq, int n_tok, const uint32_t* tree,
-                              int tree_words, int max_n_kv, const __half* gate, __half* out, Params p, int* status,
-                              cudaStream_t stream) {
+cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
+                              const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
+                              float sm_scale, int* status, cudaStream_t stream) {
   int n_max[5];
   cudaError_t e = tree_setup(n_max);
   if (e != cudaSuccess) return e;
-  const int blocks = (int)((long long)n_tok * kHPG / kRows) + n_seq;
+  const int blocks = (int)((long long)b.n_tok * kHPG / kRows) + b.n_seq;  // indices; a ragged batch leaves about half a
+  const long long likely = ((long long)b.n_tok * kHPG + kRows / 2 * (b.n_seq - 1LL) + kRows - 1) / kRows;  // block each unused
   // Cluster size: waves x (a fixed part + the tiles of a CTA), in units of one tile's time.
-  const long long longest = std::min<long long>(max_n_kv, (long long)p.identity_max + 32 * tree_words);
-  const int tiles = (int)((longest + kCells - 1) / kCells);
+  const long long longest = bits ? b.max_n_kv : std::min<long long>(b.max_n_kv, (long long)b.identity_max + 32 * b.tree_words);
+  const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
   int best = 1;
   double best_t = 0.0;
   for (int i = 0; i < 5; ++i) {
     const int C = kSizes[i];
     if (n_max[i] <= 0 || (C > 1 && C > tiles)) continue;
     const int per = (tiles + C - 1) / C;
-    const double waves = (double)(((long long)blocks * kGroups + n_max[i] - 1) / n_max[i]);
-    const double t = waves * (4.0 + per);
+    const double waves = (double)((likely * kGroups + n_max[i] - 1) / n_max[i]);
+    const double t = waves * (5.5 + 0.8 * i + per);
     if (i == 0 || t < best_t) {
       best = C;
       best_t = t;
     }
   }
-  const DenseTreeArgs a{q,    kq,   vq,         ksc,      vsc,            seqs,                 n_pool, n_seq, n_tok,
-                        tree, tree_words, max_n_kv, p.identity_max, p.sm_scale * kLog2e, gate,   out,   status};
+  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, status};
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = tree_config(best, blocks, stream, attr);
   return cudaLaunchKernelEx(&cfg, tree_dense_kernel, a, best);

@@ -146,9 +146,10 @@ def test_padding_sequences_and_tokens_leave_their_rows():
     ids, out = run_tree(pool, padded, max_n_kv=2104)
     qsa.qsa_check_device_status()
     assert torch.isnan(out[20:]).all() and (ids[20:] == -7).all()
-    cut = dict(pool, q=pool["q"][:20], tree=pool["tree"][:20])
-    ids0, out0 = run_tree(cut, seqs, max_n_kv=2104)
-    assert torch.equal(out[:20], out0) and torch.equal(ids[:20], ids0)
+    # the batch's size may change how a row's cells are split over CTAs, hence the last bits: held to the definition
+    ref, ref_ids, bound = reference(dict(pool, q=pool["q"][:20], tree=pool["tree"][:20]), seqs)
+    assert (np.abs(out[:20].double().cpu().numpy() - ref) <= bound).all()
+    np.testing.assert_array_equal(ids[:20].cpu().numpy(), ref_ids)
 
 
 @pytest.mark.parametrize("how", ["cells", "pool", "negative", "words", "max_n_kv", "pos0"])
