@@ -1,35 +1,40 @@
-// qsa_tree_attention, identity tokens (n_kv <= identity_max): attention of drafted token trees over
-// every cell that they see, on the tcgen05 tensor cores straight from the int8 cache.
+// qsa_tree_attention on the tcgen05 tensor cores, straight from the int8 cache: attention of drafted token
+// trees over every cell that they see (identity tokens, n_kv <= identity_max) or over their selected cells
+// (bitmaps of tree_select.cu).
 //
-//   out[t,h,:] = sum_c softmax_c(sm_scale q[t,h,:] . k^[c]) v^[c],  c over the committed cells and the
-//   drafted cells of token t's mask;  k^ = fp16(kq * ksc), v^ = fp16(vq * vsc).
+//   out[t,h,:] = sum_c softmax_c(sm_scale q[t,h,:] . k^[c]) v^[c],  c over the token's cells;
+//   k^ = fp16(kq * ksc), v^ = fp16(vq * vsc).
 //
-// All of a tree's tokens read the same committed cells and the 12 heads of a group share their K/V, so
-// the (token, head) rows of a sequence and group, packed 12 a token, are cut into blocks of 128 rows (the
-// M of one MMA): a tree of 32 tokens is exactly three blocks.  A cluster of C CTAs takes one block, each
-// CTA a run of its 128-cell tiles, and the CTAs merge by log-sum-exp through distributed shared memory in
-// a fixed order, so that a call of few rows still spreads over the GPU and results do not depend on timing.
+// All of a tree's tokens read the same committed cells and the 12 heads of a group share their K/V, so the
+// (token, head) rows of a sequence and group, packed 12 a token, are cut into blocks of 256 rows (21 1/3
+// tokens), the M of one MMA over a pair of CTAs (128 rows each).  Selected tokens attend through the same
+// dense tiles, their other cells masked: gathering 2,048 cells a token costs an SM about 25 us, a masked
+// 128-cell tile for 21 tokens about 1 us.  A cluster of 2 S CTAs takes one block and group, each pair a run of its
+// 128-cell tiles, and the pairs merge by log-sum-exp through distributed shared memory in a fixed order,
+// so that a call of few rows still spreads over the GPU and results do not depend on timing.
 //
-// The cache is read as int8 once per block and dequantised by producer warps into the 128B-swizzled
-// operand tiles; no fp16 mirror is written (a drafting step reads a cache a few times, and the mirror
-// would cost three times the cache's own bytes).  Per 128-cell tile an SM does 2 x 128 x 128 x 256
-// multiply-adds (about 2,050 cycles at the tensor pipe's rate), reads 64 KB of codes and writes 128 KB of
-// fp16 operands.
+// The cache is read as int8 once per block and dequantised by producer warps into 128B-swizzled operand
+// tiles; no fp16 mirror is written (a drafting step reads the cache a few times, and the mirror would cost
+// three times the cache's own bytes).  In a pair each CTA holds half of a K^ tile (64 cells) and half of
+// a V^ tile (128 dims), so per 128 cells an SM converts 32 KB of codes, moves about 210 KB through shared
+// memory (1,650 cycles) and its half of the MMAs takes about 2,050 cycles; one CTA per block instead
+// converts and stores twice as much and is bound by shared memory (3,100 cycles; measured 5,400 a tile of 128
+// rows).
 //
-//   warps 0-3    K producers: stage = 64 dims of the tile's 128 cells (16 KB), ring of four
-//   warps 4-7    V producers: stage = 32 cells x 256 dims (16 KB), ring of four
+//   warps 0-3    K producers: stage = 128 dims of this CTA's 64 cells (16 KB), ring of four (two tiles)
+//   warps 4-7    V producers: stage = 64 cells x this CTA's 128 dims (16 KB), ring of four (two tiles)
 //   warps 8-15   load Q; two softmax warpgroups, one row per thread in each, half of the columns each:
 //                mask, online softmax in base-2 units (running maximum and sum in fp32), P as fp16 into
 //                TMEM over S, lazy O rescale (only when the maximum grows by more than 2^8)
-//   warp 16      TMEM, MMA issue in the order QK(0), QK(1), PV(0), QK(2), PV(1), ...
-//                  S = Q K^T  (A = Q K-major, B = K^ K-major)      M=128 N=128, 16 K-steps
-//                  O += P V^  (A = P from TMEM, B = V^ MN-major)   M=128 N=256, 8 K-steps
+//   warp 16      TMEM; rank 0 of the pair: MMA issue in the order QK(0), QK(1), PV(0), QK(2), PV(1), ...
+//                  S = Q K^T  (A = Q K-major, B = K^ K-major)      M=256 N=128, 16 K-steps
+//                  O += P V^  (A = P from TMEM, B = V^ MN-major)   M=256 N=256, 8 K-steps
 //
 // Roundings below fp32: k^ and v^ (the values the library's prefill attends to), P (at most 2^8 after the
 // lazy rescale, so fp16 holds it with 11 bits), and the output; statistics and sums are fp32.
 //
-// TMEM columns: O [0, 256), S/P buffers [256 + 128 b, 384 + 128 b), b = 0, 1.
-// Every mbarrier wait is bounded; after a timeout the CTA still meets the cluster's barriers.
+// TMEM columns (each CTA): O [0, 256), S/P buffers [256 + 128 b, 384 + 128 b), b = 0, 1.
+// Every mbarrier wait is bounded; after a timeout a CTA still meets the cluster's barriers.
 #include <algorithm>
 #include <atomic>
 
@@ -38,19 +43,22 @@
 namespace qsa {
 namespace {
 
-constexpr int kRows = 128;                  // (token, head) rows of a block (UMMA M); 128-cell tiles are N of QK^T
-constexpr int kMaxTok = (kRows + kHPG - 2) / kHPG + 1;  // tokens a block's rows may touch
+constexpr int kRows = 128;                  // (token, head) rows of a CTA, 256 of a block (UMMA M)
+constexpr int kParts = 2;                   // ring stages per tile and operand
+constexpr int kMaxTok = (2 * kRows + kHPG - 2) / kHPG + 1;  // tokens a block's rows may touch
 constexpr int kThreads = 17 * 32;
-constexpr int kMaxC = 16;
+constexpr int kMaxS = 8;                    // pairs of a cluster at most
 constexpr int kNS = 2;
 constexpr int kOffK = 0, kOffV = kTileStages * kTileStageBytes, kOffQ = 2 * kTileStages * kTileStageBytes;
-constexpr int kOffML = kOffQ + kRows * kD * 2;          // float2 (m, l) [kMaxC][kRows], pushed by every CTA
-constexpr int kSmem = kOffML + kMaxC * kRows * 8 + 1024;  // + alignment slack
-constexpr int kOStride = kD + 4;            // floats per merged row: 16 bytes of padding spread the banks
-static_assert(kRows * kOStride * 4 <= kOffML, "the merge buffer fits over the operand tiles");
+constexpr int kOffML = kOffQ + kRows * kD * 2;          // float2 (m, l) [kMaxS][kRows], pushed by every pair
+constexpr int kSmem = kOffML + kMaxS * kRows * 8 + 1024;  // + alignment slack
+constexpr int kOStride = kD + 4;            // floats per staged output row: 16 bytes of padding spread the banks
+static_assert(kRows * kOStride * 4 <= kOffML, "the staged rows fit over the operand tiles");
 static_assert(kSmem <= 227 * 1024, "shared memory");
+static_assert(kMaxTok <= 32, "a lane per token of the block");
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr uint16_t kPair = 0x3;
 
 struct DenseTreeArgs {
   TreeBatch b;
@@ -68,20 +76,19 @@ struct DenseTreeArgs {
 };
 
 struct __align__(8) TreeBars {
+  // k_full, v_full, q_full, p_full: on rank 0 of the pair only, arrived on by the warps of both CTAs; the
+  // others receive the pair MMAs' commits in both CTAs
   uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
   uint64_t s_full[kNS], p_full[kNS], pv_done[kNS];
-  uint64_t q_full, drain;
+  uint64_t q_full, tmem_ready, drain;
 };
 
 // Index of a sequence's first block in the grid: block k of sequence s has index first_block(s) + k.
-// The sequences' ranges never meet, since floor((a + b) / 128) + 1 >= floor(a / 128) + ceil(b / 128), so
+// The sequences' ranges never meet, since floor((a + b) / 256) + 1 >= floor(a / 256) + ceil(b / 256), so
 // a block finds its sequence by a search over the table, without a prefix sum; some indices stay unused.
-__device__ __forceinline__ long long first_block(long long first_row, int s) { return first_row * kHPG / kRows + s; }
+__device__ __forceinline__ long long first_block(long long first_row, int s) { return first_row * kHPG / (2 * kRows) + s; }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
-__global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_constant__ DenseTreeArgs a, int nC) {
+__global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_constant__ DenseTreeArgs a, int S) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ TreeBars bars;
@@ -95,24 +102,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank(), g = blockIdx.y;
-  const int blk = blockIdx.x / nC;
+  const int half = rank & 1, pair = rank >> 1;  // rows 128 half .. of the block; run `pair` of its tiles
+  const int blk = blockIdx.x / (2 * S);
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kTileStages; ++i) {
-      mbar_init(&bars.k_full[i], 4);
+      mbar_init(&bars.k_full[i], 8);
       mbar_init(&bars.k_empty[i], 1);
-      mbar_init(&bars.v_full[i], 4);
+      mbar_init(&bars.v_full[i], 8);
       mbar_init(&bars.v_empty[i], 1);
     }
     for (int i = 0; i < kNS; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 8);
+      mbar_init(&bars.p_full[i], 16);
       mbar_init(&bars.pv_done[i], 1);
     }
-    mbar_init(&bars.q_full, 8);
+    mbar_init(&bars.q_full, 16);
+    mbar_init(&bars.tmem_ready, 1);
     mbar_init(&bars.drain, 1);
     fence_mbar_init();
   }
+  cluster_arrive_all();  // #0, waited for before the first remote access: every CTA's barriers are set up
   pdl_begin();
   if (blk == 0 && rank == 0 && g == 0) {  // one CTA looks over the whole table and flags bad entries
     for (int s = tid; s < a.b.n_seq; s += kThreads) {
@@ -125,10 +135,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     int4 e;
     const int T = tree_seq_tokens(a.b, sq, &e);
     const long long k = blk - first_block(e.w, sq);
-    const bool here = T > 0 && k >= 0 && k * kRows < (long long)T * kHPG;
-    const int row0 = here ? (int)k * kRows : 0;
+    const bool here = T > 0 && k >= 0 && k * 2 * kRows < (long long)T * kHPG;
+    const int row0 = here ? (int)k * 2 * kRows : 0;
     const int tok = row0 / kHPG + lane;  // lane = token of the block
-    const bool live = here && lane < kMaxTok && tok < T && tok * kHPG < row0 + kRows;
+    const bool live = here && lane < kMaxTok && tok < T && tok * kHPG < row0 + 2 * kRows;
     int n_kv = e.z;
     uint32_t m[kTreeWords];
 #pragma unroll
@@ -156,77 +166,87 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     }
   }
   __syncthreads();
-  if (!s_blk[0]) return;  // the same in every CTA of the cluster: an unused index, or no token of ours
+  if (!s_blk[0]) {  // the same in every CTA of the cluster: an unused index, or no token of ours
+    cluster_wait_all();
+    return;
+  }
   const long long cell0 = s_blk[1];
-  const int pos0 = s_blk[2], T = s_blk[3], first = s_blk[4], row0 = s_blk[5];
+  const int pos0 = s_blk[2], T = s_blk[3], first = s_blk[4], blk_row0 = s_blk[5];
+  const int row0 = blk_row0 + half * kRows;  // this CTA's first row
   const int n_scan = pos0 + T;
   const int n_tiles = (n_scan + kTileCells - 1) / kTileCells;
-  const int j_begin = n_tiles * rank / nC, J = n_tiles * (rank + 1) / nC - j_begin;
-  if (warp == 16) {
-    tmem_alloc(&s_tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  cluster_arrive();  // #0, waited for before the first remote store: every CTA has started
-  const uint32_t tmem = s_tmem;
+  const int j_begin = n_tiles * pair / S, J = n_tiles * (pair + 1) / S - j_begin;  // the same in both CTAs of a pair
+  auto pair_addr = [&](const void* p) { return mapa_shared(smem_u32(p), (uint32_t)rank & ~1u); };  // in rank 0
   float m_run = -INFINITY, l_run = 0.f;  // softmax threads: the row's running maximum (log2 units), this half's sum
   bool ok = true;
 
   if (warp < 8) {
-    const TileRun t{cell0, pos0, T, j_begin, J, g, s_union, &s_abort, a.status};
+    TileRun t{cell0, pos0, T, j_begin, J, g, s_union, &s_abort, a.status, half, 0u};
+    t.remote_full = pair_addr(warp < 4 ? bars.k_full : bars.v_full);
     if (warp < 4)
-      produce_tiles<false, false>(t, a.kq, a.ksc, smem_u32(smem + kOffK), bars.k_full, bars.k_empty, warp, lane);
+      produce_tiles<kPairK>(t, a.kq, a.ksc, smem_u32(smem + kOffK), bars.k_full, bars.k_empty, warp, lane);
     else
-      produce_tiles<true, false>(t, a.vq, a.vsc, smem_u32(smem + kOffV), bars.v_full, bars.v_empty, warp - 4, lane);
+      produce_tiles<kPairV>(t, a.vq, a.vsc, smem_u32(smem + kOffV), bars.v_full, bars.v_empty, warp - 4, lane);
+    if (J == 0) cluster_wait_all();  // #0, which the producers otherwise wait for before their first arrive
   } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0 && J > 0) {
-      const uint32_t idesc_qk = idesc_f16_f32(kRows, kTileCells, 0, 0);
-      const uint32_t idesc_pv = idesc_f16_f32(kRows, kD, 0, 1);
+    if (J > 0) {
+      tmem_alloc_pair(&s_tmem, 512);
+      tmem_relinquish_pair();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.tmem_ready);
+    }
+    cluster_wait_all();  // #0
+    if (lane == 0 && J > 0 && half == 0) {
+      tc_fence_after();
+      const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+      const uint32_t idesc_qk = idesc_f16_f32(2 * kRows, kTileCells, 0, 0);
+      const uint32_t idesc_pv = idesc_f16_f32(2 * kRows, kD, 0, 1);
       const uint32_t k0 = smem_u32(smem + kOffK), v0 = smem_u32(smem + kOffV);
       const uint64_t qdesc = sdesc_sw128(smem_u32(smem + kOffQ), 16, 1024);
       auto issue_qk = [&](int j) -> bool {
         const int b = j % kNS;
-        if (j >= kNS && !mbar_wait_poll<false>(&bars.pv_done[b], ((j / kNS) - 1) & 1, a.status, &s_abort)) return false;
-        for (int d = 0; d < kTileParts; ++d) {
-          const int s = j * kTileParts + d, slot = s % kTileStages;
-          if (!mbar_wait_poll<false>(&bars.k_full[slot], (s / kTileStages) & 1, a.status, &s_abort)) return false;
+        if (j >= kNS && !mbar_wait_poll(&bars.pv_done[b], ((j / kNS) - 1) & 1, a.status, &s_abort)) return false;
+        for (int d = 0; d < kParts; ++d) {
+          const int s = j * kParts + d, slot = s % kTileStages;
+          if (!mbar_wait_poll(&bars.k_full[slot], (s / kTileStages) & 1, a.status, &s_abort)) return false;
           tc_fence_after();
           const uint64_t kdesc = sdesc_sw128(k0 + slot * kTileStageBytes, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ss(tmem + kColS + b * kTileCells, qdesc + (uint64_t)((d * (kRows * 128) + kk * 32) >> 4),
-                    kdesc + (uint64_t)((kk * 32) >> 4), idesc_qk, (d > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&bars.k_empty[slot]);
+          for (int kk = 0; kk < 8; ++kk)
+            umma2_ss(tmem + kColS + b * kTileCells,
+                     qdesc + (uint64_t)(((2 * d + (kk >> 2)) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                     kdesc + (uint64_t)(((kk >> 2) * (kTileStageBytes / 2) + (kk & 3) * 32) >> 4), idesc_qk,
+                     (d > 0 || kk > 0) ? 1u : 0u);
+          umma2_commit(&bars.k_empty[slot], kPair << (rank & ~1));
         }
-        umma_commit(&bars.s_full[b]);
+        umma2_commit(&bars.s_full[b], kPair << (rank & ~1));
         return true;
       };
       auto issue_pv = [&](int j) -> bool {
         const int b = j % kNS;
-        if (!mbar_wait_poll<false>(&bars.p_full[b], (j / kNS) & 1, a.status, &s_abort)) return false;
-        for (int c = 0; c < kTileParts; ++c) {
-          const int s = j * kTileParts + c, slot = s % kTileStages;
-          if (!mbar_wait_poll<false>(&bars.v_full[slot], (s / kTileStages) & 1, a.status, &s_abort)) return false;
+        if (!mbar_wait_poll(&bars.p_full[b], (j / kNS) & 1, a.status, &s_abort)) return false;
+        for (int c = 0; c < kParts; ++c) {
+          const int s = j * kParts + c, slot = s % kTileStages;
+          if (!mbar_wait_poll(&bars.v_full[slot], (s / kTileStages) & 1, a.status, &s_abort)) return false;
           tc_fence_after();
-          const uint64_t vdesc = sdesc_sw128(v0 + slot * kTileStageBytes, 4096, 1024);
+          const uint64_t vdesc = sdesc_sw128(v0 + slot * kTileStageBytes, kTileStageBytes / 2, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            umma_ts(tmem + kColO, tmem + kColS + b * kTileCells + (2 * c + kk) * 8, vdesc + (uint64_t)((kk * 2048) >> 4),
-                    idesc_pv, (j > 0 || c > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&bars.v_empty[slot]);
+          for (int kk = 0; kk < 4; ++kk)
+            umma2_ts(tmem + kColO, tmem + kColS + b * kTileCells + (4 * c + kk) * 8, vdesc + (uint64_t)((kk * 2048) >> 4),
+                     idesc_pv, (j > 0 || c > 0 || kk > 0) ? 1u : 0u);
+          umma2_commit(&bars.v_empty[slot], kPair << (rank & ~1));
         }
-        umma_commit(&bars.pv_done[b]);
+        umma2_commit(&bars.pv_done[b], kPair << (rank & ~1));
         return true;
       };
-      bool go = mbar_wait_poll<false>(&bars.q_full, 0, a.status, &s_abort) && issue_qk(0);
+      bool go = mbar_wait_poll(&bars.q_full, 0, a.status, &s_abort) && issue_qk(0);
       for (int j = 0; go && j < J; ++j) {
         if (j + 1 < J) go = issue_qk(j + 1);
         go = go && issue_pv(j);
       }
-      umma_commit(&bars.drain);  // everything issued completes before TMEM is released
+      umma2_commit(&bars.drain, (uint16_t)(1u << rank));  // everything issued completes before TMEM is released
       mbar_wait(&bars.drain, 0, a.status);
     }
     __syncwarp();
@@ -234,45 +254,59 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     // ------------------------------------------------------------ Q, then softmax rows
     const int st = tid - 256, wg = warp >= 12 ? 1 : 0, quarter = warp & 3;
     {
-      const int c = st & 31;  // 16-byte chunk of a row
-#pragma unroll 1
-      for (int i0 = 0; i0 < kRows / 8; i0 += 8) {
-        uint4 w[8];
+      const int c = st & 31;  // 16-byte chunk of a row; rows past the tree are zeros
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int R = row0 + (i0 + i) * 8 + (st >> 5);
-          w[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (R < T * kHPG)
-            w[i] = __ldg(reinterpret_cast<const uint4*>(
-                             a.q + ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD) + c);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = (i0 + i) * 8 + (st >> 5);
-          *reinterpret_cast<uint4*>(smem + kOffQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[i];
-        }
+      for (int i = 0; i < kRows / 8; ++i) {
+        const int r = i * 8 + (st >> 5), R = row0 + r;
+        const bool have = R < T * kHPG;
+        const __half* src = a.q + ((size_t)(first + (have ? R / kHPG : 0)) * kHeads + g * kHPG + (have ? R % kHPG : 0)) * kD + c * 8;
+        const uint32_t dst = smem_u32(smem + kOffQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                     "r"(have ? 16 : 0)
+                     : "memory");
       }
+      cp_async_wait_all();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.q_full);
+      cluster_wait_all();  // #0
+      if (lane == 0) {
+        if (half) mbar_arrive_cluster(pair_addr(&bars.q_full));
+        else mbar_arrive(&bars.q_full);
+      }
     }
-    const int r = quarter * 32 + lane;  // TMEM lane == block row
+    uint32_t tmem = 0u;
+    if (J > 0) {
+      ok = mbar_wait_warp(&bars.tmem_ready, 0, a.status, &s_abort);
+      tc_fence_after();
+      tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    }
+    const uint32_t p_full0 = pair_addr(&bars.p_full[0]);
+    const int r = quarter * 32 + lane;  // TMEM lane == this CTA's row
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const int R = row0 + r;
-    const int ti = R / kHPG - row0 / kHPG;  // token of the block
-    const bool active = R < T * kHPG && ((s_ours >> ti) & 1), chosen = active && ((s_sel >> ti) & 1);
+    const int ti = R / kHPG - blk_row0 / kHPG;  // token of the block
+    const bool active = R < T * kHPG && ((s_ours >> min(ti, 31)) & 1), chosen = active && ((s_sel >> min(ti, 31)) & 1);
     const uint2* sel_bits = reinterpret_cast<const uint2*>(
         chosen ? a.bits + (size_t)(g * a.b.n_tok + first + R / kHPG) * a.bits_pitch : nullptr);
     uint2 m_next = make_uint2(0u, 0u);  // a selected row's bits, loaded a tile ahead
     if (chosen && J > 0) m_next = __ldg(sel_bits + 2 * j_begin + wg);
     // 32 visibility bits from drafted cell x on: cells before the drafted ones are seen, those past the mask not
     auto bits32 = [&](int x) -> uint32_t {
-      const int w = x >> 5;  // floor
+      const int w = x >> 5;  // floor (called for active rows: ti is a token of the block)
       const uint32_t lo = w < 0 ? 0xffffffffu : w < kTreeWords ? s_mask[ti][w] : 0u;
       const uint32_t hi = w + 1 < 0 ? 0xffffffffu : w + 1 < kTreeWords ? s_mask[ti][w + 1] : 0u;
       return __funnelshift_r(lo, hi, x & 31);
     };
-    for (int j = 0; j < J; ++j) {
+    // a CTA without a row of ours only keeps the pair's barriers going: its rows of S, P and O are not read
+    const bool any_row = named_bar_any(1, 256, active);
+    for (int j = 0; !any_row && j < J; ++j) {
+      if (!mbar_wait_warp(&bars.s_full[j % kNS], (j / kNS) & 1, a.status, &s_abort)) break;
+      if (lane == 0) {
+        if (half) mbar_arrive_cluster(p_full0 + 8u * (uint32_t)(j % kNS));
+        else mbar_arrive(&bars.p_full[j % kNS]);
+      }
+    }
+    for (int j = 0; any_row && j < J; ++j) {
       const int b = j % kNS;
       const bool w_ok = mbar_wait_warp(&bars.s_full[b], (j / kNS) & 1, a.status, &s_abort);
       tc_fence_after();
@@ -364,90 +398,87 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.p_full[b]);
+      if (lane == 0) {
+        if (half) mbar_arrive_cluster(p_full0 + 8u * (uint32_t)b);
+        else mbar_arrive(&bars.p_full[b]);
+      }
     }
     if (J > 0 && ok) ok = mbar_wait_warp(&bars.pv_done[(J - 1) % kNS], ((J - 1) / kNS) & 1, a.status, &s_abort);
-    // (m, l) of the row to every CTA of the cluster; a failed or empty CTA contributes nothing
+    // (m, l) of the row to the CTAs that hold the same rows; a failed or empty run contributes nothing
     const bool all_ok = !named_bar_any(1, 256, !ok);
     s_xm[wg][r] = l_run;
     named_bar_any(1, 256, false);
     if (!all_ok) m_run = -INFINITY;
-    cluster_wait();  // #0
     if (wg == 0) {
       const float l = l_run + s_xm[1][r];
-      const uint32_t at = smem_u32(smem + kOffML) + (uint32_t)(rank * kRows + r) * 8u;
-      for (int c = 0; c < nC; ++c)
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(at, c)), "f"(m_run), "f"(l) : "memory");
+      const uint32_t at = smem_u32(smem + kOffML) + (uint32_t)(pair * kRows + r) * 8u;
+      for (int c = 0; c < S; ++c)
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(at, 2 * c + half)), "f"(m_run), "f"(l)
+                     : "memory");
     }
-  }
-
-  // ---------------------------------------------------------------- merge
-  // CTA c owns the block's rows [c * 128 / nC, (c + 1) * 128 / nC).  Past this barrier every CTA's MMAs are
-  // complete, so its operand tiles take the partial rows that the others push: O 2^(m - M) / L.
-  if (warp < 8 || warp == 16) cluster_wait();  // #0
-  tc_fence_before();
-  __syncwarp();
-  cluster_arrive();
-  cluster_wait();  // #1
-  tc_fence_after();
-  const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
-  const int per = kRows / nC;
-  if (warp >= 8 && warp < 16) {
-    const int wg = warp >= 12 ? 1 : 0, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    float M = -INFINITY, L = 0.f;
-    for (int c = 0; c < nC; ++c) M = fmaxf(M, ml[c * kRows + r].x);
-    for (int c = 0; c < nC; ++c) {
-      const float2 v = ml[c * kRows + r];
-      if (v.x != -INFINITY) L = fmaf(v.y, fast_exp2(v.x - M), L);
-    }
-    const float f = m_run == -INFINITY ? 0.f : fast_exp2(m_run - M) / L;
-    const int owner = r / per;
-    const uint32_t dst = mapa_shared(smem_u32(smem) + (uint32_t)((rank * per + r % per) * kOStride) * 4u, owner);
-    if (J > 0) {  // uniform over the warp, as the TMEM loads need
+    // O (unscaled) over the operand tiles, once both CTAs' MMAs are done with them (the last PV is complete here)
+    if (J > 0 && any_row) {
+      tc_fence_after();
 #pragma unroll 1
       for (int c0 = wg * 128; c0 < wg * 128 + 128; c0 += 32) {
         uint32_t o[32];
         tmem_ld32(lane_base + kColO + c0, o);
         tmem_wait_ld();
-        if (m_run != -INFINITY) {
+        float4* dst = reinterpret_cast<float4*>(smem + (size_t)r * (kOStride * 4)) + c0 / 4;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (uint32_t)(c0 + i) * 4u),
-                         "f"(__uint_as_float(o[i]) * f), "f"(__uint_as_float(o[i + 1]) * f),
-                         "f"(__uint_as_float(o[i + 2]) * f), "f"(__uint_as_float(o[i + 3]) * f)
-                         : "memory");
-        }
+        for (int i = 0; i < 8; ++i)
+          dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                               __uint_as_float(o[4 * i + 3]));
       }
     }
   }
+
+  // ---------------------------------------------------------------- merge
+  // Run c's CTA owns the rows [c * 128 / S, (c + 1) * 128 / S) of its half: it reads them from every run's staged
+  // rows (coalesced remote loads; pushing rows to their owner as 16-byte remote stores took 13,000 cycles a
+  // block) and adds them in the runs' order: out = sum_c O_c 2^(m_c - M) / L.
   tc_fence_before();
   __syncwarp();
-  cluster_arrive();
-  cluster_wait();  // #2: no CTA touches another after this
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  cluster_arrive_all();
+  cluster_wait_all();  // #1: staged rows and statistics of every CTA are visible
+  tc_fence_after();
+  if (warp == 16 && J > 0) tmem_dealloc_pair(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
   if (warp < 16) {
+    const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
+    const int per = kRows / S;
     for (int x = tid; x < per * 32; x += 512) {
-      const int rr = x >> 5, d8 = x & 31, r = rank * per + rr, R = row0 + r;
-      const int ti = R / kHPG - row0 / kHPG;
-      if (R >= T * kHPG || !((s_ours >> ti) & 1)) continue;
+      const int r = pair * per + (x >> 5), d8 = x & 31, R = row0 + r;
+      const int ti = R / kHPG - blk_row0 / kHPG;
+      if (R >= T * kHPG || !((s_ours >> ti) & 1)) continue;  // uniform over the warp
+      float M = -INFINITY, L = 0.f;
+      for (int c = 0; c < S; ++c) M = fmaxf(M, ml[c * kRows + r].x);
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int c = 0; c < nC; ++c) {
-        if (ml[c * kRows + r].x == -INFINITY) continue;  // nothing pushed for this row
-        const float4* src = reinterpret_cast<const float4*>(smem + (size_t)((c * per + rr) * kOStride) * 4) + 2 * d8;
-        const float4 u = src[0], v = src[1];
-        acc[0] += u.x;
-        acc[1] += u.y;
-        acc[2] += u.z;
-        acc[3] += u.w;
-        acc[4] += v.x;
-        acc[5] += v.y;
-        acc[6] += v.z;
-        acc[7] += v.w;
+      const uint32_t at = smem_u32(smem) + (uint32_t)r * (kOStride * 4) + (uint32_t)d8 * 32u;
+#pragma unroll 2
+      for (int c = 0; c < S; ++c) {
+        const float2 v = ml[c * kRows + r];
+        if (v.x == -INFINITY) continue;  // nothing of this row there
+        const float f = fast_exp2(v.x - M);
+        L = fmaf(v.y, f, L);
+        const uint32_t src = mapa_shared(at, 2 * c + half);
+        float u[8];
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3])
+                     : "r"(src)
+                     : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(u[4]), "=f"(u[5]), "=f"(u[6]), "=f"(u[7])
+                     : "r"(src + 16u)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(u[i], f, acc[i]);
       }
-      const size_t at = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD + d8 * 8;
+      const float inv = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] *= inv;
+      const size_t o = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD + d8 * 8;
       if (a.gate) {
-        const uint4 gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at));
+        const uint4 gw = __ldg(reinterpret_cast<const uint4*>(a.gate + o));
         const uint32_t w[4] = {gw.x, gw.y, gw.z, gw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -456,22 +487,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
           acc[2 * i + 1] *= gate_sigmoid(v.y);
         }
       }
-      *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_half2(acc[0], acc[1]), pack_half2(acc[2], acc[3]),
-                                                         pack_half2(acc[4], acc[5]), pack_half2(acc[6], acc[7]));
+      *reinterpret_cast<uint4*>(a.out + o) = make_uint4(pack_half2(acc[0], acc[1]), pack_half2(acc[2], acc[3]),
+                                                        pack_half2(acc[4], acc[5]), pack_half2(acc[6], acc[7]));
     }
   }
+  __syncwarp();
+  cluster_arrive_all();
+  cluster_wait_all();  // #2: no CTA leaves while another may read its rows
 }
 
-constexpr int kSizes[5] = {1, 2, 4, 8, 16};
+constexpr int kSizes[4] = {1, 2, 4, 8};  // pairs per cluster
 
-cudaLaunchConfig_t tree_config(int C, int blocks, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
+cudaLaunchConfig_t tree_config(int S, int blocks, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks * C, kGroups);
+  cfg.gridDim = dim3(blocks * 2 * S, kGroups);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.x = 2 * S;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -483,9 +517,9 @@ cudaLaunchConfig_t tree_config(int C, int blocks, cudaStream_t stream, cudaLaunc
 
 // Per device, set once: the kernel's attributes, and how many clusters of each size the GPU holds at once
 // (0: none of that size); threads that race here store the same values.
-cudaError_t tree_setup(int (&n_max)[5]) {
+cudaError_t tree_setup(int (&n_max)[4]) {
   static std::atomic<int> ready[64];
-  static std::atomic<int> held[64][5];
+  static std::atomic<int> held[64][4];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -495,7 +529,7 @@ cudaError_t tree_setup(int (&n_max)[5]) {
       return e;
     if ((e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
       return e;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 4; ++i) {
       cudaLaunchAttribute attr[2];
       cudaLaunchConfig_t cfg = tree_config(kSizes[i], 1, nullptr, attr);
       int n = 0;
@@ -504,7 +538,7 @@ cudaError_t tree_setup(int (&n_max)[5]) {
     }
     ready[dev].store(1, std::memory_order_release);
   }
-  for (int i = 0; i < 5; ++i) n_max[i] = held[dev][i].load(std::memory_order_relaxed);
+  for (int i = 0; i < 4; ++i) n_max[i] = held[dev][i].load(std::memory_order_relaxed);
   return n_max[0] > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
@@ -513,24 +547,24 @@ cudaError_t tree_setup(int (&n_max)[5]) {
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                               const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
                               float sm_scale, int* status, cudaStream_t stream) {
-  int n_max[5];
+  int n_max[4];
   cudaError_t e = tree_setup(n_max);
   if (e != cudaSuccess) return e;
-  const int blocks = (int)((long long)b.n_tok * kHPG / kRows) + b.n_seq;  // indices; a ragged batch leaves about half a
-  const long long likely = ((long long)b.n_tok * kHPG + kRows / 2 * (b.n_seq - 1LL) + kRows - 1) / kRows;  // block each unused
-  // Cluster size: waves x (a fixed part + the tiles of a CTA), in units of one tile's time.
+  constexpr int kBlock = 2 * kRows;
+  const int blocks = (int)((long long)b.n_tok * kHPG / kBlock) + b.n_seq;  // indices; a ragged batch leaves about
+  const long long likely = ((long long)b.n_tok * kHPG + kBlock / 2 * (b.n_seq - 1LL) + kBlock - 1) / kBlock;  // half a block each unused
+  // Pairs per cluster: waves x (a fixed part + the tiles of a pair), in units of one tile's time.
   const long long longest = bits ? b.max_n_kv : std::min<long long>(b.max_n_kv, (long long)b.identity_max + 32 * b.tree_words);
   const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
   int best = 1;
   double best_t = 0.0;
-  for (int i = 0; i < 5; ++i) {
-    const int C = kSizes[i];
-    if (n_max[i] <= 0 || (C > 1 && C > tiles)) continue;
-    const int per = (tiles + C - 1) / C;
+  for (int i = 0; i < 4; ++i) {
+    const int S = kSizes[i];
+    if (n_max[i] <= 0 || (S > 1 && S > tiles)) continue;
     const double waves = (double)((likely * kGroups + n_max[i] - 1) / n_max[i]);
-    const double t = waves * (5.5 + 0.8 * i + per);
+    const double t = waves * (8.0 + 0.8 * i + (tiles + S - 1) / S);
     if (i == 0 || t < best_t) {
-      best = C;
+      best = S;
       best_t = t;
     }
   }

@@ -5,6 +5,10 @@
 
 namespace qsa {
 
+// The two halves of a cluster barrier, executed by every thread of the cluster once per phase.
+__device__ __forceinline__ void cluster_arrive_all() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_all() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 struct TreeBatch {
   const int4* seqs;  // per sequence {first pool cell, n_cells, pos0, first token row}
   long long n_pool;
@@ -73,7 +77,6 @@ __device__ __forceinline__ float tree_row_scale(const float* eh, const float (&k
 
 // ---------------------------------------------------------------- tile producers
 constexpr int kTileCells = 128;  // cells of a tile
-constexpr int kTileParts = 4;    // ring stages per tile and operand
 constexpr int kTileStages = 4;   // ring depth
 constexpr int kTileStageBytes = 16 * 1024;
 
@@ -84,65 +87,76 @@ struct TileRun {
   const uint32_t* seen;  // drafted cells that some token of the block sees (bits)
   volatile int* abort;
   int* status;
+  int half;              // rank within a CTA pair: which half of the tile's K cells and of V's dims is ours
+  uint32_t remote_full;  // rank 1 of a pair: rank 0's first full barrier (a shared::cluster address)
 };
 
-// The K (kV false) or V producers: four warps that turn the tiles' int8 codes into the fp16 operand stages.
-// Four lanes take the 64 codes of a (cell, scale block), a warp eight cells a load.  K stage p holds dims
-// 64 p .. of the tile's 128 cells, its warps take 8 of every 32 cells; V stage p holds cells 32 p .. of
-// the tile, warp w its dims 64 w ...  Row r of a stage lies at 128 r with its 16-byte chunks xored by
-// r mod 8, which is the lane's cell, so every store address is a constant past the stage's; two stages are
-// in flight in registers while a third is converted.  The loads are not predicated (cells past the sequence
-// read its last one): a predicated load is merged with its default as it arrives, and the thread waits
-// there for its latency.
-//
-// kCodes: the codes themselves as fp16 (exact integers) instead of code * scale; the scales are not read.
-template <bool kV, bool kCodes>
+// Four producer warps that turn the tiles' int8 codes into fp16 operand stages of 16 KB, 128B-swizzled:
+//   kScoreCodes  stage p: 128 cells x dims 64 p .. (four a tile); the codes themselves, exact integers
+//   kPairK       stage p: this CTA's 64 cells x dims 128 p .. (two a tile), code * scale
+//   kPairV       stage p: cells 64 p .. of the tile x this CTA's 128 dims (two a tile), code * scale
+// Four lanes take the 64 codes of a (cell, scale block), a warp eight cells a load, so row r of a stage lies at
+// 128 r with its 16-byte chunks xored by r mod 8, which is the lane's cell: every store address is a constant
+// past the stage's.  Two stages are in flight in registers while a third is converted.  The loads are not
+// predicated (cells past the sequence read its last one): a predicated load is merged with its default as
+// it arrives, and the thread waits there for its latency.
+enum TileMode { kScoreCodes, kPairK, kPairV };
+template <TileMode kMode>
 __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __restrict__ codes,
-                                        const __half* __restrict__ scales, uint32_t ring, uint64_t* full, uint64_t* empty,
-                                        int w4, int lane) {
-  constexpr int kStep = kV ? 8 : 32;  // cells between a thread's four loads of a stage
-  const int sub = lane >> 2, piece = lane & 3, r0 = sub + (kV ? 0 : w4 * 8);
-  const int n_scan = t.pos0 + t.T, n_st = t.J * kTileParts;
+                                              const __half* __restrict__ scales, uint32_t ring, uint64_t* full,
+                                              uint64_t* empty, int w4, int lane) {
+  constexpr bool kPair = kMode != kScoreCodes;
+  constexpr int kParts = kPair ? 2 : 4;   // stages a tile
+  constexpr int kStep = kPair ? 8 : 32;   // cells between a thread's four loads of a stage
+  const int sub = lane >> 2, piece = lane & 3;
+  const int db = kPair ? w4 & 1 : 0;      // dim block within the stage
+  const int r0 = sub + (kPair ? (w4 >> 1) * 32 : w4 * 8);
+  const int n_scan = t.pos0 + t.T, n_st = t.J * kParts;
   const size_t row0 = (size_t)t.cell0 * kGroups + t.g;
-  const int8_t* my_codes = codes + row0 * kD + piece * 16 + (kV ? w4 * kBlk : 0);
-  const uint16_t* my_scales = reinterpret_cast<const uint16_t*>(scales) + row0 * kNB + (kV ? w4 : 0);
-  const uint32_t dst0 = ring + (kV ? w4 * 4096 : 0) + r0 * 128 + (((2 * piece) ^ sub) << 4);
-  const uint32_t dst1 = ring + (kV ? w4 * 4096 : 0) + r0 * 128 + (((2 * piece + 1) ^ sub) << 4);
+  const int8_t* my_codes = codes + row0 * kD + piece * 16;
+  const uint16_t* my_scales = reinterpret_cast<const uint16_t*>(scales) + row0 * kNB;
+  const uint32_t dst0 = ring + db * (kTileStageBytes / 2) + r0 * 128 + (((2 * piece) ^ sub) << 4);
+  const uint32_t dst1 = ring + db * (kTileStageBytes / 2) + r0 * 128 + (((2 * piece + 1) ^ sub) << 4);
+  auto first_cell = [&](int tile, int part) {  // the thread's first cell of a stage
+    return tile * kTileCells + r0 + (kMode == kPairK ? t.half * 64 : kMode == kPairV ? part * 64 : 0);
+  };
   auto load = [&](int s, uint4 (&w)[4], uint16_t (&sc)[4]) {
-    const int part = s & 3, c0 = (t.j_begin + (s >> 2)) * kTileCells + r0 + (kV ? part * 32 : 0);
-    const int8_t* cp = my_codes + (kV ? 0 : part * kBlk);
-    const uint16_t* sp = my_scales + (kV ? 0 : part);
-    if ((t.j_begin + (s >> 2) + 1) * kTileCells <= n_scan) {
+    const int tile = t.j_begin + s / kParts, part = s % kParts, c0 = first_cell(tile, part);
+    const int blk = kMode == kScoreCodes ? part : kMode == kPairK ? 2 * part + db : 2 * t.half + db;
+    const int8_t* cp = my_codes + blk * kBlk;
+    const uint16_t* sp = my_scales + blk;
+    if ((tile + 1) * kTileCells <= n_scan) {
       cp += (size_t)c0 * (kGroups * kD);
       sp += (size_t)c0 * (kGroups * kNB);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         w[i] = __ldg(reinterpret_cast<const uint4*>(cp + i * kStep * (kGroups * kD)));
-        if (!kCodes) sc[i] = __ldg(sp + i * kStep * (kGroups * kNB));
+        if (kPair) sc[i] = __ldg(sp + i * kStep * (kGroups * kNB));
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const size_t cell = min(c0 + i * kStep, n_scan - 1);
         w[i] = __ldg(reinterpret_cast<const uint4*>(cp + cell * (kGroups * kD)));
-        if (!kCodes) sc[i] = __ldg(sp + cell * (kGroups * kNB));
+        if (kPair) sc[i] = __ldg(sp + cell * (kGroups * kNB));
       }
     }
   };
   auto store = [&](int s, const uint4 (&w)[4], uint16_t (&sc)[4]) -> bool {
-    const int slot = s % kTileStages, tile = t.j_begin + (s >> 2);
+    const int slot = s % kTileStages, tile = t.j_begin + s / kParts;
     if (s >= kTileStages && !mbar_wait_warp(&empty[slot], ((s / kTileStages) & 1) ^ 1, t.status, t.abort)) return false;
-    if (!kCodes && (tile + 1) * kTileCells > t.pos0) {  // cells past the sequence, and drafted ones that nobody here sees: zeros
+    if (kPair && (tile + 1) * kTileCells > t.pos0) {  // cells past the sequence, and drafted ones unseen here: zeros
+      const int c0 = first_cell(tile, s % kParts);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int dj = tile * kTileCells + r0 + (kV ? (s & 3) * 32 : 0) + i * kStep - t.pos0;
+        const int dj = c0 + i * kStep - t.pos0;
         if (dj >= 0 && (dj >= t.T || !((t.seen[dj >> 5] >> (dj & 31)) & 1u))) sc[i] = 0;
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t lo[4], hi[4];
-      const __half2 s2 = __half2half2(__ushort_as_half(kCodes ? (uint16_t)0x3C00 : sc[i]));
+      const __half2 s2 = __half2half2(__ushort_as_half(kPair ? sc[i] : (uint16_t)0x3C00));
       dequant8(w[i].x, w[i].y, s2, lo);
       dequant8(w[i].z, w[i].w, s2, hi);
       const uint32_t at = slot * kTileStageBytes + i * kStep * 128;
@@ -151,9 +165,12 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst1 + at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
                    : "memory");
     }
-    fence_proxy_async_smem();
+    fence_proxy_async_smem();  // this thread's part is visible to the tensor core before the arrive
     __syncwarp();
-    if (lane == 0) mbar_arrive(&full[slot]);
+    if (lane == 0) {
+      if (kPair && t.half) mbar_arrive_cluster(t.remote_full + 8u * (uint32_t)slot);
+      else mbar_arrive(&full[slot]);
+    }
     return true;
   };
   if (n_st == 0) return;
@@ -161,7 +178,8 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
   uint16_t sa[4] = {}, sb[4] = {};
   load(0, wa, sa);
   load(1, wb, sb);
-  for (int s = 0; s < n_st; s += 2) {  // n_st is a multiple of kTileParts
+  if (kPair) cluster_wait_all();  // the other CTA's barriers are initialised before the first remote arrive
+  for (int s = 0; s < n_st; s += 2) {  // n_st is even
     if (!store(s, wa, sa)) break;
     if (s + 2 < n_st) load(s + 2, wa, sa);
     if (!store(s + 1, wb, sb)) break;

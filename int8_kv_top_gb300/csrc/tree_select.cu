@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const int N = (n_here + 15) / 16 * 16;
 
   if (warp < 4) {
-    const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status};
-    produce_tiles<false, true>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp, lane);
+    const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0, 0u};
+    produce_tiles<kScoreCodes>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp, lane);
   } else if (warp == 8) {
     if (lane == 0) {
       const uint32_t idesc = idesc_f16_f32(kTileCells, N, 0, 0);
@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       for (int j = 0; go && j < J; ++j) {
         const int buf = j & 1;
         if (j >= 2 && !mbar_wait_poll<false>(&bars.acc_empty[buf], ((j >> 1) - 1) & 1, status, &s_abort)) break;
-        for (int d = 0; go && d < kTileParts; ++d) {
-          const int st = j * kTileParts + d, slot = st % kTileStages;
+        for (int d = 0; go && d < kNB; ++d) {
+          const int st = j * kNB + d, slot = st % kTileStages;
           go = mbar_wait_poll<false>(&bars.full[slot], (st / kTileStages) & 1, status, &s_abort);
           if (!go) break;
           tc_fence_after();
