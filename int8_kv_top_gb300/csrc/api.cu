@@ -567,7 +567,9 @@ int qsa_cache_read(const int8_t* kq, const uint16_t* ksc, const int8_t* vq, cons
 size_t qsa_tree_attention_workspace_bytes(int n_seq, int n_tok, int max_n_kv, const qsa_params* params) {
   qsa::Params p{};
   if (n_seq < 1 || n_tok < 1 || max_n_kv < 1 || resolve_params(params, &p) != QSA_OK) return 0;
-  return tree_selects_together(n_seq, n_tok, max_n_kv, p) ? qsa::tree_select_layout(n_seq, n_tok, max_n_kv, nullptr, nullptr) : 0;
+  const bool together = tree_selects_together(n_seq, n_tok, max_n_kv, p);
+  return qsa::tree_dense_workspace_bytes(n_seq, n_tok, max_n_kv, p.identity_max, together) +
+         (together ? qsa::tree_select_layout(n_seq, n_tok, max_n_kv, nullptr, nullptr) : 0);
 }
 
 int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, const uint16_t* ksc, const uint16_t* vsc,
@@ -618,11 +620,15 @@ int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, co
   qsa::TreeSelect w{};
   cudaError_t e;
   if (together) {
-    qsa::tree_select_layout(n_seq, n_tok, max_n_kv, ws, &w);
+    qsa::tree_select_layout(n_seq, n_tok, max_n_kv,
+                            static_cast<uint8_t*>(ws) +
+                                qsa::tree_dense_workspace_bytes(n_seq, n_tok, max_n_kv, p.identity_max, true),
+                            &w);
     e = qsa::launch_tree_select(b, w, hq, kq, hksc, ids, p, st, s);
     if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention (selection) launch");
   }
-  e = qsa::launch_tree_dense(b, hq, kq, vq, hksc, hvsc, w.bits, w.pitch / 32, hg, hout, p.sm_scale, st, s);
+  e = qsa::launch_tree_dense(b, hq, kq, vq, hksc, hvsc, w.bits, w.pitch / 32, hg, hout, static_cast<float*>(ws),
+                             p.sm_scale, st, s);
   if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention launch");
   if (max_n_kv > p.identity_max && !together) {
     e = qsa::launch_decode_layer(hq, kq, vq, hksc, hvsc, sq, n_seq, (long long)n_pool, 0, 0, n_tok, max_n_kv, ids, hg,

@@ -150,7 +150,8 @@ cudaError_t launch_tree_topk(const TreeBatch& b, const TreeSelect& w, const __ha
                              const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream);
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                               const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
-                              float sm_scale, int* status, cudaStream_t stream);
+                              float* part, float sm_scale, int* status, cudaStream_t stream);
+size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected);
 
 // Output gate: the elementwise logistic function of the gate input, in fp32, 1 / (1 + e^-x).  The
 // exponential takes the special-function unit; the reciprocal of d = 1 + e^-x (d >= 1, and finite

@@ -10,8 +10,10 @@
 // tokens), the M of one MMA over a pair of CTAs (128 rows each).  Selected tokens attend through the same
 // dense tiles, their other cells masked: gathering 2,048 cells a token costs an SM about 25 us, a masked
 // 128-cell tile for 21 tokens about 1 us.  A cluster of 2 S CTAs takes one block and group, each pair a run of its
-// 128-cell tiles, and the pairs merge by log-sum-exp through distributed shared memory in a fixed order,
-// so that a call of few rows still spreads over the GPU and results do not depend on timing.
+// 128-cell tiles, and the pairs merge by log-sum-exp in a fixed order, so that a call of few rows still
+// spreads over the GPU and results do not depend on timing.  The statistics are exchanged through
+// distributed shared memory, the rows through a workspace that stays in L2: 128 KB a CTA by remote shared
+// memory took 6.5 us, stores or coalesced loads alike.
 //
 // The cache is read as int8 once per block and dequantised by producer warps into 128B-swizzled operand
 // tiles; no fp16 mirror is written (a drafting step reads the cache a few times, and the mirror would cost
@@ -72,6 +74,7 @@ struct DenseTreeArgs {
   float scale_log2;
   const __half* gate;
   __half* out;
+  float* part;           // unmerged O rows, [CTA of the grid][kRows][kD]; null for one pair per cluster
   int* status;
 };
 
@@ -254,16 +257,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     // ------------------------------------------------------------ Q, then softmax rows
     const int st = tid - 256, wg = warp >= 12 ? 1 : 0, quarter = warp & 3;
     {
-      const int c = st & 31;  // 16-byte chunk of a row; rows past the tree are zeros
+      // 16-byte chunk c of rows st / 32 + 8 i; rows past the tree are zeros
+      const int c = st & 31, r0 = st >> 5;
+      int h = (row0 + r0) % kHPG;
+      const __half* src = a.q + ((size_t)(first + (row0 + r0) / kHPG) * kHeads + g * kHPG + h) * kD + c * 8;
+      uint32_t dst = smem_u32(smem + kOffQ) + (c >> 3) * (kRows * 128) + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4);
+      int left = T * kHPG - row0 - r0;  // rows from this one on
 #pragma unroll
       for (int i = 0; i < kRows / 8; ++i) {
-        const int r = i * 8 + (st >> 5), R = row0 + r;
-        const bool have = R < T * kHPG;
-        const __half* src = a.q + ((size_t)(first + (have ? R / kHPG : 0)) * kHeads + g * kHPG + (have ? R % kHPG : 0)) * kD + c * 8;
-        const uint32_t dst = smem_u32(smem + kOffQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
-                     "r"(have ? 16 : 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                     "l"(reinterpret_cast<uint64_t>(left > 0 ? src : a.q)), "r"(left > 0 ? 16 : 0)
                      : "memory");
+        left -= 8;
+        dst += 8 * 128;
+        h += 8;
+        src += 8 * kD;
+        if (h >= kHPG) {  // on to the next token's rows of this group
+          h -= kHPG;
+          src += (kHeads - kHPG) * kD;
+        }
       }
       cp_async_wait_all();
       fence_proxy_async_smem();
@@ -416,31 +428,41 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(at, 2 * c + half)), "f"(m_run), "f"(l)
                      : "memory");
     }
-    // O (unscaled) over the operand tiles, once both CTAs' MMAs are done with them (the last PV is complete here)
+    // O (unscaled): to the workspace, or over the operand tiles when the block has one pair (the last PV is
+    // complete, so both CTAs' MMAs are done with them)
     if (J > 0 && any_row) {
       tc_fence_after();
+      float* grow = a.part + ((size_t)(blockIdx.y * gridDim.x + blockIdx.x) * kRows + r) * kD;
 #pragma unroll 1
       for (int c0 = wg * 128; c0 < wg * 128 + 128; c0 += 32) {
         uint32_t o[32];
         tmem_ld32(lane_base + kColO + c0, o);
         tmem_wait_ld();
-        float4* dst = reinterpret_cast<float4*>(smem + (size_t)r * (kOStride * 4)) + c0 / 4;
+        if (S == 1) {
+          float4* dst = reinterpret_cast<float4*>(smem + (size_t)r * (kOStride * 4)) + c0 / 4;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                               __uint_as_float(o[4 * i + 3]));
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
+                                 __uint_as_float(o[4 * i + 3]));
+        } else if (m_run != -INFINITY) {  // 32-byte stores: whole sectors
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(grow + c0 + i), "r"(o[i]),
+                         "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
+                         "r"(o[i + 7])
+                         : "memory");
+        }
       }
     }
   }
 
   // ---------------------------------------------------------------- merge
-  // Run c's CTA owns the rows [c * 128 / S, (c + 1) * 128 / S) of its half: it reads them from every run's staged
-  // rows (coalesced remote loads; pushing rows to their owner as 16-byte remote stores took 13,000 cycles a
-  // block) and adds them in the runs' order: out = sum_c O_c 2^(m_c - M) / L.
+  // Run c's CTA owns the rows [c * 128 / S, (c + 1) * 128 / S) of its half and adds every run's part in the
+  // runs' order: out = sum_c O_c 2^(m_c - M) / L.
   tc_fence_before();
   __syncwarp();
   cluster_arrive_all();
-  cluster_wait_all();  // #1: staged rows and statistics of every CTA are visible
+  cluster_wait_all();  // #1: the cluster's rows and statistics are visible; no CTA touches another after this
   tc_fence_after();
   if (warp == 16 && J > 0) tmem_dealloc_pair(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
   if (warp < 16) {
@@ -453,23 +475,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       float M = -INFINITY, L = 0.f;
       for (int c = 0; c < S; ++c) M = fmaxf(M, ml[c * kRows + r].x);
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      const uint32_t at = smem_u32(smem) + (uint32_t)r * (kOStride * 4) + (uint32_t)d8 * 32u;
-#pragma unroll 2
+      // CTA 0 of the cluster with this half's rows; the next pair's are 2 kRows further
+      const float* src = a.part + ((size_t)(blockIdx.y * gridDim.x + blockIdx.x - 2 * pair) * kRows + r) * kD + d8 * 8;
+#pragma unroll 4
       for (int c = 0; c < S; ++c) {
         const float2 v = ml[c * kRows + r];
         if (v.x == -INFINITY) continue;  // nothing of this row there
         const float f = fast_exp2(v.x - M);
         L = fmaf(v.y, f, L);
-        const uint32_t src = mapa_shared(at, 2 * c + half);
-        float u[8];
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3])
-                     : "r"(src)
-                     : "memory");
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(u[4]), "=f"(u[5]), "=f"(u[6]), "=f"(u[7])
-                     : "r"(src + 16u)
-                     : "memory");
+        float4 x, y;
+        if (S == 1) {
+          const float4* local = reinterpret_cast<const float4*>(smem + (size_t)r * (kOStride * 4)) + 2 * d8;
+          x = local[0];
+          y = local[1];
+        } else {
+          x = __ldcg(reinterpret_cast<const float4*>(src + (size_t)c * (2 * kRows * kD)));
+          y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)c * (2 * kRows * kD)) + 1);
+        }
+        const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(u[i], f, acc[i]);
       }
@@ -491,12 +514,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
                                                         pack_half2(acc[4], acc[5]), pack_half2(acc[6], acc[7]));
     }
   }
-  __syncwarp();
-  cluster_arrive_all();
-  cluster_wait_all();  // #2: no CTA leaves while another may read its rows
 }
 
-constexpr int kSizes[4] = {1, 2, 4, 8};  // pairs per cluster
+// How a call is cut: blocks (grid indices; a ragged batch leaves about half a block a sequence unused) and pairs
+// per cluster.  A launch takes about waves x (a fixed part + the tiles of a pair), in units of one tile's time
+// (1.9 us); a wave is as many clusters of that size as a GB300 holds at once (a cluster stays inside a GPC).
+struct DensePlan {
+  int blocks, pairs;
+};
+constexpr int kSizes[4] = {1, 2, 4, 8};
+constexpr int kHeld[4] = {76, 36, 16, 8};
+
+DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
+  constexpr int kBlock = 2 * kRows;
+  DensePlan d{(int)((long long)n_tok * kHPG / kBlock) + n_seq, 1};
+  const long long likely = ((long long)n_tok * kHPG + kBlock / 2 * (n_seq - 1LL) + kBlock - 1) / kBlock;
+  const long long longest = with_selected ? max_n_kv : std::min<long long>(max_n_kv, (long long)identity_max + 32 * kTreeWords);
+  const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
+  double best_t = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    if (i > 0 && kSizes[i] > tiles) break;
+    const double waves = (double)((likely * kGroups + kHeld[i] - 1) / kHeld[i]);
+    const double t = waves * ((i == 0 ? 4.0 : 5.0) + (tiles + kSizes[i] - 1) / kSizes[i]);
+    if (i == 0 || t < best_t) {
+      d.pairs = kSizes[i];
+      best_t = t;
+    }
+  }
+  return d;
+}
 
 cudaLaunchConfig_t tree_config(int S, int blocks, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
@@ -515,63 +561,38 @@ cudaLaunchConfig_t tree_config(int S, int blocks, cudaStream_t stream, cudaLaunc
   return cfg;
 }
 
-// Per device, set once: the kernel's attributes, and how many clusters of each size the GPU holds at once
-// (0: none of that size); threads that race here store the same values.
-cudaError_t tree_setup(int (&n_max)[4]) {
+// Per device, set once: the kernel's attributes (threads that race here set the same ones).
+cudaError_t tree_setup() {
   static std::atomic<int> ready[64];
-  static std::atomic<int> held[64][4];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (ready[dev].load(std::memory_order_acquire) == 0) {
-    if ((e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess)
-      return e;
-    if ((e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-      return e;
-    for (int i = 0; i < 4; ++i) {
-      cudaLaunchAttribute attr[2];
-      cudaLaunchConfig_t cfg = tree_config(kSizes[i], 1, nullptr, attr);
-      int n = 0;
-      if ((e = cudaOccupancyMaxActiveClusters(&n, tree_dense_kernel, &cfg)) != cudaSuccess) return e;
-      held[dev][i].store(n, std::memory_order_relaxed);
-    }
-    ready[dev].store(1, std::memory_order_release);
-  }
-  for (int i = 0; i < 4; ++i) n_max[i] = held[dev][i].load(std::memory_order_relaxed);
-  return n_max[0] > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
+  if (ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return e;
+  ready[dev].store(1, std::memory_order_release);
+  return cudaSuccess;
 }
 
 }  // namespace
 
+size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
+  const DensePlan d = dense_plan(n_seq, n_tok, max_n_kv, identity_max, with_selected);
+  return d.pairs == 1 ? 0 : (size_t)d.blocks * kGroups * 2 * d.pairs * kRows * kD * sizeof(float);
+}
+
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                               const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
-                              float sm_scale, int* status, cudaStream_t stream) {
-  int n_max[4];
-  cudaError_t e = tree_setup(n_max);
+                              float* part, float sm_scale, int* status, cudaStream_t stream) {
+  cudaError_t e = tree_setup();
   if (e != cudaSuccess) return e;
-  constexpr int kBlock = 2 * kRows;
-  const int blocks = (int)((long long)b.n_tok * kHPG / kBlock) + b.n_seq;  // indices; a ragged batch leaves about
-  const long long likely = ((long long)b.n_tok * kHPG + kBlock / 2 * (b.n_seq - 1LL) + kBlock - 1) / kBlock;  // half a block each unused
-  // Pairs per cluster: waves x (a fixed part + the tiles of a pair), in units of one tile's time.
-  const long long longest = bits ? b.max_n_kv : std::min<long long>(b.max_n_kv, (long long)b.identity_max + 32 * b.tree_words);
-  const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
-  int best = 1;
-  double best_t = 0.0;
-  for (int i = 0; i < 4; ++i) {
-    const int S = kSizes[i];
-    if (n_max[i] <= 0 || (S > 1 && S > tiles)) continue;
-    const double waves = (double)((likely * kGroups + n_max[i] - 1) / n_max[i]);
-    const double t = waves * (8.0 + 0.8 * i + (tiles + S - 1) / S);
-    if (i == 0 || t < best_t) {
-      best = S;
-      best_t = t;
-    }
-  }
-  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, status};
+  const DensePlan d = dense_plan(b.n_seq, b.n_tok, b.max_n_kv, b.identity_max, bits != nullptr);
+  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, part, status};
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = tree_config(best, blocks, stream, attr);
-  return cudaLaunchKernelEx(&cfg, tree_dense_kernel, a, best);
+  cudaLaunchConfig_t cfg = tree_config(d.pairs, d.blocks, stream, attr);
+  return cudaLaunchKernelEx(&cfg, tree_dense_kernel, a, d.pairs);
 }
 
 }  // namespace qsa
