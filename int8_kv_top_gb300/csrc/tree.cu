@@ -74,7 +74,7 @@ struct DenseTreeArgs {
   float scale_log2;
   const __half* gate;
   __half* out;
-  float* part;           // unmerged O rows, [CTA of the grid][kRows][kD]; null for one pair per cluster
+  float* part;           // unmerged O, [CTA of the grid][kD / 4][kRows][4]; null for one pair per cluster
   int* status;
 };
 
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     // complete, so both CTAs' MMAs are done with them)
     if (J > 0 && any_row) {
       tc_fence_after();
-      float* grow = a.part + ((size_t)(blockIdx.y * gridDim.x + blockIdx.x) * kRows + r) * kD;
+      float4* grow = reinterpret_cast<float4*>(a.part) + (size_t)(blockIdx.y * gridDim.x + blockIdx.x) * (kRows * kD / 4) + r;
 #pragma unroll 1
       for (int c0 = wg * 128; c0 < wg * 128 + 128; c0 += 32) {
         uint32_t o[32];
@@ -444,13 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
           for (int i = 0; i < 8; ++i)
             dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
                                  __uint_as_float(o[4 * i + 3]));
-        } else if (m_run != -INFINITY) {  // 32-byte stores: whole sectors
+        } else if (m_run != -INFINITY) {  // a warp's rows lie side by side: 512 bytes a store
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(grow + c0 + i), "r"(o[i]),
-                         "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
-                         "r"(o[i + 7])
-                         : "memory");
+          for (int i = 0; i < 8; ++i)
+            grow[(size_t)(c0 / 4 + i) * kRows] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
     }
@@ -468,40 +466,51 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   if (warp < 16) {
     const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
     const int per = kRows / S;
+    // one pair: a warp a row, 8 dims a lane, from shared memory; else lanes are rows (16 at least), 8 dims each
     for (int x = tid; x < per * 32; x += 512) {
-      const int r = pair * per + (x >> 5), d8 = x & 31, R = row0 + r;
+      const int r = pair * per + (S == 1 ? x >> 5 : x % per), d8 = S == 1 ? x & 31 : x / per, R = row0 + r;
       const int ti = R / kHPG - blk_row0 / kHPG;
-      if (R >= T * kHPG || !((s_ours >> ti) & 1)) continue;  // uniform over the warp
+      if (R >= T * kHPG || !((s_ours >> ti) & 1)) continue;
+      const size_t at = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD + d8 * 8;
+      uint4 gw = make_uint4(0u, 0u, 0u, 0u);
+      if (a.gate) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at));
       float M = -INFINITY, L = 0.f;
       for (int c = 0; c < S; ++c) M = fmaxf(M, ml[c * kRows + r].x);
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      // CTA 0 of the cluster with this half's rows; the next pair's are 2 kRows further
-      const float* src = a.part + ((size_t)(blockIdx.y * gridDim.x + blockIdx.x - 2 * pair) * kRows + r) * kD + d8 * 8;
-#pragma unroll 4
-      for (int c = 0; c < S; ++c) {
-        const float2 v = ml[c * kRows + r];
-        if (v.x == -INFINITY) continue;  // nothing of this row there
+      auto add = [&](float2 v, float4 p0, float4 p1) {
+        if (v.x == -INFINITY) return;  // nothing of this row there
         const float f = fast_exp2(v.x - M);
         L = fmaf(v.y, f, L);
-        float4 x, y;
-        if (S == 1) {
-          const float4* local = reinterpret_cast<const float4*>(smem + (size_t)r * (kOStride * 4)) + 2 * d8;
-          x = local[0];
-          y = local[1];
-        } else {
-          x = __ldcg(reinterpret_cast<const float4*>(src + (size_t)c * (2 * kRows * kD)));
-          y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)c * (2 * kRows * kD)) + 1);
-        }
-        const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const float u[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = fmaf(u[i], f, acc[i]);
+      };
+      if (S == 1) {
+        const float4* src = reinterpret_cast<const float4*>(smem + (size_t)r * (kOStride * 4)) + 2 * d8;
+        add(ml[r], src[0], src[1]);
+      } else {
+        // CTA 0 of the cluster with this half's rows, the next pair's two CTAs further: all parts are loaded
+        // before any is added (a part of a run that has none is read and dropped)
+        const float4* src = reinterpret_cast<const float4*>(a.part) +
+                            (size_t)(blockIdx.y * gridDim.x + blockIdx.x - 2 * pair) * (kRows * kD / 4) +
+                            (size_t)(2 * d8) * kRows + r;
+        for (int c0 = 0; c0 < S; c0 += 4) {
+          float4 p[4][2];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float4* at4 = src + (size_t)min(c0 + u, S - 1) * (2 * kRows * kD / 4);
+            p[u][0] = __ldcg(at4);
+            p[u][1] = __ldcg(at4 + kRows);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (c0 + u < S) add(ml[(c0 + u) * kRows + r], p[u][0], p[u][1]);
+        }
       }
       const float inv = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] *= inv;
-      const size_t o = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD + d8 * 8;
       if (a.gate) {
-        const uint4 gw = __ldg(reinterpret_cast<const uint4*>(a.gate + o));
         const uint32_t w[4] = {gw.x, gw.y, gw.z, gw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -510,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
           acc[2 * i + 1] *= gate_sigmoid(v.y);
         }
       }
-      *reinterpret_cast<uint4*>(a.out + o) = make_uint4(pack_half2(acc[0], acc[1]), pack_half2(acc[2], acc[3]),
-                                                        pack_half2(acc[4], acc[5]), pack_half2(acc[6], acc[7]));
+      *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_half2(acc[0], acc[1]), pack_half2(acc[2], acc[3]),
+                                                         pack_half2(acc[4], acc[5]), pack_half2(acc[6], acc[7]));
     }
   }
 }
@@ -523,7 +532,7 @@ struct DensePlan {
   int blocks, pairs;
 };
 constexpr int kSizes[4] = {1, 2, 4, 8};
-constexpr int kHeld[4] = {76, 36, 16, 8};
+constexpr int kHeld[4] = {76, 36, 15, 7};
 
 DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
   constexpr int kBlock = 2 * kRows;
@@ -535,7 +544,7 @@ DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool 
   for (int i = 0; i < 4; ++i) {
     if (i > 0 && kSizes[i] > tiles) break;
     const double waves = (double)((likely * kGroups + kHeld[i] - 1) / kHeld[i]);
-    const double t = waves * ((i == 0 ? 4.0 : 5.0) + (tiles + kSizes[i] - 1) / kSizes[i]);
+    const double t = waves * ((i == 0 ? 5.0 : 6.0 + 0.3 * i) + (tiles + kSizes[i] - 1) / kSizes[i]);
     if (i == 0 || t < best_t) {
       d.pairs = kSizes[i];
       best_t = t;

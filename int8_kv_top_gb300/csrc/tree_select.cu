@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeBatch b, const
 }
 
 // ---------------------------------------------------------------- 2. score
-constexpr int kScoreThreads = 9 * 32;  // warps 0-3 producers, 4-7 epilogue, 8 MMA
+constexpr int kScoreThreads = 13 * 32;  // warps 0-7 producers (two teams), 8-11 epilogue, 12 MMA
 constexpr int kOffB = kTileStages * kTileStageBytes;  // hi | lo rows: 8 blocks of [64 tokens][64] SW128
 constexpr int kBBlock = kTokChunk * 128;
 constexpr int kScoreSmem = kOffB + 8 * kBBlock + 1024;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     mbar_init(&bars.drain, 1);
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 12) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
@@ -192,10 +192,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const uint32_t tmem = s_tmem;
   const int N = (n_here + 15) / 16 * 16;
 
-  if (warp < 4) {
+  if (warp < 8) {
     const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0, 0u};
-    produce_tiles<kScoreCodes>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp, lane);
-  } else if (warp == 8) {
+    produce_tiles<kScoreCodes, 2>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp & 3, lane, warp >> 2);
+  } else if (warp == 12) {
     if (lane == 0) {
       const uint32_t idesc = idesc_f16_f32(kTileCells, N, 0, 0);
       const uint64_t bdesc = sdesc_sw128(smem_u32(smem + kOffB), 16, 1024);
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     __syncwarp();
   } else {
-    const int et = tid - 128, quarter = warp & 3;
+    const int et = tid - 256, quarter = warp & 3;
     for (int i = et; i < kTokChunk * 64; i += 128) {  // 16-byte chunk c of token row r; rows of others are zeros
       const int r = i >> 6, c = i & 63;
       if (r >= N) break;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
@@ -316,11 +316,11 @@ cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __
       cudaSuccess)
     return e;
   // tiles per CTA: as few as keep the CTAs near two waves of one per SM (a CTA's set-up, its B rows above all,
-  // costs about as much as three tiles)
+  // costs about as much as three tiles); ragged batches leave about half of the grid empty
   const int tiles = (b.max_n_kv + kTileCells - 1) / kTileCells;
   const int zb = b.n_tok / kTokChunk + b.n_seq;
   int per = 2;
-  while (per < 16 && (long long)((tiles + per - 1) / per) * kGroups * zb > 304) per *= 2;
+  while (per < 16 && (long long)((tiles + per - 1) / per) * kGroups * zb > 608) per *= 2;
   e = launch_pdl(tree_score_kernel, dim3((tiles + per - 1) / per, kGroups, zb), dim3(kScoreThreads), kScoreSmem, stream, b,
                  w, kq, ksc, per, p.sm_scale, status);
   if (e != cudaSuccess) return e;
