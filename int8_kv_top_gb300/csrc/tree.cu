@@ -39,6 +39,7 @@
 // Every mbarrier wait is bounded; after a timeout a CTA still meets the cluster's barriers.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "tree_common.cuh"
 
@@ -455,8 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
 
   // ---------------------------------------------------------------- merge
-  // Run c's CTA owns the rows [c * 128 / S, (c + 1) * 128 / S) of its half and adds every run's part in the
-  // runs' order: out = sum_c O_c 2^(m_c - M) / L.
+  // Run c's CTA owns an S-th of its half's rows and adds every run's part in the runs' order: out = sum_c O_c 2^(m_c - M) / L.
   tc_fence_before();
   __syncwarp();
   cluster_arrive_all();
@@ -465,10 +465,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   if (warp == 16 && J > 0) tmem_dealloc_pair(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
   if (warp < 16) {
     const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
-    const int per = kRows / S;
+    const int per = (kRows + S - 1) / S;  // rows of an owner
     // one pair: a warp a row, 8 dims a lane, from shared memory; else lanes are rows (16 at least), 8 dims each
     for (int x = tid; x < per * 32; x += 512) {
       const int r = pair * per + (S == 1 ? x >> 5 : x % per), d8 = S == 1 ? x & 31 : x / per, R = row0 + r;
+      if (r >= kRows) continue;
       const int ti = R / kHPG - blk_row0 / kHPG;
       if (R >= T * kHPG || !((s_ours >> ti) & 1)) continue;
       const size_t at = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD + d8 * 8;
@@ -527,12 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
 
 // How a call is cut: blocks (grid indices; a ragged batch leaves about half a block a sequence unused) and pairs
 // per cluster.  A launch takes about waves x (a fixed part + the tiles of a pair), in units of one tile's time
-// (1.9 us); a wave is as many clusters of that size as a GB300 holds at once (a cluster stays inside a GPC).
+// (1.9 us; fixed: 9 us for one pair, 11 to 13 with a merge); a wave is as many clusters of that size as a GB300
+// holds at once (a cluster stays inside a GPC).  Lengths are on the device: waves is between the whole waves
+// that equal lengths take and what lengths spread over (0, max_n_kv) take, for which 0.6 of a wave is filled.
 struct DensePlan {
   int blocks, pairs;
 };
-constexpr int kSizes[4] = {1, 2, 4, 8};
-constexpr int kHeld[4] = {76, 36, 15, 7};
+constexpr int kSizes[7] = {1, 2, 3, 4, 5, 6, 8};
+constexpr int kHeld[7] = {76, 36, 24, 15, 14, 8, 7};
 
 DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
   constexpr int kBlock = 2 * kRows;
@@ -541,12 +544,13 @@ DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool 
   const long long longest = with_selected ? max_n_kv : std::min<long long>(max_n_kv, (long long)identity_max + 32 * kTreeWords);
   const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
   double best_t = 0.0;
-  for (int i = 0; i < 4; ++i) {
-    if (i > 0 && kSizes[i] > tiles) break;
-    const double waves = (double)((likely * kGroups + kHeld[i] - 1) / kHeld[i]);
-    const double t = waves * ((i == 0 ? 5.0 : 6.0 + 0.3 * i) + (tiles + kSizes[i] - 1) / kSizes[i]);
+  for (int i = 0; i < 7; ++i) {
+    const int S = kSizes[i];
+    const double w = (double)(likely * kGroups) / kHeld[i];
+    const double waves = w <= 1.0 ? 1.0 : 0.5 * (std::ceil(w) + (n_seq > 1 ? 0.4 + 0.6 * w : std::ceil(w)));
+    const double t = waves * ((S == 1 ? 5.0 : 6.0 + 0.1 * S) + (tiles + S - 1) / S);
     if (i == 0 || t < best_t) {
-      d.pairs = kSizes[i];
+      d.pairs = S;
       best_t = t;
     }
   }

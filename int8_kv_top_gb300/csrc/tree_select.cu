@@ -9,10 +9,11 @@
 //  1. tree_prep   Qsum = hi + lo + residual of every selected (token, group) with its error terms, and the
 //                 largest |ksc| of every 2,048 cells (bounds; only cells that some token sees count).
 //  2. tree_score  the tree's tokens are few and the cells many, so the operands are swapped: M = 128 cells
-//                 (A = the codes as fp16, made from int8 by producer warps as in tree.cu), N = up to 64 tokens
-//                 (B = their hi | lo rows), one TMEM accumulator per scale block.  An epilogue thread owns a
-//                 cell, so its four K scales are in registers.  Cells that a token does not see score -inf.
-//                 Per tile 64 MMAs of N = 64 against 32 KB of codes: bound by the producers' conversion.
+//                 (A = the codes as fp16, made from int8 by producer warps as in tree.cu), N = the hi rows and
+//                 behind them the lo rows of up to 32 tokens, one TMEM accumulator per scale block.  An epilogue
+//                 thread owns a cell, so its four K scales are in registers.  Cells that a token does not see
+//                 score -inf.  An MMA of N = 64 takes about 52 cycles (A's 4 KB through shared memory), 16 of them a
+//                 tile; hi and lo in one N instead of two MMAs each halves their number.
 //  3. topk_kernel<V, true>.
 #include "select_math.cuh"
 #include "tree_common.cuh"
@@ -20,7 +21,7 @@
 namespace qsa {
 namespace {
 
-constexpr int kTokChunk = 64;  // tokens per score CTA (UMMA N at most)
+constexpr int kTokChunk = 32;  // tokens per score CTA: UMMA N is at most twice that
 
 // ---------------------------------------------------------------- 1. prep
 // Blocks [0, 2 n_tok): (token row, group), thread = dim.  Blocks behind them: (sequence, chunk of cells).
@@ -111,16 +112,16 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeBatch b, const
 }
 
 // ---------------------------------------------------------------- 2. score
-constexpr int kScoreThreads = 13 * 32;  // warps 0-7 producers (two teams), 8-11 epilogue, 12 MMA
-constexpr int kOffB = kTileStages * kTileStageBytes;  // hi | lo rows: 8 blocks of [64 tokens][64] SW128
-constexpr int kBBlock = kTokChunk * 128;
-constexpr int kScoreSmem = kOffB + 8 * kBBlock + 1024;
+constexpr int kScoreThreads = 9 * 32;  // warps 0-3 producers, 4-7 epilogue, 8 MMA
+constexpr int kOffB = kTileStages * kTileStageBytes;  // 4 dim blocks of [hi rows, lo rows][64] SW128
+constexpr int kBBlock = 2 * kTokChunk * 128;
+constexpr int kScoreSmem = kOffB + kNB * kBBlock + 1024;
 
 struct __align__(8) TreeScoreBars {
   uint64_t full[kTileStages], empty[kTileStages], acc_full[2], acc_empty[2], b_full, drain;
 };
 
-// First token chunk of a sequence: as first_block in tree.cu, for chunks of 64 tokens.
+// First token chunk of a sequence: as first_block in tree.cu, for chunks of 32 tokens.
 __device__ __forceinline__ long long first_chunk(long long first_row, int s) { return first_row / kTokChunk + s; }
 
 __global__ void __launch_bounds__(kScoreThreads, 1)
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     mbar_init(&bars.drain, 1);
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 8) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
@@ -190,12 +191,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int N = (n_here + 15) / 16 * 16;
+  const int n16 = (n_here + 15) / 16 * 16, N = 2 * n16;  // row n: hi of token n; row n16 + n: lo
 
-  if (warp < 8) {
+  if (warp < 4) {
     const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0, 0u};
-    produce_tiles<kScoreCodes, 2>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp & 3, lane, warp >> 2);
-  } else if (warp == 12) {
+    produce_tiles<kScoreCodes>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp, lane);
+  } else if (warp == 8) {
     if (lane == 0) {
       const uint32_t idesc = idesc_f16_f32(kTileCells, N, 0, 0);
       const uint64_t bdesc = sdesc_sw128(smem_u32(smem + kOffB), 16, 1024);
@@ -210,12 +211,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           tc_fence_after();
           const uint64_t adesc = sdesc_sw128(smem_u32(smem) + slot * kTileStageBytes, 16, 1024);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)  // hi, then lo against the same codes
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ss(tmem + buf * 256 + d * kTokChunk, adesc + (uint64_t)((kk * 32) >> 4),
-                      bdesc + (uint64_t)(((2 * d + part) * kBBlock + kk * 32) >> 4), idesc,
-                      (part > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ss(tmem + buf * 256 + d * (2 * kTokChunk), adesc + (uint64_t)((kk * 32) >> 4),
+                    bdesc + (uint64_t)((d * kBBlock + kk * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
           umma_commit(&bars.empty[slot]);
         }
         if (go) umma_commit(&bars.acc_full[buf]);
@@ -225,13 +223,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     __syncwarp();
   } else {
-    const int et = tid - 256, quarter = warp & 3;
-    for (int i = et; i < kTokChunk * 64; i += 128) {  // 16-byte chunk c of token row r; rows of others are zeros
-      const int r = i >> 6, c = i & 63;
-      if (r >= N) break;
+    const int et = tid - 128, quarter = warp & 3;
+    for (int i = et; i < n16 * 64; i += 128) {  // 16-byte chunk c of token r's hi | lo row; rows of others are zeros
+      const int r = i >> 6, c = i & 63, d = c >> 4, row = r + (c & 8 ? n16 : 0);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (s_scale[r] != 0.f) v = __ldg(reinterpret_cast<const uint4*>(w.qhl + (size_t)(g * b.n_tok + t0 + r) * (2 * kD)) + c);
-      *reinterpret_cast<uint4*>(smem + kOffB + (c >> 3) * kBBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      *reinterpret_cast<uint4*>(smem + kOffB + d * kBBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -251,15 +248,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const float2 s23 = __half22float2(*reinterpret_cast<const __half2*>(&sw.y));
       if (!mbar_wait_warp(&bars.acc_full[buf], (j >> 1) & 1, status, &s_abort)) break;
       tc_fence_after();
-      for (int n0 = 0; n0 < N; n0 += 16) {
-        uint32_t v0[16], v1[16], v2[16], v3[16];
-        const uint32_t at = lane_base + buf * 256 + n0;
-        tmem_ld16(at, v0);
-        tmem_ld16(at + kTokChunk, v1);
-        tmem_ld16(at + 2 * kTokChunk, v2);
-        tmem_ld16(at + 3 * kTokChunk, v3);
-        tmem_wait_ld();
-        if (n0 + 16 >= N) {  // the accumulators are in registers
+      for (int n0 = 0; n0 < n16; n0 += 16) {
+        float acc[16];
+#pragma unroll
+        for (int d = 0; d < kNB; ++d) {
+          uint32_t hi[16], lo[16];
+          const uint32_t at = lane_base + buf * 256 + d * (2 * kTokChunk) + n0;
+          tmem_ld16(at, hi);
+          tmem_ld16(at + n16, lo);
+          tmem_wait_ld();
+          const float sd = d == 0 ? s01.x : d == 1 ? s01.y : d == 2 ? s23.x : s23.y;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+            acc[i] = d == 0 ? sd * x : fmaf(sd, x, acc[i]);
+          }
+        }
+        if (n0 + 16 >= n16) {  // the accumulators are in registers
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
@@ -269,12 +274,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           const int n = n0 + i;
           const float sc = s_scale[n];
           if (sc == 0.f) continue;  // warp-uniform
-          float v = s01.x * __uint_as_float(v0[i]);
-          v = fmaf(s01.y, __uint_as_float(v1[i]), v);
-          v = fmaf(s23.x, __uint_as_float(v2[i]), v);
-          v = fmaf(s23.y, __uint_as_float(v3[i]), v);
           const bool seen = dj < 0 || (dj < T && ((s_mask[n][dj >> 5] >> (dj & 31)) & 1u));
-          if (cell < n_scan) dst0[(size_t)n * w.pitch + cell] = seen ? __float2half_rn(v * sc) : __ushort_as_half(0xFC00);
+          if (cell < n_scan) dst0[(size_t)n * w.pitch + cell] = seen ? __float2half_rn(acc[i] * sc) : __ushort_as_half(0xFC00);
         }
       }
     }
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
@@ -320,7 +321,7 @@ cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __
   const int tiles = (b.max_n_kv + kTileCells - 1) / kTileCells;
   const int zb = b.n_tok / kTokChunk + b.n_seq;
   int per = 2;
-  while (per < 16 && (long long)((tiles + per - 1) / per) * kGroups * zb > 608) per *= 2;
+  while (per < 8 && (long long)((tiles + per - 1) / per) * kGroups * zb > 304) per *= 2;
   e = launch_pdl(tree_score_kernel, dim3((tiles + per - 1) / per, kGroups, zb), dim3(kScoreThreads), kScoreSmem, stream, b,
                  w, kq, ksc, per, p.sm_scale, status);
   if (e != cudaSuccess) return e;
