@@ -766,13 +766,10 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     n_kv = e.z + T;
     kq += (size_t)e.x * (kGroups * kD);
     ksc += (size_t)e.x * (kGroups * kNB);
-    const float* kc = kmax + (size_t)s * ts.chunks * (kGroups * kNB) + g * kNB;
-#pragma unroll
-    for (int b = 0; b < kNB; ++b) km[b] = 0.f;
-    for (int c = 0; c * kTreeChunk < n_kv; ++c)
-#pragma unroll
-      for (int b = 0; b < kNB; ++b) km[b] = fmaxf(km[b], __ldg(kc + c * (kGroups * kNB) + b));
-    row_scale = tree_row_scale(eh + ((size_t)g * T_sel + r) * 8, km, sm_scale);
+    if (warp == 0) {  // for the thread that sets the bound
+      warp_kmax(ts, s, g, n_kv, lane, km);
+      row_scale = tree_row_scale(eh + ((size_t)g * T_sel + r) * 8, km, sm_scale);
+    }
   } else {
 #pragma unroll
     for (int b = 0; b < kNB; ++b) km[b] = kmax[g * kNB + b];

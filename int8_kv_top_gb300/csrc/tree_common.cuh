@@ -66,6 +66,22 @@ struct TreeSelect {
 };
 constexpr int kTreeChunk = 2048;  // cells of a kmax chunk
 
+// max |ksc| per scale block of group g over the cells of sequence s (n_scan of them), by a whole warp: every lane
+// loads a chunk's maxima at once (32 chunks are the 65,536 cells that the score path holds).
+__device__ __forceinline__ void warp_kmax(const TreeSelect& w, int s, int g, int n_scan, int lane, float (&km)[kNB]) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (lane * kTreeChunk < n_scan)
+    v = __ldg(reinterpret_cast<const float4*>(w.kmax + ((size_t)s * w.chunks + lane) * (kGroups * kNB) + g * kNB));
+  km[0] = v.x;
+  km[1] = v.y;
+  km[2] = v.z;
+  km[3] = v.w;
+#pragma unroll
+  for (int b = 0; b < kNB; ++b)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) km[b] = fmaxf(km[b], __shfl_xor_sync(0xffffffffu, km[b], o));
+}
+
 // A power of two that keeps a row's scores inside fp16: |score| <= sm_scale 128 sum_b kmax_b H_b.
 __device__ __forceinline__ float tree_row_scale(const float* eh, const float (&kmax)[kNB], float sm_scale) {
   float h = 0.f;

@@ -118,7 +118,7 @@ constexpr int kBBlock = 2 * kTokChunk * 128;
 constexpr int kScoreSmem = kOffB + kNB * kBBlock + 1024;
 
 struct __align__(8) TreeScoreBars {
-  uint64_t full[kTileStages], empty[kTileStages], acc_full[2], acc_empty[2], b_full, drain;
+  uint64_t full[kTileStages], empty[kTileStages], acc_full[2], acc_empty[2], b_full, tmem_ready, drain;
 };
 
 // First token chunk of a sequence: as first_block in tree.cu, for chunks of 32 tokens.
@@ -147,28 +147,6 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (T <= 0 || kc < 0 || kc * kTokChunk >= T || J <= 0 || n_scan <= b.identity_max) return;  // uniform
   const int t0 = e4.w + (int)kc * kTokChunk;  // first token row
   const int n_here = min(kTokChunk, T - (int)kc * kTokChunk);
-  bool sel = false;
-  if (tid < kTokChunk) {
-    int seen = pos0;
-#pragma unroll
-    for (int i = 0; i < kTreeWords; ++i) {
-      const uint32_t m = tid < n_here ? tree_mask_word(b, t0 + tid, i, T) : 0u;
-      s_mask[tid][i] = m;
-      seen += __popc(m);
-    }
-    sel = tid < n_here && seen > b.identity_max;
-    float sc = 0.f;
-    if (sel) {
-      float km[kNB] = {0.f, 0.f, 0.f, 0.f};
-      for (int c = 0; c * kTreeChunk < n_scan; ++c)
-#pragma unroll
-        for (int i = 0; i < kNB; ++i)
-          km[i] = fmaxf(km[i], __ldg(w.kmax + ((size_t)sq * w.chunks + c) * (kGroups * kNB) + g * kNB + i));
-      sc = sm_scale * tree_row_scale(w.eh + (size_t)(g * b.n_tok + t0 + tid) * 8, km, sm_scale);
-    }
-    s_scale[tid] = sc;
-  }
-  if (!__syncthreads_or(sel)) return;
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kTileStages; ++i) {
@@ -180,24 +158,25 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       mbar_init(&bars.acc_empty[i], 4);
     }
     mbar_init(&bars.b_full, 4);
+    mbar_init(&bars.tmem_ready, 1);
     mbar_init(&bars.drain, 1);
     fence_mbar_init();
   }
-  if (warp == 8) {
-    tmem_alloc(&s_tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
   const int n16 = (n_here + 15) / 16 * 16, N = 2 * n16;  // row n: hi of token n; row n16 + n: lo
 
   if (warp < 4) {
     const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0, 0u};
     produce_tiles<kScoreCodes>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp, lane);
   } else if (warp == 8) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+    __syncwarp();
     if (lane == 0) {
+      mbar_arrive(&bars.tmem_ready);
+      tc_fence_after();
+      const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
       const uint32_t idesc = idesc_f16_f32(kTileCells, N, 0, 0);
       const uint64_t bdesc = sdesc_sw128(smem_u32(smem + kOffB), 16, 1024);
       bool go = mbar_wait_poll<false>(&bars.b_full, 0, status, &s_abort);
@@ -224,6 +203,21 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     __syncwarp();
   } else {
     const int et = tid - 128, quarter = warp & 3;
+    if (warp == 4) {  // lane = token: its mask and what its scores are multiplied by
+      float km[kNB];
+      warp_kmax(w, sq, g, n_scan, lane, km);
+      int seen = pos0;
+#pragma unroll
+      for (int i = 0; i < kTreeWords; ++i) {
+        const uint32_t m = lane < n_here ? tree_mask_word(b, t0 + lane, i, T) : 0u;
+        s_mask[lane][i] = m;
+        seen += __popc(m);
+      }
+      s_scale[lane] = lane < n_here && seen > b.identity_max
+                          ? sm_scale * tree_row_scale(w.eh + (size_t)(g * b.n_tok + t0 + lane) * 8, km, sm_scale)
+                          : 0.f;
+    }
+    named_bar_any(1, 128, false);
     for (int i = et; i < n16 * 64; i += 128) {  // 16-byte chunk c of token r's hi | lo row; rows of others are zeros
       const int r = i >> 6, c = i & 63, d = c >> 4, row = r + (c & 8 ? n16 : 0);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -233,14 +227,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.b_full);
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const bool t_ok = mbar_wait_warp(&bars.tmem_ready, 0, status, &s_abort);
+    tc_fence_after();
+    const uint32_t lane_base = *reinterpret_cast<volatile uint32_t*>(&s_tmem) + ((uint32_t)(quarter * 32) << 16);
     auto scales_of = [&](int j) {  // this thread's cell: the four K scales of the group
       const size_t c = min((j_begin + j) * kTileCells + quarter * 32 + lane, n_scan - 1);
       return __ldg(reinterpret_cast<const uint2*>(ksc + ((size_t)e4.x + c) * (kGroups * kNB) + g * kNB));
     };
     uint2 sw_next = scales_of(0);
     __half* dst0 = w.scores + (size_t)(g * b.n_tok + t0) * w.pitch;
-    for (int j = 0; j < J; ++j) {
+    for (int j = 0; t_ok && j < J; ++j) {
       const int buf = j & 1, cell = (j_begin + j) * kTileCells + quarter * 32 + lane, dj = cell - pos0;
       const uint2 sw = sw_next;
       if (j + 1 < J) sw_next = scales_of(j + 1);
@@ -283,7 +279,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 8) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
 }
 
 }  // namespace
