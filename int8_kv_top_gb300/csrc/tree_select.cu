@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeBatch b, const
 }
 
 // ---------------------------------------------------------------- 2. score
-constexpr int kScoreThreads = 9 * 32;  // warps 0-3 producers, 4-7 epilogue, 8 MMA
+constexpr int kScoreThreads = 13 * 32;  // warps 0-3 producers, 4-11 epilogue (16 tokens each half), 12 MMA
 constexpr int kOffB = kTileStages * kTileStageBytes;  // 4 dim blocks of [hi rows, lo rows][64] SW128
 constexpr int kBBlock = 2 * kTokChunk * 128;
 constexpr int kScoreSmem = kOffB + kNB * kBBlock + 1024;
@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.acc_full[i], 1);
-      mbar_init(&bars.acc_empty[i], 4);
+      mbar_init(&bars.acc_empty[i], 8);
     }
-    mbar_init(&bars.b_full, 4);
+    mbar_init(&bars.b_full, 8);
     mbar_init(&bars.tmem_ready, 1);
     mbar_init(&bars.drain, 1);
     fence_mbar_init();
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   if (warp < 4) {
     const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0, 0u};
     produce_tiles<kScoreCodes>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp, lane);
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
     tc_fence_before();
@@ -202,7 +202,27 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     __syncwarp();
   } else {
-    const int et = tid - 128, quarter = warp & 3;
+    const int et = tid - 128, quarter = warp & 3, n0 = 16 * ((warp - 4) >> 2);  // this warp's cells and tokens
+    {
+      // 16-byte chunk c of token r's hi | lo row: four rows' loads before any store.  Rows of tokens that do not
+      // select were not written by tree_prep: what they hold only reaches their own scores, which are not stored.
+      const int c = et & 63, d = c >> 4;
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = (et >> 6) + 4 * i;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < n_here) v[i] = __ldg(reinterpret_cast<const uint4*>(w.qhl + (size_t)(g * b.n_tok + t0 + r) * (2 * kD)) + c);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = (et >> 6) + 4 * i, row = r + (c & 8 ? n16 : 0);
+        if (r < n16) *reinterpret_cast<uint4*>(smem + kOffB + d * kBBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[i];
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.b_full);
     if (warp == 4) {  // lane = token: its mask and what its scores are multiplied by
       float km[kNB];
       warp_kmax(w, sq, g, n_scan, lane, km);
@@ -217,25 +237,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                           ? sm_scale * tree_row_scale(w.eh + (size_t)(g * b.n_tok + t0 + lane) * 8, km, sm_scale)
                           : 0.f;
     }
-    named_bar_any(1, 128, false);
-    for (int i = et; i < n16 * 64; i += 128) {  // 16-byte chunk c of token r's hi | lo row; rows of others are zeros
-      const int r = i >> 6, c = i & 63, d = c >> 4, row = r + (c & 8 ? n16 : 0);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (s_scale[r] != 0.f) v = __ldg(reinterpret_cast<const uint4*>(w.qhl + (size_t)(g * b.n_tok + t0 + r) * (2 * kD)) + c);
-      *reinterpret_cast<uint4*>(smem + kOffB + d * kBBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.b_full);
     const bool t_ok = mbar_wait_warp(&bars.tmem_ready, 0, status, &s_abort);
     tc_fence_after();
-    const uint32_t lane_base = *reinterpret_cast<volatile uint32_t*>(&s_tmem) + ((uint32_t)(quarter * 32) << 16);
+    named_bar_any(1, 256, false);  // masks and scales are in shared memory
+    const uint32_t lane_base = *reinterpret_cast<volatile uint32_t*>(&s_tmem) + ((uint32_t)(quarter * 32) << 16) + n0;
     auto scales_of = [&](int j) {  // this thread's cell: the four K scales of the group
       const size_t c = min((j_begin + j) * kTileCells + quarter * 32 + lane, n_scan - 1);
       return __ldg(reinterpret_cast<const uint2*>(ksc + ((size_t)e4.x + c) * (kGroups * kNB) + g * kNB));
     };
     uint2 sw_next = scales_of(0);
-    __half* dst0 = w.scores + (size_t)(g * b.n_tok + t0) * w.pitch;
+    __half* dst0 = w.scores + (size_t)(g * b.n_tok + t0 + n0) * w.pitch;
     for (int j = 0; t_ok && j < J; ++j) {
       const int buf = j & 1, cell = (j_begin + j) * kTileCells + quarter * 32 + lane, dj = cell - pos0;
       const uint2 sw = sw_next;
@@ -244,12 +255,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const float2 s23 = __half22float2(*reinterpret_cast<const __half2*>(&sw.y));
       if (!mbar_wait_warp(&bars.acc_full[buf], (j >> 1) & 1, status, &s_abort)) break;
       tc_fence_after();
-      for (int n0 = 0; n0 < n16; n0 += 16) {
-        float acc[16];
+      float acc[16];
+      if (n0 < n16) {
 #pragma unroll
         for (int d = 0; d < kNB; ++d) {
           uint32_t hi[16], lo[16];
-          const uint32_t at = lane_base + buf * 256 + d * (2 * kTokChunk) + n0;
+          const uint32_t at = lane_base + buf * 256 + d * (2 * kTokChunk);
           tmem_ld16(at, hi);
           tmem_ld16(at + n16, lo);
           tmem_wait_ld();
@@ -260,26 +271,28 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
             acc[i] = d == 0 ? sd * x : fmaf(sd, x, acc[i]);
           }
         }
-        if (n0 + 16 >= n16) {  // the accumulators are in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-        }
+      }
+      tc_fence_before();  // the accumulators are in registers
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+      if (n0 >= n16 || cell >= n_scan) continue;
+      __half* dst = dst0 + cell;
+      const bool drafted = (j_begin + j + 1) * kTileCells > pos0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int n = n0 + i;
-          const float sc = s_scale[n];
-          if (sc == 0.f) continue;  // warp-uniform
-          const bool seen = dj < 0 || (dj < T && ((s_mask[n][dj >> 5] >> (dj & 31)) & 1u));
-          if (cell < n_scan) dst0[(size_t)n * w.pitch + cell] = seen ? __float2half_rn(acc[i] * sc) : __ushort_as_half(0xFC00);
+      for (int i = 0; i < 16; ++i) {
+        const float sc = s_scale[n0 + i];
+        if (sc != 0.f) {  // the same for the whole warp
+          const bool seen = !drafted || dj < 0 || ((s_mask[n0 + i][dj >> 5] >> (dj & 31)) & 1u);
+          *dst = seen ? __float2half_rn(acc[i] * sc) : __ushort_as_half(0xFC00);
         }
+        dst += w.pitch;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
+  if (warp == 12) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
 }
 
 }  // namespace
