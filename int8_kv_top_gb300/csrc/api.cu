@@ -137,9 +137,14 @@ int decode_layer_limit(int* rc) {
 }
 
 // Whether a tree call selects for its tokens together (tree_select.cu, then one tensor-core attention for all)
-// or gives each selected (token, group) a cluster of its own.
+// or gives each selected (token, group) a cluster of its own.  Together costs by the sequences and their cells,
+// the clusters cost by the tokens.  Measured (together / clusters, us a call of equal trees): one sequence of 8,192
+// cells with 4 tokens 53 / 37, 8 tokens 54 / 54, 32 tokens 55 / 89; of 30,000 cells with 8 tokens 114 / 102, 16
+// tokens 108 / 104, 32 tokens 117 / 197; 16 sequences of 8,192 cells with 3 tokens 183 / 160, 6 tokens 188 / 254;
+// of 30,000 cells with 4 tokens 539 / 386, 6 tokens 546 / 571, 16 tokens 567 / 1,412.
 bool tree_selects_together(int n_seq, int n_tok, int max_n_kv, const qsa::Params& p) {
-  return max_n_kv > p.identity_max && max_n_kv <= qsa::select_max_cells() && n_tok >= 2LL * n_seq;
+  const long long least = (max_n_kv <= 16384 ? 4 : 6) * (n_seq < 4 ? 2 : 1);  // tokens a sequence
+  return max_n_kv > p.identity_max && max_n_kv <= qsa::select_max_cells() && n_tok >= least * n_seq;
 }
 
 // Selection over a cache longer than the score-GEMM path holds: the single-launch decode layer's
