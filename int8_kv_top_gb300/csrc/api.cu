@@ -629,11 +629,10 @@ int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, co
                             static_cast<uint8_t*>(ws) +
                                 qsa::tree_dense_workspace_bytes(n_seq, n_tok, max_n_kv, p.identity_max, true),
                             &w);
-    e = qsa::launch_tree_select(b, w, hq, kq, hksc, ids, p, st, s);
+    e = qsa::launch_tree_select(b, w, hq, kq, hksc, ids, qsa::tree_dense_plan(b, true, ws), p, st, s);
     if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention (selection) launch");
   }
-  e = qsa::launch_tree_dense(b, hq, kq, vq, hksc, hvsc, w.bits, w.pitch / 32, hg, hout, static_cast<float*>(ws),
-                             p.sm_scale, st, s);
+  e = qsa::launch_tree_dense(b, hq, kq, vq, hksc, hvsc, w.bits, w.pitch / 32, hg, hout, ws, p.sm_scale, st, s);
   if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention launch");
   if (max_n_kv > p.identity_max && !together) {
     e = qsa::launch_decode_layer(hq, kq, vq, hksc, hvsc, sq, n_seq, (long long)n_pool, 0, 0, n_tok, max_n_kv, ids, hg,

@@ -145,12 +145,13 @@ struct TreeBatch;
 struct TreeSelect;
 size_t tree_select_layout(int n_seq, int n_tok, int max_n_kv, void* ws, TreeSelect* out);
 cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __half* q, const int8_t* kq,
-                               const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream);
+                               const __half* ksc, int32_t* ids, int4* plan, Params p, int* status, cudaStream_t stream);
 cudaError_t launch_tree_topk(const TreeBatch& b, const TreeSelect& w, const __half* q, const int8_t* kq,
                              const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream);
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                               const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
-                              float* part, float sm_scale, int* status, cudaStream_t stream);
+                              void* ws, float sm_scale, int* status, cudaStream_t stream);
+int4* tree_dense_plan(const TreeBatch& b, bool with_selected, void* ws);  // where its list of blocks goes, or null
 size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected);
 
 // Output gate: the elementwise logistic function of the gate input, in fp32, 1 / (1 + e^-x).  The

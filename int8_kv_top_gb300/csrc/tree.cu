@@ -46,7 +46,7 @@
 namespace qsa {
 namespace {
 
-constexpr int kRows = 128;                  // (token, head) rows of a CTA, 256 of a block (UMMA M)
+constexpr int kRows = kTreeBlock / 2;       // (token, head) rows of a CTA, 256 of a block (UMMA M)
 constexpr int kParts = 2;                   // ring stages per tile and operand
 constexpr int kMaxTok = (2 * kRows + kHPG - 2) / kHPG + 1;  // tokens a block's rows may touch
 constexpr int kThreads = 17 * 32;
@@ -75,6 +75,7 @@ struct DenseTreeArgs {
   float scale_log2;
   const __half* gate;
   __half* out;
+  const int4* plan;      // the blocks, longest first (tree_plan_blocks), or null: in the table's order
   float* part;           // unmerged O, [CTA of the grid][kD / 4][kRows][4]; null for one pair per cluster
   int* status;
 };
@@ -92,6 +93,11 @@ struct __align__(8) TreeBars {
 // a block finds its sequence by a search over the table, without a prefix sum; some indices stay unused.
 __device__ __forceinline__ long long first_block(long long first_row, int s) { return first_row * kHPG / (2 * kRows) + s; }
 
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeBatch b, int4* __restrict__ plan) {
+  pdl_begin();
+  tree_plan_blocks(b, false, plan, tree_blocks_most(b.n_seq, b.n_tok));
+}
+
 __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_constant__ DenseTreeArgs a, int S) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -105,9 +111,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   __shared__ float s_xm[2][kRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_ctarank(), g = blockIdx.y;
+  const int rank = (int)cluster_ctarank();
   const int half = rank & 1, pair = rank >> 1;  // rows 128 half .. of the block; run `pair` of its tiles
-  const int blk = blockIdx.x / (2 * S);
+  const int blk = blockIdx.x / (2 * S) / kGroups, g = blockIdx.x / (2 * S) % kGroups;
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kTileStages; ++i) {
@@ -135,11 +141,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     }
   }
   if (warp == 0) {
-    const int sq = warp_find_seq(a.b.n_seq, blk, [&](int s) { return first_block(__ldg(&a.b.seqs[s].w), s); });
+    int sq;
+    long long k;
+    bool listed = true;
+    if (a.plan != nullptr) {
+      const int4 head = __ldg(&a.plan[0]), at = __ldg(&a.plan[1 + blk]);
+      listed = blk < head.x;
+      sq = listed ? at.x : 0;
+      k = at.y;
+    } else {
+      sq = warp_find_seq(a.b.n_seq, blk, [&](int s) { return first_block(__ldg(&a.b.seqs[s].w), s); });
+      k = blk - first_block(__ldg(&a.b.seqs[sq].w), sq);
+    }
     int4 e;
     const int T = tree_seq_tokens(a.b, sq, &e);
-    const long long k = blk - first_block(e.w, sq);
-    const bool here = T > 0 && k >= 0 && k * 2 * kRows < (long long)T * kHPG;
+    const bool here = listed && T > 0 && k >= 0 && k * 2 * kRows < (long long)T * kHPG;
     const int row0 = here ? (int)k * 2 * kRows : 0;
     const int tok = row0 / kHPG + lane;  // lane = token of the block
     const bool live = here && lane < kMaxTok && tok < T && tok * kHPG < row0 + 2 * kRows;
@@ -433,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     // complete, so both CTAs' MMAs are done with them)
     if (J > 0 && any_row) {
       tc_fence_after();
-      float4* grow = reinterpret_cast<float4*>(a.part) + (size_t)(blockIdx.y * gridDim.x + blockIdx.x) * (kRows * kD / 4) + r;
+      float4* grow = reinterpret_cast<float4*>(a.part) + (size_t)blockIdx.x * (kRows * kD / 4) + r;
 #pragma unroll 1
       for (int c0 = wg * 128; c0 < wg * 128 + 128; c0 += 32) {
         uint32_t o[32];
@@ -493,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
         // CTA 0 of the cluster with this half's rows, the next pair's two CTAs further: all parts are loaded
         // before any is added (a part of a run that has none is read and dropped)
         const float4* src = reinterpret_cast<const float4*>(a.part) +
-                            (size_t)(blockIdx.y * gridDim.x + blockIdx.x - 2 * pair) * (kRows * kD / 4) +
+                            (size_t)(blockIdx.x - 2 * pair) * (kRows * kD / 4) +
                             (size_t)(2 * d8) * kRows + r;
         for (int c0 = 0; c0 < S; c0 += 4) {
           float4 p[4][2];
@@ -538,9 +554,8 @@ constexpr int kSizes[7] = {1, 2, 3, 4, 5, 6, 8};
 constexpr int kHeld[7] = {76, 36, 24, 15, 14, 8, 7};
 
 DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
-  constexpr int kBlock = 2 * kRows;
-  DensePlan d{(int)((long long)n_tok * kHPG / kBlock) + n_seq, 1};
-  const long long likely = ((long long)n_tok * kHPG + kBlock / 2 * (n_seq - 1LL) + kBlock - 1) / kBlock;
+  DensePlan d{tree_blocks_most(n_seq, n_tok), 1};
+  const long long likely = ((long long)n_tok * kHPG + kTreeBlock / 2 * (n_seq - 1LL) + kTreeBlock - 1) / kTreeBlock;
   const long long longest = with_selected ? max_n_kv : std::min<long long>(max_n_kv, (long long)identity_max + 32 * kTreeWords);
   const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
   double best_t = 0.0;
@@ -559,7 +574,7 @@ DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool 
 
 cudaLaunchConfig_t tree_config(int S, int blocks, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks * 2 * S, kGroups);
+  cfg.gridDim = dim3(blocks * kGroups * 2 * S);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
@@ -591,18 +606,36 @@ cudaError_t tree_setup() {
 
 }  // namespace
 
+namespace {
+size_t part_bytes(const DensePlan& d) {
+  return d.pairs == 1 ? 0 : (size_t)d.blocks * kGroups * 2 * d.pairs * kRows * kD * sizeof(float);
+}
+}  // namespace
+
 size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
   const DensePlan d = dense_plan(n_seq, n_tok, max_n_kv, identity_max, with_selected);
-  return d.pairs == 1 ? 0 : (size_t)d.blocks * kGroups * 2 * d.pairs * kRows * kD * sizeof(float);
+  return part_bytes(d) + (n_seq >= kPlanSeqs ? ((1 + (size_t)d.blocks) * sizeof(int4) + 255) / 256 * 256 : 0);
+}
+
+int4* tree_dense_plan(const TreeBatch& b, bool with_selected, void* ws) {
+  if (b.n_seq < kPlanSeqs) return nullptr;
+  return reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) +
+                                 part_bytes(dense_plan(b.n_seq, b.n_tok, b.max_n_kv, b.identity_max, with_selected)));
 }
 
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                               const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
-                              float* part, float sm_scale, int* status, cudaStream_t stream) {
+                              void* ws, float sm_scale, int* status, cudaStream_t stream) {
   cudaError_t e = tree_setup();
   if (e != cudaSuccess) return e;
   const DensePlan d = dense_plan(b.n_seq, b.n_tok, b.max_n_kv, b.identity_max, bits != nullptr);
-  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, part, status};
+  int4* plan = tree_dense_plan(b, bits != nullptr, ws);
+  if (plan && !bits) {  // with selected tokens the selection's first launch has made it
+    e = launch_pdl(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, b, plan);
+    if (e != cudaSuccess) return e;
+  }
+  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, plan,
+                        static_cast<float*>(ws), status};
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = tree_config(d.pairs, d.blocks, stream, attr);
   return cudaLaunchKernelEx(&cfg, tree_dense_kernel, a, d.pairs);

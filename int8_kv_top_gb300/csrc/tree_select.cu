@@ -24,9 +24,11 @@ namespace {
 constexpr int kTokChunk = 32;  // tokens per score CTA: UMMA N is at most twice that
 
 // ---------------------------------------------------------------- 1. prep
-// Blocks [0, 2 n_tok): (token row, group), thread = dim.  Blocks behind them: (sequence, chunk of cells).
+// Blocks [0, 2 n_tok): (token row, group), thread = dim.  Blocks behind them: (sequence, chunk of cells); then, where
+// a plan is wanted, one that lists the attention's blocks.
 __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeBatch b, const TreeSelect w,
-                                                        const __half* __restrict__ q, const __half* __restrict__ ksc) {
+                                                        const __half* __restrict__ q, const __half* __restrict__ ksc,
+                                                        int4* __restrict__ plan) {
   __shared__ long long s_e[8], s_h[8];
   __shared__ uint32_t s_union[kTreeWords];
   __shared__ float s_max[8][kGroups * kNB];
@@ -67,6 +69,11 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeBatch b, const
     return;
   }
   x -= kGroups * b.n_tok;
+  if (x == b.n_seq * w.chunks) {
+    static_assert(kPlanThreads == 256, "this kernel's block");
+    tree_plan_blocks(b, true, plan, tree_blocks_most(b.n_seq, b.n_tok));
+    return;
+  }
   const int s = x / w.chunks, ch = x % w.chunks;
   int4 e4;
   const int T = tree_seq_tokens(b, s, &e4);
@@ -318,9 +325,9 @@ size_t tree_select_layout(int n_seq, int n_tok, int max_n_kv, void* ws, TreeSele
 }
 
 cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __half* q, const int8_t* kq,
-                               const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(tree_prep_kernel, dim3(kGroups * b.n_tok + b.n_seq * w.chunks), dim3(256), 0, stream, b, w,
-                             q, ksc);
+                               const __half* ksc, int32_t* ids, int4* plan, Params p, int* status, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(tree_prep_kernel, dim3(kGroups * b.n_tok + b.n_seq * w.chunks + (plan ? 1 : 0)), dim3(256), 0,
+                             stream, b, w, q, ksc, plan);
   if (e != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(tree_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem)) !=
       cudaSuccess)

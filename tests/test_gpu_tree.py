@@ -182,6 +182,25 @@ def test_a_bad_sequence_is_skipped_and_flagged(how):
     np.testing.assert_array_equal(ids.cpu().numpy()[use], ref_ids[use])
 
 
+@pytest.mark.parametrize("pos0", [100, 2100])
+def test_tables_whose_rows_go_back_are_flagged(pos0):
+    # first token rows 0, 40, 0, 40, ...: every other entry goes back; the listed blocks would be many times the rows'
+    pool, _ = make_batch([(pos0, 40)], seed=26)
+    seqs = np.array([[0, pos0 + 40, pos0, 40 * (i & 1)] for i in range(300)], np.int32)
+    run_tree(pool, seqs, max_n_kv=pos0 + 40)
+    with pytest.raises(qsa.QSAError) as e:
+        qsa.qsa_check_device_status()
+    assert e.value.code == qsa.QSA_ERR_DEVICE
+    check(*make_batch([(pos0, 40)], seed=27))  # the device goes on
+
+
+@pytest.mark.parametrize("n_seq", [7, 8, 40])
+def test_trees_of_equal_and_of_no_length(n_seq):
+    # sequences without drafted tokens among the others, on both sides of where the blocks are listed first
+    pool, seqs = make_batch([(300 if i % 3 else 0, 0 if i % 4 == 1 else 25) for i in range(n_seq)], seed=28)
+    check(pool, seqs)
+
+
 def test_a_chain_equals_the_batched_prefill():
     # a chain of drafted tokens is what a prefill of the same tokens computes
     pool, seqs = make_batch([(1990, list(range(-1, 24))), (300, list(range(-1, 39)))], seed=19)
