@@ -178,14 +178,15 @@ struct TileRun {
 //   kPairV       stage p: cells 64 p .. of the tile x this CTA's 128 dims (two a tile), code * scale
 // Four lanes take the 64 codes of a (cell, scale block), a warp eight cells a load, so row r of a stage lies at
 // 128 r with its 16-byte chunks xored by r mod 8, which is the lane's cell: every store address is a constant
-// past the stage's.  Two stages are in flight in registers while a third is converted.  The loads are not
+// past the stage's.  Two stages are in flight in registers while a third is converted (kTeams
+// teams of four warps take the stages in turn).  The loads are not
 // predicated (cells past the sequence read its last one): a predicated load is merged with its default as
 // it arrives, and the thread waits there for its latency.
 enum TileMode { kScoreCodes, kPairK, kPairV };
-template <TileMode kMode>
+template <TileMode kMode, int kTeams = 1>
 __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __restrict__ codes,
                                               const __half* __restrict__ scales, uint32_t ring, uint64_t* full,
-                                              uint64_t* empty, int w4, int lane) {
+                                              uint64_t* empty, int w4, int lane, int team = 0) {
   constexpr bool kPair = kMode != kScoreCodes;
   constexpr int kParts = kPair ? 2 : 4;   // stages a tile
   constexpr int kStep = kPair ? 8 : 32;   // cells between a thread's four loads of a stage
@@ -257,14 +258,14 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
   if (n_st == 0) return;
   uint4 wa[4], wb[4];
   uint16_t sa[4] = {}, sb[4] = {};
-  load(0, wa, sa);
-  load(1, wb, sb);
+  load(team, wa, sa);
+  load(team + kTeams, wb, sb);
   if (kPair) cluster_wait_all();  // the other CTA's barriers are initialised before the first remote arrive
-  for (int s = 0; s < n_st; s += 2) {  // n_st is even
+  for (int s = team; s < n_st; s += 2 * kTeams) {  // n_st is a multiple of 2 kTeams
     if (!store(s, wa, sa)) break;
-    if (s + 2 < n_st) load(s + 2, wa, sa);
-    if (!store(s + 1, wb, sb)) break;
-    if (s + 3 < n_st) load(s + 3, wb, sb);
+    if (s + 2 * kTeams < n_st) load(s + 2 * kTeams, wa, sa);
+    if (!store(s + kTeams, wb, sb)) break;
+    if (s + 3 * kTeams < n_st) load(s + 3 * kTeams, wb, sb);
   }
 }
 

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeBatch b, const
 }
 
 // ---------------------------------------------------------------- 2. score
-constexpr int kScoreThreads = 13 * 32;  // warps 0-3 producers, 4-11 epilogue (16 tokens each half), 12 MMA
+constexpr int kScoreThreads = 17 * 32;  // warps 0-7 producers (two teams), 8-15 epilogue (16 tokens each half), 16 MMA
 constexpr int kOffB = kTileStages * kTileStageBytes;  // 4 dim blocks of [hi rows, lo rows][64] SW128
 constexpr int kBBlock = 2 * kTokChunk * 128;
 constexpr int kScoreSmem = kOffB + kNB * kBBlock + 1024;
@@ -172,10 +172,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   __syncthreads();
   const int n16 = (n_here + 15) / 16 * 16, N = 2 * n16;  // row n: hi of token n; row n16 + n: lo
 
-  if (warp < 4) {
+  if (warp < 8) {
     const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0, 0u};
-    produce_tiles<kScoreCodes>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp, lane);
-  } else if (warp == 12) {
+    produce_tiles<kScoreCodes, 2>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp & 3, lane, warp >> 2);
+  } else if (warp == 16) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
     tc_fence_before();
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     __syncwarp();
   } else {
-    const int et = tid - 128, quarter = warp & 3, n0 = 16 * ((warp - 4) >> 2);  // this warp's cells and tokens
+    const int et = tid - 256, quarter = warp & 3, n0 = 16 * ((warp - 8) >> 2);  // this warp's cells and tokens
     {
       // 16-byte chunk c of token r's hi | lo row: four rows' loads before any store.  Rows of tokens that do not
       // select were not written by tree_prep: what they hold only reaches their own scores, which are not stored.
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.b_full);
-    if (warp == 4) {  // lane = token: its mask and what its scores are multiplied by
+    if (warp == 8) {  // lane = token: its mask and what its scores are multiplied by
       float km[kNB];
       warp_kmax(w, sq, g, n_scan, lane, km);
       int seen = pos0;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
+  if (warp == 16) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
 }
 
 }  // namespace
