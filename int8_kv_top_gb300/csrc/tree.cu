@@ -93,6 +93,20 @@ struct __align__(8) TreeBars {
 // a block finds its sequence by a search over the table, without a prefix sum; some indices stay unused.
 __device__ __forceinline__ long long first_block(long long first_row, int s) { return first_row * kHPG / (2 * kRows) + s; }
 
+// Eight dims of an output row: the gate's sigmoid, and the rounding to fp16.
+__device__ __forceinline__ void apply_gate(float (&v)[8], uint4 gw) {
+  const uint32_t w[4] = {gw.x, gw.y, gw.z, gw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] *= gate_sigmoid(f.x);
+    v[2 * i + 1] *= gate_sigmoid(f.y);
+  }
+}
+__device__ __forceinline__ uint4 pack_out(const float (&v)[8]) {
+  return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+}
+
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeBatch b, int4* __restrict__ plan) {
   pdl_begin();
   tree_plan_blocks(b, false, plan, tree_blocks_most(b.n_seq, b.n_tok));
@@ -141,22 +155,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     }
   }
   if (warp == 0) {
-    int sq;
-    long long k;
-    bool listed = true;
-    if (a.plan != nullptr) {
-      const int4 head = __ldg(&a.plan[0]), at = __ldg(&a.plan[1 + blk]);
-      listed = blk < head.x;
-      sq = listed ? at.x : 0;
-      k = at.y;
-    } else {
-      sq = warp_find_seq(a.b.n_seq, blk, [&](int s) { return first_block(__ldg(&a.b.seqs[s].w), s); });
-      k = blk - first_block(__ldg(&a.b.seqs[sq].w), sq);
-    }
     int4 e;
-    const int T = tree_seq_tokens(a.b, sq, &e);
-    const bool here = listed && T > 0 && k >= 0 && k * 2 * kRows < (long long)T * kHPG;
-    const int row0 = here ? (int)k * 2 * kRows : 0;
+    int T, row0;
+    bool here;
+    if (a.plan != nullptr) {
+      const int4 head = __ldg(&a.plan[0]), at = __ldg(&a.plan[1 + 2 * blk]);
+      row0 = __ldg(&a.plan[2 + 2 * blk].x);
+      here = blk < head.x;
+      e = make_int4(at.x, 0, at.y, at.w);
+      T = at.z;
+    } else {
+      const int sq = warp_find_seq(a.b.n_seq, blk, [&](int s) { return first_block(__ldg(&a.b.seqs[s].w), s); });
+      T = tree_seq_tokens(a.b, sq, &e);
+      const long long k = blk - first_block(e.w, sq);
+      here = T > 0 && k >= 0 && k * kTreeBlock < (long long)T * kHPG;
+      row0 = here ? (int)k * kTreeBlock : 0;
+    }
     const int tok = row0 / kHPG + lane;  // lane = token of the block
     const bool live = here && lane < kMaxTok && tok < T && tok * kHPG < row0 + 2 * kRows;
     int n_kv = e.z;
@@ -482,62 +496,80 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   if (warp < 16) {
     const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
     const int per = (kRows + S - 1) / S;  // rows of an owner
-    // one pair: a warp a row, 8 dims a lane, from shared memory; else lanes are rows (16 at least), 8 dims each
-    for (int x = tid; x < per * 32; x += 512) {
-      const int r = pair * per + (S == 1 ? x >> 5 : x % per), d8 = S == 1 ? x & 31 : x / per, R = row0 + r;
-      if (r >= kRows) continue;
-      const int ti = R / kHPG - blk_row0 / kHPG;
-      if (R >= T * kHPG || !((s_ours >> ti) & 1)) continue;
-      const size_t at = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD + d8 * 8;
-      uint4 gw = make_uint4(0u, 0u, 0u, 0u);
-      if (a.gate) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at));
-      float M = -INFINITY, L = 0.f;
-      for (int c = 0; c < S; ++c) M = fmaxf(M, ml[c * kRows + r].x);
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      auto add = [&](float2 v, float4 p0, float4 p1) {
-        if (v.x == -INFINITY) return;  // nothing of this row there
-        const float f = fast_exp2(v.x - M);
-        L = fmaf(v.y, f, L);
-        const float u[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+    auto row_at = [&](int r, size_t* at) {  // this CTA's row r: is it one of ours, and where its output starts
+      const int R = row0 + r, ti = R / kHPG - blk_row0 / kHPG;
+      if (r >= kRows || R >= T * kHPG || !((s_ours >> ti) & 1)) return false;
+      *at = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD;
+      return true;
+    };
+    if (S == 1) {  // a warp a row, 8 dims a lane, from shared memory; four rows' gates are loaded before any is used
+      const int d8 = tid & 31;
+#pragma unroll 1
+      for (int r0 = tid >> 5; r0 < kRows; r0 += 64) {
+        size_t at[4];
+        uint4 gw[4];
+        bool mine[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(u[i], f, acc[i]);
-      };
-      if (S == 1) {
-        const float4* src = reinterpret_cast<const float4*>(smem + (size_t)r * (kOStride * 4)) + 2 * d8;
-        add(ml[r], src[0], src[1]);
-      } else {
+        for (int u = 0; u < 4; ++u) {
+          mine[u] = row_at(r0 + 16 * u, &at[u]);
+          if (a.gate && mine[u]) gw[u] = __ldg(reinterpret_cast<const uint4*>(a.gate + at[u]) + d8);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (!mine[u]) continue;
+          const int r = r0 + 16 * u;
+          const float l = ml[r].x == -INFINITY ? 0.f : ml[r].y, inv = l > 0.f ? 1.f / l : 0.f;  // sees nothing: zeros
+          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (l > 0.f) {
+            const float4* src = reinterpret_cast<const float4*>(smem + (size_t)r * (kOStride * 4)) + 2 * d8;
+            const float4 x = src[0], y = src[1];
+            const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = f[i] * inv;
+          }
+          if (a.gate) apply_gate(v, gw[u]);
+          reinterpret_cast<uint4*>(a.out + at[u])[d8] = pack_out(v);
+        }
+      }
+    } else {  // lanes are rows (16 at least), 8 dims each
+      for (int x = tid; x < per * 32; x += 512) {
+        const int r = pair * per + x % per, d8 = x / per;
+        size_t at;
+        if (x % per + pair * per >= kRows || !row_at(r, &at)) continue;
+        uint4 gw = make_uint4(0u, 0u, 0u, 0u);
+        if (a.gate) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at) + d8);
+        float M = -INFINITY, L = 0.f;
+        for (int c = 0; c < S; ++c) M = fmaxf(M, ml[c * kRows + r].x);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         // CTA 0 of the cluster with this half's rows, the next pair's two CTAs further: all parts are loaded
         // before any is added (a part of a run that has none is read and dropped)
-        const float4* src = reinterpret_cast<const float4*>(a.part) +
-                            (size_t)(blockIdx.x - 2 * pair) * (kRows * kD / 4) +
+        const float4* src = reinterpret_cast<const float4*>(a.part) + (size_t)(blockIdx.x - 2 * pair) * (kRows * kD / 4) +
                             (size_t)(2 * d8) * kRows + r;
         for (int c0 = 0; c0 < S; c0 += 4) {
           float4 p[4][2];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const float4* at4 = src + (size_t)min(c0 + u, S - 1) * (2 * kRows * kD / 4);
-            p[u][0] = __ldcg(at4);
-            p[u][1] = __ldcg(at4 + kRows);
+            const float4* from = src + (size_t)min(c0 + u, S - 1) * (2 * kRows * kD / 4);
+            p[u][0] = __ldcg(from);
+            p[u][1] = __ldcg(from + kRows);
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (c0 + u < S) add(ml[(c0 + u) * kRows + r], p[u][0], p[u][1]);
-        }
-      }
-      const float inv = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
+          for (int u = 0; u < 4; ++u) {
+            const float2 st = ml[min(c0 + u, S - 1) * kRows + r];
+            if (c0 + u >= S || st.x == -INFINITY) continue;  // past the last run, or nothing of this row there
+            const float f = fast_exp2(st.x - M);
+            L = fmaf(st.y, f, L);
+            const float y[8] = {p[u][0].x, p[u][0].y, p[u][0].z, p[u][0].w, p[u][1].x, p[u][1].y, p[u][1].z, p[u][1].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] *= inv;
-      if (a.gate) {
-        const uint32_t w[4] = {gw.x, gw.y, gw.z, gw.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-          acc[2 * i] *= gate_sigmoid(v.x);
-          acc[2 * i + 1] *= gate_sigmoid(v.y);
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(y[i], f, v[i]);
+          }
         }
+        const float inv = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= inv;
+        if (a.gate) apply_gate(v, gw);
+        reinterpret_cast<uint4*>(a.out + at)[d8] = pack_out(v);
       }
-      *reinterpret_cast<uint4*>(a.out + at) = make_uint4(pack_half2(acc[0], acc[1]), pack_half2(acc[2], acc[3]),
-                                                         pack_half2(acc[4], acc[5]), pack_half2(acc[6], acc[7]));
     }
   }
 }
@@ -614,7 +646,7 @@ size_t part_bytes(const DensePlan& d) {
 
 size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
   const DensePlan d = dense_plan(n_seq, n_tok, max_n_kv, identity_max, with_selected);
-  return part_bytes(d) + (n_seq >= kPlanSeqs ? ((1 + (size_t)d.blocks) * sizeof(int4) + 255) / 256 * 256 : 0);
+  return part_bytes(d) + (n_seq >= kPlanSeqs ? ((1 + 2 * (size_t)d.blocks) * sizeof(int4) + 255) / 256 * 256 : 0);
 }
 
 int4* tree_dense_plan(const TreeBatch& b, bool with_selected, void* ws) {
