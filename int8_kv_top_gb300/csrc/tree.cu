@@ -61,7 +61,7 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 static_assert(kMaxTok <= 32, "a lane per token of the block");
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-constexpr uint16_t kPair = 0x3;
+constexpr uint16_t kBoth = 0x3;
 
 struct DenseTreeArgs {
   TreeBatch b;
@@ -216,11 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
 
   if (warp < 8) {
     TileRun t{cell0, pos0, T, j_begin, J, g, s_union, &s_abort, a.status, half, 0u};
-    t.remote_full = pair_addr(warp < 4 ? bars.k_full : bars.v_full);
-    if (warp < 4)
-      produce_tiles<kPairK>(t, a.kq, a.ksc, smem_u32(smem + kOffK), bars.k_full, bars.k_empty, warp, lane);
-    else
-      produce_tiles<kPairV>(t, a.vq, a.vsc, smem_u32(smem + kOffV), bars.v_full, bars.v_empty, warp - 4, lane);
+    const bool is_v = warp >= 4;
+    uint64_t* full = is_v ? bars.v_full : bars.k_full;
+    t.remote_full = pair_addr(full);
+    produce_tiles<kPair>(t, is_v ? a.vq : a.kq, is_v ? a.vsc : a.ksc, smem_u32(smem + (is_v ? kOffV : kOffK)), full,
+                         is_v ? bars.v_empty : bars.k_empty, warp & 3, lane, 0, is_v);
     if (J == 0) cluster_wait_all();  // #0, which the producers otherwise wait for before their first arrive
   } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issue
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
                      qdesc + (uint64_t)(((2 * d + (kk >> 2)) * (kRows * 128) + (kk & 3) * 32) >> 4),
                      kdesc + (uint64_t)(((kk >> 2) * (kTileStageBytes / 2) + (kk & 3) * 32) >> 4), idesc_qk,
                      (d > 0 || kk > 0) ? 1u : 0u);
-          umma2_commit(&bars.k_empty[slot], kPair << (rank & ~1));
+          umma2_commit(&bars.k_empty[slot], kBoth << (rank & ~1));
         }
-        umma2_commit(&bars.s_full[b], kPair << (rank & ~1));
+        umma2_commit(&bars.s_full[b], kBoth << (rank & ~1));
         return true;
       };
       auto issue_pv = [&](int j) -> bool {
@@ -270,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
           for (int kk = 0; kk < 4; ++kk)
             umma2_ts(tmem + kColO, tmem + kColS + b * kTileCells + (4 * c + kk) * 8, vdesc + (uint64_t)((kk * 2048) >> 4),
                      idesc_pv, (j > 0 || c > 0 || kk > 0) ? 1u : 0u);
-          umma2_commit(&bars.v_empty[slot], kPair << (rank & ~1));
+          umma2_commit(&bars.v_empty[slot], kBoth << (rank & ~1));
         }
-        umma2_commit(&bars.pv_done[b], kPair << (rank & ~1));
+        umma2_commit(&bars.pv_done[b], kBoth << (rank & ~1));
         return true;
       };
       bool go = mbar_wait_poll(&bars.q_full, 0, a.status, &s_abort) && issue_qk(0);

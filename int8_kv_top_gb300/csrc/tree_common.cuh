@@ -179,25 +179,26 @@ struct TileRun {
 
 // Four producer warps that turn the tiles' int8 codes into fp16 operand stages of 16 KB, 128B-swizzled:
 //   kScoreCodes  stage p: 128 cells x dims 64 p .. (four a tile); the codes themselves, exact integers
-//   kPairK       stage p: this CTA's 64 cells x dims 128 p .. (two a tile), code * scale
-//   kPairV       stage p: cells 64 p .. of the tile x this CTA's 128 dims (two a tile), code * scale
+//   kPair        K stage p: this CTA's 64 cells x dims 128 p .. (two a tile), code * scale;
+//                V stage p (is_v): cells 64 p .. of the tile x this CTA's 128 dims (two a tile).  One body serves
+//                both: the kernel's roles share the SM's instruction cache (see tree.cu)
 // Four lanes take the 64 codes of a (cell, scale block), a warp eight cells a load, so row r of a stage lies at
 // 128 r with its 16-byte chunks xored by r mod 8, which is the lane's cell: every store address is a constant
 // past the stage's.  Two stages are in flight in registers while a third is converted (kTeams
 // teams of four warps take the stages in turn).  The loads are not
 // predicated (cells past the sequence read its last one): a predicated load is merged with its default as
 // it arrives, and the thread waits there for its latency.
-enum TileMode { kScoreCodes, kPairK, kPairV };
+enum TileMode { kScoreCodes, kPair };
 template <TileMode kMode, int kTeams = 1>
 __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __restrict__ codes,
                                               const __half* __restrict__ scales, uint32_t ring, uint64_t* full,
-                                              uint64_t* empty, int w4, int lane, int team = 0) {
-  constexpr bool kPair = kMode != kScoreCodes;
-  constexpr int kParts = kPair ? 2 : 4;   // stages a tile
-  constexpr int kStep = kPair ? 8 : 32;   // cells between a thread's four loads of a stage
+                                              uint64_t* empty, int w4, int lane, int team = 0, bool is_v = false) {
+  constexpr bool kScaled = kMode == kPair;
+  constexpr int kParts = kScaled ? 2 : 4;   // stages a tile
+  constexpr int kStep = kScaled ? 8 : 32;   // cells between a thread's four loads of a stage
   const int sub = lane >> 2, piece = lane & 3;
-  const int db = kPair ? w4 & 1 : 0;      // dim block within the stage
-  const int r0 = sub + (kPair ? (w4 >> 1) * 32 : w4 * 8);
+  const int db = kScaled ? w4 & 1 : 0;      // dim block within the stage
+  const int r0 = sub + (kScaled ? (w4 >> 1) * 32 : w4 * 8);
   const int n_scan = t.pos0 + t.T, n_st = t.J * kParts;
   const size_t row0 = (size_t)t.cell0 * kGroups + t.g;
   const int8_t* my_codes = codes + row0 * kD + piece * 16;
@@ -205,34 +206,25 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
   const uint32_t dst0 = ring + db * (kTileStageBytes / 2) + r0 * 128 + (((2 * piece) ^ sub) << 4);
   const uint32_t dst1 = ring + db * (kTileStageBytes / 2) + r0 * 128 + (((2 * piece + 1) ^ sub) << 4);
   auto first_cell = [&](int tile, int part) {  // the thread's first cell of a stage
-    return tile * kTileCells + r0 + (kMode == kPairK ? t.half * 64 : kMode == kPairV ? part * 64 : 0);
+    return tile * kTileCells + r0 + (kScaled ? (is_v ? part : t.half) * 64 : 0);
   };
   auto load = [&](int s, uint4 (&w)[4], uint16_t (&sc)[4]) {
     const int tile = t.j_begin + s / kParts, part = s % kParts, c0 = first_cell(tile, part);
-    const int blk = kMode == kScoreCodes ? part : kMode == kPairK ? 2 * part + db : 2 * t.half + db;
-    const int8_t* cp = my_codes + blk * kBlk;
-    const uint16_t* sp = my_scales + blk;
-    if ((tile + 1) * kTileCells <= n_scan) {
-      cp += (size_t)c0 * (kGroups * kD);
-      sp += (size_t)c0 * (kGroups * kNB);
+    const int blk = !kScaled ? part : 2 * (is_v ? t.half : part) + db;
+    const int past = n_scan - 1 - c0;  // the sequence's last cell, from the thread's first
+    const int8_t* cp = my_codes + blk * kBlk + (int64_t)c0 * (kGroups * kD);
+    const uint16_t* sp = my_scales + blk + (int64_t)c0 * (kGroups * kNB);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = __ldg(reinterpret_cast<const uint4*>(cp + i * kStep * (kGroups * kD)));
-        if (kPair) sc[i] = __ldg(sp + i * kStep * (kGroups * kNB));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const size_t cell = min(c0 + i * kStep, n_scan - 1);
-        w[i] = __ldg(reinterpret_cast<const uint4*>(cp + cell * (kGroups * kD)));
-        if (kPair) sc[i] = __ldg(sp + cell * (kGroups * kNB));
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int c = min(i * kStep, past);
+      w[i] = __ldg(reinterpret_cast<const uint4*>(cp + c * (kGroups * kD)));
+      if (kScaled) sc[i] = __ldg(sp + c * (kGroups * kNB));
     }
   };
   auto store = [&](int s, const uint4 (&w)[4], uint16_t (&sc)[4]) -> bool {
     const int slot = s % kTileStages, tile = t.j_begin + s / kParts;
     if (s >= kTileStages && !mbar_wait_warp(&empty[slot], ((s / kTileStages) & 1) ^ 1, t.status, t.abort)) return false;
-    if (kPair && (tile + 1) * kTileCells > t.pos0) {  // cells past the sequence, and drafted ones unseen here: zeros
+    if (kScaled && (tile + 1) * kTileCells > t.pos0) {  // cells past the sequence, and drafted ones unseen here: zeros
       const int c0 = first_cell(tile, s % kParts);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -243,7 +235,7 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t lo[4], hi[4];
-      const __half2 s2 = __half2half2(__ushort_as_half(kPair ? sc[i] : (uint16_t)0x3C00));
+      const __half2 s2 = __half2half2(__ushort_as_half(kScaled ? sc[i] : (uint16_t)0x3C00));
       dequant8(w[i].x, w[i].y, s2, lo);
       dequant8(w[i].z, w[i].w, s2, hi);
       const uint32_t at = slot * kTileStageBytes + i * kStep * 128;
@@ -255,7 +247,7 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
     fence_proxy_async_smem();  // this thread's part is visible to the tensor core before the arrive
     __syncwarp();
     if (lane == 0) {
-      if (kPair && t.half) mbar_arrive_cluster(t.remote_full + 8u * (uint32_t)slot);
+      if (kScaled && t.half) mbar_arrive_cluster(t.remote_full + 8u * (uint32_t)slot);
       else mbar_arrive(&full[slot]);
     }
     return true;
@@ -265,7 +257,7 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
   uint16_t sa[4] = {}, sb[4] = {};
   load(team, wa, sa);
   load(team + kTeams, wb, sb);
-  if (kPair) cluster_wait_all();  // the other CTA's barriers are initialised before the first remote arrive
+  if (kScaled) cluster_wait_all();  // the other CTA's barriers are initialised before the first remote arrive
   for (int s = team; s < n_st; s += 2 * kTeams) {  // n_st is a multiple of 2 kTeams
     if (!store(s, wa, sa)) break;
     if (s + 2 * kTeams < n_st) load(s + 2 * kTeams, wa, sa);
