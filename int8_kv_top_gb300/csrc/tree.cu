@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     }
     uint32_t tmem = 0u;
     if (J > 0) {
-      ok = mbar_wait_warp(&bars.tmem_ready, 0, a.status, &s_abort);
+      ok = tile_wait_warp(&bars.tmem_ready, 0, a.status, &s_abort);
       tc_fence_after();
       tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
     }
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     // a CTA without a row of ours only keeps the pair's barriers going: its rows of S, P and O are not read
     const bool any_row = named_bar_any(1, 256, active);
     for (int j = 0; !any_row && j < J; ++j) {
-      if (!mbar_wait_warp(&bars.s_full[j % kNS], (j / kNS) & 1, a.status, &s_abort)) break;
+      if (!tile_wait_warp(&bars.s_full[j % kNS], (j / kNS) & 1, a.status, &s_abort)) break;
       if (lane == 0) {
         if (half) mbar_arrive_cluster(p_full0 + 8u * (uint32_t)(j % kNS));
         else mbar_arrive(&bars.p_full[j % kNS]);
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     }
     for (int j = 0; any_row && j < J; ++j) {
       const int b = j % kNS;
-      const bool w_ok = mbar_wait_warp(&bars.s_full[b], (j / kNS) & 1, a.status, &s_abort);
+      const bool w_ok = tile_wait_warp(&bars.s_full[b], (j / kNS) & 1, a.status, &s_abort);
       tc_fence_after();
       float s[64];
       {
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
         } else {
           const bool need = m_new > m_run + kRescaleThreshold;  // the same in both warpgroups
           if (__any_sync(0xffffffffu, need)) {
-            if (mbar_wait_warp(&bars.pv_done[(j - 1) % kNS], ((j - 1) / kNS) & 1, a.status, &s_abort)) {
+            if (tile_wait_warp(&bars.pv_done[(j - 1) % kNS], ((j - 1) / kNS) & 1, a.status, &s_abort)) {
               tc_fence_after();
               const float f = need ? fast_exp2(m_run - m_new) : 1.f;
 #pragma unroll 1
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
         else mbar_arrive(&bars.p_full[b]);
       }
     }
-    if (J > 0 && ok) ok = mbar_wait_warp(&bars.pv_done[(J - 1) % kNS], ((J - 1) / kNS) & 1, a.status, &s_abort);
+    if (J > 0 && ok) ok = tile_wait_warp(&bars.pv_done[(J - 1) % kNS], ((J - 1) / kNS) & 1, a.status, &s_abort);
     // (m, l) of the row to the CTAs that hold the same rows; a failed or empty run contributes nothing
     const bool all_ok = !named_bar_any(1, 256, !ok);
     s_xm[wg][r] = l_run;

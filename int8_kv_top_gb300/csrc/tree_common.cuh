@@ -162,6 +162,26 @@ __device__ __forceinline__ void tree_plan_blocks(const TreeBatch& b, bool with_s
   }
 }
 
+// ---------------------------------------------------------------- waits
+// Bounded waits in few instructions: the roles of a kernel run different loops at the same time, and their
+// code has to fit the SM's instruction cache together.  A failed probe suspends the thread for up to
+// kSuspendHintNs, so kWaitProbes of them take at most about two seconds.
+constexpr int kWaitProbes = 1000000;
+template <bool kCluster = false>
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+#pragma unroll 1
+  for (int it = 0; it < kWaitProbes; ++it) {
+    if (mbar_try_wait<kCluster>(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  set_dev_status(status, QSA_DEV_WAIT_TIMEOUT);
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool tile_wait_warp(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  return __all_sync(0xffffffffu, tile_wait(bar, parity, status, abort));
+}
+
 // ---------------------------------------------------------------- tile producers
 constexpr int kTileStages = 4;   // ring depth
 constexpr int kTileStageBytes = 16 * 1024;
@@ -223,7 +243,7 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
   };
   auto store = [&](int s, const uint4 (&w)[4], uint16_t (&sc)[4]) -> bool {
     const int slot = s % kTileStages, tile = t.j_begin + s / kParts;
-    if (s >= kTileStages && !mbar_wait_warp(&empty[slot], ((s / kTileStages) & 1) ^ 1, t.status, t.abort)) return false;
+    if (s >= kTileStages && !tile_wait_warp(&empty[slot], ((s / kTileStages) & 1) ^ 1, t.status, t.abort)) return false;
     if (kScaled && (tile + 1) * kTileCells > t.pos0) {  // cells past the sequence, and drafted ones unseen here: zeros
       const int c0 = first_cell(tile, s % kParts);
 #pragma unroll

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                           ? sm_scale * tree_row_scale(w.eh + (size_t)(g * b.n_tok + t0 + lane) * 8, km, sm_scale)
                           : 0.f;
     }
-    const bool t_ok = mbar_wait_warp(&bars.tmem_ready, 0, status, &s_abort);
+    const bool t_ok = tile_wait_warp(&bars.tmem_ready, 0, status, &s_abort);
     tc_fence_after();
     named_bar_any(1, 256, false);  // masks and scales are in shared memory
     const uint32_t lane_base = *reinterpret_cast<volatile uint32_t*>(&s_tmem) + ((uint32_t)(quarter * 32) << 16) + n0;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (j + 1 < J) sw_next = scales_of(j + 1);
       const float2 s01 = __half22float2(*reinterpret_cast<const __half2*>(&sw.x));
       const float2 s23 = __half22float2(*reinterpret_cast<const __half2*>(&sw.y));
-      if (!mbar_wait_warp(&bars.acc_full[buf], (j >> 1) & 1, status, &s_abort)) break;
+      if (!tile_wait_warp(&bars.acc_full[buf], (j >> 1) & 1, status, &s_abort)) break;
       tc_fence_after();
       float acc[16];
       if (n0 < n16) {
