@@ -424,20 +424,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
         }
       }
       const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
-      float lsum = 0.f;
+      const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-m_use, -m_use);
+      float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float p0 = fast_exp2(fmaf(s[32 * hf + 2 * i], a.scale_log2, -m_use));
-          const float p1 = fast_exp2(fmaf(s[32 * hf + 2 * i + 1], a.scale_log2, -m_use));
-          lsum += p0 + p1;
-          p[i] = pack_half2(p0, p1);
+          float2 e = fma2(make_float2(s[32 * hf + 2 * i], s[32 * hf + 2 * i + 1]), sc2, nm2);
+          e.x = fast_exp2(e.x);
+          e.y = fast_exp2(e.y);
+          lsum = add2(lsum, e);
+          p[i] = pack_half2(e.x, e.y);
         }
         tmem_st16(lane_base + kColS + b * kTileCells + wg * 32 + 16 * hf, p);
       }
-      l_run += lsum;
+      l_run += lsum.x + lsum.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
