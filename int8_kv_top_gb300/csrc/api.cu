@@ -138,12 +138,15 @@ int decode_layer_limit(int* rc) {
 
 // Whether a tree call selects for its tokens together (tree_select.cu, then one tensor-core attention for all)
 // or gives each selected (token, group) a cluster of its own.  Together costs by the sequences and their cells,
-// the clusters cost by the tokens.  Measured (together / clusters, us a call of equal trees): one sequence of 8,192
-// cells with 4 tokens 53 / 37, 8 tokens 54 / 54, 32 tokens 55 / 89; of 30,000 cells with 8 tokens 114 / 102, 16
-// tokens 108 / 104, 32 tokens 117 / 197; 16 sequences of 8,192 cells with 3 tokens 183 / 160, 6 tokens 188 / 254;
-// of 30,000 cells with 4 tokens 539 / 386, 6 tokens 546 / 571, 16 tokens 567 / 1,412.
+// the clusters cost by the tokens, so the rule is on the tokens a sequence: eight where fewer than four sequences
+// leave the clusters room, five up to 15 sequences, four from 16 on, and more above 32,768 cells.  Measured
+// (together / clusters, us a call of equal trees): 1 sequence of 8,192 cells with 6 tokens 51 / 37, 8 tokens
+// 52 / 55, of 60,000 with 12 tokens 188 / 157; 3 of 12,000 with 6 tokens 69 / 61, 8 tokens 69 / 103; 8 of 12,000
+// with 4 tokens 134 / 103, 5 tokens 134 / 173; 16 of 24,000 with 3 tokens 325 / 272, 4 tokens 327 / 352; 16 of
+// 60,000 with 4 tokens 744 / 690, 5 tokens 772 / 844.
 bool tree_selects_together(int n_seq, int n_tok, int max_n_kv, const qsa::Params& p) {
-  const long long least = (max_n_kv <= 16384 ? 4 : 6) * (n_seq < 4 ? 2 : 1);  // tokens a sequence
+  long long least = n_seq < 4 ? 8 : n_seq < 16 ? 5 : 4;  // tokens a sequence
+  if (max_n_kv > 32768) least += n_seq == 1 ? 5 : 1;
   return max_n_kv > p.identity_max && max_n_kv <= qsa::select_max_cells() && n_tok >= least * n_seq;
 }
 

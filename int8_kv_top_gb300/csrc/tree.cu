@@ -578,25 +578,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
 
 // How a call is cut: blocks (grid indices; a ragged batch leaves about half a block a sequence unused) and pairs
 // per cluster.  A launch takes about waves x (a fixed part + the tiles of a pair), in units of one tile's time
-// (1.9 us; fixed: 9 us for one pair, 11 to 13 with a merge); a wave is as many clusters of that size as a GB300
-// holds at once (a cluster stays inside a GPC).  Lengths are on the device: waves is between the whole waves
-// that equal lengths take and what lengths spread over (0, max_n_kv) take, for which 0.6 of a wave is filled.
+// (1.7 us; fixed: 8 us for one pair, 10 to 12 with a merge); a wave is as many clusters of that size as a GB300
+// holds at once (a cluster stays inside a GPC).  How many tokens and cells a sequence has is on the device, so
+// blocks and waves are means of two cases: equal sequences (each one's blocks rounded up; whole waves) and spread
+// ones (half a block of rounding a sequence; lengths over (0, max_n_kv), for which w clusters a
+// place took 0.9 w waves).  Measured with 1, 2, 3, 4, 5, 6, 8 pairs a cluster (us a call):
+//   16 trees of 22 tokens after 8,192 cells   234 253 263 311 287 369 359
+//   16 trees of  6                            207 140 173 190 174 200 197
+//   24 trees of 1-32 after 200-16,000         353 248 264 296 304 378 362
+//    4 trees of 33-48 after 29,000-31,000     451 232 156 229 193 241 190
+//    1 tree  of 61 after 30,000               504 287 211 176 151 139 119
 struct DensePlan {
   int blocks, pairs;
 };
 constexpr int kSizes[7] = {1, 2, 3, 4, 5, 6, 8};
-constexpr int kHeld[7] = {76, 36, 24, 15, 14, 8, 7};
+constexpr int kHeld[7] = {76, 36, 23, 15, 13, 8, 7};
 
 DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
   DensePlan d{tree_blocks_most(n_seq, n_tok), 1};
-  const long long likely = ((long long)n_tok * kHPG + kTreeBlock / 2 * (n_seq - 1LL) + kTreeBlock - 1) / kTreeBlock;
+  const long long rows = (long long)n_tok * kHPG;
+  const long long even = n_seq * ((rows + (long long)n_seq * kTreeBlock - 1) / ((long long)n_seq * kTreeBlock));
+  const long long spread =
+      std::max<long long>(n_seq, (rows + kTreeBlock / 2 * (long long)n_seq + kTreeBlock - 1) / kTreeBlock);
+  const double clusters = (double)((n_seq > 1 ? (even + spread) / 2 : even) * kGroups);
   const long long longest = with_selected ? max_n_kv : std::min<long long>(max_n_kv, (long long)identity_max + 32 * kTreeWords);
   const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
   double best_t = 0.0;
   for (int i = 0; i < 7; ++i) {
     const int S = kSizes[i];
-    const double w = (double)(likely * kGroups) / kHeld[i];
-    const double waves = w <= 1.0 ? 1.0 : 0.5 * (std::ceil(w) + (n_seq > 1 ? 0.4 + 0.6 * w : std::ceil(w)));
+    const double w = clusters / kHeld[i];
+    const double waves = n_seq > 1 ? 0.5 * (std::ceil(w) + std::max(1.0, 0.9 * w)) : std::ceil(w);
     const double t = waves * ((S == 1 ? 5.0 : 6.0 + 0.1 * S) + (tiles + S - 1) / S);
     if (i == 0 || t < best_t) {
       d.pairs = S;
