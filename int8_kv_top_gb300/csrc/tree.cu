@@ -9,7 +9,7 @@
 // (token, head) rows of a sequence and group, packed 12 a token, are cut into blocks of 256 rows (21 1/3
 // tokens), the M of one MMA over a pair of CTAs (128 rows each).  Selected tokens attend through the same
 // dense tiles, their other cells masked: gathering 2,048 cells a token costs an SM about 25 us, a masked
-// 128-cell tile for 21 tokens about 1 us.  A cluster of 2 S CTAs takes one block and group, each pair a run of its
+// 128-cell tile for 21 tokens 1.7 us of a pair.  A cluster of 2 S CTAs takes one block and group, each pair a run of its
 // 128-cell tiles, and the pairs merge by log-sum-exp in a fixed order, so that a call of few rows still
 // spreads over the GPU and results do not depend on timing.  The statistics are exchanged through
 // distributed shared memory, the rows through a workspace that stays in L2: 128 KB a CTA by remote shared
@@ -19,9 +19,17 @@
 // tiles; no fp16 mirror is written (a drafting step reads the cache a few times, and the mirror would cost
 // three times the cache's own bytes).  In a pair each CTA holds half of a K^ tile (64 cells) and half of
 // a V^ tile (128 dims), so per 128 cells an SM converts 32 KB of codes, moves about 210 KB through shared
-// memory (1,650 cycles) and its half of the MMAs takes about 2,050 cycles; one CTA per block instead
-// converts and stores twice as much and is bound by shared memory (3,100 cycles; measured 5,400 a tile of 128
-// rows).
+// memory (1,650 cycles) and its half of the MMAs takes about 2,050 cycles; measured 3,500 cycles a tile.  One CTA
+// per block instead converts and stores twice as much and is bound by shared memory (3,100 cycles; measured
+// 5,400 a tile of 128 rows).
+//
+// 4 trees of 33-48 tokens after 30,000 cells, all of them attended to: 156 us, 0.40 of the measured bf16 rate over
+// the call; over the CTAs' own time the tensor pipe is 57% active and no role is saturated: 0.45 instructions a
+// cycle and scheduler, the producers waiting on their loads and the softmax on S.  The roles run at once, so the
+// loop bodies share the instruction cache: with separate K and V producer bodies a quarter of all stalls were
+// instruction fetches, and the call took 196 us.  A single S buffer with P kept apart (so that QK never waits on
+// a PV): 208 us.  Persistent pairs over an even share of all tiles, merged by a second launch: 217 against 221
+// us then, and slower by 5 to 60 us for short caches, whose calls a second launch and the write-out weigh down.
 //
 //   warps 0-3    K producers: stage = 128 dims of this CTA's 64 cells (16 KB), ring of four (two tiles)
 //   warps 4-7    V producers: stage = 64 cells x this CTA's 128 dims (16 KB), ring of four (two tiles)

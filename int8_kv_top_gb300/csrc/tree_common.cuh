@@ -103,7 +103,7 @@ __host__ __device__ __forceinline__ int tree_blocks_most(int n_seq, int n_tok) {
 // The list, by one CTA of kPlanThreads: plan[0].x blocks, then for block i plan[1 + 2 i] = {first pool cell,
 // committed cells, drafted tokens, first token row} of its sequence and plan[2 + 2 i].x = its first row, in decreasing
 // order of tiles (a counting sort), so that the long blocks of a ragged batch start first and the short ones
-// fill the gaps (24 trees after 200-16,000 cells: attention 213 -> 159 us).  Blocks of equal length come in
+// fill the gaps (24 trees after 200-16,000 cells: attention 213 -> 159 us when it was added).  Blocks of equal length come in
 // any order, which no result depends on.  A table whose rows overlap (its bad entries are flagged elsewhere) may
 // name more blocks than the list holds: those past `cap` are dropped.
 __device__ __forceinline__ void tree_plan_blocks(const TreeBatch& b, bool with_selected, int4* __restrict__ plan, int cap) {
