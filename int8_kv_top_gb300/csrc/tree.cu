@@ -31,6 +31,10 @@
 // a PV): 208 us.  Persistent pairs over an even share of all tiles, merged by a second launch: 217 against 221
 // us then, and slower by 5 to 60 us for short caches, whose calls a second launch and the write-out weigh down.
 //
+// A cluster holds eight pairs at most, and with few sequences over long caches that leaves most of the GPU idle; then
+// pairs of their own (up to half of the GPU's a block and group) take the tiles and a second launch joins their parts.
+// One tree of 16 tokens after 8,192 cells (selection included) 52 -> 43 us, after 30,000 106 -> 68.
+//
 //   warps 0-3    K producers: stage = 128 dims of this CTA's 64 cells (16 KB), ring of four (two tiles)
 //   warps 4-7    V producers: stage = 64 cells x this CTA's 128 dims (16 KB), ring of four (two tiles)
 //   warps 8-15   load Q; two softmax warpgroups, one row per thread in each, half of the columns each:
@@ -60,6 +64,7 @@ constexpr int kMaxTok = (2 * kRows + kHPG - 2) / kHPG + 1;  // tokens a block's 
 constexpr int kThreads = 17 * 32;
 constexpr int kMaxS = 8;                    // pairs of a cluster at most
 constexpr int kNS = 2;
+constexpr int kMaxRuns = 38;                // clusters of one pair that a block and group may share: half of the GPU's
 constexpr int kOffK = 0, kOffV = kTileStages * kTileStageBytes, kOffQ = 2 * kTileStages * kTileStageBytes;
 constexpr int kOffML = kOffQ + kRows * kD * 2;          // float2 (m, l) [kMaxS][kRows], pushed by every pair
 constexpr int kSmem = kOffML + kMaxS * kRows * 8 + 1024;  // + alignment slack
@@ -84,7 +89,9 @@ struct DenseTreeArgs {
   const __half* gate;
   __half* out;
   const int4* plan;      // the blocks, longest first (tree_plan_blocks), or null: in the table's order
-  float* part;           // unmerged O, [CTA of the grid][kD / 4][kRows][4]; null for one pair per cluster
+  float* part;           // unmerged O, [CTA of the grid][kD / 4][kRows][4]; null for one pair per block
+  float2* part_ml;       // and its (m, l), [CTA of the grid][kRows], where the parts are joined by a launch of their own
+  int runs;              // clusters that share a block: 1, or (with one pair a cluster) more and tree_join_kernel
   int* status;
 };
 
@@ -115,6 +122,44 @@ __device__ __forceinline__ uint4 pack_out(const float (&v)[8]) {
   return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
 }
 
+// Block `blk` of the grid, by a warp: whether there is one, its sequence's {first pool cell, -, committed cells, first
+// token row}, drafted tokens and the block's first row; for lane = token of the block its mask words, whether it is
+// computed here and whether it is a selected one.
+struct BlockAt {
+  int4 e;
+  int T, row0;
+  uint32_t m[kTreeWords];
+  bool ours, sel;
+};
+__device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4* plan, bool with_selected, int blk, int lane) {
+  BlockAt x;
+  bool here;
+  if (plan != nullptr) {
+    const int4 head = __ldg(&plan[0]), at = __ldg(&plan[1 + 2 * blk]);
+    x.row0 = __ldg(&plan[2 + 2 * blk].x);
+    here = blk < head.x;
+    x.e = make_int4(at.x, 0, at.y, at.w);
+    x.T = at.z;
+  } else {
+    const int sq = warp_find_seq(b.n_seq, blk, [&](int s) { return first_block(__ldg(&b.seqs[s].w), s); });
+    x.T = tree_seq_tokens(b, sq, &x.e);
+    const long long k = blk - first_block(x.e.w, sq);
+    here = x.T > 0 && k >= 0 && k * kTreeBlock < (long long)x.T * kHPG;
+    x.row0 = here ? (int)k * kTreeBlock : 0;
+  }
+  const int tok = x.row0 / kHPG + lane;
+  const bool live = here && lane < kMaxTok && tok < x.T && tok * kHPG < x.row0 + 2 * kRows;
+  int n_kv = x.e.z;
+#pragma unroll
+  for (int w = 0; w < kTreeWords; ++w) {
+    x.m[w] = live ? tree_mask_word(b, x.e.w + tok, w, x.T) : 0u;
+    n_kv += __popc(x.m[w]);
+  }
+  x.sel = live && n_kv > b.identity_max;
+  x.ours = live && (!x.sel || with_selected);
+  return x;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeBatch b, int4* __restrict__ plan) {
   pdl_begin();
   tree_plan_blocks(b, false, plan, tree_blocks_most(b.n_seq, b.n_tok));
@@ -134,8 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank();
-  const int half = rank & 1, pair = rank >> 1;  // rows 128 half .. of the block; run `pair` of its tiles
-  const int blk = blockIdx.x / (2 * S) / kGroups, g = blockIdx.x / (2 * S) % kGroups;
+  const int half = rank & 1, pair = rank >> 1;  // rows 128 half .. of the block
+  const int pairs = S * a.runs, run = (blockIdx.x >> 1) % pairs;  // of the block; run `run` of its tiles
+  const int blk = (blockIdx.x >> 1) / pairs / kGroups, g = (blockIdx.x >> 1) / pairs % kGroups;
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kTileStages; ++i) {
@@ -156,55 +202,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
   cluster_arrive_all();  // #0, waited for before the first remote access: every CTA's barriers are set up
   pdl_begin();
-  if (blk == 0 && rank == 0 && g == 0) {  // one CTA looks over the whole table and flags bad entries
+  if (blockIdx.x == 0) {  // one CTA looks over the whole table and flags bad entries
     for (int s = tid; s < a.b.n_seq; s += kThreads) {
       int4 e;
       if (tree_seq_tokens(a.b, s, &e) < 0) set_dev_status(a.status, QSA_DEV_BAD_ID);
     }
   }
   if (warp == 0) {
-    int4 e;
-    int T, row0;
-    bool here;
-    if (a.plan != nullptr) {
-      const int4 head = __ldg(&a.plan[0]), at = __ldg(&a.plan[1 + 2 * blk]);
-      row0 = __ldg(&a.plan[2 + 2 * blk].x);
-      here = blk < head.x;
-      e = make_int4(at.x, 0, at.y, at.w);
-      T = at.z;
-    } else {
-      const int sq = warp_find_seq(a.b.n_seq, blk, [&](int s) { return first_block(__ldg(&a.b.seqs[s].w), s); });
-      T = tree_seq_tokens(a.b, sq, &e);
-      const long long k = blk - first_block(e.w, sq);
-      here = T > 0 && k >= 0 && k * kTreeBlock < (long long)T * kHPG;
-      row0 = here ? (int)k * kTreeBlock : 0;
-    }
-    const int tok = row0 / kHPG + lane;  // lane = token of the block
-    const bool live = here && lane < kMaxTok && tok < T && tok * kHPG < row0 + 2 * kRows;
-    int n_kv = e.z;
-    uint32_t m[kTreeWords];
+    const BlockAt x = tree_block_at(a.b, a.plan, a.bits != nullptr, blk, lane);
+    const unsigned all_ours = __ballot_sync(0xffffffffu, x.ours), all_sel = __ballot_sync(0xffffffffu, x.sel);
 #pragma unroll
     for (int w = 0; w < kTreeWords; ++w) {
-      m[w] = live ? tree_mask_word(a.b, e.w + tok, w, T) : 0u;
-      n_kv += __popc(m[w]);
-    }
-    const bool sel = live && n_kv > a.b.identity_max, ours = live && (!sel || a.bits != nullptr);
-    const unsigned all_ours = __ballot_sync(0xffffffffu, ours), all_sel = __ballot_sync(0xffffffffu, sel);
-#pragma unroll
-    for (int w = 0; w < kTreeWords; ++w) {
-      const uint32_t u = __reduce_or_sync(0xffffffffu, ours ? m[w] : 0u);
-      if (lane < kMaxTok) s_mask[lane][w] = m[w];
+      const uint32_t u = __reduce_or_sync(0xffffffffu, x.ours ? x.m[w] : 0u);
+      if (lane < kMaxTok) s_mask[lane][w] = x.m[w];
       if (lane == 0) s_union[w] = u;
     }
     if (lane == 0) {
       s_ours = (int)all_ours;
       s_sel = (int)all_sel;
       s_blk[0] = all_ours != 0u;
-      s_blk[1] = e.x;
-      s_blk[2] = e.z;
-      s_blk[3] = T;
-      s_blk[4] = e.w;
-      s_blk[5] = row0;
+      s_blk[1] = x.e.x;
+      s_blk[2] = x.e.z;
+      s_blk[3] = x.T;
+      s_blk[4] = x.e.w;
+      s_blk[5] = x.row0;
     }
   }
   __syncthreads();
@@ -217,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   const int row0 = blk_row0 + half * kRows;  // this CTA's first row
   const int n_scan = pos0 + T;
   const int n_tiles = (n_scan + kTileCells - 1) / kTileCells;
-  const int j_begin = n_tiles * pair / S, J = n_tiles * (pair + 1) / S - j_begin;  // the same in both CTAs of a pair
+  const int j_begin = n_tiles * run / pairs, J = n_tiles * (run + 1) / pairs - j_begin;  // the same in both CTAs of a pair
   auto pair_addr = [&](const void* p) { return mapa_shared(smem_u32(p), (uint32_t)rank & ~1u); };  // in rank 0
   float m_run = -INFINITY, l_run = 0.f;  // softmax threads: the row's running maximum (log2 units), this half's sum
   bool ok = true;
@@ -464,12 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     if (!all_ok) m_run = -INFINITY;
     if (wg == 0) {
       const float l = l_run + s_xm[1][r];
+      if (a.runs > 1) a.part_ml[(size_t)blockIdx.x * kRows + r] = make_float2(m_run, l);
       const uint32_t at = smem_u32(smem + kOffML) + (uint32_t)(pair * kRows + r) * 8u;
       for (int c = 0; c < S; ++c)
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(at, 2 * c + half)), "f"(m_run), "f"(l)
                      : "memory");
     }
-    // O (unscaled): to the workspace, or over the operand tiles when the block has one pair (the last PV is
+    // O (unscaled): to the workspace, or over the operand tiles when the block has but one pair (the last PV is
     // complete, so both CTAs' MMAs are done with them)
     if (J > 0 && any_row) {
       tc_fence_after();
@@ -479,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
         uint32_t o[32];
         tmem_ld32(lane_base + kColO + c0, o);
         tmem_wait_ld();
-        if (S == 1) {
+        if (pairs == 1) {
           float4* dst = reinterpret_cast<float4*>(smem + (size_t)r * (kOStride * 4)) + c0 / 4;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -503,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   cluster_wait_all();  // #1: the cluster's rows and statistics are visible; no CTA touches another after this
   tc_fence_after();
   if (warp == 16 && J > 0) tmem_dealloc_pair(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
-  if (warp < 16) {
+  if (warp < 16 && a.runs == 1) {  // else tree_join_kernel merges
     const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
     const int per = (kRows + S - 1) / S;  // rows of an owner
     auto row_at = [&](int r, size_t* at) {  // this CTA's row r: is it one of ours, and where its output starts
@@ -584,50 +606,152 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
 }
 
-// How a call is cut: blocks (grid indices; a ragged batch leaves about half a block a sequence unused) and pairs
-// per cluster.  A launch takes about waves x (a fixed part + the tiles of a pair), in units of one tile's time
-// (1.7 us; fixed: 8 us for one pair, 10 to 12 with a merge); a wave is as many clusters of that size as a GB300
-// holds at once (a cluster stays inside a GPC).  How many tokens and cells a sequence has is on the device, so
-// blocks and waves are means of two cases: equal sequences (each one's blocks rounded up; whole waves) and spread
-// ones (half a block of rounding a sequence; lengths over (0, max_n_kv), for which w clusters a
-// place took 0.9 w waves).  Measured with 1, 2, 3, 4, 5, 6, 8 pairs a cluster (us a call):
-//   16 trees of 22 tokens after 8,192 cells   234 253 263 311 287 369 359
-//   16 trees of  6                            207 140 173 190 174 200 197
-//   24 trees of 1-32 after 200-16,000         353 248 264 296 304 378 362
-//    4 trees of 33-48 after 29,000-31,000     451 232 156 229 193 241 190
-//    1 tree  of 61 after 30,000               504 287 211 176 151 139 119
+// Joins the parts of blocks that several clusters share, in the runs' order within a slice and then slice by
+// slice.  A CTA owns four rows of a block and group (so that one block's rows spread over 128 CTAs), a thread
+// eight dims of a row and every fourth part, four of them loaded at once: a few round trips to L2.
+constexpr int kJoinRows = 4, kJoinSlices = 4, kJoinDepth = 4, kJoinItems = kJoinRows * (kD / 8);
+constexpr int kJoinThreads = kJoinItems * kJoinSlices;
+__global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid_constant__ DenseTreeArgs a) {
+  __shared__ float2 s_ml[kMaxRuns][kJoinRows];
+  __shared__ float s_v[kJoinSlices - 1][9][kJoinItems];
+  __shared__ int s_blk[3];
+  __shared__ unsigned s_ours;
+  pdl_begin();
+  constexpr int kChunks = 2 * kRows / kJoinRows;
+  const int tid = threadIdx.x;
+  const int chunk = blockIdx.x % kChunks, g = blockIdx.x / kChunks % kGroups, blk = blockIdx.x / kChunks / kGroups;
+  const int half = chunk / (kChunks / 2), r0 = chunk % (kChunks / 2) * kJoinRows;
+  if (tid < 32) {
+    const BlockAt x = tree_block_at(a.b, a.plan, a.bits != nullptr, blk, tid);
+    const unsigned all_ours = __ballot_sync(0xffffffffu, x.ours);
+    if (tid == 0) {
+      s_ours = all_ours;
+      s_blk[0] = x.T;
+      s_blk[1] = x.e.w;
+      s_blk[2] = x.row0;
+    }
+  }
+  __syncthreads();
+  const int T = s_blk[0], first = s_blk[1], blk_row0 = s_blk[2];
+  const int row0 = blk_row0 + half * kRows + r0;
+  if (!s_ours || row0 >= T * kHPG) return;  // the same in all threads; without tokens of ours no part was written
+  const size_t cta0 = (size_t)(blk * kGroups + g) * a.runs * 2 + half;  // run 0's CTA with these rows
+  for (int i = tid; i < a.runs * kJoinRows; i += kJoinThreads)
+    s_ml[i / kJoinRows][i % kJoinRows] = __ldcg(&a.part_ml[(cta0 + 2 * (i / kJoinRows)) * kRows + r0 + i % kJoinRows]);
+  __syncthreads();
+  const int rr = tid % kJoinRows, d8 = tid / kJoinRows % (kD / 8), slice = tid / kJoinItems;
+  const int R = row0 + rr, ti = R / kHPG - blk_row0 / kHPG;
+  const bool mine = R < T * kHPG && ((s_ours >> ti) & 1);
+  const size_t at = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD;
+  uint4 gw = make_uint4(0u, 0u, 0u, 0u);
+  if (a.gate && mine && slice == 0) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at) + d8);
+  float M = -INFINITY, L = 0.f;
+  for (int c = 0; c < a.runs; ++c) M = fmaxf(M, s_ml[c][rr].x);
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const float4* src = reinterpret_cast<const float4*>(a.part) + cta0 * (kRows * kD / 4) + (size_t)(2 * d8) * kRows + r0 + rr;
+  for (int c0 = slice; mine && c0 < a.runs; c0 += kJoinDepth * kJoinSlices) {
+    float4 p[kJoinDepth][2];
+#pragma unroll
+    for (int u = 0; u < kJoinDepth; ++u) {
+      const float4* from = src + (size_t)min(c0 + u * kJoinSlices, a.runs - 1) * (2 * kRows * kD / 4);
+      p[u][0] = __ldcg(from);
+      p[u][1] = __ldcg(from + kRows);
+    }
+#pragma unroll
+    for (int u = 0; u < kJoinDepth; ++u) {
+      const int c = c0 + u * kJoinSlices;
+      const float2 st = s_ml[min(c, a.runs - 1)][rr];
+      if (c >= a.runs || st.x == -INFINITY) continue;  // a run that has nothing of this row wrote nothing
+      const float f = fast_exp2(st.x - M);
+      L = fmaf(st.y, f, L);
+      const float y[8] = {p[u][0].x, p[u][0].y, p[u][0].z, p[u][0].w, p[u][1].x, p[u][1].y, p[u][1].z, p[u][1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fmaf(y[i], f, v[i]);
+    }
+  }
+  const int item = tid % kJoinItems;
+  if (slice > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_v[slice - 1][i][item] = v[i];
+    s_v[slice - 1][8][item] = L;
+  }
+  __syncthreads();
+  if (slice == 0 && mine) {
+#pragma unroll
+    for (int c = 0; c < kJoinSlices - 1; ++c) {
+      L += s_v[c][8][item];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += s_v[c][i][item];
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= inv;
+    if (a.gate) apply_gate(v, gw);
+    reinterpret_cast<uint4*>(a.out + at)[d8] = pack_out(v);
+  }
+}
+
+// How a call is cut: blocks (grid indices; a ragged batch leaves about half a block a sequence unused), and for each
+// block and group either one cluster of `pairs` pairs that merge in it, or `runs` clusters of one pair whose parts
+// tree_join_kernel joins.  A launch takes about waves x (a fixed part + the tiles of a pair), in units of one tile's
+// time (1.7 us; fixed: 8 us for one pair, 10 to 12 with a merge in the cluster), and the join its own time by the
+// blocks and their parts.  A wave is as many clusters of that size as a GB300 holds at once (a cluster stays inside a
+// GPC).  How many tokens and cells a sequence has is on the device, so waves is the mean of what equal and spread
+// sequences give, each with equal and with spread lengths: the blocks of equal sequences rounded up, or half a block
+// of rounding a sequence; whole waves, or 0.9 of a wave for every filling of the GPU.  Measured (us a call):
+//                                         pairs 1   2   3   5   6   8     runs 2   4   6   9  12  19  38
+//    1 tree  of 61 after  1,984 cells          38  27  23  20  19  16       28  22  21  20  20  29  29
+//    1 tree  of 16 after  8,192               156 100  79  62  58  53       98  69  58  52  48  46  44
+//    1 tree  of 16 after 30,000               490 275 200 141 127 106      274 159 123 100  88  76  68
+//    2 trees of 61 after 30,000               539 317 237 173 248 209      321 203 166 199 176 189 235
+//    4 trees of 44 after 30,000               597 361 444 323 385 388      371 372 300 308 315 340 406
+//    8 trees of 16 after 30,000               624 364 275 323 291 320      374 241 289 238 259 260 315
+//   12 trees of 61 after  8,192               285 305 373 385 470 465      337 366 393 425 453 534 760
+//   24 trees of 1-32 after 200-16,000         352 247 264 304 378 362      265 281 298   -  348   -   -
 struct DensePlan {
-  int blocks, pairs;
+  int blocks, pairs, runs;
 };
+constexpr double kJoinBlock = 0.2, kJoinPart = 0.02;  // tree_join_kernel's time a block and group, and a part of it
 constexpr int kSizes[7] = {1, 2, 3, 4, 5, 6, 8};
 constexpr int kHeld[7] = {76, 36, 23, 15, 13, 8, 7};
 
 DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
-  DensePlan d{tree_blocks_most(n_seq, n_tok), 1};
+  DensePlan d{tree_blocks_most(n_seq, n_tok), 1, 1};
   const long long rows = (long long)n_tok * kHPG;
   const long long even = n_seq * ((rows + (long long)n_seq * kTreeBlock - 1) / ((long long)n_seq * kTreeBlock));
   const long long spread =
-      std::max<long long>(n_seq, (rows + kTreeBlock / 2 * (long long)n_seq + kTreeBlock - 1) / kTreeBlock);
-  const double clusters = (double)((n_seq > 1 ? (even + spread) / 2 : even) * kGroups);
+      n_seq == 1 ? even : std::max<long long>(n_seq, (rows + kTreeBlock / 2 * (long long)n_seq + kTreeBlock - 1) / kTreeBlock);
   const long long longest = with_selected ? max_n_kv : std::min<long long>(max_n_kv, (long long)identity_max + 32 * kTreeWords);
   const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
+  auto waves = [&](double a_cluster, int held) {  // of `a_cluster` clusters a block and group
+    const double we = (double)(even * kGroups) * a_cluster / held, ws = (double)(spread * kGroups) * a_cluster / held;
+    if (n_seq == 1) return std::ceil(we);
+    return 0.25 * (std::ceil(we) + std::max(1.0, 0.9 * we) + std::ceil(ws) + std::max(1.0, 0.9 * ws));
+  };
   double best_t = 0.0;
   for (int i = 0; i < 7; ++i) {
     const int S = kSizes[i];
-    const double w = clusters / kHeld[i];
-    const double waves = n_seq > 1 ? 0.5 * (std::ceil(w) + std::max(1.0, 0.9 * w)) : std::ceil(w);
-    const double t = waves * ((S == 1 ? 5.0 : 6.0 + 0.1 * S) + (tiles + S - 1) / S);
+    const double t = waves(1.0, kHeld[i]) * ((S == 1 ? 5.0 : 6.0 + 0.1 * S) + (tiles + S - 1) / S);
     if (i == 0 || t < best_t) {
       d.pairs = S;
+      best_t = t;
+    }
+  }
+  const double clusters = 0.5 * (double)((even + spread) * kGroups);
+  for (int runs = 2; runs <= std::min(kMaxRuns, tiles) && runs * clusters <= 4 * kHeld[0]; ++runs) {
+    const double t = waves(runs, kHeld[0]) * (5.0 + (tiles + runs - 1) / runs) + 2.5 + (kJoinBlock + kJoinPart * runs) * clusters;
+    if (t < best_t) {
+      d.pairs = 1;
+      d.runs = runs;
       best_t = t;
     }
   }
   return d;
 }
 
-cudaLaunchConfig_t tree_config(int S, int blocks, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
+cudaLaunchConfig_t tree_config(int S, int clusters, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks * kGroups * 2 * S);
+  cfg.gridDim = dim3(clusters * 2 * S);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
@@ -660,8 +784,11 @@ cudaError_t tree_setup() {
 }  // namespace
 
 namespace {
+size_t part_rows(const DensePlan& d) {  // rows of the unmerged parts
+  return d.pairs * d.runs == 1 ? 0 : (size_t)d.blocks * kGroups * 2 * d.pairs * d.runs * kRows;
+}
 size_t part_bytes(const DensePlan& d) {
-  return d.pairs == 1 ? 0 : (size_t)d.blocks * kGroups * 2 * d.pairs * kRows * kD * sizeof(float);
+  return part_rows(d) * (kD * sizeof(float) + (d.runs > 1 ? sizeof(float2) : 0));
 }
 }  // namespace
 
@@ -688,10 +815,13 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
     if (e != cudaSuccess) return e;
   }
   const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, plan,
-                        static_cast<float*>(ws), status};
+                        static_cast<float*>(ws),
+                        d.runs > 1 ? reinterpret_cast<float2*>(static_cast<float*>(ws) + part_rows(d) * kD) : nullptr,
+                        d.runs, status};
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = tree_config(d.pairs, d.blocks, stream, attr);
-  return cudaLaunchKernelEx(&cfg, tree_dense_kernel, a, d.pairs);
+  cudaLaunchConfig_t cfg = tree_config(d.pairs, d.blocks * kGroups * d.runs, stream, attr);
+  if ((e = cudaLaunchKernelEx(&cfg, tree_dense_kernel, a, d.pairs)) != cudaSuccess || d.runs == 1) return e;
+  return launch_pdl(tree_join_kernel, dim3(d.blocks * kGroups * (2 * kRows / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace qsa

@@ -72,6 +72,26 @@ def test_dense_over_long_caches():
     check(pool, seqs, params=(2048, 131072, SCALE))
 
 
+@pytest.mark.parametrize("specs,params,gated", [
+    ([(9000, 16)], None, True),                            # selected tokens
+    ([(4500, 12), (0, 3), (9000, 10)], None, False),       # short sequences: pairs without a tile
+    ([(7000, 30)], (2048, 131072, SCALE), True),           # two blocks, the second ends inside its rows
+    ([(20000, 2)] + [(5, 1), (300, 4)] * 4, (2048, 131072, SCALE), False),
+    ([(6000, 1)], (2048, 131072, SCALE), False),
+])
+def test_blocks_shared_by_many_pairs(specs, params, gated):
+    # few sequences over long caches: a block's cells are split over pairs of CTAs and the parts joined afterwards
+    pool, seqs = make_batch(specs, seed=31)
+    if (0, 3) in specs:
+        pool["tree"][13] = 0  # sees nothing
+    torch.full((128 << 20,), 255, dtype=torch.uint8, device="cuda")  # freed at once: the workspace starts with NaN
+    gate = synth.gate_input(pool["q"].shape[0], seed=62) if gated else None
+    first = check(pool, seqs, params=params, gate=gate)
+    for _ in range(2):
+        again = run_tree(pool, seqs, None, params, gate)[1]
+        assert np.array_equal(again.double().cpu().numpy(), first)
+
+
 def test_many_short_trees():
     rng = np.random.default_rng(10)
     pool, seqs = make_batch([(int(rng.integers(0, 300)), int(rng.integers(1, 26))) for _ in range(60)], seed=10)
