@@ -138,15 +138,13 @@ int decode_layer_limit(int* rc) {
 
 // Whether a tree call selects for its tokens together (tree_select.cu, then one tensor-core attention for all)
 // or gives each selected (token, group) a cluster of its own.  Together costs by the sequences and their cells,
-// the clusters cost by the tokens, so the rule is on the tokens a sequence: eight where fewer than four sequences
-// leave the clusters room, five up to 15 sequences, four from 16 on, and more above 32,768 cells.  Measured
-// (together / clusters, us a call of equal trees): 1 sequence of 8,192 cells with 6 tokens 51 / 37, 8 tokens
-// 52 / 55, of 60,000 with 12 tokens 188 / 157; 3 of 12,000 with 6 tokens 69 / 61, 8 tokens 69 / 103; 8 of 12,000
-// with 4 tokens 134 / 103, 5 tokens 134 / 173; 16 of 24,000 with 3 tokens 325 / 272, 4 tokens 327 / 352; 16 of
-// 60,000 with 4 tokens 744 / 690, 5 tokens 772 / 844.
+// the clusters cost by the tokens, so the rule is on the tokens a sequence.  Measured (together / clusters, us a
+// call of equal trees): 1 sequence of 16,000 cells with 7 tokens 45 / 44, 8 tokens 45 / 70; 2 with 3 tokens 57 / 47,
+// 4 tokens 57 / 72; 4 with 4 tokens 86 / 71, 5 tokens 87 / 121; 8 with 4 tokens 137 / 130, 5 tokens 138 / 194; 16 of
+// 24,000 with 3 tokens 325 / 272, 4 tokens 327 / 352; of 60,000 cells 1 with 7 tokens 95 / 87, 8 tokens 96 / 148, 4
+// with 4 tokens 222 / 230, 8 with 4 tokens 383 / 383.
 bool tree_selects_together(int n_seq, int n_tok, int max_n_kv, const qsa::Params& p) {
-  long long least = n_seq < 4 ? 8 : n_seq < 16 ? 5 : 4;  // tokens a sequence
-  if (max_n_kv > 32768) least += n_seq == 1 ? 5 : 1;
+  const long long least = n_seq == 1 ? 8 : n_seq == 2 || n_seq >= 16 ? 4 : 5;  // tokens a sequence
   return max_n_kv > p.identity_max && max_n_kv <= qsa::select_max_cells() && n_tok >= least * n_seq;
 }
 
