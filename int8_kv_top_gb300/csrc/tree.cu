@@ -103,6 +103,14 @@ struct __align__(8) TreeBars {
   uint64_t q_full, tmem_ready, drain;
 };
 
+// Rows of a block that exist are shared out evenly: its CTA `half` of each pair has rows [x, x + n) of the tree, so
+// that the loads of Q and the stores of O, 1 KB a row, are halved where a block is not full.
+__device__ __forceinline__ int cta_rows(int T, int blk_row0, int half, int* x) {
+  const int n = min(2 * kRows, T * kHPG - blk_row0), first = (n + 1) / 2;
+  *x = blk_row0 + half * first;
+  return half ? n - first : first;
+}
+
 // Index of a sequence's first block in the grid: block k of sequence s has index first_block(s) + k.
 // The sequences' ranges never meet, since floor((a + b) / 256) + 1 >= floor(a / 256) + ceil(b / 256), so
 // a block finds its sequence by a search over the table, without a prefix sum; some indices stay unused.
@@ -182,22 +190,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   const int half = rank & 1, pair = rank >> 1;  // rows 128 half .. of the block
   const int pairs = S * a.runs, run = (blockIdx.x >> 1) % pairs;  // of the block; run `run` of its tiles
   const int blk = (blockIdx.x >> 1) / pairs / kGroups, g = (blockIdx.x >> 1) / pairs % kGroups;
-  if (tid == 0) {
-    s_abort = 0;
-    for (int i = 0; i < kTileStages; ++i) {
-      mbar_init(&bars.k_full[i], 8);
-      mbar_init(&bars.k_empty[i], 1);
-      mbar_init(&bars.v_full[i], 8);
-      mbar_init(&bars.v_empty[i], 1);
-    }
-    for (int i = 0; i < kNS; ++i) {
-      mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 16);
-      mbar_init(&bars.pv_done[i], 1);
-    }
-    mbar_init(&bars.q_full, 16);
-    mbar_init(&bars.tmem_ready, 1);
-    mbar_init(&bars.drain, 1);
+  if (tid == 0) s_abort = 0;
+  if (tid < 32) {
+    // a lane a barrier, in the order of the members
+    static_assert(sizeof(TreeBars) == (4 * kTileStages + 3 * kNS + 3) * 8 && sizeof(TreeBars) <= 32 * 8, "a lane a barrier");
+    const int i = lane - 4 * kTileStages;
+    const uint32_t count = i < 0 ? ((lane / kTileStages) & 1 ? 1u : 8u)           // k_full, k_empty, v_full, v_empty
+                                 : i >= kNS && i < 2 * kNS || i == 3 * kNS ? 16u  // p_full, q_full
+                                                                           : 1u;  // s_full, pv_done, tmem_ready, drain
+    if (lane < (int)(sizeof(TreeBars) / 8)) mbar_init(reinterpret_cast<uint64_t*>(&bars) + lane, count);
     fence_mbar_init();
   }
   cluster_arrive_all();  // #0, waited for before the first remote access: every CTA's barriers are set up
@@ -235,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
   const long long cell0 = s_blk[1];
   const int pos0 = s_blk[2], T = s_blk[3], first = s_blk[4], blk_row0 = s_blk[5];
-  const int row0 = blk_row0 + half * kRows;  // this CTA's first row
+  int row0;  // this CTA's first row
+  const int n_rows = cta_rows(T, blk_row0, half, &row0);
   const int n_scan = pos0 + T;
   const int n_tiles = (n_scan + kTileCells - 1) / kTileCells;
   const int j_begin = n_tiles * run / pairs, J = n_tiles * (run + 1) / pairs - j_begin;  // the same in both CTAs of a pair
@@ -317,24 +319,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     // ------------------------------------------------------------ Q, then softmax rows
     const int st = tid - 256, wg = warp >= 12 ? 1 : 0, quarter = warp & 3;
     {
-      // 16-byte chunk c of rows st / 32 + 8 i; rows past the tree are zeros
+      // 16-byte chunk c of rows st / 32 + 8 i.  Rows past the last are not loaded: whatever their place holds gives
+      // rows of S that are masked as a whole and rows of O that nothing reads.
       const int c = st & 31, r0 = st >> 5;
       int h = (row0 + r0) % kHPG;
       const __half* src = a.q + ((size_t)(first + (row0 + r0) / kHPG) * kHeads + g * kHPG + h) * kD + c * 8;
       uint32_t dst = smem_u32(smem + kOffQ) + (c >> 3) * (kRows * 128) + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4);
-      int left = T * kHPG - row0 - r0;  // rows from this one on
-#pragma unroll
-      for (int i = 0; i < kRows / 8; ++i) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                     "l"(reinterpret_cast<uint64_t>(left > 0 ? src : a.q)), "r"(left > 0 ? 16 : 0)
-                     : "memory");
-        left -= 8;
+#pragma unroll 4
+      for (int left = n_rows - r0; left > 0; left -= 8) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
         dst += 8 * 128;
         h += 8;
         src += 8 * kD;
         if (h >= kHPG) {  // on to the next token's rows of this group
           h -= kHPG;
           src += (kHeads - kHPG) * kD;
+        }
+      }
+      if (a.gate && pairs == 1) {  // 512 bytes a row: into L2 while the tiles run
+        for (int i = st; i < n_rows * 4; i += 256) {
+          const int R = row0 + (i >> 2);
+          const __half* at = a.gate + ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD + (i & 3) * 64;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
         }
       }
       cp_async_wait_all();
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const int R = row0 + r;
     const int ti = R / kHPG - blk_row0 / kHPG;  // token of the block
-    const bool active = R < T * kHPG && ((s_ours >> min(ti, 31)) & 1), chosen = active && ((s_sel >> min(ti, 31)) & 1);
+    const bool active = r < n_rows && ((s_ours >> min(ti, 31)) & 1), chosen = active && ((s_sel >> min(ti, 31)) & 1);
     const uint2* sel_bits = reinterpret_cast<const uint2*>(
         chosen ? a.bits + (size_t)(g * a.b.n_tok + first + R / kHPG) * a.bits_pitch : nullptr);
     uint2 m_next = make_uint2(0u, 0u);  // a selected row's bits, loaded a tile ahead
@@ -527,17 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   if (warp == 16 && J > 0) tmem_dealloc_pair(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
   if (warp < 16 && a.runs == 1) {  // else tree_join_kernel merges
     const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
-    const int per = (kRows + S - 1) / S;  // rows of an owner
+    const int per = ((n_rows + S - 1) / S + 7) & ~7;  // rows of an owner: stores and loads of 128 bytes at least
     auto row_at = [&](int r, size_t* at) {  // this CTA's row r: is it one of ours, and where its output starts
       const int R = row0 + r, ti = R / kHPG - blk_row0 / kHPG;
-      if (r >= kRows || R >= T * kHPG || !((s_ours >> ti) & 1)) return false;
+      if (r >= n_rows || !((s_ours >> ti) & 1)) return false;
       *at = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD;
       return true;
     };
     if (S == 1) {  // a warp a row, 8 dims a lane, from shared memory; four rows' gates are loaded before any is used
       const int d8 = tid & 31;
 #pragma unroll 1
-      for (int r0 = tid >> 5; r0 < kRows; r0 += 64) {
+      for (int r0 = tid >> 5; r0 < n_rows; r0 += 64) {
         size_t at[4];
         uint4 gw[4];
         bool mine[4];
@@ -567,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       for (int x = tid; x < per * 32; x += 512) {
         const int r = pair * per + x % per, d8 = x / per;
         size_t at;
-        if (x % per + pair * per >= kRows || !row_at(r, &at)) continue;
+        if (!row_at(r, &at)) continue;
         uint4 gw = make_uint4(0u, 0u, 0u, 0u);
         if (a.gate) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at) + d8);
         float M = -INFINITY, L = 0.f;
@@ -633,15 +639,16 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
   }
   __syncthreads();
   const int T = s_blk[0], first = s_blk[1], blk_row0 = s_blk[2];
-  const int row0 = blk_row0 + half * kRows + r0;
-  if (!s_ours || row0 >= T * kHPG) return;  // the same in all threads; without tokens of ours no part was written
+  int row0;
+  const int n_rows = s_ours ? cta_rows(T, blk_row0, half, &row0) - r0 : 0;
+  if (n_rows <= 0) return;  // the same in all threads; without tokens of ours no part was written
   const size_t cta0 = (size_t)(blk * kGroups + g) * a.runs * 2 + half;  // run 0's CTA with these rows
   for (int i = tid; i < a.runs * kJoinRows; i += kJoinThreads)
     s_ml[i / kJoinRows][i % kJoinRows] = __ldcg(&a.part_ml[(cta0 + 2 * (i / kJoinRows)) * kRows + r0 + i % kJoinRows]);
   __syncthreads();
   const int rr = tid % kJoinRows, d8 = tid / kJoinRows % (kD / 8), slice = tid / kJoinItems;
-  const int R = row0 + rr, ti = R / kHPG - blk_row0 / kHPG;
-  const bool mine = R < T * kHPG && ((s_ours >> ti) & 1);
+  const int R = row0 + r0 + rr, ti = R / kHPG - blk_row0 / kHPG;
+  const bool mine = rr < n_rows && ((s_ours >> min(ti, 31)) & 1);
   const size_t at = ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD;
   uint4 gw = make_uint4(0u, 0u, 0u, 0u);
   if (a.gate && mine && slice == 0) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at) + d8);
