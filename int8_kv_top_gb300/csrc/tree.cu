@@ -528,12 +528,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   tc_fence_before();
   __syncwarp();
   cluster_arrive_all();
+  const int per = ((n_rows + S - 1) / S + 7) & ~7;  // rows of an owner: loads of 128 bytes at least
   cluster_wait_all();  // #1: the cluster's rows and statistics are visible; no CTA touches another after this
   tc_fence_after();
   if (warp == 16 && J > 0) tmem_dealloc_pair(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
   if (warp < 16 && a.runs == 1) {  // else tree_join_kernel merges
     const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
-    const int per = ((n_rows + S - 1) / S + 7) & ~7;  // rows of an owner: stores and loads of 128 bytes at least
     auto row_at = [&](int r, size_t* at) {  // this CTA's row r: is it one of ours, and where its output starts
       const int R = row0 + r, ti = R / kHPG - blk_row0 / kHPG;
       if (r >= n_rows || !((s_ours >> ti) & 1)) return false;
@@ -569,38 +569,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
           reinterpret_cast<uint4*>(a.out + at[u])[d8] = pack_out(v);
         }
       }
-    } else {  // lanes are rows (16 at least), 8 dims each
-      for (int x = tid; x < per * 32; x += 512) {
-        const int r = pair * per + x % per, d8 = x / per;
+    } else {  // eight rows at a time, by half of the threads each: a lane has 8 dims of a row
+      const int d8 = (tid >> 3) & 31;
+      for (int x = (tid >> 8) * 8 + (tid & 7); x < per; x += 16) {
+        const int r = pair * per + x;
         size_t at;
         if (!row_at(r, &at)) continue;
+        // CTA 0 of the cluster with this half's rows, the next pair's two CTAs further: all parts are loaded at once
+        // (a part of a run that has none is read and dropped)
+        const float4* src = reinterpret_cast<const float4*>(a.part) + (size_t)(blockIdx.x - 2 * pair) * (kRows * kD / 4) +
+                            (size_t)(2 * d8) * kRows + r;
+        float4 p[kMaxS][2];
+#pragma unroll
+        for (int c = 0; c < kMaxS; ++c) {
+          const float4* from = src + (size_t)min(c, S - 1) * (2 * kRows * kD / 4);
+          p[c][0] = __ldcg(from);
+          p[c][1] = __ldcg(from + kRows);
+        }
         uint4 gw = make_uint4(0u, 0u, 0u, 0u);
         if (a.gate) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at) + d8);
         float M = -INFINITY, L = 0.f;
         for (int c = 0; c < S; ++c) M = fmaxf(M, ml[c * kRows + r].x);
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        // CTA 0 of the cluster with this half's rows, the next pair's two CTAs further: all parts are loaded
-        // before any is added (a part of a run that has none is read and dropped)
-        const float4* src = reinterpret_cast<const float4*>(a.part) + (size_t)(blockIdx.x - 2 * pair) * (kRows * kD / 4) +
-                            (size_t)(2 * d8) * kRows + r;
-        for (int c0 = 0; c0 < S; c0 += 4) {
-          float4 p[4][2];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float4* from = src + (size_t)min(c0 + u, S - 1) * (2 * kRows * kD / 4);
-            p[u][0] = __ldcg(from);
-            p[u][1] = __ldcg(from + kRows);
-          }
+        for (int c = 0; c < kMaxS; ++c) {
+          const float2 st = ml[min(c, S - 1) * kRows + r];
+          if (c >= S || st.x == -INFINITY) continue;  // past the last run, or nothing of this row there
+          const float f = fast_exp2(st.x - M);
+          L = fmaf(st.y, f, L);
+          const float y[8] = {p[c][0].x, p[c][0].y, p[c][0].z, p[c][0].w, p[c][1].x, p[c][1].y, p[c][1].z, p[c][1].w};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float2 st = ml[min(c0 + u, S - 1) * kRows + r];
-            if (c0 + u >= S || st.x == -INFINITY) continue;  // past the last run, or nothing of this row there
-            const float f = fast_exp2(st.x - M);
-            L = fmaf(st.y, f, L);
-            const float y[8] = {p[u][0].x, p[u][0].y, p[u][0].z, p[u][0].w, p[u][1].x, p[u][1].y, p[u][1].z, p[u][1].w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(y[i], f, v[i]);
-          }
+          for (int i = 0; i < 8; ++i) v[i] = fmaf(y[i], f, v[i]);
         }
         const float inv = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
 #pragma unroll
