@@ -442,17 +442,22 @@ cudaError_t launch_prep_batched(const __half* q_raw, const __half* k_raw, const 
                                 const int32_t* pos, int axes, const int32_t* cells, int n_tok, int64_t n_pool,
                                 double base, int rotary_dim, float eps, const int* sections, __half* qcur, __half* kcur,
                                 int8_t* kq, __half* ksc, int8_t* vq, __half* vsc, int* status, cudaStream_t stream) {
-  BatchedCfg cfg{};
-  // base^(-2i / rd) as products of the powers for i = 1, 2, 4, ...: a few roundings of a double each
-  cfg.turns[0] = (uint64_t)llround(ldexp(1.0 / 6.283185307179586, 64));
-  double inv[kD / 2];
-  inv[0] = 1.0;
-  for (int w = 1; w < rotary_dim / 2; w *= 2) {
-    const double f = pow(base, -2.0 * w / rotary_dim);
-    for (int i = 0; i < w; ++i) {
-      inv[w + i] = inv[i] * f;
-      cfg.turns[w + i] = (uint64_t)(inv[w + i] * (18446744073709551616.0 / 6.283185307179586));
+  // The angles' table depends on (base, rd) alone: a thread's calls form it again only when these change (3 us).
+  static thread_local BatchedCfg cfg{};
+  static thread_local double cfg_base = 0.0;
+  if (cfg_base != base || cfg.rotary_dim != rotary_dim) {
+    // base^(-2i / rd) as products of the powers for i = 1, 2, 4, ...: a few roundings of a double each
+    cfg.turns[0] = (uint64_t)llround(ldexp(1.0 / 6.283185307179586, 64));
+    double inv[kD / 2];
+    inv[0] = 1.0;
+    for (int w = 1; w < rotary_dim / 2; w *= 2) {
+      const double f = pow(base, -2.0 * w / rotary_dim);
+      for (int i = 0; i < w; ++i) {
+        inv[w + i] = inv[i] * f;
+        cfg.turns[w + i] = (uint64_t)(inv[w + i] * (18446744073709551616.0 / 6.283185307179586));
+      }
     }
+    cfg_base = base;
   }
   cfg.rotary_dim = rotary_dim;
   cfg.sec0 = sections[0];

@@ -130,15 +130,16 @@ def _params(params):
 
 
 @functools.lru_cache(maxsize=64)
-def _rope_of(base: float, rd: int, eps: float, sec: tuple) -> qsa_rope:
-    return qsa_rope(base, rd, eps, (ctypes.c_int * 3)(*sec))
+def _rope_of(rope: tuple) -> qsa_rope:
+    base, rd, eps, sec = rope
+    return qsa_rope(float(base), int(rd), float(eps), (ctypes.c_int * 3)(*sec))
 
 
 def _rope(rope):
     if rope is None:
         return None
     base, rd, eps, sec = rope
-    return _rope_of(float(base), int(rd), float(eps), tuple(sec))
+    return _rope_of(rope if type(rope) is tuple and type(sec) is tuple else (base, rd, eps, tuple(sec)))
 
 
 def _check(rc: int):
@@ -241,22 +242,22 @@ def qsa_flash_prefill_batched(q, kq, vq, ksc, vsc, n_pool: int, seqs, n_seq: int
                                             ws_bytes, _params(params), _stream(stream)))
 
 
-def _row_stride(t, width: int) -> int:
+def _row_stride(t, width: int, n_tok: int) -> int:
     """Elements between two tokens' rows of a raw projection [n_tok, ...] (a slice of a wider one, say); the
     elements of a token's own row lie side by side."""
-    return width if t.shape[0] <= 1 else t.stride(0)
+    return width if n_tok <= 1 else t.stride(0)
 
 
 def qsa_prep_batched(q_raw, k_raw, v_raw, q_gamma, k_gamma, pos, cells, n_tok: int, n_pool: int, qcur, kcur, kq, ksc, vq,
                      vsc, rope=None, stream=None):
     """qsa_prep for tokens of any sequences: pos int32 [n_tok] or [n_tok, 1 or 3], cells int32 [n_tok] (-1: padding).
     q_raw, k_raw and v_raw may be slices along a token's row of a fused projection; kcur may be None."""
-    axes = pos.shape[1] if pos.dim() > 1 else 1
+    axes = pos.size(1) if pos.dim() > 1 else 1
     kv = N_GROUPS * HEAD_DIM
-    _check(load().qsa_prep_batched(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _row_stride(q_raw, N_HEADS * HEAD_DIM),
-                                   _row_stride(k_raw, kv), _row_stride(v_raw, kv), _ptr(q_gamma), _ptr(k_gamma), _ptr(pos),
-                                   axes, _ptr(cells), _rope(rope), n_tok, n_pool, _ptr(qcur), _ptr(kcur), _ptr(kq),
-                                   _ptr(ksc), _ptr(vq), _ptr(vsc), _stream(stream)))
+    _check(load().qsa_prep_batched(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _row_stride(q_raw, N_HEADS * HEAD_DIM, n_tok),
+                                   _row_stride(k_raw, kv, n_tok), _row_stride(v_raw, kv, n_tok), _ptr(q_gamma),
+                                   _ptr(k_gamma), _ptr(pos), axes, _ptr(cells), _rope(rope), n_tok, n_pool, _ptr(qcur),
+                                   _ptr(kcur), _ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), _stream(stream)))
 
 
 def qsa_cache_read(kq, ksc, vq, vsc, n_pool: int, cells, n: int, k16, v16, stream=None):
