@@ -19,13 +19,14 @@
 // tiles; no fp16 mirror is written (a drafting step reads the cache a few times, and the mirror would cost
 // three times the cache's own bytes).  In a pair each CTA holds half of a K^ tile (64 cells) and half of
 // a V^ tile (128 dims), so per 128 cells an SM converts 32 KB of codes, moves about 210 KB through shared
-// memory (1,650 cycles) and its half of the MMAs takes about 2,050 cycles; measured 3,500 cycles a tile.  One CTA
+// memory (1,650 cycles) and its half of the MMAs takes about 2,050 cycles; measured 3,300 cycles a tile.  One CTA
 // per block instead converts and stores twice as much and is bound by shared memory (3,100 cycles; measured
 // 5,400 a tile of 128 rows).
 //
-// 4 trees of 33-48 tokens after 30,000 cells, all of them attended to: 156 us, 0.40 of the measured bf16 rate over
-// the call; over the CTAs' own time the tensor pipe is 57% active and no role is saturated: 0.45 instructions a
-// cycle and scheduler, the producers waiting on their loads and the softmax on S.  The roles run at once, so the
+// 4 trees of 33-48 tokens after 30,000 cells, all of them attended to: 155 us, 0.40 of the measured bf16 rate over
+// the call; over the CTAs' own time the tensor pipe is 57% active.  0.45 instructions are issued a cycle and
+// scheduler; the MMA thread takes about 95 cycles an instruction (of 64 and 128 cycles of arithmetic), and a tile's
+// softmax about 2,400.  The roles run at once, so the
 // loop bodies share the instruction cache: with separate K and V producer bodies a quarter of all stalls were
 // instruction fetches, and the call took 196 us.  A single S buffer with P kept apart (so that QK never waits on
 // a PV): 208 us.  Persistent pairs over an even share of all tiles, merged by a second launch: 217 against 221
