@@ -130,16 +130,15 @@ def _params(params):
 
 
 @functools.lru_cache(maxsize=64)
-def _rope_of(rope: tuple) -> qsa_rope:
-    base, rd, eps, sec = rope
-    return qsa_rope(float(base), int(rd), float(eps), (ctypes.c_int * 3)(*sec))
+def _rope_of(base: float, rd: int, eps: float, sec: tuple) -> qsa_rope:
+    return qsa_rope(base, rd, eps, (ctypes.c_int * 3)(*sec))
 
 
 def _rope(rope):
     if rope is None:
         return None
     base, rd, eps, sec = rope
-    return _rope_of(rope if type(rope) is tuple and type(sec) is tuple else (base, rd, eps, tuple(sec)))
+    return _rope_of(float(base), int(rd), float(eps), tuple(sec))
 
 
 def _check(rc: int):

@@ -244,21 +244,22 @@ def test_repeated_calls_give_the_same_bits():
         assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
 
 
-def test_on_another_stream_and_in_graphs():
-    pool, seqs = make_batch([(700, 17), (2300, 6)], seed=21)
+@pytest.mark.parametrize("specs", [[(700, 17), (2300, 6)], [(9000, 16)], [(5000, 30), (7000, 12)]])
+def test_on_another_stream_and_in_graphs(specs):
+    pool, seqs = make_batch(specs, seed=21)
     want_ids, want = run_tree(pool, seqs)
-    n_tok, n_pool, max_n_kv = pool["q"].shape[0], pool["kq"].shape[0], 2306
+    n_tok, n_pool, n_seq, max_n_kv = pool["q"].shape[0], pool["kq"].shape[0], len(specs), max(p + n for p, n in specs)
     dev = {k: torch.from_numpy(v).cuda() for k, v in pool.items() if k != "tree"}
     tree = torch.from_numpy(pool["tree"].view(np.int32)).cuda()
     table = torch.from_numpy(seqs).cuda()
-    need = qsa.qsa_tree_attention_workspace_bytes(2, n_tok, max_n_kv)
+    need = qsa.qsa_tree_attention_workspace_bytes(n_seq, n_tok, max_n_kv)
 
     def buffers():
         return (torch.full((n_tok, 2, 2048), -7, dtype=torch.int32, device="cuda"), torch.zeros_like(want),
                 torch.empty(max(need, 1), dtype=torch.uint8, device="cuda"))
 
     def call(ids, out, ws):
-        qsa.qsa_tree_attention(dev["q"], dev["kq"], dev["vq"], dev["ksc"], dev["vsc"], n_pool, table, 2, n_tok, tree,
+        qsa.qsa_tree_attention(dev["q"], dev["kq"], dev["vq"], dev["ksc"], dev["vsc"], n_pool, table, n_seq, n_tok, tree,
                                max_n_kv, ids, out, ws)
 
     torch.cuda.synchronize()
