@@ -278,10 +278,10 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
   load(team, wa, sa);
   load(team + kTeams, wb, sb);
   if (kScaled) cluster_wait_all();  // the other CTA's barriers are initialised before the first remote arrive
-  for (int s = team; s < n_st; s += 2 * kTeams) {  // n_st is a multiple of 2 kTeams
+  for (int s = team; s < n_st; s += 2 * kTeams) {  // n_st is a multiple of kParts
     if (!store(s, wa, sa)) break;
     if (s + 2 * kTeams < n_st) load(s + 2 * kTeams, wa, sa);
-    if (!store(s + kTeams, wb, sb)) break;
+    if ((kParts % (2 * kTeams) && s + kTeams >= n_st) || !store(s + kTeams, wb, sb)) break;
     if (s + 3 * kTeams < n_st) load(s + 3 * kTeams, wb, sb);
   }
 }

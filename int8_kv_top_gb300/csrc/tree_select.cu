@@ -124,7 +124,9 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeBatch b, const
 }
 
 // ---------------------------------------------------------------- 2. score
-constexpr int kScoreThreads = 17 * 32;  // warps 0-7 producers (two teams), 8-15 epilogue (16 tokens each half), 16 MMA
+constexpr int kTeams = 4;            // of producers, four warps each: a stage of every tile each
+constexpr int kEpiWarp = 4 * kTeams, kMmaWarp = kEpiWarp + 8;  // epilogue (16 tokens each half of it), then MMA
+constexpr int kScoreThreads = (kMmaWarp + 1) * 32;
 constexpr int kOffB = kTileStages * kTileStageBytes;  // 4 dim blocks of [hi rows, lo rows][64] SW128
 constexpr int kBBlock = 2 * kTokChunk * 128;
 constexpr int kScoreSmem = kOffB + kNB * kBBlock + 1024;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ uint32_t s_mask[kTokChunk][kTreeWords];
-  __shared__ float s_scale[kTokChunk];  // sm_scale x the row's power of two; 0: not a selected token
+  __shared__ __align__(16) float s_scale[kTokChunk];  // sm_scale x the row's power of two; 0: not a selected token
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = blockIdx.y;
   pdl_begin();
@@ -177,10 +179,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   __syncthreads();
   const int n16 = (n_here + 15) / 16 * 16, N = 2 * n16;  // row n: hi of token n; row n16 + n: lo
 
-  if (warp < 8) {
+  if (warp < kEpiWarp) {
     const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0, 0u};
-    produce_tiles<kScoreCodes, 2>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp & 3, lane, warp >> 2);
-  } else if (warp == 16) {
+    produce_tiles<kScoreCodes, kTeams>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp & 3, lane, warp >> 2);
+  } else if (warp == kMmaWarp) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
     tc_fence_before();
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
     __syncwarp();
   } else {
-    const int et = tid - 256, quarter = warp & 3, n0 = 16 * ((warp - 8) >> 2);  // this warp's cells and tokens
+    const int et = tid - 32 * kEpiWarp, quarter = warp & 3, n0 = 16 * ((warp - kEpiWarp) >> 2);  // this warp's cells and tokens
     {
       // 16-byte chunk c of token r's hi | lo row: four rows' loads before any store.  Rows of tokens that do not
       // select were not written by tree_prep: what they hold only reaches their own scores, which are not stored.
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.b_full);
-    if (warp == 8) {  // lane = token: its mask and what its scores are multiplied by
+    if (warp == kEpiWarp) {  // lane = token: its mask and what its scores are multiplied by
       float km[kNB];
       warp_kmax(w, sq, g, n_scan, lane, km);
       int seen = pos0;
@@ -290,13 +292,26 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       if (n0 >= n16 || cell >= n_scan) continue;
       __half* dst = dst0 + cell;
       const bool drafted = (j_begin + j + 1) * kTileCells > pos0;
+      const float4* sc4 = reinterpret_cast<const float4*>(s_scale + n0);
+      float sc[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = sc4[i];
+        sc[4 * i] = x.x;
+        sc[4 * i + 1] = x.y;
+        sc[4 * i + 2] = x.z;
+        sc[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] *= sc[i];
+      if (drafted && dj >= 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!((s_mask[n0 + i][dj >> 5] >> (dj & 31)) & 1u)) acc[i] = -INFINITY;
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float sc = s_scale[n0 + i];
-        if (sc != 0.f) {  // the same for the whole warp
-          const bool seen = !drafted || dj < 0 || ((s_mask[n0 + i][dj >> 5] >> (dj & 31)) & 1u);
-          *dst = seen ? __float2half_rn(acc[i] * sc) : __ushort_as_half(0xFC00);
-        }
+        if (sc[i] != 0.f) *dst = __float2half_rn(acc[i]);  // the same for the whole warp
         dst += w.pitch;
       }
     }
@@ -304,7 +319,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
+  if (warp == kMmaWarp) tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
 }
 
 }  // namespace
