@@ -25,7 +25,7 @@
 //
 // 4 trees of 33-48 tokens after 30,000 cells, all of them attended to: 155 us, 0.40 of the measured bf16 rate over
 // the call; over the CTAs' own time the tensor pipe is 57% active.  0.45 instructions are issued a cycle and
-// scheduler; the MMA thread takes about 95 cycles an instruction (of 64 and 128 cycles of arithmetic), and a tile's
+// scheduler; the MMAs take about 95 cycles an instruction (of 64 and 128 cycles of arithmetic), and a tile's
 // softmax about 2,400.  The roles run at once, so the
 // loop bodies share the instruction cache: with separate K and V producer bodies a quarter of all stalls were
 // instruction fetches, and the call took 196 us.  A single S buffer with P kept apart (so that QK never waits on

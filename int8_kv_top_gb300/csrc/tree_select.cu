@@ -12,14 +12,14 @@
 //                 (A = the codes as fp16, made from int8 by producer warps as in tree.cu), N = the hi rows and
 //                 behind them the lo rows of up to 32 tokens, one TMEM accumulator per scale block.  An epilogue
 //                 thread owns a cell, so its four K scales are in registers.  Cells that a token does not see
-//                 score -inf.  An MMA of N = 64 takes about 52 cycles (A's 4 KB through shared memory), 16 of them a
-//                 tile; hi and lo in one N instead of two MMAs each halves their number.
+//                 score -inf.  A tile's 16 MMAs take about 100 cycles each, whatever N (A's 4 KB come from shared
+//                 memory); hi and lo in one N instead of two MMAs each halves their number.
 //  3. topk_kernel<V, true>.
 //
-// 24 trees of 1-32 tokens after 200-16,000 cells (414 tokens): prep 15, score 52, top-k 53, the attention 142 us, each
-// launched alone from a cold L2 (249 us as the call runs).  The score reads 88 MB; an SM spends about as long on
-// making the codes fp16 as on the epilogue's 4 x 32 accumulators a cell, so neither the tensor pipe (7%) nor
-// memory bounds it.
+// 24 trees of 1-32 tokens after 200-16,000 cells (414 tokens): prep 13, score 46, top-k 52, the attention 142 us, each
+// launched alone from a cold L2 (241 us as the call runs).  The score reads 88 MB; by a clock trace a tile takes
+// 2,400 cycles, 1,900 of them the issue of its MMAs, the rest between tiles; neither memory nor arithmetic (tensor 7%)
+// bounds it.  Two teams of producers and an epilogue that read each token's scale as it stored: 247 us.
 #include "select_math.cuh"
 #include "tree_common.cuh"
 
