@@ -281,13 +281,17 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t local, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
   return r;
 }
-// Relaxed arrive on another CTA's barrier.  Callers complete what they signal before the
-// arrive (tcgen05.wait::st for TMEM rows, or a local barrier phase for TMA-written tiles), and
-// the consumer is the pair's tensor core, which reads those operands through the async proxy;
-// a release at cluster scope here measured about a microsecond per arrive.
+// Relaxed arrive on another CTA's barrier, for TMEM rows (after tcgen05.wait::st) and for TMA-written
+// tiles (after a local barrier phase): both are complete before the arrive, and the consumer is the
+// pair's tensor core.  It orders no ordinary shared-memory store, neither the caller's nor another
+// thread's: those need fence_cluster() before it.  A release at cluster scope on each arrive instead
+// measured about a microsecond per arrive.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// What this thread wrote, or saw complete by a local barrier phase, comes before whatever another CTA of
+// the cluster does after it has acquired a relaxed arrive that follows this fence.
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                "r"(ncols)

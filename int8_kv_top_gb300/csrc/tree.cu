@@ -41,7 +41,8 @@
 //   warps 8-15   load Q; two softmax warpgroups, one row per thread in each, half of the columns each:
 //                mask, online softmax in base-2 units (running maximum and sum in fp32), P as fp16 into
 //                TMEM over S, lazy O rescale (only when the maximum grows by more than 2^8)
-//   warp 16      TMEM; rank 0 of the pair: MMA issue in the order QK(0), QK(1), PV(0), QK(2), PV(1), ...
+//   warp 16      TMEM; rank 1 of the pair: forwards its CTA's completed operand stages to rank 0's barriers
+//                rank 0: MMA issue in the order QK(0), QK(1), PV(0), QK(2), PV(1), ...
 //                  S = Q K^T  (A = Q K-major, B = K^ K-major)      M=256 N=128, 16 K-steps
 //                  O += P V^  (A = P from TMEM, B = V^ MN-major)   M=256 N=256, 8 K-steps
 //
@@ -97,8 +98,9 @@ struct DenseTreeArgs {
 };
 
 struct __align__(8) TreeBars {
-  // k_full, v_full, q_full, p_full: on rank 0 of the pair only, arrived on by the warps of both CTAs; the
-  // others receive the pair MMAs' commits in both CTAs
+  // k_full, v_full, q_full: arrived on by the warps of their own CTA, and on rank 0 once more when rank 1's
+  // phase is complete.  p_full: on rank 0 only, by the warps of both.  The others receive the pair MMAs' commits
+  // in both CTAs
   uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
   uint64_t s_full[kNS], p_full[kNS], pv_done[kNS];
   uint64_t q_full, tmem_ready, drain;
@@ -196,9 +198,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     // a lane a barrier, in the order of the members
     static_assert(sizeof(TreeBars) == (4 * kTileStages + 3 * kNS + 3) * 8 && sizeof(TreeBars) <= 32 * 8, "a lane a barrier");
     const int i = lane - 4 * kTileStages;
-    const uint32_t count = i < 0 ? ((lane / kTileStages) & 1 ? 1u : 8u)           // k_full, k_empty, v_full, v_empty
-                                 : i >= kNS && i < 2 * kNS || i == 3 * kNS ? 16u  // p_full, q_full
-                                                                           : 1u;  // s_full, pv_done, tmem_ready, drain
+    const uint32_t fwd = half ? 0u : 1u;  // rank 1's phase, forwarded
+    const uint32_t count = i < 0 ? ((lane / kTileStages) & 1 ? 1u : 4u + fwd)  // k_full, k_empty, v_full, v_empty
+                                 : i >= kNS && i < 2 * kNS ? 16u               // p_full
+                                 : i == 3 * kNS ? 8u + fwd                     // q_full
+                                                : 1u;                          // s_full, pv_done, tmem_ready, drain
     if (lane < (int)(sizeof(TreeBars) / 8)) mbar_init(reinterpret_cast<uint64_t*>(&bars) + lane, count);
     fence_mbar_init();
   }
@@ -247,13 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   bool ok = true;
 
   if (warp < 8) {
-    TileRun t{cell0, pos0, T, j_begin, J, g, s_union, &s_abort, a.status, half, 0u};
+    const TileRun t{cell0, pos0, T, j_begin, J, g, s_union, &s_abort, a.status, half};
     const bool is_v = warp >= 4;
-    uint64_t* full = is_v ? bars.v_full : bars.k_full;
-    t.remote_full = pair_addr(full);
-    produce_tiles<kPair>(t, is_v ? a.vq : a.kq, is_v ? a.vsc : a.ksc, smem_u32(smem + (is_v ? kOffV : kOffK)), full,
-                         is_v ? bars.v_empty : bars.k_empty, warp & 3, lane, 0, is_v);
-    if (J == 0) cluster_wait_all();  // #0, which the producers otherwise wait for before their first arrive
+    produce_tiles<kPair>(t, is_v ? a.vq : a.kq, is_v ? a.vsc : a.ksc, smem_u32(smem + (is_v ? kOffV : kOffK)),
+                         is_v ? bars.v_full : bars.k_full, is_v ? bars.v_empty : bars.k_empty, warp & 3, lane, 0, is_v);
+    cluster_wait_all();  // #0
   } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issue
     if (J > 0) {
@@ -314,6 +316,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       }
       umma2_commit(&bars.drain, (uint16_t)(1u << rank));  // everything issued completes before TMEM is released
       mbar_wait(&bars.drain, 0, a.status);
+    } else if (lane == 0 && J > 0) {
+      // rank 1: its operands to rank 0, in the order in which the MMAs take them.  Its warps stored them with
+      // ordinary stores; this thread acquires their local phases and releases them at cluster scope, with one fence
+      // a tile (about 0.7 us, and little of it shows: 4 dense trees 155 -> 156 us, 32 trees 66 -> 68; a releasing
+      // arrive a stage 213 and 83, and by the storing warps themselves, whose loads are in flight, 207 and 84).
+      auto stored = [&](uint64_t* full, int j) -> bool {  // tile j's stages
+        bool go = true;
+        for (int s = j * kParts; go && s < (j + 1) * kParts; ++s)
+          go = mbar_wait_poll<false>(&full[s % kTileStages], (s / kTileStages) & 1, a.status, &s_abort);
+        return go;
+      };
+      auto forward = [&](uint64_t* full, int j) {
+        for (int s = j * kParts; s < (j + 1) * kParts; ++s) mbar_arrive_cluster(pair_addr(&full[s % kTileStages]));
+      };
+      bool go = mbar_wait_poll<false>(&bars.q_full, 0, a.status, &s_abort) && stored(bars.k_full, 0);
+      for (int j = -1; go && j < J; ++j) {  // K of tile j + 1, V of tile j
+        if (j >= 0) go = (j + 1 == J || stored(bars.k_full, j + 1)) && stored(bars.v_full, j);
+        if (!go) break;
+        fence_cluster();
+        if (j < 0) mbar_arrive_cluster(pair_addr(&bars.q_full));
+        if (j + 1 < J) forward(bars.k_full, j + 1);
+        if (j >= 0) forward(bars.v_full, j);
+      }
     }
     __syncwarp();
   } else {
@@ -348,10 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       fence_proxy_async_smem();
       __syncwarp();
       cluster_wait_all();  // #0
-      if (lane == 0) {
-        if (half) mbar_arrive_cluster(pair_addr(&bars.q_full));
-        else mbar_arrive(&bars.q_full);
-      }
+      if (lane == 0) mbar_arrive(&bars.q_full);
     }
     uint32_t tmem = 0u;
     if (J > 0) {

@@ -194,7 +194,6 @@ struct TileRun {
   volatile int* abort;
   int* status;
   int half;              // rank within a CTA pair: which half of the tile's K cells and of V's dims is ours
-  uint32_t remote_full;  // rank 1 of a pair: rank 0's first full barrier (a shared::cluster address)
 };
 
 // Four producer warps that turn the tiles' int8 codes into fp16 operand stages of 16 KB, 128B-swizzled:
@@ -266,10 +265,7 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
     }
     fence_proxy_async_smem();  // this thread's part is visible to the tensor core before the arrive
     __syncwarp();
-    if (lane == 0) {
-      if (kScaled && t.half) mbar_arrive_cluster(t.remote_full + 8u * (uint32_t)slot);
-      else mbar_arrive(&full[slot]);
-    }
+    if (lane == 0) mbar_arrive(&full[slot]);  // of this CTA: rank 1 of a pair has its phases forwarded to rank 0
     return true;
   };
   if (n_st == 0) return;
@@ -277,7 +273,6 @@ __device__ __forceinline__ void produce_tiles(const TileRun& t, const int8_t* __
   uint16_t sa[4] = {}, sb[4] = {};
   load(team, wa, sa);
   load(team + kTeams, wb, sb);
-  if (kScaled) cluster_wait_all();  // the other CTA's barriers are initialised before the first remote arrive
   for (int s = team; s < n_st; s += 2 * kTeams) {  // n_st is a multiple of kParts
     if (!store(s, wa, sa)) break;
     if (s + 2 * kTeams < n_st) load(s + 2 * kTeams, wa, sa);

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const int n16 = (n_here + 15) / 16 * 16, N = 2 * n16;  // row n: hi of token n; row n16 + n: lo
 
   if (warp < kEpiWarp) {
-    const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0, 0u};
+    const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0};
     produce_tiles<kScoreCodes, kTeams>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp & 3, lane, warp >> 2);
   } else if (warp == kMmaWarp) {
     tmem_alloc(&s_tmem, 512);
