@@ -46,8 +46,9 @@
 //                  S = Q K^T  (A = Q K-major, B = K^ K-major)      M=256 N=128, 16 K-steps
 //                  O += P V^  (A = P from TMEM, B = V^ MN-major)   M=256 N=256, 8 K-steps
 //
-// Roundings below fp32: k^ and v^ (the values the library's prefill attends to), P (at most 2^8 after the
-// lazy rescale, so fp16 holds it with 11 bits), and the output; statistics and sums are fp32.
+// Roundings below fp32: k^ and v^ (the values the library's prefill attends to), P (11 bits for cells down to 21
+// binades below the row's running maximum, then fewer, none below 32: kPShift), and the output; statistics and
+// sums are fp32.
 //
 // TMEM columns (each CTA): O [0, 256), S/P buffers [256 + 128 b, 384 + 128 b), b = 0, 1.
 // Every mbarrier wait is bounded; after a timeout a CTA still meets the cluster's barriers.
@@ -76,6 +77,10 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 static_assert(kMaxTok <= 32, "a lane per token of the block");
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+// P is held as 2^(s - m + 7): at most 2^15 with the lazy maximum, so that fp16 keeps its 11 bits down to 21 binades
+// below the running maximum and something down to 32.  The sum takes the same factor, which cancels in O / l.
+constexpr float kPShift = 7.0f;
+static_assert(kRescaleThreshold + kPShift < 16.0f, "P stays below fp16's largest value");
 constexpr uint16_t kBoth = 0x3;
 
 struct DenseTreeArgs {
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
         }
       }
       const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
-      const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-m_use, -m_use);
+      const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(kPShift - m_use, kPShift - m_use);
       float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {

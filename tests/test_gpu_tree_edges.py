@@ -33,3 +33,37 @@ def test_many_calls_give_the_same_bits():
     torch.cuda.synchronize()
     qsa.qsa_check_device_status()
     assert all(torch.equal(o, first) for o in outs)
+
+
+@pytest.mark.parametrize("n,n_seq", [(2000, 1), (2000, 90), (9000, 76), (131072, 1)])
+@pytest.mark.parametrize("at", [0.0, 0.6, 1.0])
+@pytest.mark.parametrize("binades", [18.3, 22.6, 25.5, 28.0])
+def test_cells_far_below_the_largest(binades, at, n, n_seq):
+    # One cell with V = 0 (a sink), `binades` above all others: the output is the others' share alone, n 2^-binades of
+    # their mean.  A row's maximum is held as 2^7 or more, so an other cell's P is 2^(7 - binades) or more and off by at
+    # most 2^-25 (half of fp16's smallest step; 2^-11 of itself where that is more); sums of n in fp32 add n 2^-24, and
+    # 16 stands for the few roundings of a logit of 18 to 28 in fp32, in units of 2^-24 of it.  q.k^ and v^ are exact.
+    rng = np.random.default_rng(int(binades * 10))
+    ln2, sink = np.log(2.0), round(at * (n - 2))  # a cell before the drafted one
+    v = rng.integers(0, 65, (n, 2, 256)).astype(np.int8)
+    v[sink] = 0
+    dev = {"kq": torch.zeros(n, 2, 256, dtype=torch.int8, device="cuda"), "vq": torch.from_numpy(v).cuda(),
+           "ksc": torch.full((n, 2, 4), 2.0 ** -7, dtype=torch.float16, device="cuda"),
+           "vsc": torch.full((n, 2, 4), 0.5, dtype=torch.float16, device="cuda")}
+    dev["kq"][sink] = 64
+    dev["ksc"][sink] = binades * ln2 / (SCALE * 256 * 64)
+    q = torch.ones(n_seq, 24, 256, dtype=torch.float16, device="cuda")
+    seqs = torch.tensor([[0, n, n - 1, i] for i in range(n_seq)], dtype=torch.int32, device="cuda")
+    tree = torch.ones(n_seq, 1, dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(q)
+    params = (2048, 131072, SCALE)
+    need = qsa.qsa_tree_attention_workspace_bytes(n_seq, n_seq, n, params)
+    qsa.qsa_tree_attention(q, dev["kq"], dev["vq"], dev["ksc"], dev["vsc"], n, seqs, n_seq, n_seq, tree, n, None, out,
+                           torch.empty(max(need, 1), dtype=torch.uint8, device="cuda"), params=params)
+    qsa.qsa_check_device_status()
+    z = SCALE * 256 * 64 * float(dev["ksc"][sink, 0, 0])
+    want = np.repeat(0.5 * v.sum(0, dtype=np.float64) / (np.exp(z) + n - 1), 12, axis=0)
+    p = 2.0 ** (7 - z / ln2)
+    rel = max(2.0 ** -25 / p, 2.0 ** -11) + n * 2.0 ** -24 + 16 * z * 2.0 ** -24
+    off = np.abs(out.double().cpu().numpy() - want)
+    assert (off <= want * (rel + 2.0 ** -11) + 2.0 ** -25).all(), f"{(off / want).max():.3e} off, {rel:.3e} allowed"
