@@ -50,6 +50,7 @@
 // mbarrier waits on the bulk copies.
 #include "common.cuh"
 #include "select_math.cuh"
+#include "tree_common.cuh"
 
 namespace qsa {
 namespace {
@@ -229,15 +230,12 @@ __device__ __forceinline__ int block_scan(int v, int* s_red, int* total) {
 
 struct Seq {
   long long cell0;  // first pool cell of the sequence
-  int n_kv, tl;     // visible cells of this token, token index within its sequence
+  int n_kv, tl;     // causal cells of this token, token index within its sequence
   bool ok;
-  // trees: committed cells, drafted tokens of the sequence, and a sequence of no cells (padding)
-  int pos0, n_draft;
-  bool padding;
 };
 
 __device__ __forceinline__ Seq resolve_seq(const FusedArgs& a, int t) {
-  Seq s{0, 0, t, true, 0, 0, false};
+  Seq s{0, 0, t, true};
   if (a.seqs == nullptr) {
     s.n_kv = a.pos0 + t + 1;
     return s;
@@ -256,18 +254,7 @@ __device__ __forceinline__ Seq resolve_seq(const FusedArgs& a, int t) {
   // the sequence must hold its tokens' cells inside the pool
   s.ok = e.x >= 0 && e.y >= 1 && e.z >= 0 && e.w <= t && t < next && (long long)e.z + (next - e.w) <= e.y &&
          (long long)e.x + e.y <= a.n_pool;
-  s.pos0 = e.z;
-  s.n_draft = next - e.w;
-  s.padding = e.y == 0;
   return s;
-}
-
-// Word w of token t's tree mask, with the bits past the sequence's drafted tokens cleared.
-__device__ __forceinline__ uint32_t tree_word(const FusedArgs& a, int t, int w, int n_draft) {
-  const int left = n_draft - 32 * w;
-  if (w >= a.tree_words || left <= 0) return 0u;
-  const uint32_t m = __ldg(a.tree + (size_t)t * a.tree_words + w);
-  return left >= 32 ? m : m & ((1u << left) - 1u);
 }
 
 // kTree: the token's cells are scanned up to the sequence's last drafted cell, and those its mask
@@ -292,26 +279,37 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const int r = (int)cluster_ctarank();
   const int g = blockIdx.y, t = blockIdx.z;
   const Params p = a.p;
-  const Seq sq = resolve_seq(a, t);
-  int n_kv = sq.n_kv, n_scan = sq.n_kv;  // visible cells; cells the cluster divides among its CTAs
+  Seq sq{0, 0, 0, true};
+  int n_scan;    // cells the cluster divides among its CTAs, of which the token sees n_kv
+  int pos0 = 0;  // trees: committed cells
   __shared__ uint32_t s_tree[kTree ? kTreeWords : 1];
   if constexpr (kTree) {
-    if (sq.padding) return;
-    n_scan = sq.pos0 + sq.n_draft;
-    n_kv = sq.pos0;
+    const TreeBatch b{a.seqs, a.n_pool, a.n_seq, (int)gridDim.z, a.tree, a.tree_words, a.max_n_kv, p.identity_max};
+    const int s = warp_find_seq(b.n_seq, t, [&](int i) { return (long long)__ldg(&b.seqs[i].w); });
+    int4 e;
+    const int T = tree_seq_tokens(b, s, &e);
+    // padding, or a sequence that breaks the contract, which tree_dense_kernel has flagged (uniform over the cluster)
+    if (T <= 0 || t < e.w || t >= e.w + T) return;
+    sq.cell0 = e.x;
+    sq.n_kv = pos0 = e.z;
+    n_scan = e.z + T;
     for (int w = 0; w < kTreeWords; ++w) {
-      const uint32_t m = sq.ok ? tree_word(a, t, w, sq.n_draft) : 0u;
-      n_kv += __popc(m);
+      const uint32_t m = tree_mask_word(b, t, w, T);
+      sq.n_kv += __popc(m);
       if (tid == w) s_tree[w] = m;
     }
+  } else {
+    sq = resolve_seq(a, t);
+    n_scan = sq.n_kv;
   }
+  const int n_kv = sq.n_kv;
   // cell c of the sequence is visible to this token
   auto visible = [&](int c) -> bool {
     if constexpr (!kTree) return true;
-    const int dj = c - sq.pos0;
+    const int dj = c - pos0;
     return dj < 0 || ((s_tree[dj >> 5] >> (dj & 31)) & 1u) != 0u;
   };
-  if (!sq.ok || n_scan > C * kMaxW || (kTree && (sq.n_draft > 32 * a.tree_words || n_scan > a.max_n_kv))) {  // uniform over the cluster: nobody touches another CTA
+  if (!sq.ok || n_scan > C * kMaxW) {  // uniform over the cluster: nobody touches another CTA
     if (tid == 0 && r == 0) set_dev_status(a.status, QSA_DEV_BAD_ID);
     return;
   }

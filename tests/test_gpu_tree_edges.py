@@ -67,3 +67,26 @@ def test_cells_far_below_the_largest(binades, at, n, n_seq):
     rel = max(2.0 ** -25 / p, 2.0 ** -11) + n * 2.0 ** -24 + 16 * z * 2.0 ** -24
     off = np.abs(out.double().cpu().numpy() - want)
     assert (off <= want * (rel + 2.0 ** -11) + 2.0 ** -25).all(), f"{(off / want).max():.3e} off, {rel:.3e} allowed"
+
+
+@pytest.mark.parametrize("path,n", [("clusters", 3), ("together", 20)])  # few tokens a sequence, and many
+@pytest.mark.parametrize("how", ["first row", "next row"])
+def test_first_rows_that_break_the_table(how, path, n):
+    # the table's first sequence starts behind row 0; a sequence's tokens end behind the call's rows.  Either is
+    # skipped and flagged, whichever way the selected tokens would have taken
+    pool, seqs = make_batch([(2200, n), (2300, n)], seed=42, slack=40)
+    bad = seqs.copy()
+    if how == "first row":
+        bad[0, 3], skipped, kept = 1, slice(0, n), range(n, 2 * n)
+    else:
+        bad = np.concatenate([seqs, [[0, 50, 10, 2 * n + 5]]]).astype(np.int32)
+        skipped, kept = slice(n, 2 * n), range(n)
+    ids, out = run_tree(pool, bad, max_n_kv=2400)
+    with pytest.raises(qsa.QSAError) as e:
+        qsa.qsa_check_device_status()
+    assert e.value.code == qsa.QSA_ERR_DEVICE
+    assert torch.isnan(out[skipped]).all() and (ids[skipped] == -7).all()
+    ref, ref_ids, bound = reference(pool, seqs, rows=set(kept))
+    use = list(kept)
+    assert (np.abs(out.double().cpu().numpy()[use] - ref[use]) <= bound[use]).all()
+    np.testing.assert_array_equal(ids.cpu().numpy()[use], ref_ids[use])
