@@ -257,8 +257,9 @@ __device__ __forceinline__ Seq resolve_seq(const FusedArgs& a, int t) {
   return s;
 }
 
-// kTree: the token's cells are scanned up to the sequence's last drafted cell, and those its mask
-// leaves out are skipped everywhere: not scored, not counted, no candidates, never gathered.
+// kTree: the selected tokens of drafted trees (the others are left to tree_dense_kernel).  A token's cells are
+// scanned up to the sequence's last drafted cell, and those its mask leaves out are skipped everywhere: not
+// scored, not counted, no candidates, never gathered.
 template <int C, bool kTree>
 __global__ void __launch_bounds__(kFThreads, 1)
     decode_fused_kernel(const FusedArgs a, const __grid_constant__ CUtensorMap tm_codes,
@@ -313,8 +314,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
     if (tid == 0 && r == 0) set_dev_status(a.status, QSA_DEV_BAD_ID);
     return;
   }
-  const bool selected = n_kv > p.identity_max;
-  if (!selected && (a.selected_only || a.ids_only)) return;  // uniform over the cluster, before any cluster barrier
+  const bool all_cells = n_kv <= p.identity_max, selected = kTree || !all_cells;
+  if (all_cells && (kTree || a.selected_only || a.ids_only)) return;  // uniform over the cluster, before any cluster barrier
   const int K = p.topk;
   const int W = (n_scan + C - 1) / C;
   const int c_lo = r * W, c_hi = min(n_scan, c_lo + W), nloc = max(0, c_hi - c_lo);
@@ -374,30 +375,6 @@ __global__ void __launch_bounds__(kFThreads, 1)
   }
 
   int n_sel = nloc;  // identity: every owned cell
-  // ascending list (s_list) of the owned cells whose status byte is 1
-  auto list_kept = [&]() {
-    constexpr int kPerT = kMaxW / kFThreads;  // 16 consecutive cells per thread
-    static_assert(kPerT == 16, "one 16-byte status read per thread");
-    const int i0 = tid * kPerT;
-    uint32_t keep = 0;  // bit u: cell i0 + u is kept
-    if (i0 < nloc) {
-      const uint4 w = *reinterpret_cast<const uint4*>(s_stat + i0);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int u = 0; u < kPerT; ++u)
-        if (i0 + u < nloc && ((ww[u >> 2] >> (8 * (u & 3))) & 0xFFu) == 1u) keep |= 1u << u;
-    }
-    int total;
-    int off = block_scan(__popc(keep), s_red, &total);
-    while (keep) {
-      const int u = __ffs(keep) - 1;
-      keep &= keep - 1;
-      s_list[off++] = (uint16_t)(i0 + u);
-    }
-    if (tid == 0) s_nlist = total;
-    __syncthreads();
-    n_sel = s_nlist;
-  };
   if (selected) {
     long long* s_qsum = reinterpret_cast<long long*>(sm + kOffQsum);
     __half* s_hl = reinterpret_cast<__half*>(sm + kOffHL);
@@ -782,7 +759,30 @@ __global__ void __launch_bounds__(kFThreads, 1)
       cluster_wait();
     }
     __syncthreads();
-    list_kept();
+    // ---- ascending list of the kept owned cells
+    {
+      constexpr int kPerT = kMaxW / kFThreads;  // 16 consecutive cells per thread
+      static_assert(kPerT == 16, "one 16-byte status read per thread");
+      const int i0 = tid * kPerT;
+      uint32_t keep = 0;  // bit u: cell i0 + u is kept
+      if (i0 < nloc) {
+        const uint4 w = *reinterpret_cast<const uint4*>(s_stat + i0);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int u = 0; u < kPerT; ++u)
+          if (i0 + u < nloc && ((ww[u >> 2] >> (8 * (u & 3))) & 0xFFu) == 1u) keep |= 1u << u;
+      }
+      int total;
+      int off = block_scan(__popc(keep), s_red, &total);
+      while (keep) {
+        const int u = __ffs(keep) - 1;
+        keep &= keep - 1;
+        s_list[off++] = (uint16_t)(i0 + u);
+      }
+      if (tid == 0) s_nlist = total;
+      __syncthreads();
+      n_sel = s_nlist;
+    }
     if (a.ids_only) {  // uniform: the kept counts to every CTA, then the ids; no attention
       if (tid < C) st_cluster_u32(mapa_shared(smem_u32(&s_nsel_all[r]), tid), (uint32_t)n_sel);
       cluster_arrive();
@@ -793,14 +793,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
   } else {
     // identity: the V rows to L2 while the first batch is set up
-    for (int i = tid; i < nloc; i += kFThreads) {
-      prefetch_l2_256(vq + ((size_t)(c_lo + i) * kGroups + g) * kD);
-      if constexpr (kTree) s_stat[i] = visible(c_lo + i) ? 1 : 0;
-    }
-    if constexpr (kTree) {
-      __syncthreads();
-      list_kept();
-    }
+    for (int i = tid; i < nloc; i += kFThreads) prefetch_l2_256(vq + ((size_t)(c_lo + i) * kGroups + g) * kD);
   }
 
   // ---- 4. attention over the kept owned cells, batches of 64 (bulk copies, two stages)
@@ -814,7 +807,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const int nb = (n_sel + kBatch - 1) / kBatch;
     __half* s_vh = reinterpret_cast<__half*>(sm + kOffVh);
     __half* s_p = reinterpret_cast<__half*>(sm + kOffP);
-    auto cell_of = [&](int i) -> int { return c_lo + (selected || kTree ? (int)s_list[i] : i); };
+    auto cell_of = [&](int i) -> int { return c_lo + (selected ? (int)s_list[i] : i); };
     // cp.async of the batch's K and V rows (16 bytes a piece, 16 pieces a row) and scale lines
     auto issue = [&](int bi) {
       if (bi < nb) {
@@ -1025,7 +1018,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       L = fmaf(r_l[qq * 12 + h], w, L);
       O = fmaf(r_o[qq * kPerCta + e], w, O);
     }
-    float v = kTree && L == 0.f ? 0.f : O / L;  // a mask may leave a token no cell at all
+    float v = O / L;
     if (a.gate) v *= gate_sigmoid(__half2float(a.gate[((size_t)t * kHeads + g * kHPG + h) * kD + d]));
     const size_t o = ((size_t)t * kHeads + g * kHPG + h) * kD + d;
     if (a.out16) a.out16[o] = __float2half_rn(v);

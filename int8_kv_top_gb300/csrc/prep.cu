@@ -260,14 +260,14 @@ __device__ __forceinline__ float warp_sum4(const float (&v)[4], int lane) {
 
 // The quantiser of one 256-element row (fp16 values) held in two 4-dim runs a lane, at dims a and b.  Eight
 // lanes' runs never leave a 64-element block pair, so the block maxima take 8 shuffles: over 8 lanes, and over
-// 16 where the block is that wide (wide_a, wide_b); `one` says that both runs lie in one block.
+// 16 where the block is that wide (`wide`); `one` says that both runs lie in one block.
 //
 // code = round-half-away(fp32(x / s)) is formed without a division: with x and s fp16 and |h| <= 127.5 a half
 // integer, x - h s is a multiple of half the smaller step of the two, so x / s is either exactly h or at least
 // 2^-12 away from it (also for subnormal s: multiples of 2^-25 against s < 2^-14).  The quotient by an
 // approximate reciprocal is within 2^-15, so adding 1/2 + 2^-13 before truncating decides every case as the
 // correctly rounded quotient does.
-__device__ __forceinline__ void quantize_row_fast(const float2 (&x)[4], int a, int b, bool wide_a, bool wide_b, bool one,
+__device__ __forceinline__ void quantize_row_fast(const float2 (&x)[4], int a, int b, bool wide, bool one,
                                                   int8_t* codes, __half* scales) {
   float ma = fmaxf(fmaxf(fabsf(x[0].x), fabsf(x[0].y)), fmaxf(fabsf(x[1].x), fabsf(x[1].y)));
   float mb = fmaxf(fmaxf(fabsf(x[2].x), fabsf(x[2].y)), fmaxf(fabsf(x[3].x), fabsf(x[3].y)));
@@ -278,8 +278,8 @@ __device__ __forceinline__ void quantize_row_fast(const float2 (&x)[4], int a, i
     mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
   }
   const float ma8 = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 8)), mb8 = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 8));
-  ma = wide_a ? ma8 : ma;
-  mb = wide_b ? mb8 : mb;
+  ma = wide ? ma8 : ma;
+  mb = wide ? mb8 : mb;
   const __half ha = __float2half_rn(__fdiv_rn(ma, 127.0f)), hb = __float2half_rn(__fdiv_rn(mb, 127.0f));
   const float fa = __half2float(ha), fb = __half2float(hb);
   const float ra = fa != 0.f ? __fdividef(1.f, fa) : 0.f, rb = fb != 0.f ? __fdividef(1.f, fb) : 0.f;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps, kWarps == 1 ?
       if (is_kv) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          quantize_row_fast(x[j], da, db, wide, wide, one, (j < 2 ? kq : vq) + ((size_t)cell * kGroups + (j & 1)) * kD,
+          quantize_row_fast(x[j], da, db, wide, one, (j < 2 ? kq : vq) + ((size_t)cell * kGroups + (j & 1)) * kD,
                             (j < 2 ? ksc : vsc) + ((size_t)cell * kGroups + (j & 1)) * kNB);
       }
     }

@@ -167,11 +167,10 @@ __device__ __forceinline__ void tree_plan_blocks(const TreeBatch& b, bool with_s
 // code has to fit the SM's instruction cache together.  A failed probe suspends the thread for up to
 // kSuspendHintNs, so kWaitProbes of them take at most about two seconds.
 constexpr int kWaitProbes = 1000000;
-template <bool kCluster = false>
 __device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
 #pragma unroll 1
   for (int it = 0; it < kWaitProbes; ++it) {
-    if (mbar_try_wait<kCluster>(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
   }
   set_dev_status(status, QSA_DEV_WAIT_TIMEOUT);
