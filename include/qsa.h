@@ -372,7 +372,10 @@ QSA_API int qsa_cache_read(const int8_t* kq, const uint16_t* ksc, const int8_t* 
                            const int32_t* cells, int64_t n, uint16_t* k16, uint16_t* v16, void* stream);
 
 /*
- * Bytes of device workspace qsa_tree_attention needs (0 when it needs none or for invalid arguments).
+ * Bytes of device workspace qsa_tree_attention needs (0 when it needs none or for invalid arguments).  For
+ * given params it grows with each of n_seq, n_tok and max_n_kv, so a workspace for a server's largest values
+ * serves every call of smaller ones.  It is at most 430 MB for the parts of an attention that is split over
+ * the GPU, and, where 8 tokens or more may select, 2 n_tok rows of 2.2 bytes a cell (up to 65,536 cells).
  */
 QSA_API size_t qsa_tree_attention_workspace_bytes(int n_seq, int n_tok, int max_n_kv, const qsa_params* params);
 

@@ -1,6 +1,7 @@
 // C ABI of the QSA layer: argument validation, the device status word, the per-thread
 // last-error string, and dispatch to the kernel launchers.  Declarations and the
 // contract of every entry point are in include/qsa.h.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -573,9 +574,11 @@ int qsa_cache_read(const int8_t* kq, const uint16_t* ksc, const int8_t* vq, cons
 size_t qsa_tree_attention_workspace_bytes(int n_seq, int n_tok, int max_n_kv, const qsa_params* params) {
   qsa::Params p{};
   if (n_seq < 1 || n_tok < 1 || max_n_kv < 1 || resolve_params(params, &p) != QSA_OK) return 0;
-  const bool together = tree_selects_together(n_seq, n_tok, max_n_kv, p);
-  return qsa::tree_dense_workspace_bytes(n_seq, n_tok, max_n_kv, p.identity_max, together) +
-         (together ? qsa::tree_select_layout(n_seq, n_tok, max_n_kv, nullptr, nullptr) : 0);
+  // Selecting together takes its part where this call or a smaller one (all tokens in one sequence, fewer cells) does.
+  const int cells = std::min(max_n_kv, qsa::select_max_cells());
+  const bool together = tree_selects_together(1, n_tok, cells, p);
+  return qsa::tree_dense_workspace_bytes(n_seq, n_tok, max_n_kv) +
+         (together ? qsa::tree_select_layout(n_seq, n_tok, cells, nullptr, nullptr) : 0);
 }
 
 int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, const uint16_t* ksc, const uint16_t* vsc,
@@ -628,9 +631,9 @@ int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, co
   if (together) {
     qsa::tree_select_layout(n_seq, n_tok, max_n_kv,
                             static_cast<uint8_t*>(ws) +
-                                qsa::tree_dense_workspace_bytes(n_seq, n_tok, max_n_kv, p.identity_max, true),
+                                qsa::tree_dense_workspace_bytes(n_seq, n_tok, max_n_kv),
                             &w);
-    e = qsa::launch_tree_select(b, w, hq, kq, hksc, ids, qsa::tree_dense_plan(b, true, ws), p, st, s);
+    e = qsa::launch_tree_select(b, w, hq, kq, hksc, ids, qsa::tree_dense_plan(b, ws), p, st, s);
     if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_attention (selection) launch");
   }
   e = qsa::launch_tree_dense(b, hq, kq, vq, hksc, hvsc, w.bits, w.pitch / 32, hg, hout, ws, p.sm_scale, st, s);

@@ -151,8 +151,8 @@ cudaError_t launch_tree_topk(const TreeBatch& b, const TreeSelect& w, const __ha
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                               const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
                               void* ws, float sm_scale, int* status, cudaStream_t stream);
-int4* tree_dense_plan(const TreeBatch& b, bool with_selected, void* ws);  // where its list of blocks goes, or null
-size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected);
+int4* tree_dense_plan(const TreeBatch& b, void* ws);  // where its list of blocks goes, or null
+size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv);  // grows with each argument
 
 // Output gate: the elementwise logistic function of the gate input, in fp32, 1 / (1 + e^-x).  The
 // exponential takes the special-function unit; the reciprocal of d = 1 + e^-x (d >= 1, and finite

@@ -742,9 +742,25 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
 //    8 trees of 16 after 30,000               624 364 275 323 291 320      374 241 289 238 259 260 315
 //   12 trees of 61 after  8,192               285 305 373 385 470 465      337 366 393 425 453 534 760
 //   24 trees of 1-32 after 200-16,000         352 247 264 304 378 362      265 281 298   -  348   -   -
+//
+// Several pairs to a block write unmerged parts, 264 KB a pair.  What a call may write is bounded by its arguments
+// alone, in a way that grows with each of them (parts_most), so that a workspace for a server's largest batch serves
+// every smaller one: the plans above stay inside it but for a few that gain under 5%.
 struct DensePlan {
   int blocks, pairs, runs;
 };
+constexpr int kFewPairs = 480, kMostPairs = 1600;
+
+int plan_tiles(long long cells) { return (int)((cells + kTileCells - 1) / kTileCells); }
+
+// Pairs that may write parts in a call.
+long long parts_most(int n_seq, int n_tok, int max_n_kv) {
+  const long long blocks = tree_blocks_most(n_seq, n_tok);
+  const int tiles = plan_tiles(max_n_kv);
+  if (tiles < 2) return 0;
+  return std::min(blocks * kGroups * std::min(kMaxRuns, tiles + 1),
+                  std::min<long long>(kMostPairs, std::max<long long>(kFewPairs, 4 * blocks)));
+}
 constexpr double kJoinBlock = 0.2, kJoinPart = 0.02;  // tree_join_kernel's time a block and group, and a part of it
 constexpr int kSizes[7] = {1, 2, 3, 4, 5, 6, 8};
 constexpr int kHeld[7] = {76, 36, 23, 15, 13, 8, 7};
@@ -756,7 +772,9 @@ DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool 
   const long long spread =
       n_seq == 1 ? even : std::max<long long>(n_seq, (rows + kTreeBlock / 2 * (long long)n_seq + kTreeBlock - 1) / kTreeBlock);
   const long long longest = with_selected ? max_n_kv : std::min<long long>(max_n_kv, (long long)identity_max + 32 * kTreeWords);
-  const int tiles = (int)((longest + kTileCells - 1) / kTileCells);
+  const int tiles = plan_tiles(longest);
+  const long long most = parts_most(n_seq, n_tok, max_n_kv);
+  auto fits = [&](int split) { return split == 1 || (long long)d.blocks * kGroups * split <= most; };
   auto waves = [&](double a_cluster, int held) {  // of `a_cluster` clusters a block and group
     const double we = (double)(even * kGroups) * a_cluster / held, ws = (double)(spread * kGroups) * a_cluster / held;
     if (n_seq == 1) return std::ceil(we);
@@ -765,6 +783,7 @@ DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool 
   double best_t = 0.0;
   for (int i = 0; i < 7; ++i) {
     const int S = kSizes[i];
+    if (!fits(S)) break;
     const double t = waves(1.0, kHeld[i]) * ((S == 1 ? 5.0 : 6.0 + 0.1 * S) + (tiles + S - 1) / S);
     if (i == 0 || t < best_t) {
       d.pairs = S;
@@ -772,7 +791,7 @@ DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool 
     }
   }
   const double clusters = 0.5 * (double)((even + spread) * kGroups);
-  for (int runs = 2; runs <= std::min(kMaxRuns, tiles) && runs * clusters <= 4 * kHeld[0]; ++runs) {
+  for (int runs = 2; runs <= std::min(kMaxRuns, tiles) && runs * clusters <= 4 * kHeld[0] && fits(runs); ++runs) {
     const double t = waves(runs, kHeld[0]) * (5.0 + (tiles + runs - 1) / runs) + 2.5 + (kJoinBlock + kJoinPart * runs) * clusters;
     if (t < best_t) {
       d.pairs = 1;
@@ -818,23 +837,21 @@ cudaError_t tree_setup() {
 }  // namespace
 
 namespace {
-size_t part_rows(const DensePlan& d) {  // rows of the unmerged parts
-  return d.pairs * d.runs == 1 ? 0 : (size_t)d.blocks * kGroups * 2 * d.pairs * d.runs * kRows;
-}
-size_t part_bytes(const DensePlan& d) {
-  return part_rows(d) * (kD * sizeof(float) + (d.runs > 1 ? sizeof(float2) : 0));
+// Rows of the unmerged parts, [kD] floats and a float2 (m, l) each, at the start of the workspace.
+size_t part_rows(int n_seq, int n_tok, int max_n_kv) { return (size_t)parts_most(n_seq, n_tok, max_n_kv) * 2 * kRows; }
+size_t part_bytes(int n_seq, int n_tok, int max_n_kv) {
+  return part_rows(n_seq, n_tok, max_n_kv) * (kD * sizeof(float) + sizeof(float2));
 }
 }  // namespace
 
-size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
-  const DensePlan d = dense_plan(n_seq, n_tok, max_n_kv, identity_max, with_selected);
-  return part_bytes(d) + (n_seq >= kPlanSeqs ? ((1 + 2 * (size_t)d.blocks) * sizeof(int4) + 255) / 256 * 256 : 0);
+size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv) {
+  const size_t list = (1 + 2 * (size_t)tree_blocks_most(n_seq, n_tok)) * sizeof(int4);
+  return part_bytes(n_seq, n_tok, max_n_kv) + (n_seq >= kPlanSeqs ? (list + 255) / 256 * 256 : 0);
 }
 
-int4* tree_dense_plan(const TreeBatch& b, bool with_selected, void* ws) {
+int4* tree_dense_plan(const TreeBatch& b, void* ws) {
   if (b.n_seq < kPlanSeqs) return nullptr;
-  return reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) +
-                                 part_bytes(dense_plan(b.n_seq, b.n_tok, b.max_n_kv, b.identity_max, with_selected)));
+  return reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + part_bytes(b.n_seq, b.n_tok, b.max_n_kv));
 }
 
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
@@ -843,14 +860,14 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
   cudaError_t e = tree_setup();
   if (e != cudaSuccess) return e;
   const DensePlan d = dense_plan(b.n_seq, b.n_tok, b.max_n_kv, b.identity_max, bits != nullptr);
-  int4* plan = tree_dense_plan(b, bits != nullptr, ws);
+  int4* plan = tree_dense_plan(b, ws);
   if (plan && !bits) {  // with selected tokens the selection's first launch has made it
     e = launch_pdl(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, b, plan);
     if (e != cudaSuccess) return e;
   }
   const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, plan,
                         static_cast<float*>(ws),
-                        d.runs > 1 ? reinterpret_cast<float2*>(static_cast<float*>(ws) + part_rows(d) * kD) : nullptr,
+                        reinterpret_cast<float2*>(static_cast<float*>(ws) + part_rows(b.n_seq, b.n_tok, b.max_n_kv) * kD),
                         d.runs, status};
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = tree_config(d.pairs, d.blocks * kGroups * d.runs, stream, attr);

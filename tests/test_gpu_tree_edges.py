@@ -90,3 +90,27 @@ def test_first_rows_that_break_the_table(how, path, n):
     use = list(kept)
     assert (np.abs(out.double().cpu().numpy()[use] - ref[use]) <= bound[use]).all()
     np.testing.assert_array_equal(ids.cpu().numpy()[use], ref_ids[use])
+
+
+@pytest.mark.parametrize("params", [None, (2048, 131072, SCALE)])
+def test_one_workspace_for_every_smaller_call(params):
+    # the workspace of a server's largest batch, between guards, serves calls of all kinds; each writes inside what its
+    # own query says
+    calls = [[(1950, 8)] * 16, [(9000, 5)] * 3, [(16000, 16)], [(700, 30), (4000, 9), (0, 1)], [(300, 4)] * 40, [(2500, 2)] * 5]
+    whole = qsa.qsa_tree_attention_workspace_bytes(40, 160, 16016, params)
+    ws = torch.full((whole + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    for i, specs in enumerate(calls):
+        pool, seqs = make_batch(specs, seed=70 + i)
+        n_tok, max_n_kv = pool["q"].shape[0], max(p + n for p, n in specs)
+        need = qsa.qsa_tree_attention_workspace_bytes(len(specs), n_tok, max_n_kv, params)
+        assert need <= whole
+        ws.fill_(0x5A)
+        dev = {k: torch.from_numpy(v).cuda() for k, v in pool.items() if k != "tree"}
+        out = torch.zeros(n_tok, 24, 256, dtype=torch.float16, device="cuda")
+        qsa.qsa_tree_attention(dev["q"], dev["kq"], dev["vq"], dev["ksc"], dev["vsc"], len(pool["kq"]),
+                               torch.from_numpy(seqs).cuda(), len(specs), n_tok, torch.from_numpy(pool["tree"].view(np.int32)).cuda(),
+                               max_n_kv, None, out, ws[:whole], params=params)
+        qsa.qsa_check_device_status()
+        assert (ws[need:] == 0x5A).all()
+        ref, _, bound = reference(pool, seqs, *(params or (2048, 2051, SCALE)))
+        assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all(), specs
