@@ -52,9 +52,7 @@
 //
 // TMEM columns (each CTA): O [0, 256), S/P buffers [256 + 128 b, 384 + 128 b), b = 0, 1.
 // Every mbarrier wait is bounded; after a timeout a CTA still meets the cluster's barriers.
-#include <algorithm>
 #include <atomic>
-#include <cmath>
 
 #include "tree_common.cuh"
 
@@ -65,9 +63,8 @@ constexpr int kRows = kTreeBlock / 2;       // (token, head) rows of a CTA, 256 
 constexpr int kParts = 2;                   // ring stages per tile and operand
 constexpr int kMaxTok = (2 * kRows + kHPG - 2) / kHPG + 1;  // tokens a block's rows may touch
 constexpr int kThreads = 17 * 32;
-constexpr int kMaxS = 8;                    // pairs of a cluster at most
+constexpr int kMaxS = kPlanSizes[kPlanSizesN - 1];  // pairs of a cluster at most
 constexpr int kNS = 2;
-constexpr int kMaxRuns = 38;                // clusters of one pair that a block and group may share: half of the GPU's
 constexpr int kOffK = 0, kOffV = kTileStages * kTileStageBytes, kOffQ = 2 * kTileStages * kTileStageBytes;
 constexpr int kOffML = kOffQ + kRows * kD * 2;          // float2 (m, l) [kMaxS][kRows], pushed by every pair
 constexpr int kSmem = kOffML + kMaxS * kRows * 8 + 1024;  // + alignment slack
@@ -75,6 +72,9 @@ constexpr int kOStride = kD + 4;            // floats per staged output row: 16 
 static_assert(kRows * kOStride * 4 <= kOffML, "the staged rows fit over the operand tiles");
 static_assert(kSmem <= 227 * 1024, "shared memory");
 static_assert(kMaxTok <= 32, "a lane per token of the block");
+static_assert(kPlanRows == kTreeBlock && kPlanCells == kTileCells && kPlanHeads == kHPG && kPlanGroups == kGroups &&
+                  kPlanDrafted == 32 * kTreeWords && 2 * kMaxS <= 16,
+              "the plan's sizes are this kernel's");
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 // P is held as 2^(s - m + 7): at most 2^15 with the lazy maximum, so that fp16 keeps its 11 bits down to 21 binades
@@ -725,83 +725,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
   }
 }
 
-// How a call is cut: blocks (grid indices; a ragged batch leaves about half a block a sequence unused), and for each
-// block and group either one cluster of `pairs` pairs that merge in it, or `runs` clusters of one pair whose parts
-// tree_join_kernel joins.  A launch takes about waves x (a fixed part + the tiles of a pair), in units of one tile's
-// time (1.7 us; fixed: 8 us for one pair, 10 to 12 with a merge in the cluster), and the join its own time by the
-// blocks and their parts.  A wave is as many clusters of that size as a GB300 holds at once (a cluster stays inside a
-// GPC).  How many tokens and cells a sequence has is on the device, so waves is the mean of what equal and spread
-// sequences give, each with equal and with spread lengths: the blocks of equal sequences rounded up, or half a block
-// of rounding a sequence; whole waves, or 0.9 of a wave for every filling of the GPU.  Measured (us a call):
-//                                         pairs 1   2   3   5   6   8     runs 2   4   6   9  12  19  38
-//    1 tree  of 61 after  1,984 cells          38  27  23  20  19  16       28  22  21  20  20  29  29
-//    1 tree  of 16 after  8,192               156 100  79  62  58  53       98  69  58  52  48  46  44
-//    1 tree  of 16 after 30,000               490 275 200 141 127 106      274 159 123 100  88  76  68
-//    2 trees of 61 after 30,000               539 317 237 173 248 209      321 203 166 199 176 189 235
-//    4 trees of 44 after 30,000               597 361 444 323 385 388      371 372 300 308 315 340 406
-//    8 trees of 16 after 30,000               624 364 275 323 291 320      374 241 289 238 259 260 315
-//   12 trees of 61 after  8,192               285 305 373 385 470 465      337 366 393 425 453 534 760
-//   24 trees of 1-32 after 200-16,000         352 247 264 304 378 362      265 281 298   -  348   -   -
-//
-// Several pairs to a block write unmerged parts, 264 KB a pair.  What a call may write is bounded by its arguments
-// alone, in a way that grows with each of them (parts_most), so that a workspace for a server's largest batch serves
-// every smaller one: the plans above stay inside it but for a few that gain under 5%.
-struct DensePlan {
-  int blocks, pairs, runs;
-};
-constexpr int kFewPairs = 480, kMostPairs = 1600;
-
-int plan_tiles(long long cells) { return (int)((cells + kTileCells - 1) / kTileCells); }
-
-// Pairs that may write parts in a call.
-long long parts_most(int n_seq, int n_tok, int max_n_kv) {
-  const long long blocks = tree_blocks_most(n_seq, n_tok);
-  const int tiles = plan_tiles(max_n_kv);
-  if (tiles < 2) return 0;
-  return std::min(blocks * kGroups * std::min(kMaxRuns, tiles + 1),
-                  std::min<long long>(kMostPairs, std::max<long long>(kFewPairs, 4 * blocks)));
-}
-constexpr double kJoinBlock = 0.2, kJoinPart = 0.02;  // tree_join_kernel's time a block and group, and a part of it
-constexpr int kSizes[7] = {1, 2, 3, 4, 5, 6, 8};
-constexpr int kHeld[7] = {76, 36, 23, 15, 13, 8, 7};
-
-DensePlan dense_plan(int n_seq, int n_tok, int max_n_kv, int identity_max, bool with_selected) {
-  DensePlan d{tree_blocks_most(n_seq, n_tok), 1, 1};
-  const long long rows = (long long)n_tok * kHPG;
-  const long long even = n_seq * ((rows + (long long)n_seq * kTreeBlock - 1) / ((long long)n_seq * kTreeBlock));
-  const long long spread =
-      n_seq == 1 ? even : std::max<long long>(n_seq, (rows + kTreeBlock / 2 * (long long)n_seq + kTreeBlock - 1) / kTreeBlock);
-  const long long longest = with_selected ? max_n_kv : std::min<long long>(max_n_kv, (long long)identity_max + 32 * kTreeWords);
-  const int tiles = plan_tiles(longest);
-  const long long most = parts_most(n_seq, n_tok, max_n_kv);
-  auto fits = [&](int split) { return split == 1 || (long long)d.blocks * kGroups * split <= most; };
-  auto waves = [&](double a_cluster, int held) {  // of `a_cluster` clusters a block and group
-    const double we = (double)(even * kGroups) * a_cluster / held, ws = (double)(spread * kGroups) * a_cluster / held;
-    if (n_seq == 1) return std::ceil(we);
-    return 0.25 * (std::ceil(we) + std::max(1.0, 0.9 * we) + std::ceil(ws) + std::max(1.0, 0.9 * ws));
-  };
-  double best_t = 0.0;
-  for (int i = 0; i < 7; ++i) {
-    const int S = kSizes[i];
-    if (!fits(S)) break;
-    const double t = waves(1.0, kHeld[i]) * ((S == 1 ? 5.0 : 6.0 + 0.1 * S) + (tiles + S - 1) / S);
-    if (i == 0 || t < best_t) {
-      d.pairs = S;
-      best_t = t;
-    }
-  }
-  const double clusters = 0.5 * (double)((even + spread) * kGroups);
-  for (int runs = 2; runs <= std::min(kMaxRuns, tiles) && runs * clusters <= 4 * kHeld[0] && fits(runs); ++runs) {
-    const double t = waves(runs, kHeld[0]) * (5.0 + (tiles + runs - 1) / runs) + 2.5 + (kJoinBlock + kJoinPart * runs) * clusters;
-    if (t < best_t) {
-      d.pairs = 1;
-      d.runs = runs;
-      best_t = t;
-    }
-  }
-  return d;
-}
-
 cudaLaunchConfig_t tree_config(int S, int clusters, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * 2 * S);
@@ -819,18 +742,33 @@ cudaLaunchConfig_t tree_config(int S, int clusters, cudaStream_t stream, cudaLau
   return cfg;
 }
 
-// Per device, set once: the kernel's attributes (threads that race here set the same ones).
-cudaError_t tree_setup() {
+// Per device, once: the kernel's attributes, and how many clusters of each size the GPU holds (threads that race here
+// find the same).  On a GB300 76, 36, 23, 15, 13, 8 and 7.
+cudaError_t tree_setup(PlanHeld* held) {
   static std::atomic<int> ready[64];
+  static std::atomic<int> counts[64][kPlanSizesN];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  if ((e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-    return e;
-  ready[dev].store(1, std::memory_order_release);
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    if ((e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+      return e;
+    for (int i = 0; i < kPlanSizesN; ++i) {
+      cudaLaunchAttribute attr[2];
+      const cudaLaunchConfig_t cfg = tree_config(kPlanSizes[i], 1, nullptr, attr);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, tree_dense_kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();  // a size that this GPU does not take
+        n = 0;
+      }
+      counts[dev][i].store(n, std::memory_order_relaxed);
+    }
+    if (counts[dev][0].load(std::memory_order_relaxed) <= 0) return cudaErrorInvalidConfiguration;
+    ready[dev].store(1, std::memory_order_release);
+  }
+  for (int i = 0; i < kPlanSizesN; ++i) held->n[i] = counts[dev][i].load(std::memory_order_relaxed);
   return cudaSuccess;
 }
 
@@ -857,9 +795,10 @@ int4* tree_dense_plan(const TreeBatch& b, void* ws) {
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                               const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
                               void* ws, float sm_scale, int* status, cudaStream_t stream) {
-  cudaError_t e = tree_setup();
+  PlanHeld held;
+  cudaError_t e = tree_setup(&held);
   if (e != cudaSuccess) return e;
-  const DensePlan d = dense_plan(b.n_seq, b.n_tok, b.max_n_kv, b.identity_max, bits != nullptr);
+  const DensePlan d = dense_plan(held, b.n_seq, b.n_tok, b.max_n_kv, b.identity_max, bits != nullptr);
   int4* plan = tree_dense_plan(b, ws);
   if (plan && !bits) {  // with selected tokens the selection's first launch has made it
     e = launch_pdl(tree_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, b, plan);

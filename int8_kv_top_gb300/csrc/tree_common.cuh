@@ -2,6 +2,7 @@
 // drafted token sees.
 #pragma once
 #include "common.cuh"
+#include "tree_plan.cuh"
 
 namespace qsa {
 
@@ -96,9 +97,6 @@ constexpr int kTileCells = 128;    // cells of a tile
 constexpr int kTreeBlock = 256;    // (token, head) rows of a block: a CTA pair's UMMA M
 constexpr int kPlanSeqs = 8;       // sequences from which on a launch takes its blocks from a list, longest first
 constexpr int kPlanThreads = 256;
-__host__ __device__ __forceinline__ int tree_blocks_most(int n_seq, int n_tok) {
-  return (int)((long long)n_tok * kHPG / kTreeBlock) + n_seq;
-}
 
 // The list, by one CTA of kPlanThreads: plan[0].x blocks, then for block i plan[1 + 2 i] = {first pool cell,
 // committed cells, drafted tokens, first token row} of its sequence and plan[2 + 2 i].x = its first row, in decreasing
