@@ -241,28 +241,53 @@ def qsa_flash_prefill_batched(q, kq, vq, ksc, vsc, n_pool: int, seqs, n_seq: int
                                             ws_bytes, _params(params), _stream(stream)))
 
 
-def _row_stride(t, width: int, n_tok: int) -> int:
+def _table(t, name: str, n: int):
+    """An array of 32-bit integers, n at least, read as packed."""
+    if not isinstance(t, torch.Tensor):
+        return _ptr(t)
+    d = t.dtype
+    if (d is torch.int32 or d is torch.uint32) and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    raise QSAError(QSA_ERR_INVALID_ARG, f"{name} must be a contiguous int32 tensor of at least {n} elements (got {d}, "
+                                        f"shape {tuple(t.shape)}, strides {t.stride()})")
+
+
+def _row_stride(t, name: str, width: int, n_tok: int) -> int:
     """Elements between two tokens' rows of a raw projection [n_tok, ...] (a slice of a wider one, say); the
     elements of a token's own row lie side by side."""
-    return width if n_tok <= 1 else t.stride(0)
+    if not isinstance(t, torch.Tensor) or n_tok <= 1 and t.is_contiguous():
+        return width
+    size, stride = t.shape, t.stride()
+    row = 1
+    for d in range(len(size) - 1, 0, -1):
+        if stride[d] != row and size[d] != 1:
+            row = -1
+            break
+        row *= size[d]
+    if row < width or size[0] < n_tok:
+        raise QSAError(QSA_ERR_INVALID_ARG, f"{name} must have rows of {width} elements side by side for {n_tok} tokens "
+                                            f"(got shape {tuple(size)}, strides {stride})")
+    return stride[0]
 
 
 def qsa_prep_batched(q_raw, k_raw, v_raw, q_gamma, k_gamma, pos, cells, n_tok: int, n_pool: int, qcur, kcur, kq, ksc, vq,
                      vsc, rope=None, stream=None):
-    """qsa_prep for tokens of any sequences: pos int32 [n_tok] or [n_tok, 1 or 3], cells int32 [n_tok] (-1: padding).
-    q_raw, k_raw and v_raw may be slices along a token's row of a fused projection; kcur may be None."""
+    """qsa_prep for tokens of any sequences: pos int32 [n_tok] or [n_tok, 1 or 3], cells int32 [n_tok] (-1: padding),
+    both contiguous.  q_raw, k_raw and v_raw may be slices along a token's row of a fused projection; kcur may be None."""
     axes = pos.size(1) if pos.dim() > 1 else 1
     kv = N_GROUPS * HEAD_DIM
-    _check(load().qsa_prep_batched(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _row_stride(q_raw, N_HEADS * HEAD_DIM, n_tok),
-                                   _row_stride(k_raw, kv, n_tok), _row_stride(v_raw, kv, n_tok), _ptr(q_gamma),
-                                   _ptr(k_gamma), _ptr(pos), axes, _ptr(cells), _rope(rope), n_tok, n_pool, _ptr(qcur),
-                                   _ptr(kcur), _ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), _stream(stream)))
+    _check(load().qsa_prep_batched(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw),
+                                   _row_stride(q_raw, "q_raw", N_HEADS * HEAD_DIM, n_tok),
+                                   _row_stride(k_raw, "k_raw", kv, n_tok), _row_stride(v_raw, "v_raw", kv, n_tok),
+                                   _ptr(q_gamma), _ptr(k_gamma), _table(pos, "pos", n_tok * axes), axes,
+                                   _table(cells, "cells", n_tok), _rope(rope), n_tok, n_pool, _ptr(qcur), _ptr(kcur),
+                                   _ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), _stream(stream)))
 
 
 def qsa_cache_read(kq, ksc, vq, vsc, n_pool: int, cells, n: int, k16, v16, stream=None):
     """Cells of the pool as fp16 rows; k16 or v16 may be None."""
-    _check(load().qsa_cache_read(_ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), n_pool, _ptr(cells), n, _ptr(k16), _ptr(v16),
-                                 _stream(stream)))
+    _check(load().qsa_cache_read(_ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), n_pool, _table(cells, "cells", n), n,
+                                 _ptr(k16), _ptr(v16), _stream(stream)))
 
 
 def qsa_tree_attention_workspace_bytes(n_seq: int, n_tok: int, max_n_kv: int, params=None) -> int:
@@ -271,17 +296,21 @@ def qsa_tree_attention_workspace_bytes(n_seq: int, n_tok: int, max_n_kv: int, pa
 
 def qsa_tree_attention(q, kq, vq, ksc, vsc, n_pool: int, seqs, n_seq: int, n_tok: int, tree, max_n_kv: int, ids, out,
                        ws=None, params=None, stream=None, gate=None):
-    """Attention of drafted token trees; tree is an int32 or uint32 tensor [n_tok, words] of mask bits."""
+    """Attention of drafted token trees; tree is a contiguous int32 or uint32 tensor [n_tok, words] of mask bits."""
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(load().qsa_tree_attention(_ptr(q), _ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), n_pool, _ptr(seqs), n_seq, n_tok,
-                                     _ptr(tree), tree.shape[1], max_n_kv, _ptr(ids), _ptr(gate), _ptr(out), _ptr(ws),
-                                     ws_bytes, _params(params), _stream(stream)))
+    words = tree.shape[1]
+    _check(load().qsa_tree_attention(_ptr(q), _ptr(kq), _ptr(vq), _ptr(ksc), _ptr(vsc), n_pool,
+                                     _table(seqs, "seqs", 4 * n_seq), n_seq, n_tok, _table(tree, "tree", n_tok * words),
+                                     words, max_n_kv, _ptr(ids), _ptr(gate), _ptr(out), _ptr(ws), ws_bytes,
+                                     _params(params), _stream(stream)))
 
 
 def qsa_cache_commit(kq, ksc, vq, vsc, n_pool: int, seqs, n_seq: int, path, n_path, stream=None):
     """The accepted paths (path int32 [n_seq, cap], n_path int32 [n_seq]) moved to the front of the drafted cells."""
-    _check(load().qsa_cache_commit(_ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), n_pool, _ptr(seqs), n_seq, _ptr(path),
-                                   _ptr(n_path), path.shape[1], _stream(stream)))
+    cap = path.shape[1]
+    _check(load().qsa_cache_commit(_ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), n_pool, _table(seqs, "seqs", 4 * n_seq), n_seq,
+                                   _table(path, "path", n_seq * cap), _table(n_path, "n_path", n_seq), cap,
+                                   _stream(stream)))
 
 
 def qsa_debug_wait_probe(budget_ns: int, stream=None):
