@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -138,7 +139,7 @@ def _rope(rope):
     if rope is None:
         return None
     base, rd, eps, sec = rope
-    return _rope_of(float(base), int(rd), float(eps), tuple(sec))
+    return _rope_of(float(base), int(rd), float(eps), tuple(map(operator.index, sec)))
 
 
 def _check(rc: int):

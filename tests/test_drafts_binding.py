@@ -132,3 +132,17 @@ def test_nothing_to_do(lib):
     qsa.qsa_cache_read(Z, Z, Z, Z, POOL, ints(0), 0, Z, Z)
     prep(n=0, q=FUSED[:0, :6144], k=FUSED[:0, :512], v=FUSED[:0, :512], pos=ints(0), cells=ints(0))
     assert len(lib) == 4
+
+
+def test_sections_are_whole_numbers_each_time():
+    # the parameter blocks are kept by value: an equal float, or a tensor that changes, must not find an earlier one
+    good = (10000.0, 256, 1e-6, (32, 48, 48))
+    assert list(qsa._rope(good).sections) == [32, 48, 48]
+    assert list(qsa._rope((1e4, 256, 1e-6, [32, 48, 48])).sections) == [32, 48, 48]
+    with pytest.raises(TypeError):
+        qsa._rope((10000.0, 256, 1e-6, (32.0, 48.0, 48.0)))
+    sec = [torch.tensor(32), torch.tensor(48), torch.tensor(48)]
+    assert list(qsa._rope((1e4, 256, 1e-6, sec)).sections) == [32, 48, 48]
+    sec[0].fill_(16)
+    sec[1].fill_(64)
+    assert list(qsa._rope((1e4, 256, 1e-6, sec)).sections) == [16, 64, 48]
