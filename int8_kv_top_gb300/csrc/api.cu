@@ -137,6 +137,8 @@ int decode_layer_limit(int* rc) {
   return c * qsa::decode_layer_cells_per_cta();
 }
 
+constexpr int kTreeMost = 65535;  // tokens, and sequences, of a tree call
+
 // Whether a tree call selects for its tokens together (tree_select.cu, then one tensor-core attention for all)
 // or gives each selected (token, group) a cluster of its own.  Together costs by the sequences and their cells,
 // the clusters cost by the tokens, so the rule is on the tokens a sequence.  Measured (together / clusters, us a
@@ -455,8 +457,8 @@ int qsa_flash_prefill_batched(const uint16_t* q, const int8_t* kq, const int8_t*
   if (gate && !aligned16(gate)) return fail(QSA_ERR_INVALID_ARG, "gate is not 16-byte aligned");
   if (n_pool <= 0) return fail(QSA_ERR_INVALID_ARG, "n_pool must be positive");
   if (n_seq < 1 || n_tok < 1) return fail(QSA_ERR_INVALID_ARG, "need n_seq >= 1 and n_tok >= 1 (got %d, %d)", n_seq, n_tok);
-  if (n_tok > 65535 || n_seq > 65535)
-    return fail(QSA_ERR_UNSUPPORTED, "n_tok and n_seq must be at most 65535 (got %d, %d)", n_tok, n_seq);
+  if (n_tok > kTreeMost || n_seq > kTreeMost)
+    return fail(QSA_ERR_UNSUPPORTED, "n_tok and n_seq must be at most %d (got %d, %d)", kTreeMost, n_tok, n_seq);
   const bool any_selected = max_n_kv > p.identity_max;
   int limit = 131072;  // the dense work list counts up to 1024 super-chunks of 128 cells
   if (any_selected) {
@@ -573,7 +575,8 @@ int qsa_cache_read(const int8_t* kq, const uint16_t* ksc, const int8_t* vq, cons
 
 size_t qsa_tree_attention_workspace_bytes(int n_seq, int n_tok, int max_n_kv, const qsa_params* params) {
   qsa::Params p{};
-  if (n_seq < 1 || n_tok < 1 || max_n_kv < 1 || resolve_params(params, &p) != QSA_OK) return 0;
+  if (n_seq < 1 || n_tok < 1 || n_seq > kTreeMost || n_tok > kTreeMost || max_n_kv < 1 || resolve_params(params, &p) != QSA_OK)
+    return 0;
   // Selecting together takes its part where this call or a smaller one (all tokens in one sequence, fewer cells) does.
   const int cells = std::min(max_n_kv, qsa::select_max_cells());
   const bool together = tree_selects_together(1, n_tok, cells, p);
@@ -590,8 +593,8 @@ int qsa_tree_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, co
   if (rc) return rc;
   if (n_seq < 0 || n_tok < 0)
     return fail(QSA_ERR_INVALID_ARG, "n_seq and n_tok must be >= 0 (got %d, %d)", n_seq, n_tok);
-  if (n_tok > 65535 || n_seq > 65535)
-    return fail(QSA_ERR_UNSUPPORTED, "n_tok and n_seq must be at most 65535 (got %d, %d)", n_tok, n_seq);
+  if (n_tok > kTreeMost || n_seq > kTreeMost)
+    return fail(QSA_ERR_UNSUPPORTED, "n_tok and n_seq must be at most %d (got %d, %d)", kTreeMost, n_tok, n_seq);
   if (tree_words < 1 || tree_words > qsa::kTreeWords)
     return fail(QSA_ERR_UNSUPPORTED, "tree_words must be in [1, %d] (got %d)", qsa::kTreeWords, tree_words);
   if (n_pool <= 0 || n_pool > 0x7fffffffLL)

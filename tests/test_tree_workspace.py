@@ -99,3 +99,9 @@ def test_a_plan_launches_clusters_that_the_gpu_holds(plan, held):
         assert held[SIZES.index(pairs)] > 0, at
         largest = max(largest, plan(GB300, *at)[1])
     assert largest == 8  # a GB300 takes clusters of 16 for some of them
+
+
+def test_sizes_that_the_call_refuses_need_none():
+    for args in ((65536, 65536, 50), (1, 65536, 50), (65536, 1, 50), (2**31 - 1, 2**31 - 1, 2**31 - 1), (3, 2**31 - 1, 9000)):
+        assert qsa.qsa_tree_attention_workspace_bytes(*args) == 0
+    assert qsa.qsa_tree_attention_workspace_bytes(65535, 65535, 131072) > 0
