@@ -291,8 +291,8 @@ __device__ __forceinline__ void quantize_row_fast(const float2 (&x)[4], int a, i
     const int c = (int)fminf(fmaxf(q, -127.f), 127.f);
     w[u >> 2] |= (uint32_t)(c & 0xFF) << (8 * (u & 3));
   }
-  *reinterpret_cast<uint32_t*>(codes + a) = w[0];
-  *reinterpret_cast<uint32_t*>(codes + b) = w[1];
+  *reinterpret_cast<uint32_t*>(codes + a) = fa != 0.f ? w[0] : 0u;  // scale 0: codes 0, those of NaN too
+  *reinterpret_cast<uint32_t*>(codes + b) = fb != 0.f ? w[1] : 0u;
   if ((a & 63) == 0) scales[a >> 6] = ha;  // the lane that holds a block's first dims stores its scale
   if ((b & 63) == 0) scales[b >> 6] = hb;
 }
