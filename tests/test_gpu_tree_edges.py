@@ -114,3 +114,51 @@ def test_one_workspace_for_every_smaller_call(params):
         assert (ws[need:] == 0x5A).all()
         ref, _, bound = reference(pool, seqs, *(params or (2048, 2051, SCALE)))
         assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all(), specs
+
+
+def random_pool(n, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = lambda: torch.randint(-127, 128, (n, 2, 256), generator=g, device="cuda", dtype=torch.int8)
+    scales = lambda: (torch.rand(n, 2, 4, generator=g, device="cuda") * 0.015 + 0.005).half()
+    return {"kq": codes(), "vq": codes(), "ksc": scales(), "vsc": scales()}
+
+
+@pytest.mark.parametrize("n_seq,pos0,params", [
+    (65535, 3, None),                # as many sequences as a call takes, one token each
+    (257, 100, (40, 71, SCALE)),     # as many tokens: trees of 255, selecting together
+    (32768, 90, (40, 71, SCALE)),    # two tokens each, a cluster for each of them
+])
+def test_the_largest_calls(n_seq, pos0, params):
+    each = 65535 // n_seq
+    n_tok = each * n_seq
+    rng = np.random.default_rng(n_seq)
+    base = rng.integers(0, pos0 + 1, n_seq)  # committed cells, 0 among them
+    size = base + each
+    cell0 = np.concatenate([[0], np.cumsum(size)[:-1]])
+    seqs = np.stack([cell0, size, base, np.arange(n_seq) * each], 1).astype(np.int32)
+    words = (each + 31) // 32
+    masks = np.zeros((n_tok, words), np.uint32)
+    row = np.arange(n_tok) % each
+    for w in range(words):  # chains
+        left = np.clip(row + 1 - 32 * w, 0, 32)
+        masks[:, w] = ((np.uint64(1) << left.astype(np.uint64)) - np.uint64(1)).astype(np.uint32)
+    pool = random_pool(int(size.sum()), n_seq)
+    g = torch.Generator(device="cuda").manual_seed(n_seq)
+    q = torch.randn(n_tok, 24, 256, generator=g, device="cuda").half()
+    topk, max_n_kv = (params or (2048,))[0], int(size.max())
+    ids = torch.full((n_tok, 2, topk), -7, dtype=torch.int32, device="cuda") if params else None
+    out = torch.full_like(q, float("nan"))
+    need = qsa.qsa_tree_attention_workspace_bytes(n_seq, n_tok, max_n_kv, params)
+    qsa.qsa_tree_attention(q, pool["kq"], pool["vq"], pool["ksc"], pool["vsc"], len(pool["kq"]), torch.from_numpy(seqs).cuda(),
+                           n_seq, n_tok, torch.from_numpy(masks.view(np.int32)).cuda(), max_n_kv, ids, out,
+                           torch.empty(max(need, 1), dtype=torch.uint8, device="cuda"), params=params)
+    qsa.qsa_check_device_status()
+    assert torch.isfinite(out).all()
+    for s in sorted({0, 1, n_seq // 2, n_seq - 2, n_seq - 1, *rng.integers(0, n_seq, 8)}):
+        a, b = int(cell0[s]), int(cell0[s] + size[s])
+        t = slice(s * each, (s + 1) * each)
+        one = {k: v[a:b].cpu().numpy() for k, v in pool.items()} | {"q": q[t].cpu().numpy(), "tree": masks[t]}
+        ref, ref_ids, bound = reference(one, np.array([[0, b - a, base[s], 0]]), *(params or (2048, 2051, SCALE)))
+        assert (np.abs(out[t].double().cpu().numpy() - ref) <= bound).all(), s
+        if params:
+            np.testing.assert_array_equal(ids[t].cpu().numpy(), ref_ids)
