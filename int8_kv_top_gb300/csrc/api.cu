@@ -142,10 +142,10 @@ constexpr int kTreeMost = 65535;  // tokens, and sequences, of a tree call
 // Whether a tree call selects for its tokens together (tree_select.cu, then one tensor-core attention for all)
 // or gives each selected (token, group) a cluster of its own.  Together costs by the sequences and their cells,
 // the clusters cost by the tokens, so the rule is on the tokens a sequence.  Measured (together / clusters, us a
-// call of equal trees): 1 sequence of 16,000 cells with 7 tokens 45 / 44, 8 tokens 45 / 70; 2 with 3 tokens 57 / 47,
-// 4 tokens 57 / 72; 4 with 4 tokens 86 / 71, 5 tokens 87 / 121; 8 with 4 tokens 137 / 130, 5 tokens 138 / 194; 16 of
-// 24,000 with 3 tokens 325 / 272, 4 tokens 327 / 352; of 60,000 cells 1 with 7 tokens 95 / 87, 8 tokens 96 / 148, 4
-// with 4 tokens 222 / 230, 8 with 4 tokens 383 / 383.
+// call of equal trees): 1 sequence of 16,000 cells with 7 tokens 45 / 44, 8 tokens 45 / 70; 2 with 3 tokens 60 / 48,
+// 4 tokens 60 / 72; 4 with 4 tokens 87 / 72, 5 tokens 88 / 122; 8 with 4 tokens 135 / 131, 5 tokens 136 / 192; 16 of
+// 24,000 with 3 tokens 316 / 268, 4 tokens 315 / 349; of 60,000 cells 1 with 7 tokens 98 / 87, 8 tokens 97 / 148, 4
+// with 4 tokens 217 / 231, 8 with 4 tokens 374 / 383.
 bool tree_selects_together(int n_seq, int n_tok, int max_n_kv, const qsa::Params& p) {
   const long long least = n_seq == 1 ? 8 : n_seq == 2 || n_seq >= 16 ? 4 : 5;  // tokens a sequence
   return max_n_kv > p.identity_max && max_n_kv <= qsa::select_max_cells() && n_tok >= least * n_seq;

@@ -10,7 +10,7 @@
 // tokens), the M of one MMA over a pair of CTAs (128 rows each).  Selected tokens attend through the same
 // dense tiles, their other cells masked: gathering 2,048 cells a token costs an SM about 25 us, a masked
 // 128-cell tile for 21 tokens 1.7 us of a pair.  A cluster of 2 S CTAs takes one block and group, each pair a run of its
-// 128-cell tiles, and the pairs merge by log-sum-exp in a fixed order, so that a call of few rows still
+// 128-cell tiles (how many: tree_plan.cuh), and the pairs merge by log-sum-exp in a fixed order, so that a call of few rows still
 // spreads over the GPU and results do not depend on timing.  The statistics are exchanged through
 // distributed shared memory, the rows through a workspace that stays in L2: 128 KB a CTA by remote shared
 // memory took 6.5 us, stores or coalesced loads alike.
@@ -23,18 +23,20 @@
 // per block instead converts and stores twice as much and is bound by shared memory (3,100 cycles; measured
 // 5,400 a tile of 128 rows).
 //
-// 4 trees of 33-48 tokens after 30,000 cells, all of them attended to: 155 us, 0.40 of the measured bf16 rate over
-// the call; over the CTAs' own time the tensor pipe is 57% active.  0.45 instructions are issued a cycle and
-// scheduler; the MMAs take about 95 cycles an instruction (of 64 and 128 cycles of arithmetic), and a tile's
-// softmax about 2,400.  The roles run at once, so the
+// 4 trees of 33-48 tokens after 30,000 cells, all of them attended to: 156 us, 0.40 of the measured bf16 rate over
+// the call, in seven runs a block; over the CTAs' own time the tensor pipe is 54% active.  0.45 instructions are
+// issued a cycle and scheduler; the MMAs take about 95 cycles an instruction (of 64 and 128 cycles of arithmetic), and a
+// tile's softmax about 2,400.  The roles run at once, so the
 // loop bodies share the instruction cache: with separate K and V producer bodies a quarter of all stalls were
 // instruction fetches, and the call took 196 us.  A single S buffer with P kept apart (so that QK never waits on
-// a PV): 208 us.  Persistent pairs over an even share of all tiles, merged by a second launch: 217 against 221
-// us then, and slower by 5 to 60 us for short caches, whose calls a second launch and the write-out weigh down.
+// a PV): 208 us.  Persistent pairs over an even share of all tiles, merged by a second launch, were measured only
+// with the separate bodies: 217 against 221 us then, and slower by 5 to 60 us for short caches, whose calls a second
+// launch and the write-out weigh down.
 //
 // A cluster holds eight pairs at most, and with few sequences over long caches that leaves most of the GPU idle; then
 // pairs of their own (up to half of the GPU's a block and group) take the tiles and a second launch joins their parts.
-// One tree of 16 tokens after 8,192 cells (selection included) 52 -> 43 us, after 30,000 106 -> 68.
+// One tree of 16 tokens after 8,192 cells (selection included) 53 us with a cluster of eight pairs and 44 with pairs of
+// their own, after 30,000 107 and 69.
 //
 //   warps 0-3    K producers: stage = 128 dims of this CTA's 64 cells (16 KB), ring of four (two tiles)
 //   warps 4-7    V producers: stage = 64 cells x this CTA's 128 dims (16 KB), ring of four (two tiles)
@@ -48,7 +50,10 @@
 //
 // Roundings below fp32: k^ and v^ (the values the library's prefill attends to), P (11 bits for cells down to 21
 // binades below the row's running maximum, then fewer, none below 32: kPShift), and the output; statistics and
-// sums are fp32.
+// sums are fp32.  Each is 2.1e-4 rms of the output on random data, 4.2e-4 together.  k^ or v^ in two fp16 parts each would
+// double its half of the MMAs and of the operand tiles.  The MMAs' own sums are fp32 with about one bit more: a product
+// more than some 25 binades below the output that has been added up so far is cut off whatever P holds (131,072 cells
+// 17 nats below one of the same V: up to 0.3% of the output).
 //
 // TMEM columns (each CTA): O [0, 256), S/P buffers [256 + 128 b, 384 + 128 b), b = 0, 1.
 // Every mbarrier wait is bounded; after a timeout a CTA still meets the cluster's barriers.

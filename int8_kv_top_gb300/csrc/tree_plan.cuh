@@ -23,14 +23,17 @@ inline int tree_blocks_most(int n_seq, int n_tok) { return (int)((long long)n_to
 // sequences give, each with equal and with spread lengths: the blocks of equal sequences rounded up, or half a block
 // of rounding a sequence; whole waves, or 0.9 of a wave for every filling of the GPU.  Measured on a GB300 (us a call):
 //                                         pairs 1   2   3   5   6   8     runs 2   4   6   9  12  19  38
-//    1 tree  of 61 after  1,984 cells          38  27  23  20  19  16       28  22  21  20  20  29  29
-//    1 tree  of 16 after  8,192               156 100  79  62  58  53       98  69  58  52  48  46  44
-//    1 tree  of 16 after 30,000               490 275 200 141 127 106      274 159 123 100  88  76  68
-//    2 trees of 61 after 30,000               539 317 237 173 248 209      321 203 166 199 176 189 235
-//    4 trees of 44 after 30,000               597 361 444 323 385 388      371 372 300 308 315 340 406
-//    8 trees of 16 after 30,000               624 364 275 323 291 320      374 241 289 238 259 260 315
-//   12 trees of 61 after  8,192               285 305 373 385 470 465      337 366 393 425 453 534 760
-//   24 trees of 1-32 after 200-16,000         352 247 264 304 378 362      265 281 298   -  348   -   -
+//    1 tree  of 61 after  1,984 cells          38  29  25  20  18  16       29  23  22  20  21  32  43
+//    1 tree  of 16 after  8,192               158  99  78  61  56  53       98  68  58  52  48  45  44
+//    1 tree  of 16 after 30,000               494 272 200 141 126 107      272 162 125 100  88  77  69
+//    2 trees of 61 after 30,000               542 320 239 173 249 209      323 204 167 199 175 190 238
+//    4 trees of 44 after 30,000               607 364 433 323 387 387      373 373 302 310 318 345 415
+//    8 trees of 16 after 30,000               637 368 271 317 285 315      373 236 284 232 253 255 311
+//   12 trees of 61 after  8,192               285 309 378 386 474 471      339 370 399 431 461 546 784
+//   32 trees of 4-64 after 64-1,984            68 121 150 201 303 314      156 205 247 296 341 438 653
+//   24 trees of 1-32 after 200-16,000         353 245 259 295 368 360      258 277 297 323 350 415 579
+//    4 trees of 33-48 after 30,000, all cells 448 223 153 189 239 190      238 237 173 181 189 185 258
+// (the last takes 157 in the seven runs that the estimate picks, which counts a part-filled wave as less than a whole one)
 //
 // Several pairs to a block write unmerged parts, 264 KB a pair.  What a call may write is bounded by its arguments
 // alone, in a way that grows with each of them (parts_most), so that a workspace for a server's largest batch serves

@@ -16,8 +16,8 @@
 //                 memory); hi and lo in one N instead of two MMAs each halves their number.
 //  3. topk_kernel<V, true>.
 //
-// 24 trees of 1-32 tokens after 200-16,000 cells (414 tokens): prep 13, score 46, top-k 52, the attention 142 us, each
-// launched alone from a cold L2 (241 us as the call runs).  The score reads 88 MB; by a clock trace a tile takes
+// 24 trees of 1-32 tokens after 200-16,000 cells (414 tokens): prep 14, score 47, top-k 54, the attention 145 us, each
+// launched alone from a cold L2 (243 us as the call runs).  The score reads 88 MB; by a clock trace a tile takes
 // 2,400 cycles, 1,900 of them the issue of its MMAs, the rest between tiles; neither memory nor arithmetic (tensor 7%)
 // bounds it.  Two teams of producers and an epilogue that read each token's scale as it stored: 247 us.
 #include "select_math.cuh"
