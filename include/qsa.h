@@ -438,6 +438,79 @@ QSA_API int qsa_cache_commit(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vs
                              int n_seq, const int32_t* path, const int32_t* n_path, int path_cap, void* stream);
 
 /*
+ * Sequences that share a prompt.  The pages have no counterpart of the operators below; the layer, the cache
+ * layouts and the pool are those above.  Samples, beams and chats behind one prompt keep that prompt's cells once, as
+ * a prefix of a table, and their own cells in runs of their own: qsa_cache_copy forks a sequence's own
+ * cells, qsa_prefix_attention attends over the shared and the own cells, qsa_tree_verify settles which drafted path is
+ * accepted (qsa_cache_commit then moves its cells), and qsa_cache_compact closes the holes that ended sequences leave.
+ *
+ * qsa_tree_verify - which path of each drafted tree the target model accepts, from its probabilities and given random
+ * numbers, and the token that follows the path.  Speculative sampling, so that accepted and following tokens are
+ * distributed as the target's own samples.  Token 0 of a sequence is its root: a token that is settled already, always
+ * accepted.  With cur the token accepted last (the root at first), w = p[cur] and c = 1, the children of cur are tried in the
+ * order of their rows; child k with vocabulary entry x = token[k]:
+ *   u[k] c d[cur][x] < w[x]: accepted; cur = k, w = p[k], c = 1, and k's children are tried
+ *   else refused: w = max(w - c d[cur], 0), c = sum w, and the next child is tried
+ * d[cur] being the distribution from which the children of cur were drawn.  Without d (NULL) drafted tokens are
+ * certain choices: accepted where u[k] c < w[x], else c = c - w[x], w[x] = 0.  When no child is left:
+ *   next = the first entry j with w[0] + .. + w[j] > u_end sum w  (w = p[cur] where nothing is left of w)
+ *   p      DEVICE [n_tok] rows of vocab fp32: the target's probabilities behind each token of the call, each row's
+ *          sum 1 up to roundings, row t at p + t * p_stride (elements, at least vocab).  Values below 0 and NaN count as
+ *          0, values above 1 as 1; a probability counts in units of 2^-44 (6e-14), and sums are exact in these units
+ *   d      the drafter's, likewise with d_stride, or NULL; rows of tokens without children are not read
+ *   token, parent  DEVICE [n_tok] int32: the vocabulary entry, and the parent's index in the sequence (lower than the token's
+ *          own; -1 for the root and for it alone).  token of a root is not read
+ *   u, u_end  DEVICE fp32 [n_tok] and [n_seq]: uniform random numbers in [0, 1); a root's u is not used
+ *   seqs   as in qsa_tree_attention, of which first token rows and, to tell padding, n_cells are read; at most 256 tokens
+ *          a sequence
+ *   path   DEVICE [n_seq][path_cap] int32 (written up to n_path[s]): the accepted tokens' indices in the sequence,
+ *          ascending, the root's 0 first: what qsa_cache_commit takes.  After path_cap tokens no child is tried and
+ *          next follows the last
+ *   n_path, next  DEVICE [n_seq] int32 (written); next is -1 where the row has no mass at all
+ * A sequence without tokens (padding, or no rows) gets n_path 0 and next -1, and so does one whose entry, parents or
+ * tokens break these rules, which is also flagged in the status word (QSA_ERR_DEVICE).  Pointers are aligned to their
+ * elements (seqs to 16 bytes); rows that start on 16 bytes are read faster.  vocab 1 .. 262144, n_tok and n_seq at
+ * most 65535; n_seq 0 does nothing.
+ */
+QSA_API int qsa_tree_verify(const float* p, int64_t p_stride, const float* d, int64_t d_stride, int vocab, const int32_t* token,
+                            const int32_t* parent, const float* u, const float* u_end, const int32_t* seqs, int n_seq, int n_tok,
+                            int32_t* path, int path_cap, int32_t* n_path, int32_t* next, void* stream);
+
+/*
+ * qsa_cache_copy - runs of cells (codes and scales of K and V) copied from place to place in the pool: for run r and
+ * i < runs[r][2], cell runs[r][0] + i is copied to cell runs[r][1] + i.
+ *   runs   DEVICE [n_run][4] int32 {first source cell, first destination cell, cells, -}, 16-byte aligned; sources may
+ *          overlap one another.  A cell that is the destination of two runs, or source and destination in one
+ *          call, is left with unspecified contents (a run onto itself changes nothing); so is what is read from it.
+ *   max_cells  an upper bound on every run's cells
+ * A run outside the pool, or of more than max_cells cells, is skipped and flagged in the status word
+ * (QSA_ERR_DEVICE).  n_run at most 65535; n_run 0 or max_cells 0 does nothing.
+ */
+QSA_API int qsa_cache_copy(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64_t n_pool, const int32_t* runs, int n_run,
+                           int max_cells, void* stream);
+
+/* Bytes of device workspace qsa_cache_compact needs (0 for invalid arguments); grows with each argument. */
+QSA_API size_t qsa_cache_compact_workspace_bytes(int64_t n_pool, int n_prefix, int n_seq);
+
+/*
+ * qsa_cache_compact - the runs of a server's tables moved together: the runs {first pool cell, n_cells} of all
+ * prefixes and sequences, in the order in which they lie in the pool, are moved side by side to cells 0, 1, ...; in
+ * place, every cell read before it is overwritten.  A run that a sequence has left free is one that no entry names.
+ *   prefixes, seqs  DEVICE [n_prefix][4] and [n_seq][4] int32 {first pool cell, n_cells, -, -}, in any order; entries
+ *          with n_cells 0 are left alone.  Either may be NULL where its count is 0
+ *   prefixes_out, seqs_out  DEVICE, the tables with their new first cells (written; may be the tables themselves)
+ *   used   DEVICE int32 (written), or NULL: the number of cells in use, the first free cell
+ *   ws     qsa_cache_compact_workspace_bytes(n_pool, n_prefix, n_seq) bytes, 16-byte aligned, clobbered.  Calls that
+ *          overlap on the GPU need a workspace each.
+ * Cells from `used` on keep what they held.  Where an entry leaves the pool or two runs share a cell, nothing is
+ * moved: the tables are copied as they are, `used` is -1, and the status word is set (QSA_ERR_DEVICE).
+ * n_prefix + n_seq at most 65535; 0 does nothing but set `used` to 0.
+ */
+QSA_API int qsa_cache_compact(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64_t n_pool, const int32_t* prefixes,
+                              int n_prefix, const int32_t* seqs, int n_seq, int32_t* prefixes_out, int32_t* seqs_out,
+                              int32_t* used, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * qsa_debug_wait_probe - a test hook for the failure path of the bounded device waits; the
  * pages have no counterpart.  Launches one CTA whose bounded mbarrier wait (the wait every
  * pipeline of this library uses) is given budget_ns (1 us .. 2 s) on a barrier that nothing

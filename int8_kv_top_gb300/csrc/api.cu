@@ -673,6 +673,113 @@ int qsa_cache_commit(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64
   return ok();
 }
 
+int qsa_tree_verify(const float* p, int64_t p_stride, const float* d, int64_t d_stride, int vocab, const int32_t* token,
+                    const int32_t* parent, const float* u, const float* u_end, const int32_t* seqs, int n_seq, int n_tok,
+                    int32_t* path, int path_cap, int32_t* n_path, int32_t* next, void* stream) {
+  if (n_seq < 0 || n_tok < 0)
+    return fail(QSA_ERR_INVALID_ARG, "n_seq and n_tok must be >= 0 (got %d, %d)", n_seq, n_tok);
+  if (n_tok > kTreeMost || n_seq > kTreeMost)
+    return fail(QSA_ERR_UNSUPPORTED, "n_tok and n_seq must be at most %d (got %d, %d)", kTreeMost, n_tok, n_seq);
+  if (vocab < 1) return fail(QSA_ERR_INVALID_ARG, "vocab must be positive (got %d)", vocab);
+  if (vocab > qsa::verify_max_vocab())
+    return fail(QSA_ERR_UNSUPPORTED, "vocab must be at most %d (got %d)", qsa::verify_max_vocab(), vocab);
+  if (path_cap < 1) return fail(QSA_ERR_INVALID_ARG, "path_cap must be positive (got %d)", path_cap);
+  if (p_stride < vocab || (d && d_stride < vocab))
+    return fail(QSA_ERR_INVALID_ARG, "%s must be at least vocab = %d (got %lld)", p_stride < vocab ? "p_stride" : "d_stride", vocab,
+                (long long)(p_stride < vocab ? p_stride : d_stride));
+  if (n_seq == 0) return ok();
+  CHECK_PTR(seqs, "seqs");
+  const struct {
+    const void* at;
+    const char* name;
+    bool rows;  // read for tokens alone
+  } arrays[] = {{p, "p", true}, {token, "token", true}, {parent, "parent", true}, {u, "u", true}, {u_end, "u_end", false},
+                {path, "path", false}, {n_path, "n_path", false}, {next, "next", false}};
+  for (const auto& x : arrays) {
+    if (!x.at && (!x.rows || n_tok > 0)) return fail(QSA_ERR_INVALID_ARG, "%s is NULL", x.name);
+    if (reinterpret_cast<uintptr_t>(x.at) & 3u) return fail(QSA_ERR_INVALID_ARG, "%s is not 4-byte aligned", x.name);
+  }
+  if (reinterpret_cast<uintptr_t>(d) & 3u) return fail(QSA_ERR_INVALID_ARG, "d is not 4-byte aligned");
+  int rc = 0;
+  int* st = status_ptr(&rc);
+  if (!st) return rc;
+  cudaError_t e = qsa::launch_tree_verify(p, p_stride, d, d_stride, vocab, token, parent, u, u_end,
+                                          reinterpret_cast<const int4*>(seqs), n_seq, n_tok, path, path_cap, n_path, next, st,
+                                          static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_tree_verify launch");
+  return ok();
+}
+
+int qsa_cache_copy(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64_t n_pool, const int32_t* runs, int n_run,
+                   int max_cells, void* stream) {
+  if (n_run < 0) return fail(QSA_ERR_INVALID_ARG, "n_run must be >= 0 (got %d)", n_run);
+  if (n_run > kTreeMost) return fail(QSA_ERR_UNSUPPORTED, "n_run must be at most %d (got %d)", kTreeMost, n_run);
+  if (max_cells < 0) return fail(QSA_ERR_INVALID_ARG, "max_cells must be >= 0 (got %d)", max_cells);
+  if (n_pool <= 0 || n_pool > 0x7fffffffLL)
+    return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
+  if (n_run == 0 || max_cells == 0) return ok();
+  CHECK_PTR(kq, "kq");
+  CHECK_PTR(ksc, "ksc");
+  CHECK_PTR(vq, "vq");
+  CHECK_PTR(vsc, "vsc");
+  CHECK_PTR(runs, "runs");
+  int rc = 0;
+  int* st = status_ptr(&rc);
+  if (!st) return rc;
+  cudaError_t e = qsa::launch_cache_copy(kq, reinterpret_cast<__half*>(ksc), vq, reinterpret_cast<__half*>(vsc), n_pool,
+                                         reinterpret_cast<const int4*>(runs), n_run, max_cells, st,
+                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_cache_copy launch");
+  return ok();
+}
+
+size_t qsa_cache_compact_workspace_bytes(int64_t n_pool, int n_prefix, int n_seq) {
+  if (n_pool <= 0 || n_pool > 0x7fffffffLL || n_prefix < 0 || n_seq < 0 || (long long)n_prefix + n_seq > kTreeMost) return 0;
+  return qsa::cache_compact_workspace_bytes(n_pool, n_prefix + n_seq);
+}
+
+int qsa_cache_compact(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64_t n_pool, const int32_t* prefixes,
+                      int n_prefix, const int32_t* seqs, int n_seq, int32_t* prefixes_out, int32_t* seqs_out, int32_t* used,
+                      void* ws, size_t ws_bytes, void* stream) {
+  if (n_prefix < 0 || n_seq < 0)
+    return fail(QSA_ERR_INVALID_ARG, "n_prefix and n_seq must be >= 0 (got %d, %d)", n_prefix, n_seq);
+  if ((long long)n_prefix + n_seq > kTreeMost)
+    return fail(QSA_ERR_UNSUPPORTED, "n_prefix + n_seq must be at most %d (got %d, %d)", kTreeMost, n_prefix, n_seq);
+  if (n_pool <= 0 || n_pool > 0x7fffffffLL)
+    return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
+  if (reinterpret_cast<uintptr_t>(used) & 3u) return fail(QSA_ERR_INVALID_ARG, "used is not 4-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n_prefix + n_seq == 0) {
+    cudaError_t e = used ? cudaMemsetAsync(used, 0, sizeof(int32_t), s) : cudaSuccess;
+    return e == cudaSuccess ? ok() : cuda_fail(e, "qsa_cache_compact memset");
+  }
+  CHECK_PTR(kq, "kq");
+  CHECK_PTR(ksc, "ksc");
+  CHECK_PTR(vq, "vq");
+  CHECK_PTR(vsc, "vsc");
+  if (n_prefix) {
+    CHECK_PTR(prefixes, "prefixes");
+    CHECK_PTR(prefixes_out, "prefixes_out");
+  }
+  if (n_seq) {
+    CHECK_PTR(seqs, "seqs");
+    CHECK_PTR(seqs_out, "seqs_out");
+  }
+  const size_t need = qsa_cache_compact_workspace_bytes(n_pool, n_prefix, n_seq);
+  if (!ws || ws_bytes < need)
+    return fail(QSA_ERR_WORKSPACE, "compaction workspace of %zu bytes given, %zu needed", ws ? ws_bytes : (size_t)0, need);
+  if (!aligned16(ws)) return fail(QSA_ERR_INVALID_ARG, "ws is not 16-byte aligned");
+  int rc = 0;
+  int* st = status_ptr(&rc);
+  if (!st) return rc;
+  cudaError_t e = qsa::launch_cache_compact(kq, reinterpret_cast<__half*>(ksc), vq, reinterpret_cast<__half*>(vsc), n_pool,
+                                            reinterpret_cast<const int4*>(prefixes), n_prefix,
+                                            reinterpret_cast<const int4*>(seqs), n_seq, reinterpret_cast<int4*>(prefixes_out),
+                                            reinterpret_cast<int4*>(seqs_out), used, ws, st, s);
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_cache_compact launch");
+  return ok();
+}
+
 }  // extern "C"
 
 namespace {

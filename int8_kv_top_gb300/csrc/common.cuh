@@ -201,6 +201,21 @@ cudaError_t launch_cache_commit(int8_t* kq, __half* ksc, int8_t* vq, __half* vsc
                                 int n_seq, const int32_t* path, const int32_t* n_path, int path_cap, int* status,
                                 cudaStream_t stream);
 
+// Runs of cells (cache_runs.cu): copied from place to place (runs {source, destination, cells, -}), and the runs of
+// a prefix and a sequence table put side by side at the front of the pool, in place.
+cudaError_t launch_cache_copy(int8_t* kq, __half* ksc, int8_t* vq, __half* vsc, int64_t n_pool, const int4* runs, int n_run,
+                              int max_cells, int* status, cudaStream_t stream);
+size_t cache_compact_workspace_bytes(int64_t n_pool, int n_entries);
+cudaError_t launch_cache_compact(int8_t* kq, __half* ksc, int8_t* vq, __half* vsc, int64_t n_pool, const int4* prefixes,
+                                 int n_prefix, const int4* seqs, int n_seq, int4* prefixes_out, int4* seqs_out, int* used,
+                                 void* ws, int* status, cudaStream_t stream);
+
+// Verification of drafted trees (verify.cu): the accepted path of each sequence and the token behind it.  d may be null.
+int verify_max_vocab();
+cudaError_t launch_tree_verify(const float* p, int64_t p_stride, const float* d, int64_t d_stride, int vocab, const int32_t* token,
+                               const int32_t* parent, const float* u, const float* u_end, const int4* seqs, int n_seq, int n_tok,
+                               int32_t* path, int path_cap, int32_t* n_path, int32_t* next, int* status, cudaStream_t stream);
+
 // The score-GEMM and top-k selection holds caches of up to select_max_cells() cells; longer
 // caches are selected by the single-launch decode layer's cluster kernel (ids only).
 int select_max_cells();

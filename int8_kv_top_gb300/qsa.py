@@ -34,7 +34,8 @@ EXPORTS = ("qsa_last_error", "qsa_prep_quantize", "qsa_prep", "qsa_select_worksp
            "qsa_flash_prefill_gated", "qsa_decode_partial", "qsa_merge", "qsa_merge_gated", "qsa_decode_layer",
            "qsa_decode_layer_batched", "qsa_flash_prefill_batched_workspace_bytes", "qsa_flash_prefill_batched",
            "qsa_check_device_status", "qsa_select_noalloc", "qsa_debug_wait_probe", "qsa_prep_batched", "qsa_cache_read",
-           "qsa_tree_attention_workspace_bytes", "qsa_tree_attention", "qsa_cache_commit")
+           "qsa_tree_attention_workspace_bytes", "qsa_tree_attention", "qsa_cache_commit", "qsa_tree_verify", "qsa_cache_copy",
+           "qsa_cache_compact_workspace_bytes", "qsa_cache_compact")
 
 
 class QSAError(RuntimeError):
@@ -91,12 +92,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qsa_tree_attention_workspace_bytes.restype = SZ
     lib.qsa_tree_attention.argtypes = [P, P, P, P, P, I64, P, I, I, P, I, I, P, P, P, P, SZ, PP, P]
     lib.qsa_cache_commit.argtypes = [P, P, P, P, I64, P, I, P, P, I, P]
+    lib.qsa_tree_verify.argtypes = [P, I64, P, I64, I, P, P, P, P, P, I, I, P, I, P, P, P]
+    lib.qsa_cache_copy.argtypes = [P, P, P, P, I64, P, I, I, P]
+    lib.qsa_cache_compact_workspace_bytes.argtypes = [I64, I, I]
+    lib.qsa_cache_compact_workspace_bytes.restype = SZ
+    lib.qsa_cache_compact.argtypes = [P, P, P, P, I64, P, I, P, I, P, P, P, P, SZ, P]
     lib.qsa_check_device_status.argtypes = [P]
     lib.qsa_debug_wait_probe.argtypes = [ctypes.c_uint64, P]
     lib.qsa_select_noalloc.argtypes = [P, P, P, I, I, I, P, PP, P]
     for name in EXPORTS:
         if name not in ("qsa_last_error", "qsa_select_workspace_bytes", "qsa_flash_prefill_workspace_bytes",
-                        "qsa_flash_prefill_batched_workspace_bytes", "qsa_tree_attention_workspace_bytes"):
+                        "qsa_flash_prefill_batched_workspace_bytes", "qsa_tree_attention_workspace_bytes",
+                        "qsa_cache_compact_workspace_bytes"):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -312,6 +319,78 @@ def qsa_cache_commit(kq, ksc, vq, vsc, n_pool: int, seqs, n_seq: int, path, n_pa
     _check(load().qsa_cache_commit(_ptr(kq), _ptr(ksc), _ptr(vq), _ptr(vsc), n_pool, _table(seqs, "seqs", 4 * n_seq), n_seq,
                                    _table(path, "path", n_seq * cap), _table(n_path, "n_path", n_seq), cap,
                                    _stream(stream)))
+
+
+_F16, _I8, _I32, _F32 = (torch.float16, torch.uint16), (torch.int8,), (torch.int32, torch.uint32), (torch.float32,)
+
+
+def _array(t, name: str, dtypes: tuple, n: int, optional: bool = False):
+    """The pointer of a packed array of at least n elements on the current device."""
+    if t is None and (optional or n <= 0) or isinstance(t, int):
+        return t
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous() and t.numel() >= n
+            and (t.is_cuda and t.get_device() == torch.cuda.current_device() or not t.numel())):
+        return t.data_ptr()
+    raise QSAError(QSA_ERR_INVALID_ARG, f"{name} must be a contiguous {dtypes[0]} tensor of at least {n} elements on the current "
+                                        f"device (got {_what(t)})")
+
+
+def _what(t) -> str:
+    if not isinstance(t, torch.Tensor):
+        return repr(t)
+    return f"{t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, {t.device}"
+
+
+def _pool(kq, ksc, vq, vsc, n_pool: int):
+    codes, scales = n_pool * (N_GROUPS * HEAD_DIM), n_pool * (N_GROUPS * 4)
+    return (_array(kq, "kq", _I8, codes), _array(ksc, "ksc", _F16, scales), _array(vq, "vq", _I8, codes),
+            _array(vsc, "vsc", _F16, scales))
+
+
+def _probabilities(t, name: str, vocab: int, n_tok: int):
+    """The pointer and row stride of fp32 rows [n_tok, vocab or more]; entries of a row lie side by side."""
+    if t is None or isinstance(t, int):
+        return t, vocab
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.dim() == 2 and t.shape[0] >= n_tok and t.shape[1] >= vocab
+            and (t.stride(1) == 1 or vocab == 1) and (n_tok <= 1 or t.stride(0) >= vocab)
+            and (t.is_cuda and t.get_device() == torch.cuda.current_device() or not t.numel())):
+        return t.data_ptr(), max(t.stride(0), vocab)
+    raise QSAError(QSA_ERR_INVALID_ARG, f"{name} must be a float32 tensor [{n_tok}, {vocab}] on the current device whose rows have "
+                                        f"their elements side by side (got {_what(t)})")
+
+
+def qsa_tree_verify(p, d, vocab: int, token, parent, u, u_end, seqs, n_seq: int, n_tok: int, path, n_path, next, stream=None):
+    """The accepted path of each drafted tree and the token behind it.  p and d float32 [n_tok, vocab or more] (d may be
+    None), token and parent int32 [n_tok], u float32 [n_tok], u_end float32 [n_seq], path int32 [n_seq, cap]."""
+    pp, ps = _probabilities(p, "p", vocab, n_tok)
+    dp, ds = _probabilities(d, "d", vocab, n_tok)
+    cap = path.shape[1]
+    _check(load().qsa_tree_verify(pp, ps, dp, ds, vocab, _array(token, "token", _I32, n_tok), _array(parent, "parent", _I32, n_tok),
+                                  _array(u, "u", _F32, n_tok), _array(u_end, "u_end", _F32, n_seq),
+                                  _array(seqs, "seqs", _I32, 4 * n_seq), n_seq, n_tok, _array(path, "path", _I32, n_seq * cap), cap,
+                                  _array(n_path, "n_path", _I32, n_seq), _array(next, "next", _I32, n_seq), _stream(stream)))
+
+
+def qsa_cache_copy(kq, ksc, vq, vsc, n_pool: int, runs, n_run: int, max_cells: int, stream=None):
+    """Runs of cells copied inside the pool; runs int32 [n_run, 4] {source, destination, cells, -} of at most max_cells."""
+    _check(load().qsa_cache_copy(*_pool(kq, ksc, vq, vsc, n_pool), n_pool, _array(runs, "runs", _I32, 4 * n_run), n_run, max_cells,
+                                 _stream(stream)))
+
+
+def qsa_cache_compact_workspace_bytes(n_pool: int, n_prefix: int, n_seq: int) -> int:
+    return int(load().qsa_cache_compact_workspace_bytes(n_pool, n_prefix, n_seq))
+
+
+def qsa_cache_compact(kq, ksc, vq, vsc, n_pool: int, prefixes, n_prefix: int, seqs, n_seq: int, prefixes_out, seqs_out, used, ws,
+                      stream=None):
+    """The runs of a prefix and a sequence table (int32 [n, 4]) moved together to the front of the pool, in place; used
+    is an int32 tensor of one element, or None."""
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(load().qsa_cache_compact(*_pool(kq, ksc, vq, vsc, n_pool), n_pool, _array(prefixes, "prefixes", _I32, 4 * n_prefix),
+                                    n_prefix, _array(seqs, "seqs", _I32, 4 * n_seq), n_seq,
+                                    _array(prefixes_out, "prefixes_out", _I32, 4 * n_prefix),
+                                    _array(seqs_out, "seqs_out", _I32, 4 * n_seq), _array(used, "used", _I32, 1, True), _ptr(ws),
+                                    ws_bytes, _stream(stream)))
 
 
 def qsa_debug_wait_probe(budget_ns: int, stream=None):
