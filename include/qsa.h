@@ -476,6 +476,48 @@ QSA_API int qsa_tree_verify(const float* p, int64_t p_stride, const float* d, in
                             const int32_t* parent, const float* u, const float* u_end, const int32_t* seqs, int n_seq, int n_tok,
                             int32_t* path, int path_cap, int32_t* n_path, int32_t* next, void* stream);
 
+/* Bytes of device workspace qsa_prefix_attention needs (0 for invalid arguments).  For given params it grows with each
+ * of its arguments, so a workspace for a server's largest values serves every call of smaller ones. */
+QSA_API size_t qsa_prefix_attention_workspace_bytes(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv,
+                                                    const qsa_params* params);
+
+/*
+ * qsa_prefix_attention - attention of many sequences' tokens (decoded, drafted) behind shared prefixes, whose cells are
+ * read, scored and attended to once for all of them.  Token i of sequence s is row seqs[s][3] + i of q / tree / ids / out,
+ * its K/V are already in the sequence's own cell pos0 + i (pos0 = seqs[s][2] own cells are committed).  It sees
+ * the P cells of its sequence's prefix, the own cells 0 .. pos0 - 1, and the own cells pos0 + j whose bit j is set in its
+ * mask, as in qsa_tree_attention; without masks (tree NULL) j <= i.  Cells are counted prefix first: own cell c is
+ * cell P + c.  n_kv of a token is the number of cells it sees; it attends to all of them while n_kv <= identity_max,
+ * else to the topk of them with the largest selection score (the exact ranking of qsa_select, equal scores going to the
+ * lower cell):
+ *   out[t,h,:] = fp16( sum_{c in set(t,g)} softmax_c(sm_scale * q[t,h,:] . k^[c,g,:]) * v^[c,g,:]
+ *                      * (gate ? 1 / (1 + exp(-gate[t,h,:])) : 1) )
+ * with k^ = fp16(kq * ksc) and v^ = fp16(vq * vsc), the values that the prefill attends to and qsa_cache_read gives;
+ * softmax weights are held in fp16 relative to the row's largest, statistics and sums in fp32.  A token that sees no
+ * cell gets zeros.  Own cells that no token sees may hold anything; cells that some token sees must be finite, as in
+ * qsa_tree_attention.
+ *   prefixes  DEVICE [n_prefix][4] int32 {first pool cell, cells, first sequence, -}, 16-byte aligned: prefix p is that of the
+ *         sequences prefixes[p][2] .. prefixes[p + 1][2] - 1 (the first begins with sequence 0, the last runs to n_seq); a
+ *         prefix of 0 cells is none.  NULL with n_prefix 0: no sequence has one
+ *   seqs  DEVICE [n_seq][4] int32 {first pool cell, n_cells, pos0, first token row} of the own cells, as in
+ *         qsa_tree_attention; n_cells 0: padding, whose rows are left as they are.  At most 32 * tree_words tokens a
+ *         sequence, 256 without masks
+ *   tree  DEVICE [n_tok][tree_words] uint32, tree_words 1 .. 8, or NULL
+ *   max_prefix, max_n_kv  upper bounds on every prefix's cells and on every sequence's P + pos0 + token count; max_n_kv at
+ *         most 1048576, and at most 65409 where it exceeds identity_max
+ *   ids   [n_tok][2][topk] int32, or NULL: the cells of selected tokens, ascending (rows of other tokens are not written)
+ *   gate, out  [n_tok][24][256] fp16; gate may be NULL
+ *   ws    qsa_prefix_attention_workspace_bytes(...) bytes, 16-byte aligned, clobbered.  Calls that overlap on the GPU (two
+ *         streams, two captured graphs) need a workspace each.
+ * A sequence whose entry or prefix breaks these rules is skipped (its rows are not written) and flagged in the status
+ * word (QSA_ERR_DEVICE).  n_prefix, n_tok and n_seq at most 65535; n_tok or n_seq 0 does nothing.
+ */
+QSA_API int qsa_prefix_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, const uint16_t* ksc, const uint16_t* vsc,
+                                 int64_t n_pool, const int32_t* prefixes, int n_prefix, const int32_t* seqs, int n_seq, int n_tok,
+                                 const uint32_t* tree, int tree_words, int max_prefix, int max_n_kv, int32_t* ids,
+                                 const uint16_t* gate, uint16_t* out, void* ws, size_t ws_bytes, const qsa_params* params,
+                                 void* stream);
+
 /*
  * qsa_cache_copy - runs of cells (codes and scales of K and V) copied from place to place in the pool: for run r and
  * i < runs[r][2], cell runs[r][0] + i is copied to cell runs[r][1] + i.

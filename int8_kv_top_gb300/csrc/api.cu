@@ -138,6 +138,7 @@ int decode_layer_limit(int* rc) {
 }
 
 constexpr int kTreeMost = 65535;  // tokens, and sequences, of a tree call
+constexpr int kSharedMost = 1 << 20;  // cells that a token of a shared call may see
 
 // Whether a tree call selects for its tokens together (tree_select.cu, then one tensor-core attention for all)
 // or gives each selected (token, group) a cluster of its own.  Together costs by the sequences and their cells,
@@ -670,6 +671,66 @@ int qsa_cache_commit(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64
                                            reinterpret_cast<const int4*>(seqs), n_seq, path, n_path, path_cap, st,
                                            static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "qsa_cache_commit launch");
+  return ok();
+}
+
+size_t qsa_prefix_attention_workspace_bytes(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv,
+                                            const qsa_params* params) {
+  qsa::Params p{};
+  if (n_prefix < 0 || n_seq < 1 || n_tok < 1 || n_prefix > kTreeMost || n_seq > kTreeMost || n_tok > kTreeMost || max_prefix < 0 ||
+      max_n_kv < 1 || max_prefix > max_n_kv || max_n_kv > kSharedMost || resolve_params(params, &p) != QSA_OK)
+    return 0;
+  return qsa::prefix_attention_workspace_bytes(n_prefix, n_seq, n_tok, max_prefix, max_n_kv, p.identity_max);
+}
+
+int qsa_prefix_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, const uint16_t* ksc, const uint16_t* vsc,
+                         int64_t n_pool, const int32_t* prefixes, int n_prefix, const int32_t* seqs, int n_seq, int n_tok,
+                         const uint32_t* tree, int tree_words, int max_prefix, int max_n_kv, int32_t* ids, const uint16_t* gate,
+                         uint16_t* out, void* ws, size_t ws_bytes, const qsa_params* params, void* stream) {
+  qsa::Params p;
+  int rc = resolve_params(params, &p);
+  if (rc) return rc;
+  if (n_prefix < 0 || n_seq < 0 || n_tok < 0)
+    return fail(QSA_ERR_INVALID_ARG, "n_prefix, n_seq and n_tok must be >= 0 (got %d, %d, %d)", n_prefix, n_seq, n_tok);
+  if (n_prefix > kTreeMost || n_tok > kTreeMost || n_seq > kTreeMost)
+    return fail(QSA_ERR_UNSUPPORTED, "n_prefix, n_seq and n_tok must be at most %d (got %d, %d, %d)", kTreeMost, n_prefix, n_seq, n_tok);
+  if (tree && (tree_words < 1 || tree_words > qsa::kTreeWords))
+    return fail(QSA_ERR_UNSUPPORTED, "tree_words must be in [1, %d] (got %d)", qsa::kTreeWords, tree_words);
+  if (n_pool <= 0 || n_pool > 0x7fffffffLL)
+    return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
+  if (max_n_kv < 1) return fail(QSA_ERR_INVALID_ARG, "max_n_kv must be positive (got %d)", max_n_kv);
+  if (max_prefix < 0 || max_prefix > max_n_kv)
+    return fail(QSA_ERR_INVALID_ARG, "max_prefix must be in [0, max_n_kv = %d] (got %d)", max_n_kv, max_prefix);
+  const int limit = max_n_kv > p.identity_max ? qsa::select_max_cells() - 127 : kSharedMost;
+  if (max_n_kv > limit)
+    return fail(QSA_ERR_UNSUPPORTED, "max_n_kv must be at most %d%s (got %d)", limit,
+                limit == kSharedMost ? "" : " where it exceeds identity_max", max_n_kv);
+  if (n_tok == 0 || n_seq == 0) return ok();
+  CHECK_PTR(q, "q");
+  CHECK_PTR(kq, "kq");
+  CHECK_PTR(vq, "vq");
+  CHECK_PTR(ksc, "ksc");
+  CHECK_PTR(vsc, "vsc");
+  if (n_prefix) CHECK_PTR(prefixes, "prefixes");
+  CHECK_PTR(seqs, "seqs");
+  CHECK_PTR(out, "out");
+  if (tree && !aligned16(tree)) return fail(QSA_ERR_INVALID_ARG, "tree is not 16-byte aligned");
+  if (ids && !aligned16(ids)) return fail(QSA_ERR_INVALID_ARG, "ids is not 16-byte aligned");
+  if (gate && !aligned16(gate)) return fail(QSA_ERR_INVALID_ARG, "gate is not 16-byte aligned");
+  const size_t need = qsa_prefix_attention_workspace_bytes(n_prefix, n_seq, n_tok, max_prefix, max_n_kv, params);
+  if (!ws || ws_bytes < need)
+    return fail(QSA_ERR_WORKSPACE, "prefix attention workspace of %zu bytes given, %zu needed", ws ? ws_bytes : (size_t)0, need);
+  if (!aligned16(ws)) return fail(QSA_ERR_INVALID_ARG, "ws is not 16-byte aligned");
+  int* st = status_ptr(&rc);
+  if (!st) return rc;
+  qsa::TreeBatch b{reinterpret_cast<const int4*>(seqs), (long long)n_pool, n_seq, n_tok, tree, tree_words, max_n_kv, p.identity_max};
+  b.prefixes = reinterpret_cast<const int4*>(prefixes);
+  b.n_prefix = n_prefix;
+  b.max_prefix = max_prefix;
+  cudaError_t e = qsa::launch_prefix_attention(b, reinterpret_cast<const __half*>(q), kq, vq, reinterpret_cast<const __half*>(ksc),
+                                               reinterpret_cast<const __half*>(vsc), ids, reinterpret_cast<const __half*>(gate),
+                                               reinterpret_cast<__half*>(out), ws, p, st, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qsa_prefix_attention launch");
   return ok();
 }
 

@@ -151,6 +151,17 @@ cudaError_t launch_tree_topk(const TreeBatch& b, const TreeSelect& w, const __ha
 cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
                               const __half* vsc, const uint32_t* bits, int bits_pitch, const __half* gate, __half* out,
                               void* ws, float sm_scale, int* status, cudaStream_t stream);
+struct TreeParts {  // unmerged rows of blocks (tree.cu): O [CTA][64][128][4] and (m, l) [CTA][128], `runs` pairs a block and group
+  const float4* o;
+  const float2* ml;
+  int runs;  // 0: none
+};
+size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells);
+cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, const __half* q, const int8_t* kq, const int8_t* vq,
+                              const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
+                              float sm_scale, TreeParts* parts, int* status, cudaStream_t stream);
+cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int own_cells, const __half* q, const int8_t* kq,
+                                 const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream);
 int4* tree_dense_plan(const TreeBatch& b, void* ws);  // where its list of blocks goes, or null
 size_t tree_dense_workspace_bytes(int n_seq, int n_tok, int max_n_kv);  // grows with each argument
 
@@ -200,6 +211,12 @@ cudaError_t launch_cache_read(const int8_t* kq, const __half* ksc, const int8_t*
 cudaError_t launch_cache_commit(int8_t* kq, __half* ksc, int8_t* vq, __half* vsc, int64_t n_pool, const int4* seqs,
                                 int n_seq, const int32_t* path, const int32_t* n_path, int path_cap, int* status,
                                 cudaStream_t stream);
+
+// Attention behind shared prefixes (prefix.cu).
+size_t prefix_attention_workspace_bytes(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv, int identity_max);
+cudaError_t launch_prefix_attention(const TreeBatch& b, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc,
+                                    const __half* vsc, int32_t* ids, const __half* gate, __half* out, void* ws, Params p,
+                                    int* status, cudaStream_t stream);
 
 // Runs of cells (cache_runs.cu): copied from place to place (runs {source, destination, cells, -}), and the runs of
 // a prefix and a sequence table put side by side at the front of the pool, in place.

@@ -722,7 +722,9 @@ __device__ uint32_t first_key_warp(P pred) {
 //
 // kTree: rows are the drafted tokens of a tree batch (row, group); the scores of cells that a token does not
 // see are -inf, its selected cells go to a bitmap as well, and `ids` may be null.
-template <int V, bool kTree>
+// kShared: the rows of a shared call (qsa_prefix_attention): columns are the prefix's cells, a gap of -inf up to a whole
+// tile, and the sequence's own cells.
+template <int V, bool kTree, bool kShared = false>
 __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     topk_kernel(const __half* __restrict__ scores, const __half* __restrict__ q, const int8_t* __restrict__ kq,
                 const __half* __restrict__ ksc, const float* __restrict__ eh, const float* __restrict__ kmax,
@@ -755,7 +757,27 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
   const __half* row = scores + ((size_t)g * T_sel + r) * n_pad;
   float row_scale = 1.f;    // of the stored scores
   float km[kNB];
-  if constexpr (kTree) {
+  int shared = 0, gap = 0;        // kShared: the prefix's cells, and the columns between them and the own ones
+  long long cell0 = 0, own0 = 0;  // pool cells of column 0 and, of the own columns, of column 0 continued backwards
+  auto pool_cell = [&](int c) -> size_t { return kShared ? (size_t)(c + (c < shared ? cell0 : own0)) : (size_t)c; };
+  if constexpr (kShared) {
+    const int4 ti = __ldg(&tb.tok[t]);
+    if (ti.x < 0 || ti.y <= tb.identity_max) return;  // uniform, as all that follows
+    const int4 e = __ldg(&tb.seqs[ti.x]);
+    const int T = (ti.x + 1 < tb.n_seq ? __ldg(&tb.seqs[ti.x + 1].w) : tb.n_tok) - e.w;
+    shared = ti.z;
+    const int own = own_column(shared);
+    gap = own - shared;
+    n_kv = own + e.z + T;
+    cell0 = ti.w >= 0 ? __ldg(&tb.prefixes[ti.w].x) : 0;
+    own0 = (long long)e.x - own;
+    if (warp == 0) {
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) km[b] = 0.f;
+      shared_kmax(tb, ts, ti, e.z + T, g, lane, km);
+      row_scale = tree_row_scale(eh + ((size_t)g * T_sel + r) * 8, km, sm_scale);
+    }
+  } else if constexpr (kTree) {
     const int s = warp_find_seq(tb.n_seq, t, [&](int i) { return (long long)__ldg(&tb.seqs[i].w); });
     int4 e;
     const int T = tree_seq_tokens(tb, s, &e);
@@ -1012,11 +1034,11 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
       for (int x = tid; x < nb * 16; x += kTkThreads) {
         const int c = s_band_idx[i0 + (x >> 4)];
         cp_async16(s_stage + (x >> 4) * kStageStride + (x & 15) * 16,
-                   kq + ((size_t)c * kGroups + g) * kD + (x & 15) * 16);
+                   kq + (pool_cell(c) * kGroups + g) * kD + (x & 15) * 16);
       }
       for (int x = tid; x < nb; x += kTkThreads) {
         const int c = s_band_idx[i0 + x];
-        s_stage_sc[x] = *reinterpret_cast<const uint2*>(ksc + ((size_t)c * kGroups + g) * kNB);
+        s_stage_sc[x] = *reinterpret_cast<const uint2*>(ksc + (pool_cell(c) * kGroups + g) * kNB);
       }
       cp_async_wait_all();
       __syncthreads();
@@ -1082,8 +1104,8 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
       return k >= k_band && k < k_def;
     };
     auto bkey = [&](int c) -> unsigned __int128 {
-      unsigned __int128 kb = (unsigned __int128)exact_key(s_qsum, kq + ((size_t)c * kGroups + g) * kD,
-                                                          ksc + ((size_t)c * kGroups + g) * kNB);
+      unsigned __int128 kb = (unsigned __int128)exact_key(s_qsum, kq + (pool_cell(c) * kGroups + g) * kD,
+                                                          ksc + (pool_cell(c) * kGroups + g) * kNB);
       return kb ^ ((unsigned __int128)1 << 127);
     };
     unsigned __int128 pre = 0;
@@ -1163,7 +1185,8 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     while (k) {
       const int j = __ffs(k) - 1;
       k &= k - 1;
-      if (pos < K) dst[pos] = c0 + 8 * m + j;
+      const int c = c0 + 8 * m + j;
+      if (pos < K) dst[pos] = kShared && c >= shared ? c - gap : c;
       ++pos;
     }
   }
@@ -1304,6 +1327,13 @@ cudaError_t launch_tree_topk(const TreeBatch& b, const TreeSelect& w, const __ha
                       w.kmax, static_cast<const unsigned*>(nullptr), ids, 0, b.n_tok, w.pitch, 0, p.topk, p.sm_scale,
                       status, b, w);
   };
+  if (b.tok != nullptr) {  // a shared call: up to a tile's gap between the prefix's cells and the own ones
+    const int columns = b.max_n_kv + 127;
+    if (columns <= 16 * kTkThreads) return run(topk_kernel<16, true, true>);
+    if (columns <= 32 * kTkThreads) return run(topk_kernel<32, true, true>);
+    if (columns <= 64 * kTkThreads) return run(topk_kernel<64, true, true>);
+    return run(topk_kernel<128, true, true>);
+  }
   if (b.max_n_kv <= 16 * kTkThreads) return run(topk_kernel<16, true>);
   if (b.max_n_kv <= 32 * kTkThreads) return run(topk_kernel<32, true>);
   if (b.max_n_kv <= 64 * kTkThreads) return run(topk_kernel<64, true>);

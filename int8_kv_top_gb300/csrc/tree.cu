@@ -116,65 +116,62 @@ struct __align__(8) TreeBars {
   uint64_t q_full, tmem_ready, drain;
 };
 
-// Rows of a block that exist are shared out evenly: its CTA `half` of each pair has rows [x, x + n) of the tree, so
-// that the loads of Q and the stores of O, 1 KB a row, are halved where a block is not full.
-__device__ __forceinline__ int cta_rows(int T, int blk_row0, int half, int* x) {
-  const int n = min(2 * kRows, T * kHPG - blk_row0), first = (n + 1) / 2;
-  *x = blk_row0 + half * first;
-  return half ? n - first : first;
-}
-
-// Index of a sequence's first block in the grid: block k of sequence s has index first_block(s) + k.
-// The sequences' ranges never meet, since floor((a + b) / 256) + 1 >= floor(a / 256) + ceil(b / 256), so
-// a block finds its sequence by a search over the table, without a prefix sum; some indices stay unused.
-__device__ __forceinline__ long long first_block(long long first_row, int s) { return first_row * kHPG / (2 * kRows) + s; }
-
-// Eight dims of an output row: the gate's sigmoid, and the rounding to fp16.
-__device__ __forceinline__ void apply_gate(float (&v)[8], uint4 gw) {
-  const uint32_t w[4] = {gw.x, gw.y, gw.z, gw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] *= gate_sigmoid(f.x);
-    v[2 * i + 1] *= gate_sigmoid(f.y);
-  }
-}
-__device__ __forceinline__ uint4 pack_out(const float (&v)[8]) {
-  return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
-}
-
 // Block `blk` of the grid, by a warp: whether there is one, its sequence's {first pool cell, -, committed cells, first
-// token row}, drafted tokens and the block's first row; for lane = token of the block its mask words, whether it is
+// token row}, tokens, drafted cells and the block's first row; for lane = token of the block its mask words, whether it is
 // computed here and whether it is a selected one.
 struct BlockAt {
   int4 e;
-  int T, row0;
+  int T, drafted, row0;
   uint32_t m[kTreeWords];
   bool ours, sel;
 };
+template <CellsOf kOf>
 __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4* plan, bool with_selected, int blk, int lane) {
   BlockAt x;
   bool here;
-  if (plan != nullptr) {
+  if (kOf == kTreeCells && plan != nullptr) {
     const int4 head = __ldg(&plan[0]), at = __ldg(&plan[1 + 2 * blk]);
     x.row0 = __ldg(&plan[2 + 2 * blk].x);
     here = blk < head.x;
     x.e = make_int4(at.x, 0, at.y, at.w);
     x.T = at.z;
   } else {
-    const int sq = warp_find_seq(b.n_seq, blk, [&](int s) { return first_block(__ldg(&b.seqs[s].w), s); });
-    x.T = tree_seq_tokens(b, sq, &x.e);
+    int sq;
+    if constexpr (kOf == kPrefixCells) {
+      int4 pe;
+      sq = warp_find_seq(b.n_prefix, blk, [&](int p) {
+        int4 f;
+        prefix_tokens(b, p, &f);
+        return first_block(f.w, p);
+      });
+      x.T = prefix_tokens(b, sq, &pe);
+      if (pe.y == 0) x.T = 0;
+      x.e = make_int4(pe.x, 0, pe.y, pe.w);
+    } else {
+      sq = warp_find_seq(b.n_seq, blk, [&](int s) { return first_block(__ldg(&b.seqs[s].w), s); });
+      int p, cells;
+      x.T = kOf == kTreeCells ? tree_seq_tokens(b, sq, &x.e) : shared_seq_tokens(b, sq, &x.e, &p, &cells);
+    }
     const long long k = blk - first_block(x.e.w, sq);
     here = x.T > 0 && k >= 0 && k * kTreeBlock < (long long)x.T * kHPG;
     x.row0 = here ? (int)k * kTreeBlock : 0;
   }
+  x.drafted = kOf == kPrefixCells ? 0 : x.T;
   const int tok = x.row0 / kHPG + lane;
   const bool live = here && lane < kMaxTok && tok < x.T && tok * kHPG < x.row0 + 2 * kRows;
   int n_kv = x.e.z;
 #pragma unroll
   for (int w = 0; w < kTreeWords; ++w) {
-    x.m[w] = live ? tree_mask_word(b, x.e.w + tok, w, x.T) : 0u;
+    x.m[w] = 0u;
+    if (kOf != kPrefixCells && live)
+      x.m[w] = kOf == kTreeCells ? tree_mask_word(b, x.e.w + tok, w, x.T) : shared_mask_word(b, x.e.w + tok, tok, w, x.T);
     n_kv += __popc(x.m[w]);
+  }
+  if constexpr (kOf != kTreeCells) {
+    const int4 t = live ? b.tok[x.e.w + tok] : make_int4(-1, 0, 0, 0);
+    x.ours = t.x >= 0;
+    x.sel = x.ours && t.y > b.identity_max;
+    return x;
   }
   x.sel = live && n_kv > b.identity_max;
   x.ours = live && (!x.sel || with_selected);
@@ -186,13 +183,14 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeBatch
   tree_plan_blocks(b, false, plan, tree_blocks_most(b.n_seq, b.n_tok));
 }
 
+template <CellsOf kOf>
 __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_constant__ DenseTreeArgs a, int S) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ TreeBars bars;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_blk[8];                       // active, first pool cell, pos0, T, first token row, first row
+  __shared__ int s_blk[8];                       // active, first pool cell, pos0, T, first token row, first row, drafted cells
   __shared__ uint32_t s_mask[kMaxTok][kTreeWords];
   __shared__ uint32_t s_union[kTreeWords];       // drafted cells that some token of ours sees
   __shared__ int s_ours, s_sel;                  // bit i: token i of the block is computed here; is a selected one
@@ -218,14 +216,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
   cluster_arrive_all();  // #0, waited for before the first remote access: every CTA's barriers are set up
   pdl_begin();
-  if (blockIdx.x == 0) {  // one CTA looks over the whole table and flags bad entries
+  if (kOf == kTreeCells && blockIdx.x == 0) {  // one CTA looks over the whole table and flags bad entries
     for (int s = tid; s < a.b.n_seq; s += kThreads) {
       int4 e;
       if (tree_seq_tokens(a.b, s, &e) < 0) set_dev_status(a.status, QSA_DEV_BAD_ID);
     }
   }
   if (warp == 0) {
-    const BlockAt x = tree_block_at(a.b, a.plan, a.bits != nullptr, blk, lane);
+    const BlockAt x = tree_block_at<kOf>(a.b, a.plan, a.bits != nullptr, blk, lane);
     const unsigned all_ours = __ballot_sync(0xffffffffu, x.ours), all_sel = __ballot_sync(0xffffffffu, x.sel);
 #pragma unroll
     for (int w = 0; w < kTreeWords; ++w) {
@@ -242,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       s_blk[3] = x.T;
       s_blk[4] = x.e.w;
       s_blk[5] = x.row0;
+      s_blk[6] = x.drafted;
     }
   }
   __syncthreads();
@@ -253,15 +252,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   const int pos0 = s_blk[2], T = s_blk[3], first = s_blk[4], blk_row0 = s_blk[5];
   int row0;  // this CTA's first row
   const int n_rows = cta_rows(T, blk_row0, half, &row0);
-  const int n_scan = pos0 + T;
+  const int drafted = kOf == kTreeCells ? T : s_blk[6];  // cells behind the committed ones
+  const int n_scan = pos0 + drafted;
   const int n_tiles = (n_scan + kTileCells - 1) / kTileCells;
   const int j_begin = n_tiles * run / pairs, J = n_tiles * (run + 1) / pairs - j_begin;  // the same in both CTAs of a pair
   auto pair_addr = [&](const void* p) { return mapa_shared(smem_u32(p), (uint32_t)rank & ~1u); };  // in rank 0
+  const bool merges = kOf == kTreeCells && a.runs == 1;  // in this launch; else the parts are joined by another
   float m_run = -INFINITY, l_run = 0.f;  // softmax threads: the row's running maximum (log2 units), this half's sum
   bool ok = true;
 
   if (warp < 8) {
-    const TileRun t{cell0, pos0, T, j_begin, J, g, s_union, &s_abort, a.status, half};
+    const TileRun t{cell0, pos0, drafted, j_begin, J, g, s_union, &s_abort, a.status, half};
     const bool is_v = warp >= 4;
     produce_tiles<kPair>(t, is_v ? a.vq : a.kq, is_v ? a.vsc : a.ksc, smem_u32(smem + (is_v ? kOffV : kOffK)),
                          is_v ? bars.v_full : bars.k_full, is_v ? bars.v_empty : bars.k_empty, warp & 3, lane, 0, is_v);
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
           src += (kHeads - kHPG) * kD;
         }
       }
-      if (a.gate && pairs == 1) {  // 512 bytes a row: into L2 while the tiles run
+      if (a.gate && merges && pairs == 1) {  // 512 bytes a row: into L2 while the tiles run
         for (int i = st; i < n_rows * 4; i += 256) {
           const int R = row0 + (i >> 2);
           const __half* at = a.gate + ((size_t)(first + R / kHPG) * kHeads + g * kHPG + R % kHPG) * kD + (i & 3) * 64;
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     const bool active = r < n_rows && ((s_ours >> min(ti, 31)) & 1), chosen = active && ((s_sel >> min(ti, 31)) & 1);
     const uint2* sel_bits = reinterpret_cast<const uint2*>(
         chosen ? a.bits + (size_t)(g * a.b.n_tok + first + R / kHPG) * a.bits_pitch : nullptr);
+    if (kOf == kOwnCells && chosen) sel_bits += own_column(a.b.tok[first + R / kHPG].z) / 64;
     uint2 m_next = make_uint2(0u, 0u);  // a selected row's bits, loaded a tile ahead
     if (chosen && J > 0) m_next = __ldg(sel_bits + 2 * j_begin + wg);
     // 32 visibility bits from drafted cell x on: cells before the drafted ones are seen, those past the mask not
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     if (!all_ok) m_run = -INFINITY;
     if (wg == 0) {
       const float l = l_run + s_xm[1][r];
-      if (a.runs > 1) a.part_ml[(size_t)blockIdx.x * kRows + r] = make_float2(m_run, l);
+      if (!merges) a.part_ml[(size_t)blockIdx.x * kRows + r] = make_float2(m_run, l);
       const uint32_t at = smem_u32(smem + kOffML) + (uint32_t)(pair * kRows + r) * 8u;
       for (int c = 0; c < S; ++c)
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(at, 2 * c + half)), "f"(m_run), "f"(l)
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
         uint32_t o[32];
         tmem_ld32(lane_base + kColO + c0, o);
         tmem_wait_ld();
-        if (pairs == 1) {
+        if (merges && pairs == 1) {
           float4* dst = reinterpret_cast<float4*>(smem + (size_t)r * (kOStride * 4)) + c0 / 4;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   cluster_wait_all();  // #1: the cluster's rows and statistics are visible; no CTA touches another after this
   tc_fence_after();
   if (warp == 16 && J > 0) tmem_dealloc_pair(*reinterpret_cast<volatile uint32_t*>(&s_tmem), 512);
-  if (warp < 16 && a.runs == 1) {  // else tree_join_kernel merges
+  if (warp < 16 && merges) {  // else tree_join_kernel, or prefix_join_kernel, merges
     const float2* ml = reinterpret_cast<const float2*>(smem + kOffML);
     auto row_at = [&](int r, size_t* at) {  // this CTA's row r: is it one of ours, and where its output starts
       const int R = row0 + r, ti = R / kHPG - blk_row0 / kHPG;
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_join_kernel(const __grid
   const int chunk = blockIdx.x % kChunks, g = blockIdx.x / kChunks % kGroups, blk = blockIdx.x / kChunks / kGroups;
   const int half = chunk / (kChunks / 2), r0 = chunk % (kChunks / 2) * kJoinRows;
   if (tid < 32) {
-    const BlockAt x = tree_block_at(a.b, a.plan, a.bits != nullptr, blk, tid);
+    const BlockAt x = tree_block_at<kTreeCells>(a.b, a.plan, a.bits != nullptr, blk, tid);
     const unsigned all_ours = __ballot_sync(0xffffffffu, x.ours);
     if (tid == 0) {
       s_ours = all_ours;
@@ -757,14 +759,15 @@ cudaError_t tree_setup(PlanHeld* held) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if ((e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(tree_dense_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    for (auto* k : {tree_dense_kernel<kTreeCells>, tree_dense_kernel<kPrefixCells>, tree_dense_kernel<kOwnCells>})
+      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(tree_dense_kernel<kTreeCells>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
       return e;
     for (int i = 0; i < kPlanSizesN; ++i) {
       cudaLaunchAttribute attr[2];
       const cudaLaunchConfig_t cfg = tree_config(kPlanSizes[i], 1, nullptr, attr);
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, tree_dense_kernel, &cfg) != cudaSuccess) {
+      if (cudaOccupancyMaxActiveClusters(&n, tree_dense_kernel<kTreeCells>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();  // a size that this GPU does not take
         n = 0;
       }
@@ -815,8 +818,31 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
                         d.runs, status};
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = tree_config(d.pairs, d.blocks * kGroups * d.runs, stream, attr);
-  if ((e = cudaLaunchKernelEx(&cfg, tree_dense_kernel, a, d.pairs)) != cudaSuccess || d.runs == 1) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, tree_dense_kernel<kTreeCells>, a, d.pairs)) != cudaSuccess || d.runs == 1) return e;
   return launch_pdl(tree_join_kernel, dim3(d.blocks * kGroups * (2 * kRows / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
+}
+
+// The parts of a shared call: of its prefixes' cells, or of its sequences' own ones.
+size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells) {
+  return (size_t)shared_parts_most(n, n_tok, max_cells) * 2 * kRows * (kD * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, const __half* q, const int8_t* kq, const int8_t* vq,
+                              const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
+                              float sm_scale, TreeParts* parts, int* status, cudaStream_t stream) {
+  PlanHeld held;
+  cudaError_t e = tree_setup(&held);
+  if (e != cudaSuccess) return e;
+  const int n = own ? b.n_seq : b.n_prefix, most_cells = own ? b.max_n_kv : b.max_prefix;
+  const int runs = shared_plan_runs(held.n[0], n, b.n_tok, cells, shared_parts_most(n, b.n_tok, most_cells));
+  const size_t rows = (size_t)shared_parts_most(n, b.n_tok, most_cells) * 2 * kRows;
+  float* part = static_cast<float*>(ws);
+  float2* ml = reinterpret_cast<float2*>(part + rows * kD);
+  *parts = TreeParts{reinterpret_cast<const float4*>(part), ml, runs};
+  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, nullptr, nullptr, nullptr, part, ml, runs, status};
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = tree_config(1, tree_blocks_most(n, b.n_tok) * kGroups * runs, stream, attr);
+  return own ? cudaLaunchKernelEx(&cfg, tree_dense_kernel<kOwnCells>, a, 1) : cudaLaunchKernelEx(&cfg, tree_dense_kernel<kPrefixCells>, a, 1);
 }
 
 }  // namespace qsa

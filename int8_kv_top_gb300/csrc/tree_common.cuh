@@ -14,9 +14,17 @@ struct TreeBatch {
   const int4* seqs;  // per sequence {first pool cell, n_cells, pos0, first token row}
   long long n_pool;
   int n_seq, n_tok;
-  const uint32_t* tree;  // [n_tok][tree_words]
+  const uint32_t* tree;  // [n_tok][tree_words]; of a shared call null as well: causal
   int tree_words, max_n_kv, identity_max;
+  // shared calls (qsa_prefix_attention) alone; max_n_kv then counts the prefix's cells too
+  const int4* prefixes = nullptr;  // per prefix {first pool cell, cells, first sequence, -}
+  int n_prefix = 0, max_prefix = 0;
+  int4* tok = nullptr;             // per token {sequence or -1, n_kv, prefix cells, prefix}: made by the call's first launch
 };
+
+// What a kernel that serves both kinds of calls works on: a tree call's sequences; the prefixes of a shared call, each
+// a sequence of committed cells whose tokens are those of all its sequences; the own cells of a shared call's sequences.
+enum CellsOf { kTreeCells, kPrefixCells, kOwnCells };
 
 // Sequence s's token count, or -1 when its entry breaks the contract; a padding sequence (no cells) has none.
 __device__ __forceinline__ int tree_seq_tokens(const TreeBatch& b, int s, int4* e_out) {
@@ -38,6 +46,64 @@ __device__ __forceinline__ uint32_t tree_mask_word(const TreeBatch& b, int row, 
   const uint32_t m = __ldg(b.tree + (size_t)row * b.tree_words + w);
   return left >= 32 ? m : m & ((1u << left) - 1u);
 }
+
+// ---------------------------------------------------------------- shared calls
+// Prefix p: its tokens (rows of all its sequences), or -1 when its entry breaks the contract; *e_out = {first pool cell,
+// cells, first sequence, first token row}.
+__device__ __forceinline__ int prefix_tokens(const TreeBatch& b, int p, int4* e_out) {
+  int4 e = __ldg(&b.prefixes[p]);
+  const int next = p + 1 < b.n_prefix ? __ldg(&b.prefixes[p + 1].z) : b.n_seq;
+  const bool seqs_ok = (p == 0 ? e.z == 0 : e.z >= 0) && next >= e.z && next <= b.n_seq;
+  const int row0 = seqs_ok && e.z < b.n_seq ? __ldg(&b.seqs[e.z].w) : b.n_tok;
+  const int row1 = seqs_ok && next < b.n_seq ? __ldg(&b.seqs[next].w) : b.n_tok;
+  e.w = row0;
+  *e_out = e;
+  const bool ok = seqs_ok && row0 >= 0 && row1 >= row0 && row1 <= b.n_tok && e.x >= 0 && e.y >= 0 && e.y <= b.max_prefix &&
+                  (long long)e.x + e.y <= b.n_pool;
+  return ok ? row1 - row0 : -1;
+}
+
+// The prefix of sequence s (the last whose first sequence is not behind s); -1 without prefixes.
+__device__ __forceinline__ int prefix_of(const TreeBatch& b, int s) {
+  if (b.n_prefix == 0) return -1;
+  int lo = 0, hi = b.n_prefix - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(&b.prefixes[mid].z) <= s) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// tree_seq_tokens of a shared call's sequence, with its prefix and the prefix's cells.
+__device__ __forceinline__ int shared_seq_tokens(const TreeBatch& b, int s, int4* e_out, int* p_out, int* cells_out) {
+  const int4 e = __ldg(&b.seqs[s]);
+  const int next = s + 1 < b.n_seq ? __ldg(&b.seqs[s + 1].w) : b.n_tok;
+  *e_out = e;
+  *p_out = -1;
+  *cells_out = 0;
+  const bool rows_ok = (s == 0 ? e.w == 0 : e.w >= 0) && next >= e.w && next <= b.n_tok;
+  if (rows_ok && e.y == 0) return 0;
+  const int p = prefix_of(b, s);
+  int4 pe = make_int4(0, 0, 0, 0);
+  const bool prefix_ok = p < 0 || prefix_tokens(b, p, &pe) >= 0;
+  *p_out = p;
+  *cells_out = pe.y;
+  const long long T = (long long)next - e.w, end = (long long)e.z + T;
+  const bool ok = prefix_ok && rows_ok && e.x >= 0 && e.y >= 1 && e.z >= 0 && end <= e.y && (long long)e.x + e.y <= b.n_pool &&
+                  pe.y + end <= b.max_n_kv && T <= 32 * (b.tree ? b.tree_words : kTreeWords);
+  return ok ? (int)T : -1;
+}
+
+// Word w of the mask of token i (row `row`) of a shared call's sequence of T tokens.
+__device__ __forceinline__ uint32_t shared_mask_word(const TreeBatch& b, int row, int i, int w, int T) {
+  if (b.tree != nullptr) return tree_mask_word(b, row, w, T);
+  const int n = i + 1 - 32 * w;  // causal
+  return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
+}
+
+// Columns of a shared call's rows of scores and selected cells: the prefix's cells, a gap up to a whole tile, the own cells.
+__device__ __forceinline__ int own_column(int prefix_cells) { return (prefix_cells + 127) & ~127; }
 
 // The last sequence whose key(s) is not above `at`, by a whole warp (32 probes a step); key is increasing and
 // key(0) is at most `at` in a valid table (else some sequence, whose entry the caller checks).
@@ -64,6 +130,8 @@ struct TreeSelect {
   __half* scores;    // [2][n_tok][pitch]
   uint32_t* bits;    // [2][n_tok][pitch / 32]: the selected cells
   int pitch, chunks;
+  float* kmax_prefix;  // shared calls: [n_prefix][chunks_prefix][8], likewise; kmax then counts the own cells
+  int chunks_prefix;
 };
 constexpr int kTreeChunk = 2048;  // cells of a kmax chunk
 
@@ -83,6 +151,29 @@ __device__ __forceinline__ void warp_kmax(const TreeSelect& w, int s, int g, int
     for (int o = 16; o > 0; o >>= 1) km[b] = fmaxf(km[b], __shfl_xor_sync(0xffffffffu, km[b], o));
 }
 
+// The same by one thread, raising km (own cells of a shared call's sequence: a few chunks).
+__device__ __forceinline__ void raise_kmax(const float* kmax, int i, int chunks, int g, int n_scan, float (&km)[kNB]) {
+  for (int c = 0; c * kTreeChunk < n_scan; ++c) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(kmax + ((size_t)i * chunks + c) * (kGroups * kNB) + g * kNB));
+    km[0] = fmaxf(km[0], v.x);
+    km[1] = fmaxf(km[1], v.y);
+    km[2] = fmaxf(km[2], v.z);
+    km[3] = fmaxf(km[3], v.w);
+  }
+}
+
+// Of a shared call's token (its record, and its sequence's own cells), by a whole warp.
+__device__ __forceinline__ void shared_kmax(const TreeBatch& b, const TreeSelect& w, const int4& tok, int n_own, int g, int lane,
+                                            float (&km)[kNB]) {
+  if (tok.w >= 0) {
+    TreeSelect v = w;
+    v.kmax = w.kmax_prefix;
+    v.chunks = w.chunks_prefix;
+    warp_kmax(v, tok.w, g, tok.z, lane, km);
+  }
+  raise_kmax(w.kmax, tok.x, w.chunks, g, n_own, km);
+}
+
 // A power of two that keeps a row's scores inside fp16: |score| <= sm_scale 128 sum_b kmax_b H_b.
 __device__ __forceinline__ float tree_row_scale(const float* eh, const float (&kmax)[kNB], float sm_scale) {
   float h = 0.f;
@@ -97,6 +188,19 @@ constexpr int kTileCells = 128;    // cells of a tile
 constexpr int kTreeBlock = 256;    // (token, head) rows of a block: a CTA pair's UMMA M
 constexpr int kPlanSeqs = 8;       // sequences from which on a launch takes its blocks from a list, longest first
 constexpr int kPlanThreads = 256;
+
+// Rows of a block that exist are shared out evenly: its CTA `half` of each pair has rows [x, x + n) of the tree, so
+// that the loads of Q and the stores of O, 1 KB a row, are halved where a block is not full.
+__device__ __forceinline__ int cta_rows(int T, int blk_row0, int half, int* x) {
+  const int n = min(kTreeBlock, T * kHPG - blk_row0), first = (n + 1) / 2;
+  *x = blk_row0 + half * first;
+  return half ? n - first : first;
+}
+
+// Index of a sequence's first block in the grid: block k of sequence s has index first_block(s) + k.
+// The sequences' ranges never meet, since floor((a + b) / 256) + 1 >= floor(a / 256) + ceil(b / 256), so
+// a block finds its sequence by a search over the table, without a prefix sum; some indices stay unused.
+__device__ __forceinline__ long long first_block(long long first_row, int s) { return first_row * kHPG / kTreeBlock + s; }
 
 // The list, by one CTA of kPlanThreads: plan[0].x blocks, then for block i plan[1 + 2 i] = {first pool cell,
 // committed cells, drafted tokens, first token row} of its sequence and plan[2 + 2 i].x = its first row, in decreasing
@@ -158,6 +262,20 @@ __device__ __forceinline__ void tree_plan_blocks(const TreeBatch& b, bool with_s
       }
     }
   }
+}
+
+// Eight dims of an output row: the gate's sigmoid, and the rounding to fp16.
+__device__ __forceinline__ void apply_gate(float (&v)[8], uint4 gw) {
+  const uint32_t w[4] = {gw.x, gw.y, gw.z, gw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] *= gate_sigmoid(f.x);
+    v[2 * i + 1] *= gate_sigmoid(f.y);
+  }
+}
+__device__ __forceinline__ uint4 pack_out(const float (&v)[8]) {
+  return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
 }
 
 // ---------------------------------------------------------------- waits

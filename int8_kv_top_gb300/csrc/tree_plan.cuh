@@ -100,4 +100,29 @@ inline DensePlan dense_plan(const PlanHeld& held, int n_seq, int n_tok, int max_
   return d;
 }
 
+// Shared calls (qsa_prefix_attention): every block's parts are written, whatever the number of runs, and a later
+// launch joins them with the rest of the token's cells.  How many pairs may write parts, and the runs of a block and group.
+inline long long shared_parts_most(int n, int n_tok, int max_cells) {
+  const long long blocks = tree_blocks_most(n, n_tok);
+  return std::max(blocks * kPlanGroups, parts_most(n, n_tok, max_cells));
+}
+
+inline int shared_plan_runs(int held, int n, int n_tok, int cells, long long most) {
+  const long long blocks = tree_blocks_most(n, n_tok), rows = (long long)n_tok * kPlanHeads;
+  const long long even = n * ((rows + (long long)n * kPlanRows - 1) / ((long long)n * kPlanRows));
+  const int tiles = plan_tiles(cells);
+  int best = 1;
+  double best_t = 0.0;
+  for (int runs = 1; runs <= std::min(kMaxRuns, tiles) && (runs == 1 || blocks * kPlanGroups * runs <= most); ++runs) {
+    const double w = (double)(even * kPlanGroups) * runs / held;
+    const double waves = n == 1 ? std::ceil(w) : 0.5 * (std::ceil(w) + std::max(1.0, 0.9 * w));
+    const double t = waves * (5.0 + (tiles + runs - 1) / runs) + kJoinPart * runs * (double)(even * kPlanGroups);
+    if (runs == 1 || t < best_t) {
+      best = runs;
+      best_t = t;
+    }
+  }
+  return best;
+}
+
 }  // namespace qsa

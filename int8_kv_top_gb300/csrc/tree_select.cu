@@ -138,6 +138,9 @@ struct __align__(8) TreeScoreBars {
 // First token chunk of a sequence: as first_block in tree.cu, for chunks of 32 tokens.
 __device__ __forceinline__ long long first_chunk(long long first_row, int s) { return first_row / kTokChunk + s; }
 
+// Of a shared call: once over the prefixes' cells for the tokens of all their sequences, and once over each sequence's own
+// cells; how many there are the host does not know, so there a chunk's CTAs share its tiles evenly (tiles_per_cta 0).
+template <CellsOf kOf>
 __global__ void __launch_bounds__(kScoreThreads, 1)
     tree_score_kernel(const TreeBatch b, const TreeSelect w, const int8_t* __restrict__ kq,
                       const __half* __restrict__ ksc, int tiles_per_cta, float sm_scale, int* status) {
@@ -151,14 +154,41 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = blockIdx.y;
   pdl_begin();
-  const int sq = warp_find_seq(b.n_seq, blockIdx.z, [&](int i) { return first_chunk(__ldg(&b.seqs[i].w), i); });
+  int sq, T, drafted;  // of the sequence, or of the prefix: tokens; cells behind the committed ones
   int4 e4;
-  const int T = tree_seq_tokens(b, sq, &e4);
+  if constexpr (kOf == kPrefixCells) {
+    int4 pe;
+    sq = warp_find_seq(b.n_prefix, blockIdx.z, [&](int i) {
+      int4 f;
+      prefix_tokens(b, i, &f);
+      return first_chunk(f.w, i);
+    });
+    T = prefix_tokens(b, sq, &pe);
+    e4 = make_int4(pe.x, 0, pe.y, pe.w);
+    drafted = 0;
+  } else {
+    sq = warp_find_seq(b.n_seq, blockIdx.z, [&](int i) { return first_chunk(__ldg(&b.seqs[i].w), i); });
+    int p, cells;
+    T = kOf == kTreeCells ? tree_seq_tokens(b, sq, &e4) : shared_seq_tokens(b, sq, &e4, &p, &cells);
+    drafted = T;
+  }
   const long long kc = (long long)blockIdx.z - first_chunk(e4.w, sq);
-  const int pos0 = e4.z, n_scan = pos0 + T;
-  const int j_begin = blockIdx.x * tiles_per_cta;
-  const int J = min(tiles_per_cta, (n_scan + kTileCells - 1) / kTileCells - j_begin);
-  if (T <= 0 || kc < 0 || kc * kTokChunk >= T || J <= 0 || n_scan <= b.identity_max) return;  // uniform
+  const int pos0 = e4.z, n_scan = pos0 + drafted, tiles = (n_scan + kTileCells - 1) / kTileCells;
+  int j_begin, J;
+  if constexpr (kOf == kTreeCells) {
+    j_begin = blockIdx.x * tiles_per_cta;
+    J = min(tiles_per_cta, tiles - j_begin);
+  } else {
+    j_begin = (int)((long long)tiles * blockIdx.x / gridDim.x);
+    J = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x) - j_begin;
+  }
+  if (T <= 0 || kc < 0 || kc * kTokChunk >= T || J <= 0) return;  // uniform
+  if (kOf == kTreeCells && n_scan <= b.identity_max) return;
+  if constexpr (kOf != kTreeCells) {  // no token of the chunk selects
+    const int i = (int)kc * kTokChunk + lane;
+    const int4 ti = i < T ? __ldg(&b.tok[e4.w + i]) : make_int4(-1, 0, 0, 0);
+    if (!__any_sync(0xffffffffu, ti.x >= 0 && ti.y > b.identity_max)) return;  // the same in every warp
+  }
   const int t0 = e4.w + (int)kc * kTokChunk;  // first token row
   const int n_here = min(kTokChunk, T - (int)kc * kTokChunk);
   if (tid == 0) {
@@ -180,7 +210,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   const int n16 = (n_here + 15) / 16 * 16, N = 2 * n16;  // row n: hi of token n; row n16 + n: lo
 
   if (warp < kEpiWarp) {
-    const TileRun t{e4.x, pos0, T, j_begin, J, g, nullptr, &s_abort, status, 0};
+    const TileRun t{e4.x, pos0, drafted, j_begin, J, g, nullptr, &s_abort, status, 0};
     produce_tiles<kScoreCodes, kTeams>(t, kq, nullptr, smem_u32(smem), bars.full, bars.empty, warp & 3, lane, warp >> 2);
   } else if (warp == kMmaWarp) {
     tmem_alloc(&s_tmem, 512);
@@ -238,18 +268,43 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.b_full);
     if (warp == kEpiWarp) {  // lane = token: its mask and what its scores are multiplied by
-      float km[kNB];
-      warp_kmax(w, sq, g, n_scan, lane, km);
-      int seen = pos0;
+      if constexpr (kOf == kTreeCells) {
+        float km[kNB];
+        warp_kmax(w, sq, g, n_scan, lane, km);
+        int seen = pos0;
 #pragma unroll
-      for (int i = 0; i < kTreeWords; ++i) {
-        const uint32_t m = lane < n_here ? tree_mask_word(b, t0 + lane, i, T) : 0u;
-        s_mask[lane][i] = m;
-        seen += __popc(m);
+        for (int i = 0; i < kTreeWords; ++i) {
+          const uint32_t m = lane < n_here ? tree_mask_word(b, t0 + lane, i, T) : 0u;
+          s_mask[lane][i] = m;
+          seen += __popc(m);
+        }
+        s_scale[lane] = lane < n_here && seen > b.identity_max
+                            ? sm_scale * tree_row_scale(w.eh + (size_t)(g * b.n_tok + t0 + lane) * 8, km, sm_scale)
+                            : 0.f;
+      } else {
+        // km: the prefix's maxima, the same for all tokens here, and each token's own sequence's
+        float km[kNB] = {0.f, 0.f, 0.f, 0.f};
+        const int4 ti = lane < n_here ? __ldg(&b.tok[t0 + lane]) : make_int4(-1, 0, 0, -1);
+        const int one = max(__ffs(__ballot_sync(0xffffffffu, ti.x >= 0)) - 1, 0);
+        const int prefix = __shfl_sync(0xffffffffu, ti.w, one), cells = __shfl_sync(0xffffffffu, ti.z, one);
+        if (prefix >= 0) {
+          TreeSelect v = w;
+          v.kmax = w.kmax_prefix;
+          v.chunks = w.chunks_prefix;
+          warp_kmax(v, prefix, g, cells, lane, km);
+        }
+        float scale = 0.f;
+        if (ti.x >= 0 && ti.y > b.identity_max) {
+          const int4 e = __ldg(&b.seqs[ti.x]);
+          const int n_own = e.z + (ti.x + 1 < b.n_seq ? __ldg(&b.seqs[ti.x + 1].w) : b.n_tok) - e.w;
+          raise_kmax(w.kmax, ti.x, w.chunks, g, n_own, km);
+          scale = sm_scale * tree_row_scale(w.eh + (size_t)(g * b.n_tok + t0 + lane) * 8, km, sm_scale);
+        }
+        s_scale[lane] = scale;
+#pragma unroll
+        for (int i = 0; i < kTreeWords; ++i)
+          s_mask[lane][i] = kOf == kOwnCells && lane < n_here ? shared_mask_word(b, t0 + lane, (int)kc * kTokChunk + lane, i, T) : 0u;
       }
-      s_scale[lane] = lane < n_here && seen > b.identity_max
-                          ? sm_scale * tree_row_scale(w.eh + (size_t)(g * b.n_tok + t0 + lane) * 8, km, sm_scale)
-                          : 0.f;
     }
     const bool t_ok = tile_wait_warp(&bars.tmem_ready, 0, status, &s_abort);
     tc_fence_after();
@@ -261,6 +316,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     };
     uint2 sw_next = scales_of(0);
     __half* dst0 = w.scores + (size_t)(g * b.n_tok + t0 + n0) * w.pitch;
+    if constexpr (kOf == kOwnCells) dst0 += own_column(__ldg(&b.tok[t0]).z);
     for (int j = 0; t_ok && j < J; ++j) {
       const int buf = j & 1, cell = (j_begin + j) * kTileCells + quarter * 32 + lane, dj = cell - pos0;
       const uint2 sw = sw_next;
@@ -289,9 +345,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       tc_fence_before();  // the accumulators are in registers
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-      if (n0 >= n16 || cell >= n_scan) continue;
+      if (n0 >= n16 || (kOf != kPrefixCells && cell >= n_scan)) continue;
       __half* dst = dst0 + cell;
-      const bool drafted = (j_begin + j + 1) * kTileCells > pos0;
+      const bool tail = (j_begin + j + 1) * kTileCells > pos0;
       const float4* sc4 = reinterpret_cast<const float4*>(s_scale + n0);
       float sc[16];
 #pragma unroll
@@ -304,7 +360,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[i] *= sc[i];
-      if (drafted && dj >= 0) {
+      if (kOf == kPrefixCells && cell >= n_scan) {  // the gap before the own cells' columns
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = -INFINITY;
+      }
+      if (kOf != kPrefixCells && tail && dj >= 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (!((s_mask[n0 + i][dj >> 5] >> (dj & 31)) & 1u)) acc[i] = -INFINITY;
@@ -349,7 +409,7 @@ cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __
   cudaError_t e = launch_pdl(tree_prep_kernel, dim3(kGroups * b.n_tok + b.n_seq * w.chunks + (plan ? 1 : 0)), dim3(256), 0,
                              stream, b, w, q, ksc, plan);
   if (e != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(tree_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem)) !=
+  if ((e = cudaFuncSetAttribute(tree_score_kernel<kTreeCells>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem)) !=
       cudaSuccess)
     return e;
   // tiles per CTA: as few as keep the CTAs near two waves of one per SM (a CTA's set-up, its B rows above all,
@@ -358,9 +418,29 @@ cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __
   const int zb = b.n_tok / kTokChunk + b.n_seq;
   int per = 2;
   while (per < 8 && (long long)((tiles + per - 1) / per) * kGroups * zb > 304) per *= 2;
-  e = launch_pdl(tree_score_kernel, dim3((tiles + per - 1) / per, kGroups, zb), dim3(kScoreThreads), kScoreSmem, stream, b,
+  e = launch_pdl(tree_score_kernel<kTreeCells>, dim3((tiles + per - 1) / per, kGroups, zb), dim3(kScoreThreads), kScoreSmem, stream, b,
                  w, kq, ksc, per, p.sm_scale, status);
   if (e != cudaSuccess) return e;
+  return launch_tree_topk(b, w, q, kq, ksc, ids, p, status, stream);
+}
+
+// Scores and top-k of a shared call, whose first launch (prefix.cu) has made the queries' sums, the maxima and the tokens'
+// records.  own_cells: about how many a sequence has.
+cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int own_cells, const __half* q, const int8_t* kq,
+                                 const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream) {
+  cudaError_t e;
+  auto score = [&](auto kern, int n, int cells) -> cudaError_t {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+    if (err != cudaSuccess) return err;
+    const int tiles = (cells + kTileCells - 1) / kTileCells, zb = b.n_tok / kTokChunk + n;
+    int per = 2;  // as in a tree call
+    while (per < 8 && (long long)((tiles + per - 1) / per) * kGroups * zb > 304) per *= 2;
+    return launch_pdl(kern, dim3((tiles + per - 1) / per, kGroups, zb), dim3(kScoreThreads), kScoreSmem, stream, b, w, kq, ksc, 0,
+                      p.sm_scale, status);
+  };
+  if (b.n_prefix > 0 && b.max_prefix > 0 && (e = score(tree_score_kernel<kPrefixCells>, b.n_prefix, b.max_prefix)) != cudaSuccess)
+    return e;
+  if ((e = score(tree_score_kernel<kOwnCells>, b.n_seq, own_cells)) != cudaSuccess) return e;
   return launch_tree_topk(b, w, q, kq, ksc, ids, p, status, stream);
 }
 

@@ -35,7 +35,7 @@ EXPORTS = ("qsa_last_error", "qsa_prep_quantize", "qsa_prep", "qsa_select_worksp
            "qsa_decode_layer_batched", "qsa_flash_prefill_batched_workspace_bytes", "qsa_flash_prefill_batched",
            "qsa_check_device_status", "qsa_select_noalloc", "qsa_debug_wait_probe", "qsa_prep_batched", "qsa_cache_read",
            "qsa_tree_attention_workspace_bytes", "qsa_tree_attention", "qsa_cache_commit", "qsa_tree_verify", "qsa_cache_copy",
-           "qsa_cache_compact_workspace_bytes", "qsa_cache_compact")
+           "qsa_cache_compact_workspace_bytes", "qsa_cache_compact", "qsa_prefix_attention_workspace_bytes", "qsa_prefix_attention")
 
 
 class QSAError(RuntimeError):
@@ -97,13 +97,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.qsa_cache_compact_workspace_bytes.argtypes = [I64, I, I]
     lib.qsa_cache_compact_workspace_bytes.restype = SZ
     lib.qsa_cache_compact.argtypes = [P, P, P, P, I64, P, I, P, I, P, P, P, P, SZ, P]
+    lib.qsa_prefix_attention_workspace_bytes.argtypes = [I, I, I, I, I, PP]
+    lib.qsa_prefix_attention_workspace_bytes.restype = SZ
+    lib.qsa_prefix_attention.argtypes = [P, P, P, P, P, I64, P, I, P, I, I, P, I, I, I, P, P, P, P, SZ, PP, P]
     lib.qsa_check_device_status.argtypes = [P]
     lib.qsa_debug_wait_probe.argtypes = [ctypes.c_uint64, P]
     lib.qsa_select_noalloc.argtypes = [P, P, P, I, I, I, P, PP, P]
     for name in EXPORTS:
         if name not in ("qsa_last_error", "qsa_select_workspace_bytes", "qsa_flash_prefill_workspace_bytes",
                         "qsa_flash_prefill_batched_workspace_bytes", "qsa_tree_attention_workspace_bytes",
-                        "qsa_cache_compact_workspace_bytes"):
+                        "qsa_cache_compact_workspace_bytes", "qsa_prefix_attention_workspace_bytes"):
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -369,6 +372,26 @@ def qsa_tree_verify(p, d, vocab: int, token, parent, u, u_end, seqs, n_seq: int,
                                   _array(u, "u", _F32, n_tok), _array(u_end, "u_end", _F32, n_seq),
                                   _array(seqs, "seqs", _I32, 4 * n_seq), n_seq, n_tok, _array(path, "path", _I32, n_seq * cap), cap,
                                   _array(n_path, "n_path", _I32, n_seq), _array(next, "next", _I32, n_seq), _stream(stream)))
+
+
+def qsa_prefix_attention_workspace_bytes(n_prefix: int, n_seq: int, n_tok: int, max_prefix: int, max_n_kv: int, params=None) -> int:
+    return int(load().qsa_prefix_attention_workspace_bytes(n_prefix, n_seq, n_tok, max_prefix, max_n_kv, _params(params)))
+
+
+def qsa_prefix_attention(q, kq, vq, ksc, vsc, n_pool: int, prefixes, n_prefix: int, seqs, n_seq: int, n_tok: int, tree,
+                         max_prefix: int, max_n_kv: int, ids, out, ws=None, params=None, stream=None, gate=None):
+    """Attention behind shared prefixes; prefixes int32 [n_prefix, 4] (or None), seqs int32 [n_seq, 4], tree int32 or uint32
+    [n_tok, words] of mask bits, or None: a token sees the sequence's tokens up to itself."""
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    words = 0 if tree is None else tree.shape[1]
+    topk = 2048 if params is None else params.topk if isinstance(params, qsa_params) else int(params[0])
+    rows = n_tok * (N_HEADS * HEAD_DIM)
+    kq, ksc, vq, vsc = _pool(kq, ksc, vq, vsc, n_pool)
+    _check(load().qsa_prefix_attention(_array(q, "q", _F16, rows), kq, vq, ksc, vsc, n_pool,
+                                       _array(prefixes, "prefixes", _I32, 4 * n_prefix), n_prefix, _array(seqs, "seqs", _I32, 4 * n_seq),
+                                       n_seq, n_tok, _array(tree, "tree", _I32, n_tok * words, True), words, max_prefix, max_n_kv,
+                                       _array(ids, "ids", _I32, n_tok * N_GROUPS * topk, True), _array(gate, "gate", _F16, rows, True),
+                                       _array(out, "out", _F16, rows), _ptr(ws), ws_bytes, _params(params), _stream(stream)))
 
 
 def qsa_cache_copy(kq, ksc, vq, vsc, n_pool: int, runs, n_run: int, max_cells: int, stream=None):

@@ -29,8 +29,11 @@ VERIFY = dict(p=P(FAKE), p_stride=100, d=P(FAKE), d_stride=100, vocab=100, token
 COPY = dict(kq=P(FAKE), ksc=P(FAKE), vq=P(FAKE), vsc=P(FAKE), n_pool=100, runs=P(FAKE), n_run=3, max_cells=10, stream=None)
 COMPACT = dict(kq=P(FAKE), ksc=P(FAKE), vq=P(FAKE), vsc=P(FAKE), n_pool=100, prefixes=P(FAKE), n_prefix=1, seqs=P(FAKE), n_seq=3,
                prefixes_out=P(FAKE), seqs_out=P(FAKE), used=P(FAKE), ws=P(FAKE), ws_bytes=1 << 20, stream=None)
-FNS = {"qsa_tree_verify": VERIFY, "qsa_cache_copy": COPY, "qsa_cache_compact": COMPACT}
-MAY_BE_NULL = {"d", "used", "ws"}
+ATTEND = dict(q=P(FAKE), kq=P(FAKE), vq=P(FAKE), ksc=P(FAKE), vsc=P(FAKE), n_pool=1000, prefixes=P(FAKE), n_prefix=1, seqs=P(FAKE),
+              n_seq=2, n_tok=4, tree=P(FAKE), tree_words=1, max_prefix=100, max_n_kv=150, ids=P(FAKE), gate=P(FAKE), out=P(FAKE),
+              ws=P(FAKE), ws_bytes=1 << 40, params=None, stream=None)
+FNS = {"qsa_prefix_attention": ATTEND, "qsa_tree_verify": VERIFY, "qsa_cache_copy": COPY, "qsa_cache_compact": COMPACT}
+MAY_BE_NULL = {"d", "used", "ws", "tree", "ids", "gate"}
 ELEMENTS = {"p", "d", "token", "parent", "u", "u_end", "path", "n_path", "next", "used"}  # aligned to 4 bytes
 
 
@@ -47,7 +50,7 @@ def test_null_and_misaligned_pointers(lib, name):
             assert b"NULL" in lib.qsa_last_error()
 
 
-@pytest.mark.parametrize("name", ["qsa_cache_copy", "qsa_cache_compact"])
+@pytest.mark.parametrize("name", ["qsa_cache_copy", "qsa_cache_compact", "qsa_prefix_attention"])
 @pytest.mark.parametrize("n_pool", [0, -1, 1 << 31, 1 << 40])
 def test_pool_sizes(lib, name, n_pool):
     assert call(getattr(lib, name), FNS[name], n_pool=n_pool) == qsa.QSA_ERR_INVALID_ARG
@@ -59,6 +62,44 @@ def test_nothing_to_do_is_no_error(lib):
     assert call(lib.qsa_cache_copy, COPY, n_run=0, kq=None, runs=None) == qsa.QSA_OK
     assert call(lib.qsa_cache_copy, COPY, max_cells=0, kq=None, runs=None) == qsa.QSA_OK
     assert call(lib.qsa_cache_compact, COMPACT, n_prefix=0, n_seq=0, kq=None, used=None, ws=None, ws_bytes=0) == qsa.QSA_OK
+
+
+def test_attention_refusals(lib):
+    f, size = lib.qsa_prefix_attention, qsa.qsa_prefix_attention_workspace_bytes
+    assert call(f, ATTEND, n_tok=0, q=None) == call(f, ATTEND, n_seq=0, seqs=None) == qsa.QSA_OK
+    for k in ("n_prefix", "n_seq", "n_tok"):
+        assert call(f, ATTEND, **{k: -1}) == qsa.QSA_ERR_INVALID_ARG
+        assert call(f, ATTEND, **{k: 65536}) == qsa.QSA_ERR_UNSUPPORTED
+    for w in (0, -1, 9):
+        assert call(f, ATTEND, tree_words=w) == qsa.QSA_ERR_UNSUPPORTED
+    for over in (dict(max_n_kv=0, max_prefix=0), dict(max_prefix=-1), dict(max_prefix=151)):
+        assert call(f, ATTEND, **over) == qsa.QSA_ERR_INVALID_ARG
+    assert call(f, ATTEND, max_n_kv=65410) == qsa.QSA_ERR_UNSUPPORTED
+    dense = qsa.qsa_params(2048, 1 << 21, 0.0625)
+    assert call(f, ATTEND, max_n_kv=(1 << 20) + 1, params=ctypes.byref(dense)) == qsa.QSA_ERR_UNSUPPORTED
+    for bad in (qsa.qsa_params(0, 2051, 0.0625), qsa.qsa_params(2053, 2051, 0.0625), qsa.qsa_params(8, 20, float("nan"))):
+        assert call(f, ATTEND, params=ctypes.byref(bad)) == qsa.QSA_ERR_INVALID_ARG
+        assert size(1, 2, 4, 100, 150, bad) == 0
+    need = size(1, 2, 4, 100, 150)
+    assert need > 0
+    assert call(f, ATTEND, ws_bytes=need - 1) == qsa.QSA_ERR_WORKSPACE
+    assert call(f, ATTEND, ws=None) == qsa.QSA_ERR_WORKSPACE
+    for args in ((-1, 2, 4, 100, 150), (1, 0, 4, 100, 150), (1, 2, 0, 100, 150), (1, 2, 4, 151, 150), (1, 2, 4, 100, 0), (1, 2, 4, -1, 9)):
+        assert size(*args) == 0
+
+
+def test_attention_workspace_grows_with_each_argument(lib):
+    import random
+    rng = random.Random(1)
+    size = qsa.qsa_prefix_attention_workspace_bytes
+    for params in (None, (2048, 1 << 21, 0.0625)):
+        for _ in range(400):
+            a = [rng.choice((0, 1, 3, 70)), rng.choice((1, 2, 9, 64, 700)), rng.choice((1, 3, 8, 64, 300, 5000)), 0, 0]
+            a[3] = rng.choice((0, 1, 127, 2000, 16000, 30000))
+            a[4] = a[3] + rng.choice((1, 100, 2000, 30000))
+            b = [x + rng.choice((0, 0, 1, 5, 300)) for x in a]
+            b[4] = max(b[4], b[3])
+            assert size(*a, params=params) <= size(*b, params=params), (a, b)
 
 
 def test_verify_refusals(lib):
