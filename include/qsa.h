@@ -503,8 +503,8 @@ QSA_API size_t qsa_prefix_attention_workspace_bytes(int n_prefix, int n_seq, int
  *         qsa_tree_attention; n_cells 0: padding, whose rows are left as they are.  At most 32 * tree_words tokens a
  *         sequence, 256 without masks
  *   tree  DEVICE [n_tok][tree_words] uint32, tree_words 1 .. 8, or NULL
- *   max_prefix, max_n_kv  upper bounds on every prefix's cells and on every sequence's P + pos0 + token count; max_n_kv at
- *         most 1048576, and at most 65409 where it exceeds identity_max
+ *   max_prefix, max_n_kv  upper bounds on every prefix's cells (one without sequences may be longer than max_n_kv) and on
+ *         every sequence's P + pos0 + token count; at most 1048576, max_n_kv at most 65409 where it exceeds identity_max
  *   ids   [n_tok][2][topk] int32, or NULL: the cells of selected tokens, ascending (rows of other tokens are not written)
  *   gate, out  [n_tok][24][256] fp16; gate may be NULL
  *   ws    qsa_prefix_attention_workspace_bytes(...) bytes, 16-byte aligned, clobbered.  Calls that overlap on the GPU (two

@@ -678,7 +678,7 @@ size_t qsa_prefix_attention_workspace_bytes(int n_prefix, int n_seq, int n_tok, 
                                             const qsa_params* params) {
   qsa::Params p{};
   if (n_prefix < 0 || n_seq < 1 || n_tok < 1 || n_prefix > kTreeMost || n_seq > kTreeMost || n_tok > kTreeMost || max_prefix < 0 ||
-      max_n_kv < 1 || max_prefix > max_n_kv || max_n_kv > kSharedMost || resolve_params(params, &p) != QSA_OK)
+      max_n_kv < 1 || max_prefix > kSharedMost || max_n_kv > kSharedMost || resolve_params(params, &p) != QSA_OK)
     return 0;
   return qsa::prefix_attention_workspace_bytes(n_prefix, n_seq, n_tok, max_prefix, max_n_kv, p.identity_max);
 }
@@ -699,8 +699,8 @@ int qsa_prefix_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, 
   if (n_pool <= 0 || n_pool > 0x7fffffffLL)
     return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
   if (max_n_kv < 1) return fail(QSA_ERR_INVALID_ARG, "max_n_kv must be positive (got %d)", max_n_kv);
-  if (max_prefix < 0 || max_prefix > max_n_kv)
-    return fail(QSA_ERR_INVALID_ARG, "max_prefix must be in [0, max_n_kv = %d] (got %d)", max_n_kv, max_prefix);
+  if (max_prefix < 0) return fail(QSA_ERR_INVALID_ARG, "max_prefix must be >= 0 (got %d)", max_prefix);
+  if (max_prefix > kSharedMost) return fail(QSA_ERR_UNSUPPORTED, "max_prefix must be at most %d (got %d)", kSharedMost, max_prefix);
   const int limit = max_n_kv > p.identity_max ? qsa::select_max_cells() - 127 : kSharedMost;
   if (max_n_kv > limit)
     return fail(QSA_ERR_UNSUPPORTED, "max_n_kv must be at most %d%s (got %d)", limit,

@@ -72,9 +72,10 @@ def test_attention_refusals(lib):
         assert call(f, ATTEND, **{k: 65536}) == qsa.QSA_ERR_UNSUPPORTED
     for w in (0, -1, 9):
         assert call(f, ATTEND, tree_words=w) == qsa.QSA_ERR_UNSUPPORTED
-    for over in (dict(max_n_kv=0, max_prefix=0), dict(max_prefix=-1), dict(max_prefix=151)):
+    for over in (dict(max_n_kv=0, max_prefix=0), dict(max_prefix=-1)):
         assert call(f, ATTEND, **over) == qsa.QSA_ERR_INVALID_ARG
     assert call(f, ATTEND, max_n_kv=65410) == qsa.QSA_ERR_UNSUPPORTED
+    assert call(f, ATTEND, max_prefix=(1 << 20) + 1) == qsa.QSA_ERR_UNSUPPORTED
     dense = qsa.qsa_params(2048, 1 << 21, 0.0625)
     assert call(f, ATTEND, max_n_kv=(1 << 20) + 1, params=ctypes.byref(dense)) == qsa.QSA_ERR_UNSUPPORTED
     for bad in (qsa.qsa_params(0, 2051, 0.0625), qsa.qsa_params(2053, 2051, 0.0625), qsa.qsa_params(8, 20, float("nan"))):
@@ -84,7 +85,7 @@ def test_attention_refusals(lib):
     assert need > 0
     assert call(f, ATTEND, ws_bytes=need - 1) == qsa.QSA_ERR_WORKSPACE
     assert call(f, ATTEND, ws=None) == qsa.QSA_ERR_WORKSPACE
-    for args in ((-1, 2, 4, 100, 150), (1, 0, 4, 100, 150), (1, 2, 0, 100, 150), (1, 2, 4, 151, 150), (1, 2, 4, 100, 0), (1, 2, 4, -1, 9)):
+    for args in ((-1, 2, 4, 100, 150), (1, 0, 4, 100, 150), (1, 2, 0, 100, 150), (1, 2, 4, (1 << 20) + 1, 150), (1, 2, 4, 100, 0), (1, 2, 4, -1, 9)):
         assert size(*args) == 0
 
 
