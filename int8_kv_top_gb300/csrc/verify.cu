@@ -19,26 +19,29 @@
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTokens = 32 * kTreeWords;  // drafted tokens of a sequence
-constexpr int kBlock = 1024;                 // vocabulary entries of a warp's step, 32 a lane
-constexpr int kMaxBlocks = 256;              // 262,144 entries
+constexpr int kBlock = 2 * kThreads;         // vocabulary entries of a warp's step (16 a lane), and of the draw (two a thread)
+constexpr int kMaxBlocks = 512;              // 262,144 entries
 constexpr int kMaxCluster = 8;
 constexpr long long kUnit = 1ll << 44;
 
 // Probability x in units of 2^-44, as hi 2^22 + lo with lo in [-2^21, 2^21], by two roundings to whole numbers in
-// fp32 (adding 2^23, whose unit is 1).  Values outside [0, 1] count as the nearer end, NaN as 0.
-__device__ __forceinline__ void fixed_parts(float x, int& hi, int& lo) {
-  x = fminf(fmaxf(x, 0.f), 1.f) * 4194304.f;  // 2^22
-  const float t = x + 8388608.f;
-  hi = __float_as_int(t) - 0x4B000000;
-  const float r = x - (t - 8388608.f);  // exact
-  lo = __float_as_int(fmaf(r, 4194304.f, 12582912.f)) - 0x4B400000;
+// fp32 (adding 2^23, whose unit is 1).  hi and lo are added to sums that wrap, biased by kHiBias and kLoBias each.  x is
+// in [0, 1]: values outside count as the nearer end, NaN as 0 (saturated).
+constexpr uint32_t kHiBias = 0x4B000000u, kLoBias = 0x4B400000u;  // the bits of 2^23 and of 1.5 2^23
+struct Parts {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Parts parts_of(float x) {
+  const float t = fmaf(x, 4194304.f, 8388608.f);
+  const float r = fmaf(x, 4194304.f, 8388608.f - t);  // exact
+  return {__float_as_uint(t), __float_as_uint(fmaf(r, 4194304.f, 12582912.f))};
 }
+__device__ __forceinline__ long long units(uint32_t hi, uint32_t lo) { return ((long long)(int)hi << 22) + (int)lo; }
 __device__ __forceinline__ long long fixed(float x) {
-  int hi, lo;
-  fixed_parts(x, hi, lo);
-  return ((long long)hi << 22) + lo;
+  const Parts f = parts_of(__saturatef(x));
+  return units(f.hi - kHiBias, f.lo - kLoBias);
 }
 
 struct VerifyArgs {
@@ -71,13 +74,24 @@ __device__ __forceinline__ float4 load4(const float* row, int j, int vocab, bool
   return v;
 }
 
-// w after `refused` refusals, from the entry's p and d and the masses c[0 .. refused), each below 4 (2^46 units).
-__device__ __forceinline__ long long left_over(float p, float d, const long long* mass, int refused) {
-  long long w = fixed(p);
-  const long long df = fixed(d);
-  if (refused > 0) w = max(w - df, 0ll);  // c[0] = 1
-  for (int r = 1; r < refused; ++r) w = max(w - (long long)__umul64hi((unsigned long long)mass[r] << 18, (unsigned long long)df << 2), 0ll);
-  return w;
+// w after `refused` refusals of N entries side by side, from their p and d and the masses c[0 .. refused), each below 4 (2^46 units).
+template <int N>
+__device__ __forceinline__ void left_over(const float (&p)[N], const float (&d)[N], const long long* mass, int refused, long long (&w)[N]) {
+  unsigned long long df[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const float x = __saturatef(p[q]), y = __saturatef(d[q]);
+    const Parts f = parts_of(x), m = parts_of(refused > 0 ? fminf(x, y) : 0.f);  // c[0] = 1: max(p - d, 0) = p - min(p, d)
+    const Parts g = parts_of(y);
+    w[q] = units(f.hi - m.hi, f.lo - m.lo);
+    df[q] = (unsigned long long)units(g.hi - kHiBias, g.lo - kLoBias) << 2;
+  }
+#pragma unroll 1
+  for (int r = 1; r < refused; ++r) {
+    const unsigned long long c = (unsigned long long)mass[r] << 18;
+#pragma unroll
+    for (int q = 0; q < N; ++q) w[q] = max(w[q] - (long long)__umul64hi(c, df[q]), 0ll);
+  }
 }
 
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -86,11 +100,12 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_constant__ VerifyArgs a, int C) {
+__global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_constant__ VerifyArgs a, int C) {
   __shared__ int s_parent[kMaxTokens], s_token[kMaxTokens], s_path[kMaxTokens], s_out[kMaxTokens];
   __shared__ float s_u[kMaxTokens], s_p[kMaxTokens], s_d[kMaxTokens];
   __shared__ long long s_mass[kMaxTokens + 1];
   __shared__ long long s_block[kMaxBlocks];
+  __shared__ long long s_warp[kWarps];
   __shared__ long long s_total[2][kMaxCluster];  // a pass's sums of the cluster's CTAs
   __shared__ int s_n, s_cur, s_refused, s_out_n, s_at, s_more;
   cluster_arrive_all();  // waited for before the first remote store: every CTA of the cluster runs
@@ -159,15 +174,21 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
         double w;
         bool out = false;
         if (a.d) {
-          w = refused == 0 ? (double)fminf(fmaxf(pk, 0.f), 1.f) : (double)left_over(pk, dk, s_mass, refused) * (1.0 / kUnit);
+          if (refused == 0) {
+            w = (double)__saturatef(pk);
+          } else {
+            long long left[1];
+            left_over<1>({pk}, {dk}, s_mass, refused, left);
+            w = (double)left[0] * (1.0 / kUnit);
+          }
         } else {
           for (int i = lane; i < out_n; i += 32) out |= s_out[i] == x;  // refused before
           out = __any_sync(0xffffffffu, out);
-          w = out ? 0.0 : (double)fminf(fmaxf(pk, 0.f), 1.f);
+          w = out ? 0.0 : (double)__saturatef(pk);
         }
         const double c = refused == 0 ? 1.0 : (double)s_mass[refused] * (1.0 / kUnit);
         __syncwarp();
-        if ((double)s_u[k] * (double)fminf(fmaxf(dk, 0.f), 1.f) * c < w) {
+        if ((double)s_u[k] * (double)__saturatef(dk) * c < w) {
           if (lane == 0) s_path[n] = k;
           ++n;
           cur = k;
@@ -200,57 +221,59 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
     const float* drow = a.d && refused > 0 ? a.d + (size_t)(e.w + s_cur) * a.d_stride : nullptr;
     for (int b = b0 + warp; b < b1; b += kWarps) {
       const int j0 = b * kBlock + lane * 4;
+      constexpr int kQuads = kBlock / 128;  // loads of four entries a lane
       long long sum = 0;
       if (drow == nullptr) {
-        int hs = 0, ls = 0;
-        float4 v[8];
+        uint32_t hs = -4u * kQuads * kHiBias, ls = -4u * kQuads * kLoBias;
+        float4 v[kQuads];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = load4(prow, j0 + 128 * i, a.vocab, a.vec_p);
+        for (int i = 0; i < kQuads; ++i) v[i] = load4(prow, j0 + 128 * i, a.vocab, a.vec_p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kQuads; ++i) {
           const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            int hi, lo;
-            fixed_parts(f[q], hi, lo);
-            hs += hi;
-            ls += lo;
+            const Parts x = parts_of(__saturatef(f[q]));
+            hs += x.hi;
+            ls += x.lo;
           }
         }
-        sum = ((long long)hs << 22) + ls;
+        sum = units(hs, ls);
         for (int i = lane; i < out_n; i += 32) {
           const int x = s_out[i];
           if (x / kBlock == b) sum -= fixed(__ldg(prow + x));
         }
       } else {
+        uint32_t hs = 0u, ls = 0u;  // p - min(p, d): the biases cancel
+        static_assert(kQuads == 4, "four of each row");
+        float4 v[4], z[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float4 v[4], z[4];
+        for (int i = 0; i < 4; ++i) {
+          v[i] = load4(prow, j0 + 128 * i, a.vocab, a.vec_p);
+          z[i] = load4(drow, j0 + 128 * i, a.vocab, a.vec_d);
+        }
+        if (refused == 1) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            v[i] = load4(prow, j0 + 128 * (4 * h + i), a.vocab, a.vec_p);
-            z[i] = load4(drow, j0 + 128 * (4 * h + i), a.vocab, a.vec_d);
+            const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, g[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float x = __saturatef(f[q]);
+              const Parts y = parts_of(x), m = parts_of(fminf(x, __saturatef(g[q])));
+              hs += y.hi - m.hi;
+              ls += y.lo - m.lo;
+            }
           }
-          if (refused == 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, g[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                int fh, fl, gh, gl;
-                fixed_parts(f[q], fh, fl);
-                fixed_parts(g[q], gh, gl);
-                sum += max(((long long)(fh - gh) << 22) + (fl - gl), 0ll);
-              }
-            }
-          } else {
+        } else {
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, g[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
-              for (int q = 0; q < 4; ++q) sum += left_over(f[q], g[q], s_mass, refused);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float4 x = i < 2 ? (i == 0 ? v[0] : v[1]) : i == 2 ? v[2] : v[3], y = i < 2 ? (i == 0 ? z[0] : z[1]) : i == 2 ? z[2] : z[3];
+            long long left[4];
+            left_over<4>({x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}, s_mass, refused, left);
+            sum += left[0] + left[1] + left[2] + left[3];
           }
         }
+        sum += units(hs, ls);
       }
       sum = warp_sum(sum);
       if (lane == 0) s_block[b] = sum;
@@ -289,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
     const unsigned long long u64 = !(u > 0.f) ? 0ull : u >= 1.f ? ~0ull : (unsigned long long)((double)u * 18446744073709551616.0);
     const long long target = (long long)__umul64hi(u64, (unsigned long long)total);  // floor(u total)
     const long long mine = s_total[pass & 1][rank];
-    if (total > 0 && target >= before && target < before + mine && warp == 0) {
+    if (total > 0 && target >= before && target < before + mine) {  // the same in all threads
       long long run = before;
       int b = b0;
       for (int base = b0; base < b1; base += 32) {  // 32 blocks at a time: the one in which the sum passes the target
@@ -309,48 +332,32 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
         }
         run += __shfl_sync(0xffffffffu, x, 31);
       }
-      int found = -1;
-#pragma unroll 1
-      for (int h = 0; h < 2 && found < 0; ++h) {
-        const int j0 = b * kBlock + 512 * h + lane * 4;
-        float4 v[4], z[4];
+      // the block's entries, two a thread (a warp alone takes microseconds over them: code that runs once is fetched as it runs)
+      const int j = b * kBlock + 2 * tid;
+      float f[2] = {0.f, 0.f}, g[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = load4(prow, j0 + 128 * i, a.vocab, a.vec_p);
-          z[i] = drow ? load4(drow, j0 + 128 * i, a.vocab, a.vec_d) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = j0 + 128 * i;
-          const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, g[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
-          long long w[4], sum = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            w[q] = drow ? left_over(f[q], g[q], s_mass, refused) : fixed(f[q]);
-            for (int o = 0; o < out_n; ++o)
-              if (s_out[o] == j + q) w[q] = 0;
-            sum += w[q];
-          }
-          long long x = sum;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-          }
-          const unsigned m = __ballot_sync(0xffffffffu, run + x > target);
-          if (m && found < 0) {  // the same in all lanes
-            long long at = run + x - sum;
-            int q = 0;
-            for (; q < 3; ++q) {
-              at += w[q];
-              if (at > target) break;
-            }
-            found = __shfl_sync(0xffffffffu, j + q, __ffs(m) - 1);
-          }
-          run += __shfl_sync(0xffffffffu, x, 31);
-        }
+      for (int q = 0; q < 2; ++q) {
+        if (j + q < a.vocab) f[q] = __ldg(prow + j + q);
+        if (drow && j + q < a.vocab) g[q] = __ldg(drow + j + q);
       }
-      if (lane == 0) a.next[s] = found;
+      long long w[2];
+      left_over<2>(f, g, s_mass, drow ? refused : 0, w);
+      for (int o = 0; o < out_n; ++o) {
+        const int x = s_out[o] - j;
+        if (x == 0) w[0] = 0;
+        if (x == 1) w[1] = 0;
+      }
+      long long up = w[0] + w[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += y;
+      }
+      if (lane == 31) s_warp[warp] = up;
+      __syncthreads();
+      for (int i = 0; i < warp; ++i) run += s_warp[i];
+      up += run;  // with this thread's entries; before them up - w0 - w1
+      if (up > target && up - w[0] - w[1] <= target) a.next[s] = up - w[1] > target ? j : j + 1;
     }
     if (rank == 0) {
       const int n = s_n;
@@ -374,9 +381,9 @@ cudaError_t launch_tree_verify(const float* p, int64_t p_stride, const float* d,
   auto vec = [](const float* x, int64_t stride) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && stride % 4 == 0; };
   const VerifyArgs a{p,     d,    p_stride, d_stride, vocab,  vec(p, p_stride), vec(d, d_stride), token, parent, u, u_end,
                      seqs,  n_seq, n_tok,   path,     n_path, next,             path_cap,         status};
-  // CTAs a sequence: two on every SM of a GB300 where the sequences are few, and a block of entries a warp
+  // CTAs a sequence: four on every SM of a GB300 where the sequences are few, and a block of entries a warp
   int C = 1;
-  while (C < kMaxCluster && (long long)n_seq * C * 2 <= 2 * 152 && C * kWarps * kBlock < vocab) C *= 2;
+  while (C < kMaxCluster && (long long)n_seq * C * 2 <= 4 * 152 && C * kWarps * kBlock < vocab) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(n_seq * C));
   cfg.blockDim = dim3(kThreads);
