@@ -225,16 +225,19 @@ __device__ __forceinline__ bool wait_loaded(const uint32_t* flag, int* status) {
   return false;
 }
 
+constexpr int kNearRuns = 1024;  // a table up to so long is looked up in shared memory
 __global__ void __launch_bounds__(kThreads)
     compact_move_kernel(const Pool pool, const Tables t, const CompactWs w, int rank_ctas, int4* prefixes_out, int4* seqs_out,
                         int* used_out, int* status) {
-  __shared__ int s_ticket, s_wait[2];
+  __shared__ int4 s_runs[kNearRuns];
+  __shared__ int s_next, s_wait[2];
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_next = atomicAdd(&w.head[0], 1);
+  const int n = __ldg(&w.head[1]), used = __ldg(&w.head[2]);
   bool bad = false;
   for (int i = tid; i < rank_ctas; i += kThreads) bad |= __ldg(&w.bad[i]) != 0;
   bad = __syncthreads_or(bad);
-  const int n = __ldg(&w.head[1]), used = __ldg(&w.head[2]);
   for (int i = blockIdx.x * kThreads + tid; i < t.n; i += gridDim.x * kThreads) {
     int4 e = i < t.n_prefix ? t.prefixes[i] : t.seqs[i - t.n_prefix];
     if (!bad) e.x = __ldg(&w.place[i]);
@@ -246,60 +249,74 @@ __global__ void __launch_bounds__(kThreads)
     if (used_out) *used_out = bad ? -1 : used;
   }
   if (bad) return;  // the pool is left as it is
-  for (;;) {
+  const int4* runs = w.runs;
+  if (n <= kNearRuns) {
+    for (int i = tid; i < n; i += kThreads) s_runs[i] = __ldg(&w.runs[i]);
+    runs = s_runs;
     __syncthreads();
-    if (tid == 0) s_ticket = atomicAdd(&w.head[0], 1);
-    __syncthreads();
-    const int chunk = s_ticket;
-    if ((int64_t)chunk * kChunkCells >= used) break;
-    const int c0 = chunk * kChunkCells + warp * kCellsPerWarp;  // this warp's first cell
-    int64_t from = -1, to = -1;
-    if (c0 < used) {  // the run of cell c0, and with a lane each the eight behind it (no run is empty)
-      const int k = warp_find_seq(n, c0, [&](int i) { return (long long)__ldg(&w.runs[i]).y; });
-      const int4 e = __ldg(&w.runs[min(k + lane, n - 1)]);
-      const bool have = k + lane < n;
+  }
+  // Where this warp's eight cells of a chunk come from and go to (lane u: cell u; -1: none).
+  auto look_up = [&](int chunk, int64_t& from, int64_t& to) {
+    from = to = -1;
+    const int64_t c0 = (int64_t)chunk * kChunkCells + warp * kCellsPerWarp;
+    if (c0 >= used) return;
+    const int k = warp_find_seq(n, c0, [&](int i) { return (long long)runs[i].y; });
+    const int4 e = runs[min(k + lane, n - 1)];  // the run of cell c0, and with a lane each those behind it (no run is empty)
+    const bool have = k + lane < n;
 #pragma unroll
-      for (int u = 0; u < kCellsPerWarp; ++u) {
-        const int c = c0 + u;
-        const int r = max(__popc(__ballot_sync(0xffffffffu, have && e.y <= c)) - 1, 0);
-        const int src = __shfl_sync(0xffffffffu, e.x, r), dst = __shfl_sync(0xffffffffu, e.y, r);
-        if (lane == u && c < used) {
-          to = c;
-          from = src + (c - dst);
-        }
+    for (int u = 0; u < kCellsPerWarp; ++u) {
+      const int c = (int)c0 + u;
+      const int r = max(__popc(__ballot_sync(0xffffffffu, have && e.y <= c)) - 1, 0);
+      const int src = __shfl_sync(0xffffffffu, e.x, r), dst = __shfl_sync(0xffffffffu, e.y, r);
+      if (lane == u && c < used) {
+        to = c;
+        from = src + (c - dst);
       }
     }
+  };
+  int chunk = s_next;
+  int64_t from, to;
+  look_up(chunk, from, to);
+  while ((int64_t)chunk * kChunkCells < used) {
+    __syncthreads();  // every thread has read s_next
+    if (tid == 0) s_next = atomicAdd(&w.head[0], 1);
     const bool moves = __syncthreads_or(from != to);  // else every cell is where it belongs, and none is read
     Cells x;
-    if (moves) {
-      load_cells(pool, from, lane, x);
-      __threadfence();  // this thread's cells have been read before the flag below is seen
-    }
-    if (warp == 0) {
+    if (moves) load_cells(pool, from, lane, x);
+    // while they arrive: the next chunk's runs, and whom this one waits for
+    const int next = s_next;
+    int64_t next_from, next_to;
+    look_up(next, next_from, next_to);
+    if (warp == 0 && moves) {
       // the earlier chunks that read from places [a, b): of the first and the last cell there that is in a run
       const int a = chunk * kChunkCells, b = min(a + kChunkCells, used);
-      auto src = [&](int i) { return (long long)__ldg(&w.runs[i]).x; };
+      auto src = [&](int i) { return (long long)runs[i].x; };
       const int ka = warp_find_seq(n, a, src), kb = warp_find_seq(n, b - 1, src);
       if (lane == 0) {
-        const int4 ea = __ldg(&w.runs[ka]), eb = __ldg(&w.runs[kb]);
-        // cell a is in run ka, or the first cell behind it is the next run's first (its place at most b's chunk)
+        const int4 ea = runs[ka], eb = runs[kb];
+        // cell a is in run ka, or the first cell behind it is a run's first: the next one's, or (before all of them) run 0's
         const int xa = a >= ea.x && a - ea.x < ea.z ? ea.y + (a - ea.x) : ea.x > a ? ea.y : ea.y + ea.z;
         const int xb = eb.x > b - 1 ? -1 : eb.y + min(b - 1 - eb.x, eb.z - 1);
         s_wait[0] = xa / kChunkCells;
         s_wait[1] = xb < 0 ? -1 : xb / kChunkCells;
       }
     }
+    if (moves) __threadfence();  // this thread's cells have been read before the flag below is seen
     __syncthreads();
     if (tid == 0) {
       __threadfence();
       asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(w.loaded + chunk), "r"(1u) : "memory");
     }
-    if (!moves) continue;
-    bool ok = true;
-    const int j = s_wait[0] + tid;
-    if (j <= s_wait[1] && j < chunk) ok = wait_loaded(w.loaded + j, status);
-    if (!__syncthreads_and(ok)) return;
-    store_cells(pool, to == from ? -1 : to, lane, x);
+    if (moves) {
+      bool ok = true;
+      const int j = s_wait[0] + tid;
+      if (j <= s_wait[1] && j < chunk) ok = wait_loaded(w.loaded + j, status);
+      if (!__syncthreads_and(ok)) return;
+      store_cells(pool, to == from ? -1 : to, lane, x);
+    }
+    chunk = next;
+    from = next_from;
+    to = next_to;
   }
 }
 
