@@ -23,49 +23,31 @@ namespace qsa {
 namespace {
 
 // ---------------------------------------------------------------- 1. records, queries' sums, maxima
+// What the join needs of a token besides its record (TreeBatch::tok): its sequence's {first pool cell, committed own cells,
+// tokens, first token row}, and its prefix's {first token row, tokens, -, -}.
+struct TokMore {
+  int4 seq, prefix;
+};
+
 // Blocks, in this order: (token, group): Qsum and its error terms; (prefix, chunk of 2,048 cells) and (sequence, every
 // own_chunks-th chunk): max |ksc|; the first three only where tokens may select.  Then 256 tokens' records each.
-__global__ void __launch_bounds__(256) prefix_prep_kernel(const TreeBatch b, const TreeSelect w, bool select, int own_chunks,
-                                                          const __half* __restrict__ q, const __half* __restrict__ ksc, int* status) {
+constexpr int kNearSeqs = 1024, kNearPrefixes = 256;  // tables up to so long are searched in shared memory
+__global__ void __launch_bounds__(256) prefix_prep_kernel(const TreeBatch b, const TreeSelect w, TokMore* __restrict__ more,
+                                                          bool select, int own_chunks, const __half* __restrict__ q,
+                                                          const __half* __restrict__ ksc, int* status) {
   __shared__ long long s_e[8], s_h[8];
   __shared__ uint32_t s_union[kTreeWords];
   __shared__ float s_max[8][kGroups * kNB];
-  __shared__ int s_go;
+  __shared__ int s_row[kNearSeqs], s_seq[kNearPrefixes];
   pdl_begin();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto seq_of = [&](int t) {
-    int lo = 0, hi = b.n_seq - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(&b.seqs[mid].w) <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    return lo;
-  };
-  // {sequence or -1, n_kv, prefix cells, prefix} of a token
-  auto record = [&](int t) {
-    const int s = seq_of(t);
-    int4 e;
-    int p, cells;
-    const int T = shared_seq_tokens(b, s, &e, &p, &cells);
-    if (T <= 0 || t < e.w || t >= e.w + T) return make_int4(-1, 0, 0, -1);
-    int seen = cells + e.z;
-    for (int i = 0; i < kTreeWords; ++i) seen += __popc(shared_mask_word(b, t, t - e.w, i, T));
-    return make_int4(s, seen, cells, p);
-  };
   int x = blockIdx.x;
   if (select) {
     if (x < kGroups * b.n_tok) {
       const int t = x >> 1, g = x & 1;
-      if (tid == 0) {
-        const int4 r = record(t);
-        s_go = r.x >= 0 && r.y > b.identity_max;
-      }
       __half hi, lo;
       long long e, h_abs;
       qsum_split(q, t, g, tid, hi, lo, e, h_abs);
-      __syncthreads();
-      if (!s_go) return;
       __half* dst = w.qhl + (size_t)(g * b.n_tok + t) * (2 * kD) + (tid >> 6) * 128 + (tid & 63);
       dst[0] = hi;
       dst[64] = lo;
@@ -94,9 +76,7 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const TreeBatch b, con
       const int i = own ? (x - prefix_blocks) / own_chunks : x / w.chunks_prefix;
       const int first = own ? (x - prefix_blocks) % own_chunks : x % w.chunks_prefix;
       int4 e;
-      int T, p, cells;
-      if (own) T = shared_seq_tokens(b, i, &e, &p, &cells);
-      else T = prefix_tokens(b, i, &e);
+      const int T = own ? shared_seq_tokens(b, i, &e) : prefix_tokens(b, i, &e);
       if (T <= 0) return;
       const int pos0 = own ? e.z : e.y, n = own ? pos0 + T : pos0;
       float* out = own ? w.kmax + (size_t)i * w.chunks * (kGroups * kNB) : w.kmax_prefix + (size_t)i * w.chunks_prefix * (kGroups * kNB);
@@ -145,14 +125,40 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const TreeBatch b, con
     }
     x -= prefix_blocks + own_blocks;
   }
+  const bool near = b.n_seq <= kNearSeqs, near_prefixes = b.n_prefix <= kNearPrefixes;
+  for (int i = tid; near && i < b.n_seq; i += 256) s_row[i] = __ldg(&b.seqs[i].w);
+  for (int i = tid; near_prefixes && i < b.n_prefix; i += 256) s_seq[i] = __ldg(&b.prefixes[i].z);
+  __syncthreads();
+  auto last_at = [](int n, int at, auto key) {  // the last of n whose key is not above `at`
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (key(mid) <= at) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
+  auto prefix_at = [&](int s) {
+    if (b.n_prefix == 0) return -1;
+    return near_prefixes ? last_at(b.n_prefix, s, [&](int i) { return s_seq[i]; }) : prefix_of(b, s);
+  };
   const int n_blocks = (b.n_tok + 255) / 256;
   const int t = x * 256 + tid;
-  if (t < b.n_tok) b.tok[t] = record(t);
-  for (int s = t; s < b.n_seq; s += n_blocks * 256) {
-    int4 e;
-    int p, cells;
-    if (shared_seq_tokens(b, s, &e, &p, &cells) < 0) set_dev_status(status, QSA_DEV_BAD_ID);
+  if (t < b.n_tok) {
+    const int s = near ? last_at(b.n_seq, t, [&](int i) { return s_row[i]; }) : last_at(b.n_seq, t, [&](int i) { return __ldg(&b.seqs[i].w); });
+    const int p = prefix_at(s);
+    const SharedSeq v = shared_seq(b, s, p);
+    int4 r = make_int4(-1, 0, 0, -1);
+    if (v.T > 0 && t >= v.e.w && t < v.e.w + v.T) {
+      int seen = v.pe.y + v.e.z;
+      for (int i = 0; 32 * i < v.T; ++i) seen += __popc(shared_mask_word(b, t, t - v.e.w, i, v.T));
+      r = make_int4(s, seen, v.pe.y, p);
+      more[t] = TokMore{make_int4(v.e.x, v.e.z, v.T, v.e.w), make_int4(v.pe.w, v.pT, 0, 0)};
+    }
+    b.tok[t] = r;
   }
+  for (int s = t; s < b.n_seq; s += n_blocks * 256)
+    if (shared_seq(b, s, prefix_at(s)).T < 0) set_dev_status(status, QSA_DEV_BAD_ID);
   for (int p = t; p < b.n_prefix; p += n_blocks * 256) {
     int4 e;
     if (prefix_tokens(b, p, &e) < 0) set_dev_status(status, QSA_DEV_BAD_ID);
@@ -166,16 +172,19 @@ constexpr int kStages = 3;                     // of its ring
 constexpr int kStageBytes = 2 * kTile * kD + 2 * kTile * kNB * 2;  // codes of K and V, scales
 constexpr int kQPitch = kD * 2 + 16;           // bytes of a query row: 16 of padding spread the banks
 constexpr int kOffRing = 16 * kQPitch;
-constexpr int kJoinSmem = kOffRing + kJoinWarps * kStages * kStageBytes;
+constexpr int kOffPartMl = kOffRing + kJoinWarps * kStages * kStageBytes;  // (m, l) of the prefix's parts [kMaxRuns][kHPG]
+constexpr int kJoinSmem = kOffPartMl + kMaxRuns * kHPG * 8;
+static_assert(2 * (kJoinSmem + 1024 + 1024) <= 228 * 1024, "two CTAs on an SM");
 constexpr int kOPitch = kD + 4;                // floats of a row of an unmerged O (over the ring)
 constexpr int kOffSum = kJoinWarps * kHPG * kOPitch * 4;  // and of the CTA's merged O behind the warps'
-constexpr int kOffPartMl = kOffSum + kHPG * kOPitch * 4;  // (m, l) of the parts to be joined [2 kMaxRuns][kHPG]
-static_assert(kOffPartMl + 2 * kMaxRuns * kHPG * 8 <= kJoinWarps * kStages * kStageBytes, "the rows fit over the ring");
+static_assert(kOffSum + kHPG * kOPitch * 4 <= kJoinWarps * kStages * kStageBytes, "the rows fit over the ring");
+static_assert(2 * kMaxRuns * kHPG * 8 <= kJoinWarps * kStages * kStageBytes, "as do the (m, l) of both kinds of parts");
 static_assert(kOffRing % 16 == 0 && kStageBytes % 16 == 0, "16-byte copies");
 constexpr float kRescaleBy = 8.f, kPUp = 7.f;  // log2 units; as in tree.cu
 
 struct JoinArgs {
   TreeBatch b;
+  const TokMore* more;
   const __half* q;
   const int8_t* kq;
   const int8_t* vq;
@@ -233,19 +242,20 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __gr
   __shared__ float2 s_ml[kJoinWarps][16];   // (m, l) of the warps' rows
   __shared__ float2 s_sum[kHPG];            // and of the CTA's
   cluster_arrive_all();
-  pdl_begin();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % S, g = blockIdx.x / S % kGroups, t = blockIdx.x / S / kGroups;
-  const int4 ti = a.b.tok[t];
+  // With own cells to attend to, the launch before is the prefixes' one, if there are any: its CTAs trigger this launch once
+  // all before it are complete, and the own cells need nothing of it.
+  const bool here = a.own.runs == 0;
+  if (!here || a.prefix.runs == 0) pdl_begin();
+  const int4 ti = a.b.tok[t], e = a.more[t].seq, pe = a.more[t].prefix;
   if (ti.x < 0) {  // the same in all CTAs of the cluster
+    pdl_begin();
     cluster_wait_all();
     return;
   }
-  const int4 e = __ldg(&a.b.seqs[ti.x]);
-  const int T = (ti.x + 1 < a.b.n_seq ? __ldg(&a.b.seqs[ti.x + 1].w) : a.b.n_tok) - e.w;
-  const int i_tok = t - e.w, pos0 = e.z;
+  const int T = e.z, i_tok = t - e.w, pos0 = e.y;
   const bool chosen = a.bits != nullptr && ti.y > a.b.identity_max;
-  const bool here = a.own.runs == 0;  // own cells are attended to in this launch
   const size_t out_row = ((size_t)t * kHeads + g * kHPG) * kD;
   if (here) {
     // ---- the queries' rows; 12 .. 15 are zeros
@@ -432,20 +442,16 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __gr
         }
       }
   }
-  // ---- (m, l) of the parts to be joined (every warp is past its ring)
-  float2(*s_part)[kHPG] = reinterpret_cast<float2(*)[kHPG]>(smem + kOffRing + kOffPartMl);
-  int4 pe = make_int4(0, 0, 0, 0);
-  int pT = 0, px_runs = 0;
-  if (ti.z > 0) {
-    pT = prefix_tokens(a.b, ti.w, &pe);
-    px_runs = a.prefix.runs;
-  }
+  // ---- (m, l) of the parts to be joined
+  pdl_begin();
+  float2(*s_part)[kHPG] = reinterpret_cast<float2(*)[kHPG]>(smem + (here ? kOffPartMl : kOffRing));
+  const int px_runs = ti.z > 0 ? a.prefix.runs : 0;
   const int runs = px_runs + a.own.runs;
   // part u of row h: of the prefix, then of the own cells
   auto part_at = [&](int h, int u, size_t* cta, int* row) -> const TreeParts& {
     const bool own = u >= px_runs;
     if (own) part_row(e.w, ti.x, T, g, a.own.runs, i_tok * kHPG + h, cta, row);
-    else part_row(pe.w, ti.w, pT, g, px_runs, (t - pe.w) * kHPG + h, cta, row);
+    else part_row(pe.x, ti.w, pe.y, g, px_runs, (t - pe.x) * kHPG + h, cta, row);
     *cta += 2 * (size_t)(own ? u - px_runs : u);
     return own ? a.own : a.prefix;
   };
@@ -511,22 +517,27 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __gr
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = fmaf(z[k], f, v[k]);
     };
-    constexpr int kDepth = 4;  // parts loaded at once
-    for (int u0 = 0; u0 < runs; u0 += kDepth) {
-      float4 x[kDepth][2];
+    constexpr int kDepth = 6;  // parts loaded at once
+    auto join = [&](const TreeParts& p, int first_row, int i, int n_tok, int u_at) {  // its parts are s_part[u_at ..]
+      size_t cta;
+      int row;
+      part_row(first_row, i, n_tok, g, p.runs, (t - first_row) * kHPG + h, &cta, &row);
+      const float4* from = p.o + cta * (kTreeBlock / 2 * kD / 4) + (size_t)(2 * d8) * (kTreeBlock / 2) + row;
+      constexpr size_t kStep = 2 * (kTreeBlock / 2) * kD / 4;  // from run to run
+      for (int u0 = 0; u0 < p.runs; u0 += kDepth) {
+        float4 x[kDepth][2];
 #pragma unroll
-      for (int k = 0; k < kDepth; ++k) {
-        size_t cta;
-        int row;
-        const TreeParts& p = part_at(h, min(u0 + k, runs - 1), &cta, &row);
-        const float4* from = p.o + cta * (kTreeBlock / 2 * kD / 4) + (size_t)(2 * d8) * (kTreeBlock / 2) + row;
-        x[k][0] = __ldcg(from);
-        x[k][1] = __ldcg(from + kTreeBlock / 2);
+        for (int k = 0; k < kDepth; ++k) {
+          x[k][0] = __ldcg(from + min(u0 + k, p.runs - 1) * kStep);
+          x[k][1] = __ldcg(from + min(u0 + k, p.runs - 1) * kStep + kTreeBlock / 2);
+        }
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k)
+          if (u0 + k < p.runs) add(s_part[u_at + u0 + k][h], x[k][0], x[k][1]);
       }
-#pragma unroll
-      for (int k = 0; k < kDepth; ++k)
-        if (u0 + k < runs) add(s_part[u0 + k][h], x[k][0], x[k][1]);
-    }
+    };
+    if (px_runs) join(a.prefix, pe.x, ti.w, pe.y, 0);
+    if (!here) join(a.own, e.w, ti.x, T, px_runs);
     if (here)
       for (int c = 0; c < S; ++c) {
         const uint32_t at = mapa_shared(sum_at + (uint32_t)(h * kOPitch + d8 * 8) * 4, c);
@@ -547,7 +558,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __gr
 constexpr int kOwnTokens = 4;
 
 struct Layout {
-  size_t tok, prefix, own, select, kmax, bytes;
+  size_t tok, more, prefix, own, select, kmax, bytes;
 };
 Layout layout(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv, int identity_max) {
   Layout l{};
@@ -558,6 +569,7 @@ Layout layout(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv, 
     return at;
   };
   l.tok = take((size_t)n_tok * sizeof(int4));
+  l.more = take((size_t)n_tok * sizeof(TokMore));
   l.prefix = take(n_prefix > 0 && max_prefix > 0 ? tree_parts_workspace_bytes(n_prefix, n_tok, max_prefix) : 0);
   l.own = take(n_tok >= kOwnTokens ? tree_parts_workspace_bytes(n_seq, n_tok, max_n_kv) : 0);  // a call of fewer sequences may take it
   if (max_n_kv > identity_max) {
@@ -595,6 +607,7 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   uint8_t* base = static_cast<uint8_t*>(ws);
   TreeBatch b = batch;
   b.tok = reinterpret_cast<int4*>(base + l.tok);
+  TokMore* more = reinterpret_cast<TokMore*>(base + l.more);
   const bool select = b.max_n_kv > b.identity_max;
   // own cells of a sequence, for the shapes of launches (any number gives the same results): what the longest prefix leaves
   const int own_cells = std::max(std::min(b.max_n_kv, 128), b.max_n_kv - b.max_prefix);
@@ -607,11 +620,11 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     own_chunks = (own_cells + kTreeChunk - 1) / kTreeChunk;
   }
   const int prep = (select ? kGroups * b.n_tok + b.n_prefix * w.chunks_prefix + b.n_seq * own_chunks : 0) + (b.n_tok + 255) / 256;
-  cudaError_t e = launch_pdl(prefix_prep_kernel, dim3(prep), dim3(256), 0, stream, b, w, select, own_chunks, q, ksc, status);
+  cudaError_t e = launch_pdl(prefix_prep_kernel, dim3(prep), dim3(256), 0, stream, b, w, more, select, own_chunks, q, ksc, status);
   if (e != cudaSuccess) return e;
   if (select && (e = launch_shared_select(b, w, own_cells, q, kq, ksc, ids, p, status, stream)) != cudaSuccess) return e;
   const uint32_t* bits = select ? w.bits : nullptr;
-  JoinArgs a{b, q, kq, vq, ksc, vsc, bits, w.pitch / 32, p.sm_scale * kLog2e, gate, out, {}, {}};
+  JoinArgs a{b, more, q, kq, vq, ksc, vsc, bits, w.pitch / 32, p.sm_scale * kLog2e, gate, out, {}, {}};
   if (b.n_prefix > 0 && b.max_prefix > 0) {
     e = launch_tree_parts(b, false, b.max_prefix, q, kq, vq, ksc, vsc, bits, w.pitch / 32, base + l.prefix, p.sm_scale, &a.prefix,
                           status, stream);

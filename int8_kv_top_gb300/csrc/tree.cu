@@ -149,8 +149,7 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
       x.e = make_int4(pe.x, 0, pe.y, pe.w);
     } else {
       sq = warp_find_seq(b.n_seq, blk, [&](int s) { return first_block(__ldg(&b.seqs[s].w), s); });
-      int p, cells;
-      x.T = kOf == kTreeCells ? tree_seq_tokens(b, sq, &x.e) : shared_seq_tokens(b, sq, &x.e, &p, &cells);
+      x.T = kOf == kTreeCells ? tree_seq_tokens(b, sq, &x.e) : shared_seq_tokens(b, sq, &x.e);
     }
     const long long k = blk - first_block(x.e.w, sq);
     here = x.T > 0 && k >= 0 && k * kTreeBlock < (long long)x.T * kHPG;
@@ -216,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
   cluster_arrive_all();  // #0, waited for before the first remote access: every CTA's barriers are set up
   pdl_begin();
+  if constexpr (kOf == kPrefixCells) pdl_trigger();  // prefix_join_kernel begins with what does not need this launch
   if (kOf == kTreeCells && blockIdx.x == 0) {  // one CTA looks over the whole table and flags bad entries
     for (int s = tid; s < a.b.n_seq; s += kThreads) {
       int4 e;

@@ -75,24 +75,29 @@ __device__ __forceinline__ int prefix_of(const TreeBatch& b, int s) {
   return lo;
 }
 
-// tree_seq_tokens of a shared call's sequence, with its prefix and the prefix's cells.
-__device__ __forceinline__ int shared_seq_tokens(const TreeBatch& b, int s, int4* e_out, int* p_out, int* cells_out) {
-  const int4 e = __ldg(&b.seqs[s]);
+// A shared call's sequence, behind prefix p (-1: none): its entry, tokens as in tree_seq_tokens, and the prefix's tokens
+// and {first pool cell, cells, first sequence, first token row}.
+struct SharedSeq {
+  int4 e, pe;
+  int T, pT;
+};
+__device__ __forceinline__ SharedSeq shared_seq(const TreeBatch& b, int s, int p) {
+  SharedSeq x;
+  x.e = __ldg(&b.seqs[s]);
   const int next = s + 1 < b.n_seq ? __ldg(&b.seqs[s + 1].w) : b.n_tok;
-  *e_out = e;
-  *p_out = -1;
-  *cells_out = 0;
-  const bool rows_ok = (s == 0 ? e.w == 0 : e.w >= 0) && next >= e.w && next <= b.n_tok;
-  if (rows_ok && e.y == 0) return 0;
-  const int p = prefix_of(b, s);
-  int4 pe = make_int4(0, 0, 0, 0);
-  const bool prefix_ok = p < 0 || prefix_tokens(b, p, &pe) >= 0;
-  *p_out = p;
-  *cells_out = pe.y;
-  const long long T = (long long)next - e.w, end = (long long)e.z + T;
-  const bool ok = prefix_ok && rows_ok && e.x >= 0 && e.y >= 1 && e.z >= 0 && end <= e.y && (long long)e.x + e.y <= b.n_pool &&
-                  pe.y + end <= b.max_n_kv && T <= 32 * (b.tree ? b.tree_words : kTreeWords);
-  return ok ? (int)T : -1;
+  x.pe = make_int4(0, 0, 0, 0);
+  x.pT = p < 0 ? 0 : prefix_tokens(b, p, &x.pe);
+  const bool rows_ok = (s == 0 ? x.e.w == 0 : x.e.w >= 0) && next >= x.e.w && next <= b.n_tok;
+  const long long T = (long long)next - x.e.w, end = (long long)x.e.z + T;
+  const bool ok = x.pT >= 0 && rows_ok && x.e.x >= 0 && x.e.y >= 1 && x.e.z >= 0 && end <= x.e.y &&
+                  (long long)x.e.x + x.e.y <= b.n_pool && x.pe.y + end <= b.max_n_kv && T <= 32 * (b.tree ? b.tree_words : kTreeWords);
+  x.T = rows_ok && x.e.y == 0 ? 0 : ok ? (int)T : -1;
+  return x;
+}
+__device__ __forceinline__ int shared_seq_tokens(const TreeBatch& b, int s, int4* e_out) {
+  const SharedSeq x = shared_seq(b, s, prefix_of(b, s));
+  *e_out = x.e;
+  return x.T;
 }
 
 // Word w of the mask of token i (row `row`) of a shared call's sequence of T tokens.

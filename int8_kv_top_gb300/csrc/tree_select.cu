@@ -138,12 +138,18 @@ struct __align__(8) TreeScoreBars {
 // First token chunk of a sequence: as first_block in tree.cu, for chunks of 32 tokens.
 __device__ __forceinline__ long long first_chunk(long long first_row, int s) { return first_row / kTokChunk + s; }
 
-// Of a shared call: once over the prefixes' cells for the tokens of all their sequences, and once over each sequence's own
-// cells; how many there are the host does not know, so there a chunk's CTAs share its tiles evenly (tiles_per_cta 0).
-template <CellsOf kOf>
+// Of a shared call: CTAs over the prefixes' cells, for the tokens of all their sequences, and behind them CTAs over each
+// sequence's own cells, in one launch (two launches of few CTAs each took 30 us, 48 chats of 475 own cells behind 16,000).  How
+// many cells there are the host does not know, so a chunk's CTAs share its tiles evenly.
+struct ScoreShape {
+  int tiles_per_cta;         // tree calls, whose grid is (tiles, group, token chunk)
+  int prefix_x, prefix_z;    // shared calls: CTAs that share a chunk's tiles, and token chunks, over the prefixes' cells
+  int own_x;                 // and CTAs that share a chunk's tiles of own cells
+};
+template <bool kShared>
 __global__ void __launch_bounds__(kScoreThreads, 1)
     tree_score_kernel(const TreeBatch b, const TreeSelect w, const int8_t* __restrict__ kq,
-                      const __half* __restrict__ ksc, int tiles_per_cta, float sm_scale, int* status) {
+                      const __half* __restrict__ ksc, const ScoreShape shape, float sm_scale, int* status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ TreeScoreBars bars;
@@ -152,13 +158,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   __shared__ uint32_t s_mask[kTokChunk][kTreeWords];
   __shared__ __align__(16) float s_scale[kTokChunk];  // sm_scale x the row's power of two; 0: not a selected token
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = blockIdx.y;
   pdl_begin();
+  int x = blockIdx.x, xs = gridDim.x, g = blockIdx.y, z = blockIdx.z;  // place among the chunk's CTAs, group, token chunk
+  bool prefix = false;
+  if constexpr (kShared) {
+    const int in_prefix = shape.prefix_x * kGroups * shape.prefix_z;
+    prefix = x < in_prefix;
+    xs = prefix ? shape.prefix_x : shape.own_x;
+    const int i = prefix ? x : x - in_prefix;
+    x = i % xs;
+    g = i / xs % kGroups;
+    z = i / xs / kGroups;
+  }
   int sq, T, drafted;  // of the sequence, or of the prefix: tokens; cells behind the committed ones
   int4 e4;
-  if constexpr (kOf == kPrefixCells) {
+  if (kShared && prefix) {
     int4 pe;
-    sq = warp_find_seq(b.n_prefix, blockIdx.z, [&](int i) {
+    sq = warp_find_seq(b.n_prefix, z, [&](int i) {
       int4 f;
       prefix_tokens(b, i, &f);
       return first_chunk(f.w, i);
@@ -167,24 +183,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     e4 = make_int4(pe.x, 0, pe.y, pe.w);
     drafted = 0;
   } else {
-    sq = warp_find_seq(b.n_seq, blockIdx.z, [&](int i) { return first_chunk(__ldg(&b.seqs[i].w), i); });
-    int p, cells;
-    T = kOf == kTreeCells ? tree_seq_tokens(b, sq, &e4) : shared_seq_tokens(b, sq, &e4, &p, &cells);
+    sq = warp_find_seq(b.n_seq, z, [&](int i) { return first_chunk(__ldg(&b.seqs[i].w), i); });
+    T = kShared ? shared_seq_tokens(b, sq, &e4) : tree_seq_tokens(b, sq, &e4);
     drafted = T;
   }
-  const long long kc = (long long)blockIdx.z - first_chunk(e4.w, sq);
+  const long long kc = (long long)z - first_chunk(e4.w, sq);
   const int pos0 = e4.z, n_scan = pos0 + drafted, tiles = (n_scan + kTileCells - 1) / kTileCells;
   int j_begin, J;
-  if constexpr (kOf == kTreeCells) {
-    j_begin = blockIdx.x * tiles_per_cta;
-    J = min(tiles_per_cta, tiles - j_begin);
+  if constexpr (!kShared) {
+    j_begin = x * shape.tiles_per_cta;
+    J = min(shape.tiles_per_cta, tiles - j_begin);
   } else {
-    j_begin = (int)((long long)tiles * blockIdx.x / gridDim.x);
-    J = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x) - j_begin;
+    j_begin = (int)((long long)tiles * x / xs);
+    J = (int)((long long)tiles * (x + 1) / xs) - j_begin;
   }
   if (T <= 0 || kc < 0 || kc * kTokChunk >= T || J <= 0) return;  // uniform
-  if (kOf == kTreeCells && n_scan <= b.identity_max) return;
-  if constexpr (kOf != kTreeCells) {  // no token of the chunk selects
+  if (!kShared && n_scan <= b.identity_max) return;
+  if constexpr (kShared) {  // no token of the chunk selects
     const int i = (int)kc * kTokChunk + lane;
     const int4 ti = i < T ? __ldg(&b.tok[e4.w + i]) : make_int4(-1, 0, 0, 0);
     if (!__any_sync(0xffffffffu, ti.x >= 0 && ti.y > b.identity_max)) return;  // the same in every warp
@@ -268,7 +283,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.b_full);
     if (warp == kEpiWarp) {  // lane = token: its mask and what its scores are multiplied by
-      if constexpr (kOf == kTreeCells) {
+      if constexpr (!kShared) {
         float km[kNB];
         warp_kmax(w, sq, g, n_scan, lane, km);
         int seen = pos0;
@@ -286,12 +301,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         float km[kNB] = {0.f, 0.f, 0.f, 0.f};
         const int4 ti = lane < n_here ? __ldg(&b.tok[t0 + lane]) : make_int4(-1, 0, 0, -1);
         const int one = max(__ffs(__ballot_sync(0xffffffffu, ti.x >= 0)) - 1, 0);
-        const int prefix = __shfl_sync(0xffffffffu, ti.w, one), cells = __shfl_sync(0xffffffffu, ti.z, one);
-        if (prefix >= 0) {
+        const int p = __shfl_sync(0xffffffffu, ti.w, one), cells = __shfl_sync(0xffffffffu, ti.z, one);
+        if (p >= 0) {
           TreeSelect v = w;
           v.kmax = w.kmax_prefix;
           v.chunks = w.chunks_prefix;
-          warp_kmax(v, prefix, g, cells, lane, km);
+          warp_kmax(v, p, g, cells, lane, km);
         }
         float scale = 0.f;
         if (ti.x >= 0 && ti.y > b.identity_max) {
@@ -303,7 +318,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         s_scale[lane] = scale;
 #pragma unroll
         for (int i = 0; i < kTreeWords; ++i)
-          s_mask[lane][i] = kOf == kOwnCells && lane < n_here ? shared_mask_word(b, t0 + lane, (int)kc * kTokChunk + lane, i, T) : 0u;
+          s_mask[lane][i] = !prefix && lane < n_here ? shared_mask_word(b, t0 + lane, (int)kc * kTokChunk + lane, i, T) : 0u;
       }
     }
     const bool t_ok = tile_wait_warp(&bars.tmem_ready, 0, status, &s_abort);
@@ -316,7 +331,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     };
     uint2 sw_next = scales_of(0);
     __half* dst0 = w.scores + (size_t)(g * b.n_tok + t0 + n0) * w.pitch;
-    if constexpr (kOf == kOwnCells) dst0 += own_column(__ldg(&b.tok[t0]).z);
+    if (kShared && !prefix) dst0 += own_column(__ldg(&b.tok[t0]).z);
     for (int j = 0; t_ok && j < J; ++j) {
       const int buf = j & 1, cell = (j_begin + j) * kTileCells + quarter * 32 + lane, dj = cell - pos0;
       const uint2 sw = sw_next;
@@ -345,7 +360,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       tc_fence_before();  // the accumulators are in registers
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-      if (n0 >= n16 || (kOf != kPrefixCells && cell >= n_scan)) continue;
+      if (n0 >= n16 || (!(kShared && prefix) && cell >= n_scan)) continue;
       __half* dst = dst0 + cell;
       const bool tail = (j_begin + j + 1) * kTileCells > pos0;
       const float4* sc4 = reinterpret_cast<const float4*>(s_scale + n0);
@@ -360,11 +375,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[i] *= sc[i];
-      if (kOf == kPrefixCells && cell >= n_scan) {  // the gap before the own cells' columns
+      if (kShared && prefix && cell >= n_scan) {  // the gap before the own cells' columns
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = -INFINITY;
       }
-      if (kOf != kPrefixCells && tail && dj >= 0) {
+      if (!(kShared && prefix) && tail && dj >= 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (!((s_mask[n0 + i][dj >> 5] >> (dj & 31)) & 1u)) acc[i] = -INFINITY;
@@ -409,7 +424,7 @@ cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __
   cudaError_t e = launch_pdl(tree_prep_kernel, dim3(kGroups * b.n_tok + b.n_seq * w.chunks + (plan ? 1 : 0)), dim3(256), 0,
                              stream, b, w, q, ksc, plan);
   if (e != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(tree_score_kernel<kTreeCells>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem)) !=
+  if ((e = cudaFuncSetAttribute(tree_score_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem)) !=
       cudaSuccess)
     return e;
   // tiles per CTA: as few as keep the CTAs near two waves of one per SM (a CTA's set-up, its B rows above all,
@@ -418,8 +433,8 @@ cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __
   const int zb = b.n_tok / kTokChunk + b.n_seq;
   int per = 2;
   while (per < 8 && (long long)((tiles + per - 1) / per) * kGroups * zb > 304) per *= 2;
-  e = launch_pdl(tree_score_kernel<kTreeCells>, dim3((tiles + per - 1) / per, kGroups, zb), dim3(kScoreThreads), kScoreSmem, stream, b,
-                 w, kq, ksc, per, p.sm_scale, status);
+  e = launch_pdl(tree_score_kernel<false>, dim3((tiles + per - 1) / per, kGroups, zb), dim3(kScoreThreads), kScoreSmem, stream, b,
+                 w, kq, ksc, ScoreShape{per, 0, 0, 0}, p.sm_scale, status);
   if (e != cudaSuccess) return e;
   return launch_tree_topk(b, w, q, kq, ksc, ids, p, status, stream);
 }
@@ -428,19 +443,21 @@ cudaError_t launch_tree_select(const TreeBatch& b, const TreeSelect& w, const __
 // records.  own_cells: about how many a sequence has.
 cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int own_cells, const __half* q, const int8_t* kq,
                                  const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream) {
-  cudaError_t e;
-  auto score = [&](auto kern, int n, int cells) -> cudaError_t {
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
-    if (err != cudaSuccess) return err;
+  cudaError_t e = cudaFuncSetAttribute(tree_score_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+  if (e != cudaSuccess) return e;
+  auto shares = [&](int n, int cells) {  // CTAs that share a chunk's tiles, as in a tree call
     const int tiles = (cells + kTileCells - 1) / kTileCells, zb = b.n_tok / kTokChunk + n;
-    int per = 2;  // as in a tree call
+    int per = 2;
     while (per < 8 && (long long)((tiles + per - 1) / per) * kGroups * zb > 304) per *= 2;
-    return launch_pdl(kern, dim3((tiles + per - 1) / per, kGroups, zb), dim3(kScoreThreads), kScoreSmem, stream, b, w, kq, ksc, 0,
-                      p.sm_scale, status);
+    return (tiles + per - 1) / per;
   };
-  if (b.n_prefix > 0 && b.max_prefix > 0 && (e = score(tree_score_kernel<kPrefixCells>, b.n_prefix, b.max_prefix)) != cudaSuccess)
-    return e;
-  if ((e = score(tree_score_kernel<kOwnCells>, b.n_seq, own_cells)) != cudaSuccess) return e;
+  const bool prefixes = b.n_prefix > 0 && b.max_prefix > 0;
+  const ScoreShape shape{0, prefixes ? shares(b.n_prefix, b.max_prefix) : 0, prefixes ? b.n_tok / kTokChunk + b.n_prefix : 0,
+                         shares(b.n_seq, own_cells)};
+  const long long ctas = kGroups * ((long long)shape.prefix_x * shape.prefix_z + (long long)shape.own_x * (b.n_tok / kTokChunk + b.n_seq));
+  e = launch_pdl(tree_score_kernel<true>, dim3((unsigned)ctas), dim3(kScoreThreads), kScoreSmem, stream, b, w, kq, ksc, shape,
+                 p.sm_scale, status);
+  if (e != cudaSuccess) return e;
   return launch_tree_topk(b, w, q, kq, ksc, ids, p, status, stream);
 }
 
