@@ -172,14 +172,18 @@ constexpr int kStages = 3;                     // of its ring
 constexpr int kStageBytes = 2 * kTile * kD + 2 * kTile * kNB * 2;  // codes of K and V, scales
 constexpr int kQPitch = kD * 2 + 16;           // bytes of a query row: 16 of padding spread the banks
 constexpr int kOffRing = 16 * kQPitch;
-constexpr int kOffPartMl = kOffRing + kJoinWarps * kStages * kStageBytes;  // (m, l) of the prefix's parts [kMaxRuns][kHPG]
-constexpr int kJoinSmem = kOffPartMl + kMaxRuns * kHPG * 8;
-static_assert(2 * (kJoinSmem + 1024 + 1024) <= 228 * 1024, "two CTAs on an SM");
-constexpr int kOPitch = kD + 4;                // floats of a row of an unmerged O (over the ring)
-constexpr int kOffSum = kJoinWarps * kHPG * kOPitch * 4;  // and of the CTA's merged O behind the warps'
-static_assert(kOffSum + kHPG * kOPitch * 4 <= kJoinWarps * kStages * kStageBytes, "the rows fit over the ring");
-static_assert(2 * kMaxRuns * kHPG * 8 <= kJoinWarps * kStages * kStageBytes, "as do the (m, l) of both kinds of parts");
+constexpr int kJoinSmem = kOffRing + kJoinWarps * kStages * kStageBytes;
+constexpr int kMaxJoin = 8;                    // CTAs of a cluster
+static_assert(2 * (kJoinSmem + 3 * 1024) <= 228 * 1024, "two CTAs on an SM");
+// Over the ring, once the own cells are attended to: the CTA's slice of every CTA's own rows (pushed by them), then the
+// warps' unmerged rows and, when those are merged, the slice of the parts.
+constexpr int kOPitch = kD + 4;                // floats of a warp's unmerged row
+constexpr int kRecvBytes = kHPG * kD * 4;      // [S][kHPG][kD / S]
+constexpr int kOffRows = kRecvBytes;           // [kJoinWarps][kHPG][kOPitch]
+constexpr int kPartBytes = kJoinWarps * kStages * kStageBytes - kRecvBytes;  // behind the slices of own rows: parts of as many runs as fit
+static_assert(kJoinWarps * kHPG * kOPitch * 4 <= kPartBytes && kPartBytes >= 7 * kHPG * kD * 4, "the rows fit over the ring");
 static_assert(kOffRing % 16 == 0 && kStageBytes % 16 == 0, "16-byte copies");
+static_assert(2 * kMaxRuns * kHPG * 8 <= kOffRing, "the parts' (m, l) lie over the queries");
 constexpr float kRescaleBy = 8.f, kPUp = 7.f;  // log2 units; as in tree.cu
 
 struct JoinArgs {
@@ -213,12 +217,6 @@ __device__ __forceinline__ uint16_t lds16(uint32_t at) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-  return v;
-}
-
 // Where row R of the rows behind `first_row` (12 a token; T tokens; table index i) lies among the parts: CTA of run 0,
 // and row of that CTA.
 __device__ __forceinline__ void part_row(int first_row, int i, int T, int g, int runs, int R, size_t* cta, int* row) {
@@ -241,6 +239,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __gr
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 s_ml[kJoinWarps][16];   // (m, l) of the warps' rows
   __shared__ float2 s_sum[kHPG];            // and of the CTA's
+  __shared__ float s_wf[kJoinWarps][kHPG];  // what the warps' rows are multiplied by
+  __shared__ float2 s_own[kMaxJoin][kHPG];  // (m, l) of the CTAs' own rows; then their weights
+  __shared__ float s_inv[kHPG];
+  __shared__ size_t s_from[2][kHPG];        // where the rows of run 0's part start (prefix, own), in float4
   cluster_arrive_all();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % S, g = blockIdx.x / S % kGroups, t = blockIdx.x / S / kGroups;
@@ -428,7 +430,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __gr
     }
     __syncthreads();  // every warp is done with its ring
     // O: lane (r, i) has dims 128 hf + 32 i + {0, 16} + n of rows r and r + 8
-    float* rows = reinterpret_cast<float*>(smem + kOffRing) + warp * (kHPG * kOPitch);
+    float* rows = reinterpret_cast<float*>(smem + kOffRing + kOffRows) + warp * (kHPG * kOPitch);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
@@ -442,115 +444,174 @@ __global__ void __launch_bounds__(kJoinThreads, 2) prefix_join_kernel(const __gr
         }
       }
   }
-  // ---- (m, l) of the parts to be joined
-  pdl_begin();
-  float2(*s_part)[kHPG] = reinterpret_cast<float2(*)[kHPG]>(smem + (here ? kOffPartMl : kOffRing));
-  const int px_runs = ti.z > 0 ? a.prefix.runs : 0;
-  const int runs = px_runs + a.own.runs;
-  // part u of row h: of the prefix, then of the own cells
-  auto part_at = [&](int h, int u, size_t* cta, int* row) -> const TreeParts& {
-    const bool own = u >= px_runs;
-    if (own) part_row(e.w, ti.x, T, g, a.own.runs, i_tok * kHPG + h, cta, row);
-    else part_row(pe.x, ti.w, pe.y, g, px_runs, (t - pe.x) * kHPG + h, cta, row);
-    *cta += 2 * (size_t)(own ? u - px_runs : u);
-    return own ? a.own : a.prefix;
-  };
-  for (int i = tid; i < runs * kHPG; i += kJoinThreads) {
-    size_t cta;
-    int row;
-    const TreeParts& p = part_at(i % kHPG, i / kHPG, &cta, &row);
-    s_part[i / kHPG][i % kHPG] = __ldcg(&p.ml[cta * (kTreeBlock / 2) + row]);
-  }
-  __syncthreads();
-  // ---- the CTA's own rows: the warps' in one
-  float* sum = reinterpret_cast<float*>(smem + kOffRing + kOffSum);
+  // ---- the warps' own rows in one, each CTA's slice of 256 / S dims pushed to it
+  cluster_wait_all();    // every CTA of the cluster runs
+  cluster_arrive_all();  // this one is past its ring
+  const int dims = kD / S;
   if (here) {
+    __syncthreads();
     if (tid < kHPG) {
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_ml[w][tid].x);
-      for (int w = 0; w < kJoinWarps; ++w)
-        if (s_ml[w][tid].x != -INFINITY) l = fmaf(s_ml[w][tid].y, fast_exp2(s_ml[w][tid].x - m), l);
+#pragma unroll 1
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = s_ml[w][tid].x == -INFINITY ? 0.f : fast_exp2(s_ml[w][tid].x - m);
+        s_wf[w][tid] = f;
+        l = fmaf(s_ml[w][tid].y, f, l);
+      }
       s_sum[tid] = make_float2(m, l);
     }
     __syncthreads();
-    const float* rows = reinterpret_cast<const float*>(smem + kOffRing);
+  }
+  cluster_wait_all();  // and so are the others
+  if (here) {
+    if (tid < kHPG) {
+      const float m = s_sum[tid].x, l = s_sum[tid].y;
+#pragma unroll 1
+      for (int c = 0; c < S; ++c)
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(&s_own[rank][tid]), c)), "f"(m), "f"(l) : "memory");
+    }
+    const float* rows = reinterpret_cast<const float*>(smem + kOffRing + kOffRows);
+#pragma unroll 1
     for (int i = tid; i < kHPG * (kD / 4); i += kJoinThreads) {
       const int h = i / (kD / 4), d = i % (kD / 4) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) {
-        const float m = s_ml[w][h].x;
-        if (m == -INFINITY) continue;
-        const float f = fast_exp2(m - s_sum[h].x);
+        const float f = s_wf[w][h];
         const float4 x = *reinterpret_cast<const float4*>(rows + (w * kHPG + h) * kOPitch + d);
-        v.x = fmaf(x.x, f, v.x);
+        v.x = fmaf(x.x, f, v.x);  // a row that has seen nothing holds zeros
         v.y = fmaf(x.y, f, v.y);
         v.z = fmaf(x.z, f, v.z);
         v.w = fmaf(x.w, f, v.w);
       }
-      *reinterpret_cast<float4*>(sum + h * kOPitch + d) = v;
+      const uint32_t at = smem_u32(smem + kOffRing) + (uint32_t)((rank * kHPG + h) * dims + d % dims) * 4u;
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mapa_shared(at, d / dims)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                   : "memory");
     }
   }
-  // ---- all parts: the cluster's CTAs take the rows in turn
-  cluster_wait_all();
   cluster_arrive_all();
-  cluster_wait_all();  // every CTA's rows are in its shared memory
-  const uint32_t sum_at = smem_u32(sum), ml_at = smem_u32(s_sum);
-  const int n_rows = (kHPG - rank + S - 1) / S;
-  for (int i = tid; i < n_rows * (kD / 8); i += kJoinThreads) {
-    const int h = rank + S * (i % n_rows), d8 = i / n_rows;  // a part's rows lie side by side
-    uint4 gw = make_uint4(0u, 0u, 0u, 0u);
-    if (a.gate) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + out_row + (size_t)h * kD) + d8);
-    float M = -INFINITY, L = 0.f;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int u = 0; u < runs; ++u) M = fmaxf(M, s_part[u][h].x);
-    float2 ml[8];
-    if (here)
-      for (int c = 0; c < S; ++c) {
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml[c].x), "=f"(ml[c].y) : "r"(mapa_shared(ml_at + h * 8, c)) : "memory");
-        M = fmaxf(M, ml[c].x);
-      }
-    auto add = [&](float2 st, const float4& x, const float4& y) {
-      if (st.x == -INFINITY) return;  // nothing of this row there
-      const float f = fast_exp2(st.x - M);
-      L = fmaf(st.y, f, L);
-      const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = fmaf(z[k], f, v[k]);
-    };
-    constexpr int kDepth = 6;  // parts loaded at once
-    auto join = [&](const TreeParts& p, int first_row, int i, int n_tok, int u_at) {  // its parts are s_part[u_at ..]
+  // ---- the parts of the launches before
+  pdl_begin();
+  const int px_runs = ti.z > 0 ? a.prefix.runs : 0, runs = px_runs + a.own.runs;
+  if (tid < 2 * kHPG) {
+    const bool own = tid >= kHPG;
+    const int h = own ? tid - kHPG : tid;
+    if (own ? a.own.runs > 0 : px_runs > 0) {
       size_t cta;
       int row;
-      part_row(first_row, i, n_tok, g, p.runs, (t - first_row) * kHPG + h, &cta, &row);
-      const float4* from = p.o + cta * (kTreeBlock / 2 * kD / 4) + (size_t)(2 * d8) * (kTreeBlock / 2) + row;
-      constexpr size_t kStep = 2 * (kTreeBlock / 2) * kD / 4;  // from run to run
-      for (int u0 = 0; u0 < p.runs; u0 += kDepth) {
-        float4 x[kDepth][2];
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k) {
-          x[k][0] = __ldcg(from + min(u0 + k, p.runs - 1) * kStep);
-          x[k][1] = __ldcg(from + min(u0 + k, p.runs - 1) * kStep + kTreeBlock / 2);
-        }
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k)
-          if (u0 + k < p.runs) add(s_part[u_at + u0 + k][h], x[k][0], x[k][1]);
-      }
-    };
-    if (px_runs) join(a.prefix, pe.x, ti.w, pe.y, 0);
-    if (!here) join(a.own, e.w, ti.x, T, px_runs);
-    if (here)
-      for (int c = 0; c < S; ++c) {
-        const uint32_t at = mapa_shared(sum_at + (uint32_t)(h * kOPitch + d8 * 8) * 4, c);
-        add(ml[c], ld_cluster4(at), ld_cluster4(at + 16));
-      }
-    const float inv = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= inv;
-    if (a.gate) apply_gate(v, gw);
-    reinterpret_cast<uint4*>(a.out + out_row + (size_t)h * kD)[d8] = pack_out(v);
+      if (own) part_row(e.w, ti.x, T, g, a.own.runs, i_tok * kHPG + h, &cta, &row);
+      else part_row(pe.x, ti.w, pe.y, g, px_runs, (t - pe.x) * kHPG + h, &cta, &row);
+      s_from[own][h] = cta * (kTreeBlock / 2 * kD / 4) + row;
+    }
   }
-  cluster_arrive_all();
-  cluster_wait_all();  // no CTA leaves while another reads its rows
+  cluster_wait_all();  // the slices have arrived, and every warp here is past the rows (and the queries)
+  __syncthreads();
+  constexpr int kRowStep = kTreeBlock / 2;               // float4 between the dims of a row
+  constexpr size_t kRunStep = 2 * (size_t)kRowStep * kD / 4;  // and between runs
+  float2(*s_part)[kHPG] = reinterpret_cast<float2(*)[kHPG]>(smem);  // over the queries: (m, l), then the weight
+  const float4* parts = reinterpret_cast<const float4*>(smem + kOffRing + kRecvBytes);
+  const int quads = dims / 4, fit = kPartBytes / (kHPG * 16) / quads;  // float4 of a row's slice; runs in a round
+  auto fetch = [&](int u0, int n) {  // runs u0 .. u0 + n - 1: [run][quad][row] float4
+    const uint32_t to = smem_u32(parts);
+#pragma unroll 1
+    for (int i = tid; i < n * quads * kHPG; i += kJoinThreads) {
+      const int h = i % kHPG, x = i / kHPG, u = u0 + x / quads, d = rank * quads + x % quads;
+      const bool own = u >= px_runs;
+      const float4* from = (own ? a.own.o : a.prefix.o) + s_from[own][h] + (own ? u - px_runs : u) * kRunStep + (size_t)d * kRowStep;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 16), "l"(reinterpret_cast<uint64_t>(from)) : "memory");
+    }
+  };
+  fetch(0, min(runs, fit));
+#pragma unroll 1
+  for (int i = tid; i < runs * kHPG; i += kJoinThreads) {
+    const int h = i % kHPG, u = i / kHPG;
+    const bool own = u >= px_runs;
+    const size_t at = s_from[own][h];
+    const size_t cta = at / (kTreeBlock / 2 * kD / 4) + 2 * (own ? u - px_runs : u), row = at % (kTreeBlock / 2);
+    s_part[u][h] = __ldcg((own ? a.own.ml : a.prefix.ml) + cta * (kTreeBlock / 2) + row);
+  }
+  __syncthreads();
+  // ---- weights e^(m - M) of the parts and of the CTAs' own rows, and 1 / L: a warp a row, a lane a part
+#pragma unroll 1
+  for (int h = warp; h < kHPG; h += kJoinWarps) {
+    const int n = runs + (here ? S : 0);
+    float2* mine[3];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int u = lane + 32 * k;
+      mine[k] = u < runs ? &s_part[u][h] : u < n ? &s_own[u - runs][h] : nullptr;
+      if (mine[k]) M = fmaxf(M, mine[k]->x);
+    }
+    static_assert(2 * kMaxRuns <= 96 && kMaxRuns + kMaxJoin <= 96, "three parts a lane");
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (mine[k]) {
+        const float f = mine[k]->x == -INFINITY ? 0.f : fast_exp2(mine[k]->x - M);  // nothing of this row there: weight 0
+        if (f != 0.f) L = fmaf(mine[k]->y, f, L);
+        mine[k]->x = f;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) s_inv[h] = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
+  }
+  // ---- the sum, eight dims of a row a thread
+  float* recv = reinterpret_cast<float*>(smem + kOffRing);
+#pragma unroll 1
+  for (int u0 = 0; u0 < runs || u0 == 0; u0 += fit) {
+    const int n = min(runs - u0, fit);
+    if (u0 > 0) {
+      __syncthreads();  // the round before is read
+      fetch(u0, n);
+    }
+    cp_async_wait_all();
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < kHPG * dims / 8; i += kJoinThreads) {
+      const int h = i % kHPG, d8 = i / kHPG;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      auto add = [&](float f, const float4& p, const float4& q) {
+        x.x = fmaf(p.x, f, x.x);
+        x.y = fmaf(p.y, f, x.y);
+        x.z = fmaf(p.z, f, x.z);
+        x.w = fmaf(p.w, f, x.w);
+        y.x = fmaf(q.x, f, y.x);
+        y.y = fmaf(q.y, f, y.y);
+        y.z = fmaf(q.z, f, y.z);
+        y.w = fmaf(q.w, f, y.w);
+      };
+      float4* keep = reinterpret_cast<float4*>(recv + h * dims + d8 * 8);  // rank 0's slice; later rounds: the sum so far
+      if (u0 > 0) {
+        add(1.f, keep[0], keep[1]);
+      } else if (here) {
+#pragma unroll 1
+        for (int c = 0; c < S; ++c) {
+          const float4* z = reinterpret_cast<const float4*>(recv + (c * kHPG + h) * dims + d8 * 8);
+          add(s_own[c][h].x, z[0], z[1]);
+        }
+      }
+      const float4* z = parts + 2 * d8 * kHPG + h;
+#pragma unroll 2
+      for (int u = 0; u < n; ++u, z += quads * kHPG) {
+        const float f = s_part[u0 + u][h].x;
+        if (f != 0.f) add(f, z[0], z[kHPG]);  // a run that has nothing of the row wrote nothing
+      }
+      if (u0 + fit < runs) {
+        keep[0] = x;
+        keep[1] = y;
+        continue;
+      }
+      const size_t at = out_row + (size_t)h * kD + rank * dims + d8 * 8;
+      const float inv = s_inv[h];
+      float v[8] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv, y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+      if (a.gate) apply_gate(v, __ldg(reinterpret_cast<const uint4*>(a.gate + at)));
+      *reinterpret_cast<uint4*>(a.out + at) = pack_out(v);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- the call
@@ -635,9 +696,9 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     if (e != cudaSuccess) return e;
   }
   if ((e = join_setup()) != cudaSuccess) return e;
-  // CTAs a (token, group): as many as fit on the GPU at once (two on an SM), and 64 own cells each at least
+  // CTAs a (token, group): as many as fit on the GPU at once, two on an SM
   int S = 1;
-  while (S < 8 && (long long)b.n_tok * kGroups * S * 2 <= 2 * 152 && (a.own.runs > 0 || own_cells > 64 * S)) S *= 2;
+  while (S < 8 && (long long)b.n_tok * kGroups * S * 2 <= 2 * 152) S *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(b.n_tok * kGroups * S));
   cfg.blockDim = dim3(kJoinThreads);
