@@ -157,7 +157,7 @@ struct TreeParts {  // unmerged rows of blocks (tree.cu): O [CTA][64][128][4] an
   int runs;  // 0: none
 };
 size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells);
-cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, const __half* q, const int8_t* kq, const int8_t* vq,
+cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int beside, const __half* q, const int8_t* kq, const int8_t* vq,
                               const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
                               float sm_scale, TreeParts* parts, int* status, cudaStream_t stream);
 cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int own_cells, const __half* q, const int8_t* kq,

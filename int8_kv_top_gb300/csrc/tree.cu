@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
   cluster_arrive_all();  // #0, waited for before the first remote access: every CTA's barriers are set up
   pdl_begin();
-  if constexpr (kOf == kPrefixCells) pdl_trigger();  // prefix_join_kernel begins with what does not need this launch
+  if constexpr (kOf != kTreeCells) pdl_trigger();  // the next launch's CTAs may wait beside these for its start
   if (kOf == kTreeCells && blockIdx.x == 0) {  // one CTA looks over the whole table and flags bad entries
     for (int s = tid; s < a.b.n_seq; s += kThreads) {
       int4 e;
@@ -822,19 +822,20 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
   return launch_pdl(tree_join_kernel, dim3(d.blocks * kGroups * (2 * kRows / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
 }
 
-// The parts of a shared call: of its prefixes' cells, or of its sequences' own ones.
+// The parts of a shared call: of its prefixes' cells, or of its sequences' own ones.  cells: of the longest; beside: own cells
+// a sequence that prefix_own_kernel attends to on the SMs that this launch leaves.
 size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells) {
   return (size_t)shared_parts_most(n, n_tok, max_cells) * 2 * kRows * (kD * sizeof(float) + sizeof(float2));
 }
 
-cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, const __half* q, const int8_t* kq, const int8_t* vq,
+cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int beside, const __half* q, const int8_t* kq, const int8_t* vq,
                               const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
                               float sm_scale, TreeParts* parts, int* status, cudaStream_t stream) {
   PlanHeld held;
   cudaError_t e = tree_setup(&held);
   if (e != cudaSuccess) return e;
   const int n = own ? b.n_seq : b.n_prefix, most_cells = own ? b.max_n_kv : b.max_prefix;
-  const int runs = shared_plan_runs(held.n[0], n, b.n_tok, cells, shared_parts_most(n, b.n_tok, most_cells));
+  const int runs = shared_plan_runs(held.n[0], n, b.n_tok, cells, beside, shared_parts_most(n, b.n_tok, most_cells));
   const size_t rows = (size_t)shared_parts_most(n, b.n_tok, most_cells) * 2 * kRows;
   float* part = static_cast<float*>(ws);
   float2* ml = reinterpret_cast<float2*>(part + rows * kD);

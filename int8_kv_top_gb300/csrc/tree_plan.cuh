@@ -107,16 +107,21 @@ inline long long shared_parts_most(int n, int n_tok, int max_cells) {
   return std::max(blocks * kPlanGroups, parts_most(n, n_tok, max_cells));
 }
 
-inline int shared_plan_runs(int held, int n, int n_tok, int cells, long long most) {
+// `beside` own cells a sequence are attended to by a kernel that fills the SMs that this launch leaves, and all of them
+// when it ends: by SM, about 1.5 of a tile's time a CTA (512 cells of the longest sequence) and 0.0105 a cell and group, 0.6 of
+// the longest sequence's on average.
+inline int shared_plan_runs(int held, int n, int n_tok, int cells, int beside, long long most) {
   const long long blocks = tree_blocks_most(n, n_tok), rows = (long long)n_tok * kPlanHeads;
   const long long even = n * ((rows + (long long)n * kPlanRows - 1) / ((long long)n * kPlanRows));
   const int tiles = plan_tiles(cells);
+  const double other = beside > 0 ? (double)n_tok * kPlanGroups * (1.5 * ((beside + 511) / 512) + 0.6 * 0.0105 * beside) : 0.0;  // SM x tile times
   int best = 1;
   double best_t = 0.0;
   for (int runs = 1; runs <= std::min(kMaxRuns, tiles) && (runs == 1 || blocks * kPlanGroups * runs <= most); ++runs) {
-    const double w = (double)(even * kPlanGroups) * runs / held;
+    const double clusters = (double)(even * kPlanGroups) * runs, w = clusters / held;
     const double waves = n == 1 ? std::ceil(w) : 0.5 * (std::ceil(w) + std::max(1.0, 0.9 * w));
-    const double t = waves * (5.0 + (tiles + runs - 1) / runs) + kJoinPart * runs * (double)(even * kPlanGroups);
+    double t = waves * (5.0 + (tiles + runs - 1) / runs);
+    t += std::max(0.0, other - std::max(0.0, waves * held - clusters) * 2.0 * t / waves) / (2.0 * held) + kJoinPart * clusters;
     if (runs == 1 || t < best_t) {
       best = runs;
       best_t = t;
