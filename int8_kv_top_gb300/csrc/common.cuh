@@ -154,10 +154,11 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
 struct TreeParts {  // unmerged rows of blocks (tree.cu): O [CTA][64][128][4] and (m, l) [CTA][128], `runs` pairs a block and group
   const float4* o;
   const float2* ml;
-  int runs;  // 0: none
+  int runs;       // 0: none
+  int run_tiles;  // a block of fewer tiles has as many of these runs as it takes (shared_runs)
 };
 size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells);
-cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int beside, const __half* q, const int8_t* kq, const int8_t* vq,
+cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int beside, bool behind_dense, const __half* q, const int8_t* kq, const int8_t* vq,
                               const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
                               float sm_scale, TreeParts* parts, int* status, cudaStream_t stream);
 cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int own_cells, const __half* q, const int8_t* kq,

@@ -145,16 +145,26 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const TreeBatch b, con
         float mx[kGroups * kNB];
 #pragma unroll
         for (int j = 0; j < kGroups * kNB; ++j) mx[j] = 0.f;
-        for (int c = c0 + tid; c < c1; c += 256) {
-          const int dj = c - pos0;
-          if (dj >= 0 && !((s_union[dj >> 5] >> (dj & 31)) & 1u)) continue;  // a drafted cell that no token sees
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(ksc + ((size_t)e.x + c) * (kGroups * kNB)));
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        constexpr int kAtOnce = 4;  // cells a thread loads before it uses any
+#pragma unroll 1
+        for (int c = c0 + tid; c < c1; c += 256 * kAtOnce) {
+          uint4 v[kAtOnce];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-            mx[2 * j] = fmaxf(mx[2 * j], fabsf(f.x));
-            mx[2 * j + 1] = fmaxf(mx[2 * j + 1], fabsf(f.y));
+          for (int i = 0; i < kAtOnce; ++i) {
+            const int x = c + 256 * i, dj = x - pos0;
+            v[i] = make_uint4(0u, 0u, 0u, 0u);  // none, or a drafted cell that no token sees
+            if (x < c1 && (dj < 0 || ((s_union[dj >> 5] >> (dj & 31)) & 1u)))
+              v[i] = __ldg(reinterpret_cast<const uint4*>(ksc + ((size_t)e.x + x) * (kGroups * kNB)));
+          }
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+              mx[2 * j] = fmaxf(mx[2 * j], fabsf(f.x));
+              mx[2 * j + 1] = fmaxf(mx[2 * j + 1], fabsf(f.y));
+            }
           }
         }
 #pragma unroll
@@ -214,11 +224,6 @@ struct OwnArgs {
   float2* ml;
 };
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // Where row R of the rows behind `first_row` (12 a token; T tokens; table index i) lies among the parts: CTA of run 0,
 // and row of that CTA.
 __device__ __forceinline__ void part_row(int first_row, int i, int T, int g, int runs, int R, size_t* cta, int* row) {
@@ -518,7 +523,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   const int slice = blockIdx.x % kSlices, g = blockIdx.x / kSlices % kGroups, t = blockIdx.x / kSlices / kGroups;
   // The launch before triggered this one when the one that makes the records was complete.
   const int4 ti = __ldcg(&a.tok[t]), e = __ldcg(&a.more[t].seq), pe = __ldcg(&a.more[t].prefix);
-  const int px_runs = ti.z > 0 ? a.prefix.p.runs : 0, n = px_runs + a.own.p.runs;
+  // runs that there are: a part's slots are a.own.p.runs apart all the same
+  auto runs_of = [](const TreeParts& p, int cells) {
+    return p.runs == 0 || cells == 0 ? 0 : shared_runs((cells + kTileCells - 1) / kTileCells, p.runs, p.run_tiles);
+  };
+  const int px_runs = runs_of(a.prefix.p, ti.z), n = px_runs + (a.own.rows ? a.own.p.runs : runs_of(a.own.p, e.y + e.z));
   if (ti.x >= 0 && tid < 2 * kHPG) {
     const bool own = tid >= kHPG;
     const int h = own ? tid - kHPG : tid;
@@ -529,7 +538,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
       size_t cta;
       int row;
       if (own) part_row(e.w, ti.x, e.z, g, a.own.p.runs, (t - e.w) * kHPG + h, &cta, &row);
-      else part_row(pe.x, ti.w, pe.y, g, px_runs, (t - pe.x) * kHPG + h, &cta, &row);
+      else part_row(pe.x, ti.w, pe.y, g, a.prefix.p.runs, (t - pe.x) * kHPG + h, &cta, &row);
       s_ml[own][h] = cta * (kTreeBlock / 2) + row;
       s_from[own][h] = cta * (kTreeBlock / 2 * kD / 4) + row;
     }
@@ -626,6 +635,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------- the call
+constexpr int kOwnInTopk = 2048;
 // From how many tokens a sequence (on average) their own cells go to the tensor-core kernel.
 constexpr int kOwnTokens = 4;
 
@@ -687,6 +697,7 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   const bool select = b.max_n_kv > b.identity_max;
   // own cells of a sequence, for the shapes of launches (any number gives the same results): what the longest prefix leaves
   const int own_cells = std::max(std::min(b.max_n_kv, 128), b.max_n_kv - b.max_prefix);
+  const bool dense = b.n_prefix > 0 && b.max_prefix > 0, own_dense = (long long)b.n_tok >= (long long)kOwnTokens * b.n_seq;
   TreeSelect w{};
   int own_chunks = 1;
   if (select) {
@@ -694,8 +705,10 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     w.kmax_prefix = reinterpret_cast<float*>(base + l.kmax);
     w.chunks_prefix = (b.max_prefix + kTreeChunk - 1) / kTreeChunk;
     own_chunks = (own_cells + kTreeChunk - 1) / kTreeChunk;
+    // A few own cells of a token or two cost the top-k kernel less than CTAs of the score kernel (48 tokens of 50-900 own cells 7 us
+    // against 11; 40 sequences of 1-16 tokens and 0-400 own cells 12 against 4).
+    w.own_in_topk = own_cells <= kOwnInTopk && !own_dense;
   }
-  const bool dense = b.n_prefix > 0 && b.max_prefix > 0, own_dense = (long long)b.n_tok >= (long long)kOwnTokens * b.n_seq;
   const int prep = (select ? kGroups * b.n_tok + b.n_prefix * w.chunks_prefix + b.n_seq * own_chunks : 0) + (b.n_tok + 255) / 256;
   cudaError_t e = launch_pdl(prefix_prep_kernel, dim3(prep), dim3(256), 0, stream, b, w, more, select, own_chunks, q, ksc, status);
   if (e != cudaSuccess) return e;
@@ -703,11 +716,11 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   const uint32_t* bits = select ? w.bits : nullptr;
   const int pitch = w.pitch / 32;
   JoinArgs j{b.tok, more, {}, {}, gate, out};
-  if (dense && (e = launch_tree_parts(b, false, b.max_prefix, own_dense ? 0 : own_cells, q, kq, vq, ksc, vsc, bits, pitch,
+  if (dense && (e = launch_tree_parts(b, false, b.max_prefix, own_dense ? 0 : own_cells, false, q, kq, vq, ksc, vsc, bits, pitch,
                                       base + l.prefix, p.sm_scale, &j.prefix.p, status, stream)) != cudaSuccess)
     return e;
   if (own_dense) {
-    e = launch_tree_parts(b, true, own_cells, 0, q, kq, vq, ksc, vsc, bits, pitch, base + l.own, p.sm_scale, &j.own.p, status, stream);
+    e = launch_tree_parts(b, true, own_cells, 0, dense, q, kq, vq, ksc, vsc, bits, pitch, base + l.own, p.sm_scale, &j.own.p, status, stream);
     if (e != cudaSuccess) return e;
   } else {
     if ((e = own_setup()) != cudaSuccess) return e;
@@ -722,7 +735,7 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     const OwnArgs a{b, more, dense, q, kq, vq, ksc, vsc, bits, pitch, p.sm_scale * kLog2e, gate, last ? out : nullptr, o, ml};
     e = launch_pdl(prefix_own_kernel, dim3((unsigned)(b.n_tok * kGroups * S)), dim3(kOwnThreads), kOwnSmem, stream, a, S);
     if (e != cudaSuccess || last) return e;
-    j.own = PartSet{{reinterpret_cast<const float4*>(o), ml, S}, true};
+    j.own = PartSet{{reinterpret_cast<const float4*>(o), ml, S, 0}, true};
   }
   return launch_pdl(prefix_join_kernel, dim3((unsigned)(b.n_tok * kGroups * kSlices)), dim3(kJoinThreads), 0, stream, j);
 }

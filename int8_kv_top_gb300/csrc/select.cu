@@ -771,11 +771,59 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     n_kv = own + e.z + T;
     cell0 = ti.w >= 0 ? __ldg(&tb.prefixes[ti.w].x) : 0;
     own0 = (long long)e.x - own;
-    if (warp == 0) {
+    if (warp == 0 || ts.own_in_topk) {
 #pragma unroll
       for (int b = 0; b < kNB; ++b) km[b] = 0.f;
       shared_kmax(tb, ts, ti, e.z + T, g, lane, km);
       row_scale = tree_row_scale(eh + ((size_t)g * T_sel + r) * 8, km, sm_scale);
+    }
+    if (ts.own_in_topk) {
+      // The own cells' scores, a warp 16 cells at a time, as tree_score_kernel forms them: A = the codes, B's first two columns
+      // the hi and the lo row of Qsum.  Lane (n, i) of a k64 block has dims 16 i .. 16 i + 15, of cells n and n + 8 and of column n.
+      const int n_own = e.z + T, cell = lane >> 2, i4 = lane & 3;
+      const __half* qr = ts.qhl + (size_t)(g * tb.n_tok + t) * (2 * kD) + (cell & 1) * 64 + i4 * 16;
+      __half* dst = ts.scores + (size_t)(g * tb.n_tok + t) * n_pad + own;
+      const float scale = sm_scale * row_scale;
+      for (int c0 = warp * 16; c0 < n_own; c0 += nwarps * 16) {
+        const int ca = min(c0 + cell, n_own - 1), cb = min(c0 + cell + 8, n_own - 1);
+        const size_t ra = ((size_t)e.x + ca) * kGroups + g, rb = ((size_t)e.x + cb) * kGroups + g;
+        float sa = 0.f, sb = 0.f;
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+          const uint4 wa = __ldg(reinterpret_cast<const uint4*>(kq + ra * kD + b * kBlk + i4 * 16));
+          const uint4 wb = __ldg(reinterpret_cast<const uint4*>(kq + rb * kD + b * kBlk + i4 * 16));
+          const float xa = __half2float(ksc[ra * kNB + b]), xb = __half2float(ksc[rb * kNB + b]);
+          uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
+          if (cell < 2) {
+            q0 = __ldg(reinterpret_cast<const uint4*>(qr + b * 128));
+            q1 = __ldg(reinterpret_cast<const uint4*>(qr + b * 128) + 1);
+          }
+          const __half2 one = __half2half2(__ushort_as_half(0x3C00));
+          uint32_t a0[4], a1[4], b0[4], b1[4];
+          dequant8(wa.x, wa.y, one, a0);
+          dequant8(wa.z, wa.w, one, a1);
+          dequant8(wb.x, wb.y, one, b0);
+          dequant8(wb.z, wb.w, one, b1);
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(d, a0[0], b0[0], a0[1], b0[1], q0.x, q0.y);
+          mma16816(d, a0[2], b0[2], a0[3], b0[3], q0.z, q0.w);
+          mma16816(d, a1[0], b1[0], a1[1], b1[1], q1.x, q1.y);
+          mma16816(d, a1[2], b1[2], a1[3], b1[3], q1.z, q1.w);
+          sa = fmaf(xa, d[0] + d[1], sa);
+          sb = fmaf(xb, d[2] + d[3], sb);
+        }
+        if (i4 == 0) {
+          auto store = [&](int c, float s) {
+            if (c >= n_own) return;
+            const int dj = c - e.z;
+            const bool sees = dj < 0 || ((shared_mask_word(tb, t, t - e.w, dj >> 5, T) >> (dj & 31)) & 1u);
+            dst[c] = __float2half_rn(sees ? s * scale : -INFINITY);
+          };
+          store(c0 + cell, sa);
+          store(c0 + cell + 8, sb);
+        }
+      }
+      __syncthreads();  // the row is read below
     }
   } else if constexpr (kTree) {
     const int s = warp_find_seq(tb.n_seq, t, [&](int i) { return (long long)__ldg(&tb.seqs[i].w); });
@@ -830,7 +878,7 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     const int c = c0 + 8 * m;
     uint4 x = make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
     if (c < n_kv) {
-      x = __ldg(reinterpret_cast<const uint4*>(row + c));
+      x = kShared ? __ldcg(reinterpret_cast<const uint4*>(row + c)) : __ldg(reinterpret_cast<const uint4*>(row + c));
       if (c + 8 > n_kv) {
         uint16_t* hh = reinterpret_cast<uint16_t*>(&x);
         for (int j = 0; j < 8; ++j)

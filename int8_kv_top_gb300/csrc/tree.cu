@@ -104,6 +104,8 @@ struct DenseTreeArgs {
   float* part;           // unmerged O, [CTA of the grid][kD / 4][kRows][4]; null for one pair per block
   float2* part_ml;       // and its (m, l), [CTA of the grid][kRows], where the parts are joined by a launch of their own
   int runs;              // clusters that share a block: 1, or (with one pair a cluster) more and tree_join_kernel
+  int run_tiles;         // shared calls: tiles of a run at most, so that a shorter prefix takes fewer of them
+  bool behind_dense;     // own cells launched behind the prefixes'
   int* status;
 };
 
@@ -167,7 +169,7 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
     n_kv += __popc(x.m[w]);
   }
   if constexpr (kOf != kTreeCells) {
-    const int4 t = live ? b.tok[x.e.w + tok] : make_int4(-1, 0, 0, 0);
+    const int4 t = live ? __ldcg(&b.tok[x.e.w + tok]) : make_int4(-1, 0, 0, 0);
     x.ours = t.x >= 0;
     x.sel = x.ours && t.y > b.identity_max;
     return x;
@@ -214,8 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     fence_mbar_init();
   }
   cluster_arrive_all();  // #0, waited for before the first remote access: every CTA's barriers are set up
-  pdl_begin();
-  if constexpr (kOf != kTreeCells) pdl_trigger();  // the next launch's CTAs may wait beside these for its start
+  // Own cells need nothing of the prefixes' launch before them, which triggered this one when all launches before it were
+  // complete: one CTA waits for it at its end, so that this launch ends no earlier.
+  const bool late = kOf == kOwnCells && a.behind_dense;
+  if (!late) pdl_begin();
+  if constexpr (kOf != kTreeCells) pdl_trigger();  // the next launch's CTAs may start, or wait, beside these
   if (kOf == kTreeCells && blockIdx.x == 0) {  // one CTA looks over the whole table and flags bad entries
     for (int s = tid; s < a.b.n_seq; s += kThreads) {
       int4 e;
@@ -246,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   __syncthreads();
   if (!s_blk[0]) {  // the same in every CTA of the cluster: an unused index, or no token of ours
     cluster_wait_all();
+    if (late && blockIdx.x == 0) pdl_begin();
     return;
   }
   const long long cell0 = s_blk[1];
@@ -255,7 +261,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   const int drafted = kOf == kTreeCells ? T : s_blk[6];  // cells behind the committed ones
   const int n_scan = pos0 + drafted;
   const int n_tiles = (n_scan + kTileCells - 1) / kTileCells;
-  const int j_begin = n_tiles * run / pairs, J = n_tiles * (run + 1) / pairs - j_begin;  // the same in both CTAs of a pair
+  const int my_runs = kOf == kTreeCells ? pairs : shared_runs(n_tiles, a.runs, a.run_tiles);
+  if (kOf != kTreeCells && run >= my_runs) {  // uniform over the cluster
+    cluster_wait_all();
+    return;  // not the first CTA: run 0 there is
+  }
+  const int j_begin = n_tiles * run / my_runs, J = n_tiles * (run + 1) / my_runs - j_begin;  // the same in both CTAs of a pair
   auto pair_addr = [&](const void* p) { return mapa_shared(smem_u32(p), (uint32_t)rank & ~1u); };  // in rank 0
   const bool merges = kOf == kTreeCells && a.runs == 1;  // in this launch; else the parts are joined by another
   float m_run = -INFINITY, l_run = 0.f;  // softmax threads: the row's running maximum (log2 units), this half's sum
@@ -400,9 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     const bool active = r < n_rows && ((s_ours >> min(ti, 31)) & 1), chosen = active && ((s_sel >> min(ti, 31)) & 1);
     const uint2* sel_bits = reinterpret_cast<const uint2*>(
         chosen ? a.bits + (size_t)(g * a.b.n_tok + first + R / kHPG) * a.bits_pitch : nullptr);
-    if (kOf == kOwnCells && chosen) sel_bits += own_column(a.b.tok[first + R / kHPG].z) / 64;
+    if (kOf == kOwnCells && chosen) sel_bits += own_column(__ldcg(&a.b.tok[first + R / kHPG].z)) / 64;
     uint2 m_next = make_uint2(0u, 0u);  // a selected row's bits, loaded a tile ahead
-    if (chosen && J > 0) m_next = __ldg(sel_bits + 2 * j_begin + wg);
+    auto sel_at = [&](int j) { return kOf == kOwnCells ? __ldcg(sel_bits + 2 * j + wg) : __ldg(sel_bits + 2 * j + wg); };
+    if (chosen && J > 0) m_next = sel_at(j_begin);
     // 32 visibility bits from drafted cell x on: cells before the drafted ones are seen, those past the mask not
     auto bits32 = [&](int x) -> uint32_t {
       const int w = x >> 5;  // floor (called for active rows: ti is a token of the block)
@@ -437,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       }
       const int x0 = (j_begin + j) * kTileCells + wg * 64 - pos0;  // drafted index of this half's first cell
       const uint2 m_sel = m_next;
-      if (chosen && j + 1 < J) m_next = __ldg(sel_bits + 2 * (j_begin + j + 1) + wg);
+      if (chosen && j + 1 < J) m_next = sel_at(j_begin + j + 1);
       if (x0 + 64 > 0 || !active || chosen) {  // an identity row needs no mask over committed cells
         const uint32_t m0 = !active ? 0u : chosen ? m_sel.x : bits32(x0);
         const uint32_t m1 = !active ? 0u : chosen ? m_sel.y : bits32(x0 + 32);
@@ -644,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       }
     }
   }
+  if (late && blockIdx.x == 0) pdl_begin();
 }
 
 // Joins the parts of blocks that several clusters share, in the runs' order within a slice and then slice by
@@ -815,7 +828,7 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
   const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, plan,
                         static_cast<float*>(ws),
                         reinterpret_cast<float2*>(static_cast<float*>(ws) + part_rows(b.n_seq, b.n_tok, b.max_n_kv) * kD),
-                        d.runs, status};
+                        d.runs, 0, false, status};
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = tree_config(d.pairs, d.blocks * kGroups * d.runs, stream, attr);
   if ((e = cudaLaunchKernelEx(&cfg, tree_dense_kernel<kTreeCells>, a, d.pairs)) != cudaSuccess || d.runs == 1) return e;
@@ -828,7 +841,7 @@ size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells) {
   return (size_t)shared_parts_most(n, n_tok, max_cells) * 2 * kRows * (kD * sizeof(float) + sizeof(float2));
 }
 
-cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int beside, const __half* q, const int8_t* kq, const int8_t* vq,
+cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int beside, bool behind_dense, const __half* q, const int8_t* kq, const int8_t* vq,
                               const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
                               float sm_scale, TreeParts* parts, int* status, cudaStream_t stream) {
   PlanHeld held;
@@ -839,8 +852,9 @@ cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int besid
   const size_t rows = (size_t)shared_parts_most(n, b.n_tok, most_cells) * 2 * kRows;
   float* part = static_cast<float*>(ws);
   float2* ml = reinterpret_cast<float2*>(part + rows * kD);
-  *parts = TreeParts{reinterpret_cast<const float4*>(part), ml, runs};
-  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, nullptr, nullptr, nullptr, part, ml, runs, status};
+  const int run_tiles = (plan_tiles(cells) + runs - 1) / runs;
+  *parts = TreeParts{reinterpret_cast<const float4*>(part), ml, runs, run_tiles};
+  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, nullptr, nullptr, nullptr, part, ml, runs, run_tiles, behind_dense, status};
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = tree_config(1, tree_blocks_most(n, b.n_tok) * kGroups * runs, stream, attr);
   return own ? cudaLaunchKernelEx(&cfg, tree_dense_kernel<kOwnCells>, a, 1) : cudaLaunchKernelEx(&cfg, tree_dense_kernel<kPrefixCells>, a, 1);

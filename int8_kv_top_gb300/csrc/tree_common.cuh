@@ -137,6 +137,7 @@ struct TreeSelect {
   int pitch, chunks;
   float* kmax_prefix;  // shared calls: [n_prefix][chunks_prefix][8], likewise; kmax then counts the own cells
   int chunks_prefix;
+  bool own_in_topk;    // shared calls: the top-k kernel scores the own cells itself
 };
 constexpr int kTreeChunk = 2048;  // cells of a kmax chunk
 
@@ -179,6 +180,13 @@ __device__ __forceinline__ void shared_kmax(const TreeBatch& b, const TreeSelect
   raise_kmax(w.kmax, tok.x, w.chunks, g, n_own, km);
 }
 
+// D += A B for 16 x 8 x 16 fp16 tiles with fp32 sums, by a warp.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // A power of two that keeps a row's scores inside fp16: |score| <= sm_scale 128 sum_b kmax_b H_b.
 __device__ __forceinline__ float tree_row_scale(const float* eh, const float (&kmax)[kNB], float sm_scale) {
   float h = 0.f;
@@ -200,6 +208,11 @@ __device__ __forceinline__ int cta_rows(int T, int blk_row0, int half, int* x) {
   const int n = min(kTreeBlock, T * kHPG - blk_row0), first = (n + 1) / 2;
   *x = blk_row0 + half * first;
   return half ? n - first : first;
+}
+
+// Runs of a block and group of a shared call over n_tiles tiles: as many of run_tiles as it takes, `runs` at most.
+__device__ __forceinline__ int shared_runs(int n_tiles, int runs, int run_tiles) {
+  return max(1, min(runs, (n_tiles + run_tiles - 1) / run_tiles));
 }
 
 // Index of a sequence's first block in the grid: block k of sequence s has index first_block(s) + k.

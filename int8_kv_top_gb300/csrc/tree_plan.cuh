@@ -118,7 +118,8 @@ inline int shared_plan_runs(int held, int n, int n_tok, int cells, int beside, l
   int best = 1;
   double best_t = 0.0;
   for (int runs = 1; runs <= std::min(kMaxRuns, tiles) && (runs == 1 || blocks * kPlanGroups * runs <= most); ++runs) {
-    const double clusters = (double)(even * kPlanGroups) * runs, w = clusters / held;
+    // several prefixes: 0.6 of the longest's runs on average
+    const double clusters = (double)(even * kPlanGroups) * (n == 1 ? runs : std::max(1.0, 0.6 * runs)), w = clusters / held;
     const double waves = n == 1 ? std::ceil(w) : 0.5 * (std::ceil(w) + std::max(1.0, 0.9 * w));
     double t = waves * (5.0 + (tiles + runs - 1) / runs);
     t += std::max(0.0, other - std::max(0.0, waves * held - clusters) * 2.0 * t / waves) / (2.0 * held) + kJoinPart * clusters;

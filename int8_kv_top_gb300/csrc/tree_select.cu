@@ -445,17 +445,27 @@ cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int ow
                                  const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(tree_score_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
   if (e != cudaSuccess) return e;
-  auto shares = [&](int n, int cells) {  // CTAs that share a chunk's tiles, as in a tree call
-    const int tiles = (cells + kTileCells - 1) / kTileCells, zb = b.n_tok / kTokChunk + n;
-    int per = 2;
-    while (per < 8 && (long long)((tiles + per - 1) / per) * kGroups * zb > 304) per *= 2;
-    return (tiles + per - 1) / per;
+  // CTAs that share a chunk's tiles: as many as end first, by whole waves of one CTA an SM (whose set-up takes about three
+  // tiles' time); where the chunks of several sequences are ragged, half of one each is not there.
+  auto shares = [&](int n, int cells) {
+    const int tiles = (cells + kTileCells - 1) / kTileCells;
+    const int chunks = n == 1 ? (b.n_tok + kTokChunk - 1) / kTokChunk : b.n_tok / kTokChunk + (n + 1) / 2;
+    int best = 1;
+    long long best_t = -1;
+    for (int x = 1; x <= tiles; ++x) {
+      const long long t = ((long long)chunks * kGroups * x + 151) / 152 * (3 + (tiles + x - 1) / x);
+      if (best_t < 0 || t < best_t) {
+        best = x;
+        best_t = t;
+      }
+    }
+    return best;
   };
   const bool prefixes = b.n_prefix > 0 && b.max_prefix > 0;
   const ScoreShape shape{0, prefixes ? shares(b.n_prefix, b.max_prefix) : 0, prefixes ? b.n_tok / kTokChunk + b.n_prefix : 0,
-                         shares(b.n_seq, own_cells)};
+                         w.own_in_topk ? 0 : shares(b.n_seq, own_cells)};
   const long long ctas = kGroups * ((long long)shape.prefix_x * shape.prefix_z + (long long)shape.own_x * (b.n_tok / kTokChunk + b.n_seq));
-  e = launch_pdl(tree_score_kernel<true>, dim3((unsigned)ctas), dim3(kScoreThreads), kScoreSmem, stream, b, w, kq, ksc, shape,
+  if (ctas > 0) e = launch_pdl(tree_score_kernel<true>, dim3((unsigned)ctas), dim3(kScoreThreads), kScoreSmem, stream, b, w, kq, ksc, shape,
                  p.sm_scale, status);
   if (e != cudaSuccess) return e;
   return launch_tree_topk(b, w, q, kq, ksc, ids, p, status, stream);

@@ -324,16 +324,17 @@ def qsa_cache_commit(kq, ksc, vq, vsc, n_pool: int, seqs, n_seq: int, path, n_pa
                                    _stream(stream)))
 
 
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device  # without its set-up
 _F16, _I8, _I32, _F32 = (torch.float16, torch.uint16), (torch.int8,), (torch.int32, torch.uint32), (torch.float32,)
 
 
 def _array(t, name: str, dtypes: tuple, n: int, optional: bool = False):
     """The pointer of a packed array of at least n elements on the current device."""
-    if t is None and (optional or n <= 0) or isinstance(t, int):
+    if isinstance(t, torch.Tensor):
+        if t.dtype in dtypes and t.numel() >= n and t.is_contiguous() and (t.is_cuda and t.get_device() == _device() or not t.numel()):
+            return t.data_ptr()
+    elif isinstance(t, int) or t is None and (optional or n <= 0):
         return t
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous() and t.numel() >= n
-            and (t.is_cuda and t.get_device() == torch.cuda.current_device() or not t.numel())):
-        return t.data_ptr()
     raise QSAError(QSA_ERR_INVALID_ARG, f"{name} must be a contiguous {dtypes[0]} tensor of at least {n} elements on the current "
                                         f"device (got {_what(t)})")
 
@@ -356,7 +357,7 @@ def _probabilities(t, name: str, vocab: int, n_tok: int):
         return t, vocab
     if (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.dim() == 2 and t.shape[0] >= n_tok and t.shape[1] >= vocab
             and (t.stride(1) == 1 or vocab == 1) and (n_tok <= 1 or t.stride(0) >= vocab)
-            and (t.is_cuda and t.get_device() == torch.cuda.current_device() or not t.numel())):
+            and (t.is_cuda and t.get_device() == _device() or not t.numel())):
         return t.data_ptr(), max(t.stride(0), vocab)
     raise QSAError(QSA_ERR_INVALID_ARG, f"{name} must be a float32 tensor [{n_tok}, {vocab}] on the current device whose rows have "
                                         f"their elements side by side (got {_what(t)})")
