@@ -154,13 +154,17 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
 struct TreeParts {  // unmerged rows of blocks (tree.cu): O [CTA][64][128][4] and (m, l) [CTA][128], `runs` pairs a block and group
   const float4* o;
   const float2* ml;
-  int runs;       // 0: none
-  int run_tiles;  // a block of fewer tiles has as many of these runs as it takes (shared_runs)
+  int runs;       // 0: none; of prefixes their plan has them
+  int run_tiles;  // own cells: a block of fewer tiles has as many of these runs as it takes (shared_runs)
 };
 size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells);
-cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int beside, bool behind_dense, const __half* q, const int8_t* kq, const int8_t* vq,
-                              const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
-                              float sm_scale, TreeParts* parts, int* status, cudaStream_t stream);
+cudaError_t prefix_clusters(const TreeBatch& b, int beside, int* clusters);
+cudaError_t launch_prefix_parts(const TreeBatch& b, int clusters, const int4* plan, const __half* q, const int8_t* kq, const int8_t* vq,
+                                const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
+                                float sm_scale, TreeParts* parts, int* status, cudaStream_t stream);
+cudaError_t launch_own_parts(const TreeBatch& b, int cells, bool behind_dense, const __half* q, const int8_t* kq, const int8_t* vq,
+                             const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws, float sm_scale,
+                             TreeParts* parts, int* status, cudaStream_t stream);
 cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int own_cells, const __half* q, const int8_t* kq,
                                  const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream);
 int4* tree_dense_plan(const TreeBatch& b, void* ws);  // where its list of blocks goes, or null

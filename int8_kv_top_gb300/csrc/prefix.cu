@@ -24,10 +24,10 @@ namespace qsa {
 namespace {
 
 // ---------------------------------------------------------------- 1. records, queries' sums, maxima
-// What the join needs of a token besides its record (TreeBatch::tok): its sequence's {first pool cell, committed own cells,
-// tokens, first token row}, and its prefix's {first token row, tokens, -, -}.
+// What the later launches need of a token besides its record (TreeBatch::tok): its sequence's {first pool cell, committed own
+// cells, tokens, first token row}.
 struct TokMore {
-  int4 seq, prefix;
+  int4 seq;
 };
 
 // The tables' first rows and first sequences, in shared memory where they are short, and what is looked up in them.
@@ -65,7 +65,7 @@ struct Finder {
     if (v.T <= 0 || t < v.e.w || t >= v.e.w + v.T) return make_int4(-1, 0, 0, -1);
     int seen = v.pe.y + v.e.z;
     for (int i = 0; 32 * i < v.T; ++i) seen += __popc(shared_mask_word(b, t, t - v.e.w, i, v.T));
-    *more = TokMore{make_int4(v.e.x, v.e.z, v.T, v.e.w), make_int4(v.pe.w, v.pT, 0, 0)};
+    *more = TokMore{make_int4(v.e.x, v.e.z, v.T, v.e.w)};
     return make_int4(s, seen, v.pe.y, p);
   }
 };
@@ -80,11 +80,75 @@ __device__ __forceinline__ void check_tables(const TreeBatch& b, int first, int 
   }
 }
 
+// The runs of the prefixes' blocks, by a CTA of 256 threads: of L tiles at most each, L the smallest with which all runs
+// find a cluster and no block has more than kMaxRuns.  Beyond 256 prefixes, whose blocks are many, one run each.
+__device__ __forceinline__ void plan_prefixes(const TreeBatch& b, int4* __restrict__ plan, int clusters, int* room) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int4 e = make_int4(0, 0, 0, 0);
+  int T = 0;
+  auto look = [&](int p, int* blocks, int* tiles) {
+    T = p < b.n_prefix ? max(prefix_tokens(b, p, &e), 0) : 0;
+    *tiles = T > 0 ? (e.y + kTileCells - 1) / kTileCells : 0;
+    *blocks = *tiles > 0 ? (T * kHPG + kTreeBlock - 1) / kTreeBlock * kGroups : 0;
+  };
+  auto sum = [&](int v) {  // over the CTA
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if (lane == 0) room[warp] = v;
+    __syncthreads();
+    v = 0;
+    for (int i = 0; i < 8; ++i) v += room[i];
+    return v;
+  };
+  int blocks, tiles, L = 1 << 30;
+  look(tid, &blocks, &tiles);
+  if (b.n_prefix <= 256) {
+    int most = __reduce_max_sync(0xffffffffu, tiles);
+    __syncthreads();
+    if (lane == 0) room[warp] = most;
+    __syncthreads();
+    for (int i = 0; i < 8; ++i) most = max(most, room[i]);
+    int lo = max(1, (most + kMaxRuns - 1) / kMaxRuns), hi = max(most, lo);
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (sum(blocks * ((tiles + mid - 1) / mid)) <= clusters) hi = mid;
+      else lo = mid + 1;
+    }
+    L = lo;
+  }
+  int base = 0;
+  for (int p0 = 0; p0 < b.n_prefix; p0 += 256) {
+    if (p0 > 0) look(p0 + tid, &blocks, &tiles);
+    const int runs = blocks > 0 ? (int)(((long long)tiles + L - 1) / L) : 0, n = blocks * runs;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) room[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) before += room[i];
+      all += room[i];
+    }
+    // rows that overlap (a broken table, flagged elsewhere) may ask for more clusters than there are: those prefixes get none
+    const int first = base + before + x - n;
+    if (p0 + tid < b.n_prefix) plan[p0 + tid] = make_int4(first, first + n <= clusters ? runs : 0, e.w, T);
+    base += all;
+  }
+  if (tid == 0) plan[b.n_prefix] = make_int4(base, 0, 0, 0);
+}
+
 // Blocks, in this order: (token, group): Qsum and its error terms; (prefix, chunk of 2,048 cells) and (sequence, every
-// own_chunks-th chunk): max |ksc|; the first three only where tokens may select.  Then 256 tokens' records each.
+// own_chunks-th chunk): max |ksc|; the first three only where tokens may select.  Then 256 tokens' records each, and, where
+// prefixes are attended to, a last one that shares `clusters` CTA pairs out over them: plan[p] = {first pair, runs a block and
+// group, first token row, tokens}, plan[n_prefix] = {pairs in all}.
 __global__ void __launch_bounds__(256) prefix_prep_kernel(const TreeBatch b, const TreeSelect w, TokMore* __restrict__ more,
-                                                          bool select, int own_chunks, const __half* __restrict__ q,
-                                                          const __half* __restrict__ ksc, int* status) {
+                                                          bool select, int own_chunks, int4* __restrict__ plan, int clusters,
+                                                          const __half* __restrict__ q, const __half* __restrict__ ksc, int* status) {
   __shared__ long long s_e[8], s_h[8];
   __shared__ uint32_t s_union[kTreeWords];
   __shared__ float s_max[8][kGroups * kNB];
@@ -185,6 +249,10 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const TreeBatch b, con
     }
     x -= prefix_blocks + own_blocks;
   }
+  if (x == (b.n_tok + 255) / 256) {
+    plan_prefixes(b, plan, clusters, s_room);
+    return;
+  }
   const Finder find(b, s_room, tid, 256);
   const int t = x * 256 + tid;
   if (t < b.n_tok) b.tok[t] = find.record(t, &more[t]);
@@ -224,14 +292,13 @@ struct OwnArgs {
   float2* ml;
 };
 
-// Where row R of the rows behind `first_row` (12 a token; T tokens; table index i) lies among the parts: CTA of run 0,
-// and row of that CTA.
-__device__ __forceinline__ void part_row(int first_row, int i, int T, int g, int runs, int R, size_t* cta, int* row) {
+// Where row R of T tokens' (12 a token) lies among the parts: CTA of run 0, and row of that CTA.  first: their first pair.
+__device__ __forceinline__ void part_row(long long first, int T, int g, int runs, int R, size_t* cta, int* row) {
   const int k = R / kTreeBlock, r = R % kTreeBlock;
-  const int n = min(kTreeBlock, T * kHPG - k * kTreeBlock), first = (n + 1) / 2;
-  const int half = r >= first;
-  *cta = ((size_t)(first_block(first_row, i) + k) * kGroups + g) * runs * 2 + half;
-  *row = half ? r - first : r;
+  const int n = min(kTreeBlock, T * kHPG - k * kTreeBlock), half_rows = (n + 1) / 2;
+  const int half = r >= half_rows;
+  *cta = ((size_t)first + (size_t)(k * kGroups + g) * runs) * 2 + half;
+  *row = half ? r - half_rows : r;
 }
 
 // S CTAs a (token, group), an S-th of its tiles of 16 cells each.  The warps take the tiles in turn, each through a ring of its own:
@@ -510,6 +577,7 @@ struct JoinArgs {
   const int4* tok;
   const TokMore* more;
   PartSet prefix, own;  // runs 0: none
+  const int4* plan;     // of the prefixes' parts
   const __half* gate;
   __half* out;
 };
@@ -522,12 +590,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slice = blockIdx.x % kSlices, g = blockIdx.x / kSlices % kGroups, t = blockIdx.x / kSlices / kGroups;
   // The launch before triggered this one when the one that makes the records was complete.
-  const int4 ti = __ldcg(&a.tok[t]), e = __ldcg(&a.more[t].seq), pe = __ldcg(&a.more[t].prefix);
-  // runs that there are: a part's slots are a.own.p.runs apart all the same
-  auto runs_of = [](const TreeParts& p, int cells) {
-    return p.runs == 0 || cells == 0 ? 0 : shared_runs((cells + kTileCells - 1) / kTileCells, p.runs, p.run_tiles);
-  };
-  const int px_runs = runs_of(a.prefix.p, ti.z), n = px_runs + (a.own.rows ? a.own.p.runs : runs_of(a.own.p, e.y + e.z));
+  const int4 ti = __ldcg(&a.tok[t]), e = __ldcg(&a.more[t].seq);
+  const int4 pl = a.prefix.p.runs > 0 && ti.x >= 0 && ti.z > 0 ? __ldcg(&a.plan[ti.w]) : make_int4(0, 0, 0, 0);
+  const int px_runs = pl.y;
+  const int own_runs = a.own.rows ? a.own.p.runs : a.own.p.runs ? shared_runs((e.y + e.z + kTileCells - 1) / kTileCells, a.own.p.runs, a.own.p.run_tiles) : 0;
+  const int n = px_runs + own_runs;
   if (ti.x >= 0 && tid < 2 * kHPG) {
     const bool own = tid >= kHPG;
     const int h = own ? tid - kHPG : tid;
@@ -537,8 +604,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     } else if (own ? a.own.p.runs > 0 : px_runs > 0) {
       size_t cta;
       int row;
-      if (own) part_row(e.w, ti.x, e.z, g, a.own.p.runs, (t - e.w) * kHPG + h, &cta, &row);
-      else part_row(pe.x, ti.w, pe.y, g, a.prefix.p.runs, (t - pe.x) * kHPG + h, &cta, &row);
+      if (own) part_row(first_block(e.w, ti.x) * kGroups * a.own.p.runs, e.z, g, a.own.p.runs, (t - e.w) * kHPG + h, &cta, &row);
+      else part_row(pl.x, pl.w, g, px_runs, (t - pl.z) * kHPG + h, &cta, &row);
       s_ml[own][h] = cta * (kTreeBlock / 2) + row;
       s_from[own][h] = cta * (kTreeBlock / 2 * kD / 4) + row;
     }
@@ -642,7 +709,7 @@ constexpr int kOwnTokens = 4;
 inline int own_rows(int n_tok) { return std::max(n_tok, std::min(kMaxOwn * n_tok, kMostOwn)); }  // tokens x CTAs that share one
 
 struct Layout {
-  size_t tok, more, prefix, own, select, kmax, bytes;
+  size_t tok, more, plan, prefix, own, select, kmax, bytes;
 };
 Layout layout(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv, int identity_max) {
   Layout l{};
@@ -654,6 +721,7 @@ Layout layout(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv, 
   };
   l.tok = take((size_t)n_tok * sizeof(int4));
   l.more = take((size_t)n_tok * sizeof(TokMore));
+  l.plan = take(((size_t)n_prefix + 1) * sizeof(int4));
   l.prefix = take(n_prefix > 0 && max_prefix > 0 ? tree_parts_workspace_bytes(n_prefix, n_tok, max_prefix) : 0);
   // rows of prefix_own_kernel, or parts of the tensor-core kernel (which a call of fewer sequences may take)
   l.own = take(std::max((size_t)own_rows(n_tok) * kHeads * (kD * sizeof(float) + sizeof(float2)),
@@ -709,18 +777,22 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     // against 11; 40 sequences of 1-16 tokens and 0-400 own cells 12 against 4).
     w.own_in_topk = own_cells <= kOwnInTopk && !own_dense;
   }
-  const int prep = (select ? kGroups * b.n_tok + b.n_prefix * w.chunks_prefix + b.n_seq * own_chunks : 0) + (b.n_tok + 255) / 256;
-  cudaError_t e = launch_pdl(prefix_prep_kernel, dim3(prep), dim3(256), 0, stream, b, w, more, select, own_chunks, q, ksc, status);
+  int4* plan = reinterpret_cast<int4*>(base + l.plan);
+  int clusters = 0;
+  cudaError_t e = dense ? prefix_clusters(b, own_dense ? 0 : own_cells, &clusters) : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  const int prep = (select ? kGroups * b.n_tok + b.n_prefix * w.chunks_prefix + b.n_seq * own_chunks : 0) + (b.n_tok + 255) / 256 + dense;
+  e = launch_pdl(prefix_prep_kernel, dim3(prep), dim3(256), 0, stream, b, w, more, select, own_chunks, plan, clusters, q, ksc, status);
   if (e != cudaSuccess) return e;
   if (select && (e = launch_shared_select(b, w, own_cells, q, kq, ksc, ids, p, status, stream)) != cudaSuccess) return e;
   const uint32_t* bits = select ? w.bits : nullptr;
   const int pitch = w.pitch / 32;
-  JoinArgs j{b.tok, more, {}, {}, gate, out};
-  if (dense && (e = launch_tree_parts(b, false, b.max_prefix, own_dense ? 0 : own_cells, false, q, kq, vq, ksc, vsc, bits, pitch,
-                                      base + l.prefix, p.sm_scale, &j.prefix.p, status, stream)) != cudaSuccess)
+  JoinArgs j{b.tok, more, {}, {}, plan, gate, out};
+  if (dense && (e = launch_prefix_parts(b, clusters, plan, q, kq, vq, ksc, vsc, bits, pitch, base + l.prefix, p.sm_scale, &j.prefix.p,
+                                        status, stream)) != cudaSuccess)
     return e;
   if (own_dense) {
-    e = launch_tree_parts(b, true, own_cells, 0, dense, q, kq, vq, ksc, vsc, bits, pitch, base + l.own, p.sm_scale, &j.own.p, status, stream);
+    e = launch_own_parts(b, own_cells, dense, q, kq, vq, ksc, vsc, bits, pitch, base + l.own, p.sm_scale, &j.own.p, status, stream);
     if (e != cudaSuccess) return e;
   } else {
     if ((e = own_setup()) != cudaSuccess) return e;

@@ -124,6 +124,7 @@ struct __align__(8) TreeBars {
 struct BlockAt {
   int4 e;
   int T, drafted, row0;
+  int g, run, runs;  // of a prefix: the group, and which of the runs that share the block this is
   uint32_t m[kTreeWords];
   bool ours, sel;
 };
@@ -140,20 +141,21 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
   } else {
     int sq;
     if constexpr (kOf == kPrefixCells) {
-      int4 pe;
-      sq = warp_find_seq(b.n_prefix, blk, [&](int p) {
-        int4 f;
-        prefix_tokens(b, p, &f);
-        return first_block(f.w, p);
-      });
-      x.T = prefix_tokens(b, sq, &pe);
-      if (pe.y == 0) x.T = 0;
-      x.e = make_int4(pe.x, 0, pe.y, pe.w);
+      // `blk` is the cluster's index and `plan` the prefixes' clusters
+      sq = warp_find_seq(b.n_prefix, blk, [&](int p) { return (long long)__ldg(&plan[p]).x; });
+      const int4 at = __ldg(&plan[sq]), pe = __ldg(&b.prefixes[sq]);
+      const int all = __ldg(&plan[b.n_prefix].x), i = blk - at.x, runs = max(at.y, 1);
+      x.T = blk < all && at.y > 0 ? at.w : 0;
+      x.e = make_int4(pe.x, 0, pe.y, at.z);
+      x.g = i / runs % kGroups;
+      x.run = i % runs;
+      x.runs = runs;
+      blk = i / runs / kGroups;  // of the prefix
     } else {
       sq = warp_find_seq(b.n_seq, blk, [&](int s) { return first_block(__ldg(&b.seqs[s].w), s); });
       x.T = kOf == kTreeCells ? tree_seq_tokens(b, sq, &x.e) : shared_seq_tokens(b, sq, &x.e);
     }
-    const long long k = blk - first_block(x.e.w, sq);
+    const long long k = kOf == kPrefixCells ? blk : blk - first_block(x.e.w, sq);
     here = x.T > 0 && k >= 0 && k * kTreeBlock < (long long)x.T * kHPG;
     x.row0 = here ? (int)k * kTreeBlock : 0;
   }
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   __shared__ TreeBars bars;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_blk[8];                       // active, first pool cell, pos0, T, first token row, first row, drafted cells
+  __shared__ int s_blk[10];  // active, first pool cell, pos0, T, first token row, first row, drafted cells; of a prefix: group, run, runs
   __shared__ uint32_t s_mask[kMaxTok][kTreeWords];
   __shared__ uint32_t s_union[kTreeWords];       // drafted cells that some token of ours sees
   __shared__ int s_ours, s_sel;                  // bit i: token i of the block is computed here; is a selected one
@@ -200,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank();
   const int half = rank & 1, pair = rank >> 1;  // rows 128 half .. of the block
-  const int pairs = S * a.runs, run = (blockIdx.x >> 1) % pairs;  // of the block; run `run` of its tiles
-  const int blk = (blockIdx.x >> 1) / pairs / kGroups, g = (blockIdx.x >> 1) / pairs % kGroups;
+  const int pairs = S * a.runs;  // of the block; run `run` of its tiles
+  const int blk = kOf == kPrefixCells ? blockIdx.x >> 1 : (blockIdx.x >> 1) / pairs / kGroups;
   if (tid == 0) s_abort = 0;
   if (tid < 32) {
     // a lane a barrier, in the order of the members
@@ -246,6 +248,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
       s_blk[4] = x.e.w;
       s_blk[5] = x.row0;
       s_blk[6] = x.drafted;
+      if constexpr (kOf == kPrefixCells) {
+        s_blk[7] = x.g;
+        s_blk[8] = x.run;
+        s_blk[9] = x.runs;
+      }
     }
   }
   __syncthreads();
@@ -261,8 +268,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   const int drafted = kOf == kTreeCells ? T : s_blk[6];  // cells behind the committed ones
   const int n_scan = pos0 + drafted;
   const int n_tiles = (n_scan + kTileCells - 1) / kTileCells;
-  const int my_runs = kOf == kTreeCells ? pairs : shared_runs(n_tiles, a.runs, a.run_tiles);
-  if (kOf != kTreeCells && run >= my_runs) {  // uniform over the cluster
+  const int g = kOf == kPrefixCells ? s_blk[7] : (blockIdx.x >> 1) / pairs % kGroups;
+  const int run = kOf == kPrefixCells ? s_blk[8] : (blockIdx.x >> 1) % pairs;
+  const int my_runs = kOf == kPrefixCells ? s_blk[9] : kOf == kOwnCells ? shared_runs(n_tiles, a.runs, a.run_tiles) : pairs;
+  if (kOf == kOwnCells && run >= my_runs) {  // uniform over the cluster
     cluster_wait_all();
     return;  // not the first CTA: run 0 there is
   }
@@ -835,29 +844,55 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
   return launch_pdl(tree_join_kernel, dim3(d.blocks * kGroups * (2 * kRows / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
 }
 
-// The parts of a shared call: of its prefixes' cells, or of its sequences' own ones.  cells: of the longest; beside: own cells
-// a sequence that prefix_own_kernel attends to on the SMs that this launch leaves.
+// The parts of a shared call: of its prefixes' cells (`clusters` pairs, shared out by `plan`), or of its sequences' own
+// ones (about `cells` a sequence).
 size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells) {
   return (size_t)shared_parts_most(n, n_tok, max_cells) * 2 * kRows * (kD * sizeof(float) + sizeof(float2));
 }
 
-cudaError_t launch_tree_parts(const TreeBatch& b, bool own, int cells, int beside, bool behind_dense, const __half* q, const int8_t* kq, const int8_t* vq,
-                              const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
-                              float sm_scale, TreeParts* parts, int* status, cudaStream_t stream) {
+cudaError_t prefix_clusters(const TreeBatch& b, int beside, int* clusters) {
   PlanHeld held;
-  cudaError_t e = tree_setup(&held);
-  if (e != cudaSuccess) return e;
-  const int n = own ? b.n_seq : b.n_prefix, most_cells = own ? b.max_n_kv : b.max_prefix;
-  const int runs = shared_plan_runs(held.n[0], n, b.n_tok, cells, beside, shared_parts_most(n, b.n_tok, most_cells));
+  const cudaError_t e = tree_setup(&held);
+  if (e == cudaSuccess)
+    *clusters = shared_plan_clusters(held.n[0], b.n_prefix, b.n_tok, b.max_prefix, beside, shared_parts_most(b.n_prefix, b.n_tok, b.max_prefix));
+  return e;
+}
+
+namespace {
+template <CellsOf kOf>
+cudaError_t launch_parts(const TreeBatch& b, int clusters, int runs, int run_tiles, bool behind_dense, int n, int most_cells,
+                         const int4* plan, const __half* q, const int8_t* kq, const int8_t* vq, const __half* ksc, const __half* vsc,
+                         const uint32_t* bits, int bits_pitch, void* ws, float sm_scale, TreeParts* parts, int* status,
+                         cudaStream_t stream) {
   const size_t rows = (size_t)shared_parts_most(n, b.n_tok, most_cells) * 2 * kRows;
   float* part = static_cast<float*>(ws);
   float2* ml = reinterpret_cast<float2*>(part + rows * kD);
-  const int run_tiles = (plan_tiles(cells) + runs - 1) / runs;
   *parts = TreeParts{reinterpret_cast<const float4*>(part), ml, runs, run_tiles};
-  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, nullptr, nullptr, nullptr, part, ml, runs, run_tiles, behind_dense, status};
+  const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, nullptr, nullptr, plan, part, ml, runs, run_tiles,
+                        behind_dense, status};
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = tree_config(1, tree_blocks_most(n, b.n_tok) * kGroups * runs, stream, attr);
-  return own ? cudaLaunchKernelEx(&cfg, tree_dense_kernel<kOwnCells>, a, 1) : cudaLaunchKernelEx(&cfg, tree_dense_kernel<kPrefixCells>, a, 1);
+  const cudaLaunchConfig_t cfg = tree_config(1, clusters, stream, attr);
+  return cudaLaunchKernelEx(&cfg, tree_dense_kernel<kOf>, a, 1);
+}
+}  // namespace
+
+cudaError_t launch_prefix_parts(const TreeBatch& b, int clusters, const int4* plan, const __half* q, const int8_t* kq, const int8_t* vq,
+                                const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
+                                float sm_scale, TreeParts* parts, int* status, cudaStream_t stream) {
+  return launch_parts<kPrefixCells>(b, clusters, 1, 0, false, b.n_prefix, b.max_prefix, plan, q, kq, vq, ksc, vsc, bits, bits_pitch, ws,
+                                    sm_scale, parts, status, stream);
+}
+
+cudaError_t launch_own_parts(const TreeBatch& b, int cells, bool behind_dense, const __half* q, const int8_t* kq, const int8_t* vq,
+                             const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws, float sm_scale,
+                             TreeParts* parts, int* status, cudaStream_t stream) {
+  PlanHeld held;
+  const cudaError_t e = tree_setup(&held);
+  if (e != cudaSuccess) return e;
+  const int runs = shared_plan_runs(held.n[0], b.n_seq, b.n_tok, cells, shared_parts_most(b.n_seq, b.n_tok, b.max_n_kv));
+  return launch_parts<kOwnCells>(b, tree_blocks_most(b.n_seq, b.n_tok) * kGroups * runs, runs, (plan_tiles(cells) + runs - 1) / runs,
+                                 behind_dense, b.n_seq, b.max_n_kv, nullptr, q, kq, vq, ksc, vsc, bits, bits_pitch, ws, sm_scale, parts,
+                                 status, stream);
 }
 
 }  // namespace qsa

@@ -107,28 +107,50 @@ inline long long shared_parts_most(int n, int n_tok, int max_cells) {
   return std::max(blocks * kPlanGroups, parts_most(n, n_tok, max_cells));
 }
 
-// `beside` own cells a sequence are attended to by a kernel that fills the SMs that this launch leaves, and all of them
-// when it ends: by SM, about 1.5 of a tile's time a CTA (512 cells of the longest sequence) and 0.0105 a cell and group, 0.6 of
-// the longest sequence's on average.
-inline int shared_plan_runs(int held, int n, int n_tok, int cells, int beside, long long most) {
+// Runs of a block and group over a sequence's own cells, about `cells` of the longest.
+inline int shared_plan_runs(int held, int n, int n_tok, int cells, long long most) {
   const long long blocks = tree_blocks_most(n, n_tok), rows = (long long)n_tok * kPlanHeads;
   const long long even = n * ((rows + (long long)n * kPlanRows - 1) / ((long long)n * kPlanRows));
   const int tiles = plan_tiles(cells);
-  const double other = beside > 0 ? (double)n_tok * kPlanGroups * (1.5 * ((beside + 511) / 512) + 0.6 * 0.0105 * beside) : 0.0;  // SM x tile times
   int best = 1;
   double best_t = 0.0;
   for (int runs = 1; runs <= std::min(kMaxRuns, tiles) && (runs == 1 || blocks * kPlanGroups * runs <= most); ++runs) {
-    // several prefixes: 0.6 of the longest's runs on average
-    const double clusters = (double)(even * kPlanGroups) * (n == 1 ? runs : std::max(1.0, 0.6 * runs)), w = clusters / held;
+    const double clusters = (double)(even * kPlanGroups) * runs, w = clusters / held;
     const double waves = n == 1 ? std::ceil(w) : 0.5 * (std::ceil(w) + std::max(1.0, 0.9 * w));
-    double t = waves * (5.0 + (tiles + runs - 1) / runs);
-    t += std::max(0.0, other - std::max(0.0, waves * held - clusters) * 2.0 * t / waves) / (2.0 * held) + kJoinPart * clusters;
+    const double t = waves * (5.0 + (tiles + runs - 1) / runs) + kJoinPart * clusters;
     if (runs == 1 || t < best_t) {
       best = runs;
       best_t = t;
     }
   }
   return best;
+}
+
+// Clusters over the prefixes' cells, `cells` of the longest.  The device, which knows how many each prefix has, shares them
+// out so that no run has more tiles than it must (prefix_prep_kernel).  At least two a block; whole fillings of the GPU at best.
+// `beside` own cells a sequence are attended to by a kernel that takes the SMs that this launch leaves, and all of them when it
+// ends: by SM, about 1.5 of a tile's time a CTA (512 cells of the longest sequence) and 0.0105 a cell and group, 0.6 of
+// the longest sequence's on average.
+inline int shared_plan_clusters(int held, int n, int n_tok, int cells, int beside, long long most) {
+  const long long rows = (long long)n_tok * kPlanHeads, blocks = tree_blocks_most(n, n_tok);
+  const long long even = std::min(blocks, (rows + kPlanRows - 1) / kPlanRows + (n - 1) / 2);
+  const int tiles = plan_tiles(cells);
+  const double total = (double)(even * kPlanGroups) * tiles * (n == 1 ? 1.0 : 0.6);  // tiles of all blocks
+  const double other = (double)n_tok * kPlanGroups * (beside > 0 ? 1.5 * ((beside + 511) / 512) + 0.6 * 0.0105 * beside : 0.0);
+  const long long least = blocks * kPlanGroups;
+  const long long last = std::min<long long>(most, std::min<long long>(4LL * held, even * kPlanGroups * std::min(kMaxRuns, tiles)));
+  long long best = least;
+  double best_t = 0.0;
+  for (long long c = least; c <= std::max(least, last); ++c) {
+    const double waves = std::ceil((double)c / held), run = std::ceil(total / (double)c);
+    double t = waves * (5.0 + run);
+    t += std::max(0.0, other - (waves * held - c) * 2.0 * t / waves) / (2.0 * held) + kJoinPart * c;
+    if (c == least || t < best_t) {
+      best = c;
+      best_t = t;
+    }
+  }
+  return (int)best;
 }
 
 }  // namespace qsa

@@ -445,15 +445,17 @@ cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int ow
                                  const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(tree_score_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
   if (e != cudaSuccess) return e;
-  // CTAs that share a chunk's tiles: as many as end first, by whole waves of one CTA an SM (whose set-up takes about three
-  // tiles' time); where the chunks of several sequences are ragged, half of one each is not there.
+  // CTAs that share a chunk's tiles: as many as end first, a CTA an SM at a time, its set-up about six tiles' time.  Where the
+  // chunks of several sequences are ragged, half of one each is not there.
   auto shares = [&](int n, int cells) {
     const int tiles = (cells + kTileCells - 1) / kTileCells;
     const int chunks = n == 1 ? (b.n_tok + kTokChunk - 1) / kTokChunk : b.n_tok / kTokChunk + (n + 1) / 2;
     int best = 1;
-    long long best_t = -1;
+    double best_t = -1.0;
     for (int x = 1; x <= tiles; ++x) {
-      const long long t = ((long long)chunks * kGroups * x + 151) / 152 * (3 + (tiles + x - 1) / x);
+      // one prefix: whole waves.  Several: what all CTAs take over the GPU, 0.6 of the longest on average, and the longest one
+      const double t = n == 1 ? ((long long)chunks * kGroups * x + 151) / 152 * (6.0 + (tiles + x - 1) / x)
+                              : (double)chunks * kGroups * (6.0 * x + 0.6 * tiles) / 152 + 6.0 + (tiles + x - 1) / x;
       if (best_t < 0 || t < best_t) {
         best = x;
         best_t = t;
