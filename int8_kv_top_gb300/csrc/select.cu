@@ -878,7 +878,13 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     const int c = c0 + 8 * m;
     uint4 x = make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
     if (c < n_kv) {
-      x = kShared ? __ldcg(reinterpret_cast<const uint4*>(row + c)) : __ldg(reinterpret_cast<const uint4*>(row + c));
+      if constexpr (kShared)  // through L1 (a thread's cells share lines), and coherent: this CTA may have written the row
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "l"(row + c)
+                     : "memory");
+      else
+        x = __ldg(reinterpret_cast<const uint4*>(row + c));
       if (c + 8 > n_kv) {
         uint16_t* hh = reinterpret_cast<uint16_t*>(&x);
         for (int j = 0; j < 8; ++j)
