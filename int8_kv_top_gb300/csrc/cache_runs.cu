@@ -2,8 +2,7 @@
 // server's tables put side by side at the front of the pool, in place).
 //
 // Both are copies bound by memory: a cell is 1,056 bytes (K and V codes, 512 bytes each, and their scales, 16 bytes
-// each), read once and written once.  A warp takes eight cells, all loaded into registers before any is stored: 8.25 KB
-// in flight a warp.
+// each), read once and written once.  A warp takes several cells, all loaded into registers before any is stored.
 #include <algorithm>
 
 #include "tree_common.cuh"
@@ -12,8 +11,8 @@ namespace qsa {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCellsPerWarp = 8;
-constexpr int kChunkCells = kWarps * kCellsPerWarp;  // cells of a CTA's step
+constexpr int kCopyCells = 8, kMoveCells = 8;  // cells that a warp of a copy and of a compaction holds at once
+constexpr int kCopyChunk = kWarps * kCopyCells, kMoveChunk = kWarps * kMoveCells;  // and a CTA
 
 struct Pool {
   int8_t* kq;
@@ -22,32 +21,47 @@ struct Pool {
   __half* vsc;
 };
 
-// Eight cells in registers: codes of K and V by all lanes (16 bytes each), scales by lanes 0 .. 15 (lane 2 u: K of
+// N cells in registers: codes of K and V by all lanes (16 bytes each), scales by the first 2 N lanes (lane 2 u: K of
 // cell u, 2 u + 1: V).  Cell u of the warp is `from` of lane u; negative: none.
+template <int N>
 struct Cells {
-  uint4 k[kCellsPerWarp], v[kCellsPerWarp], s;
+  uint4 k[N], v[N], s;
 };
-__device__ __forceinline__ void load_cells(const Pool& p, int64_t from, int lane, Cells& c) {
+template <int N>
+__device__ __forceinline__ void load_cells(const Pool& p, int64_t from, int lane, Cells<N>& c) {
 #pragma unroll
-  for (int u = 0; u < kCellsPerWarp; ++u) {
+  for (int u = 0; u < N; ++u) {
     const int64_t x = __shfl_sync(0xffffffffu, from, u);
     if (x < 0) continue;  // warp-uniform
     c.k[u] = reinterpret_cast<const uint4*>(p.kq)[x * 32 + lane];
     c.v[u] = reinterpret_cast<const uint4*>(p.vq)[x * 32 + lane];
   }
-  const int64_t y = __shfl_sync(0xffffffffu, from, (lane >> 1) & (kCellsPerWarp - 1));
-  if (lane < 2 * kCellsPerWarp && y >= 0) c.s = reinterpret_cast<const uint4*>(lane & 1 ? p.vsc : p.ksc)[y];
+  const int64_t y = __shfl_sync(0xffffffffu, from, (lane >> 1) & (N - 1));
+  if (lane < 2 * N && y >= 0) c.s = reinterpret_cast<const uint4*>(lane & 1 ? p.vsc : p.ksc)[y];
 }
-__device__ __forceinline__ void store_cells(const Pool& p, int64_t to, int lane, const Cells& c) {
+// A word that depends on all of them: who has it has them all.
+template <int N>
+__device__ __forceinline__ uint32_t folded(int64_t from, int lane, const Cells<N>& c) {
+  uint32_t x = 0u;
 #pragma unroll
-  for (int u = 0; u < kCellsPerWarp; ++u) {
+  for (int u = 0; u < N; ++u)
+    if (__shfl_sync(0xffffffffu, from, u) >= 0)
+      x ^= c.k[u].x ^ c.k[u].y ^ c.k[u].z ^ c.k[u].w ^ c.v[u].x ^ c.v[u].y ^ c.v[u].z ^ c.v[u].w;
+  const int64_t y = __shfl_sync(0xffffffffu, from, (lane >> 1) & (N - 1));
+  if (lane < 2 * N && y >= 0) x ^= c.s.x ^ c.s.y ^ c.s.z ^ c.s.w;
+  return x;
+}
+template <int N>
+__device__ __forceinline__ void store_cells(const Pool& p, int64_t to, int lane, const Cells<N>& c) {
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
     const int64_t x = __shfl_sync(0xffffffffu, to, u);
     if (x < 0) continue;
     reinterpret_cast<uint4*>(p.kq)[x * 32 + lane] = c.k[u];
     reinterpret_cast<uint4*>(p.vq)[x * 32 + lane] = c.v[u];
   }
-  const int64_t y = __shfl_sync(0xffffffffu, to, (lane >> 1) & (kCellsPerWarp - 1));
-  if (lane < 2 * kCellsPerWarp && y >= 0) reinterpret_cast<uint4*>(lane & 1 ? p.vsc : p.ksc)[y] = c.s;
+  const int64_t y = __shfl_sync(0xffffffffu, to, (lane >> 1) & (N - 1));
+  if (lane < 2 * N && y >= 0) reinterpret_cast<uint4*>(lane & 1 ? p.vsc : p.ksc)[y] = c.s;
 }
 
 // ---------------------------------------------------------------- copy
@@ -92,8 +106,8 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   const int64_t total = s_end[kSliceRuns - 1];
-  for (int64_t c0 = (int64_t)blockIdx.x * kChunkCells + warp * kCellsPerWarp; c0 < total; c0 += (int64_t)gridDim.x * kChunkCells) {
-    const int64_t c = c0 + (lane & (kCellsPerWarp - 1));
+  for (int64_t c0 = (int64_t)blockIdx.x * kCopyChunk + warp * kCopyCells; c0 < total; c0 += (int64_t)gridDim.x * kCopyChunk) {
+    const int64_t c = c0 + (lane & (kCopyCells - 1));
     int64_t from = -1, to = -1;
     if (c < total) {  // the first run that ends behind c
       int lo = 0, hi = kSliceRuns - 1;
@@ -106,7 +120,7 @@ __global__ void __launch_bounds__(kThreads)
       from = s_at[lo].x + in;
       to = s_at[lo].y + in;
     }
-    Cells w;
+    Cells<kCopyCells> w;
     load_cells(pool, from, lane, w);
     store_cells(pool, to, lane, w);
   }
@@ -127,7 +141,7 @@ struct CompactWs {
   uint32_t* loaded;     // by chunk
   size_t bytes;
 };
-constexpr int kRankEntries = kThreads / 8;  // entries of a rank CTA, eight threads each
+constexpr int kRankEntries = kWarps;  // entries of a rank CTA, a warp each
 
 CompactWs compact_ws(void* ws, int64_t n_pool, int n) {
   CompactWs w{};
@@ -141,7 +155,7 @@ CompactWs compact_ws(void* ws, int64_t n_pool, int n) {
   w.place = reinterpret_cast<int*>(take((size_t)n * sizeof(int)));
   w.bad = reinterpret_cast<int*>(take((size_t)((n + kRankEntries - 1) / kRankEntries) * sizeof(int)));
   w.head = reinterpret_cast<int*>(take(4 * sizeof(int)));
-  w.loaded = reinterpret_cast<uint32_t*>(take((size_t)((n_pool + kChunkCells - 1) / kChunkCells) * sizeof(uint32_t)));
+  w.loaded = reinterpret_cast<uint32_t*>(take((size_t)((n_pool + kMoveChunk - 1) / kMoveChunk) * sizeof(uint32_t)));
   w.bytes = o;
   return w;
 }
@@ -157,9 +171,9 @@ __global__ void __launch_bounds__(kThreads) compact_rank_kernel(const Tables t, 
   __shared__ int2 s_run[kThreads];
   pdl_begin();
   const int tid = threadIdx.x;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < (n_pool + kChunkCells - 1) / kChunkCells; i += (int64_t)gridDim.x * kThreads)
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < (n_pool + kMoveChunk - 1) / kMoveChunk; i += (int64_t)gridDim.x * kThreads)
     w.loaded[i] = 0u;
-  const int i = blockIdx.x * kRankEntries + tid / 8, part = tid & 7;
+  const int i = blockIdx.x * kRankEntries + tid / 32, part = tid & 31;
   const int4 e = i < t.n ? t.at(i) : make_int4(0, 0, 0, 0);
   bool bad = e.x < 0 || e.y < 0 || (int64_t)e.x + e.y > n_pool;
   int64_t before = 0, all = 0;
@@ -174,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) compact_rank_kernel(const Tables t, 
     s_run[tid] = r;
     __syncthreads();
     const int n = min(kThreads, t.n - j0);
-    for (int k = part; k < n; k += 8) {
+    for (int k = part; k < n; k += 32) {
       const int2 f = s_run[k];
       if (f.y <= 0) continue;  // an entry without cells; one with fewer is found by its own threads
       all += f.y;
@@ -188,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) compact_rank_kernel(const Tables t, 
     }
   }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
+  for (int o = 1; o < 32; o <<= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
     all += __shfl_xor_sync(0xffffffffu, all, o);
     rank += __shfl_xor_sync(0xffffffffu, rank, o);
@@ -226,11 +240,13 @@ __device__ __forceinline__ bool wait_loaded(const uint32_t* flag, int* status) {
 }
 
 constexpr int kNearRuns = 1024;  // a table up to so long is looked up in shared memory
-__global__ void __launch_bounds__(kThreads)
+constexpr int kMoveCtas = 2;     // on an SM
+__global__ void __launch_bounds__(kThreads, kMoveCtas)
     compact_move_kernel(const Pool pool, const Tables t, const CompactWs w, int rank_ctas, int4* prefixes_out, int4* seqs_out,
                         int* used_out, int* status) {
   __shared__ int4 s_runs[kNearRuns];
   __shared__ int s_next, s_wait[2];
+  __shared__ volatile uint32_t s_sink[kThreads];
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_next = atomicAdd(&w.head[0], 1);
@@ -255,16 +271,16 @@ __global__ void __launch_bounds__(kThreads)
     runs = s_runs;
     __syncthreads();
   }
-  // Where this warp's eight cells of a chunk come from and go to (lane u: cell u; -1: none).
+  // Where this warp's cells of a chunk come from and go to (lane u: cell u; -1: none).
   auto look_up = [&](int chunk, int64_t& from, int64_t& to) {
     from = to = -1;
-    const int64_t c0 = (int64_t)chunk * kChunkCells + warp * kCellsPerWarp;
+    const int64_t c0 = (int64_t)chunk * kMoveChunk + warp * kMoveCells;
     if (c0 >= used) return;
     const int k = warp_find_seq(n, c0, [&](int i) { return (long long)runs[i].y; });
     const int4 e = runs[min(k + lane, n - 1)];  // the run of cell c0, and with a lane each those behind it (no run is empty)
     const bool have = k + lane < n;
 #pragma unroll
-    for (int u = 0; u < kCellsPerWarp; ++u) {
+    for (int u = 0; u < kMoveCells; ++u) {
       const int c = (int)c0 + u;
       const int r = max(__popc(__ballot_sync(0xffffffffu, have && e.y <= c)) - 1, 0);
       const int src = __shfl_sync(0xffffffffu, e.x, r), dst = __shfl_sync(0xffffffffu, e.y, r);
@@ -277,11 +293,11 @@ __global__ void __launch_bounds__(kThreads)
   int chunk = s_next;
   int64_t from, to;
   look_up(chunk, from, to);
-  while ((int64_t)chunk * kChunkCells < used) {
+  while ((int64_t)chunk * kMoveChunk < used) {
     __syncthreads();  // every thread has read s_next
     if (tid == 0) s_next = atomicAdd(&w.head[0], 1);
     const bool moves = __syncthreads_or(from != to);  // else every cell is where it belongs, and none is read
-    Cells x;
+    Cells<kMoveCells> x;
     if (moves) load_cells(pool, from, lane, x);
     // while they arrive: the next chunk's runs, and whom this one waits for
     const int next = s_next;
@@ -289,7 +305,7 @@ __global__ void __launch_bounds__(kThreads)
     look_up(next, next_from, next_to);
     if (warp == 0 && moves) {
       // the earlier chunks that read from places [a, b): of the first and the last cell there that is in a run
-      const int a = chunk * kChunkCells, b = min(a + kChunkCells, used);
+      const int a = chunk * kMoveChunk, b = min(a + kMoveChunk, used);
       auto src = [&](int i) { return (long long)runs[i].x; };
       const int ka = warp_find_seq(n, a, src), kb = warp_find_seq(n, b - 1, src);
       if (lane == 0) {
@@ -297,16 +313,15 @@ __global__ void __launch_bounds__(kThreads)
         // cell a is in run ka, or the first cell behind it is a run's first: the next one's, or (before all of them) run 0's
         const int xa = a >= ea.x && a - ea.x < ea.z ? ea.y + (a - ea.x) : ea.x > a ? ea.y : ea.y + ea.z;
         const int xb = eb.x > b - 1 ? -1 : eb.y + min(b - 1 - eb.x, eb.z - 1);
-        s_wait[0] = xa / kChunkCells;
-        s_wait[1] = xb < 0 ? -1 : xb / kChunkCells;
+        s_wait[0] = xa / kMoveChunk;
+        s_wait[1] = xb < 0 ? -1 : xb / kMoveChunk;
       }
     }
-    if (moves) __threadfence();  // this thread's cells have been read before the flag below is seen
+    // This thread's cells are in its registers, every thread's behind the barrier, and then the flag says so.  It says nothing
+    // of earlier stores, so nothing waits for those (a fence here did: 500 runs 97 us against 90).
+    if (moves) s_sink[tid] = folded(from, lane, x);
     __syncthreads();
-    if (tid == 0) {
-      __threadfence();
-      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(w.loaded + chunk), "r"(1u) : "memory");
-    }
+    if (tid == 0) asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(w.loaded + chunk), "r"(1u) : "memory");
     if (moves) {
       bool ok = true;
       const int j = s_wait[0] + tid;
@@ -325,7 +340,7 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_cache_copy(int8_t* kq, __half* ksc, int8_t* vq, __half* vsc, int64_t n_pool, const int4* runs, int n_run,
                               int max_cells, int* status, cudaStream_t stream) {
   const int slices = (n_run + kSliceRuns - 1) / kSliceRuns;
-  const int64_t most = ((int64_t)std::min(n_run, kSliceRuns) * max_cells + kChunkCells - 1) / kChunkCells;
+  const int64_t most = ((int64_t)std::min(n_run, kSliceRuns) * max_cells + kCopyChunk - 1) / kCopyChunk;
   const int64_t want = std::max<int64_t>(1, 152 * 4 / slices);
   return launch_pdl(cache_copy_kernel, dim3((unsigned)std::min(most, want), slices), dim3(kThreads), 0, stream,
                     Pool{kq, ksc, vq, vsc}, n_pool, runs, n_run, max_cells, status);
@@ -341,8 +356,8 @@ cudaError_t launch_cache_compact(int8_t* kq, __half* ksc, int8_t* vq, __half* vs
   const int ranks = (t.n + kRankEntries - 1) / kRankEntries;
   cudaError_t e = launch_pdl(compact_rank_kernel, dim3(ranks), dim3(kThreads), 0, stream, t, n_pool, w);
   if (e != cudaSuccess) return e;
-  const int64_t chunks = (n_pool + kChunkCells - 1) / kChunkCells;
-  return launch_pdl(compact_move_kernel, dim3((unsigned)std::min<int64_t>(chunks, 152 * 2)), dim3(kThreads), 0, stream,
+  const int64_t chunks = (n_pool + kMoveChunk - 1) / kMoveChunk;
+  return launch_pdl(compact_move_kernel, dim3((unsigned)std::min<int64_t>(chunks, 152 * kMoveCtas)), dim3(kThreads), 0, stream,
                     Pool{kq, ksc, vq, vsc}, t, w, ranks, prefixes_out, seqs_out, used, status);
 }
 
