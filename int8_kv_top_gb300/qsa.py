@@ -339,6 +339,15 @@ def _array(t, name: str, dtypes: tuple, n: int, optional: bool = False):
                                         f"device (got {_what(t)})")
 
 
+def _scratch(ws):
+    """The pointer and bytes of a workspace on the current device."""
+    if ws is None:
+        return None, 0
+    if isinstance(ws, torch.Tensor) and ws.is_contiguous() and (ws.is_cuda and ws.get_device() == _device() or not ws.numel()):
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+    raise QSAError(QSA_ERR_INVALID_ARG, f"ws must be a contiguous tensor on the current device (got {_what(ws)})")
+
+
 def _what(t) -> str:
     if not isinstance(t, torch.Tensor):
         return repr(t)
@@ -368,6 +377,8 @@ def qsa_tree_verify(p, d, vocab: int, token, parent, u, u_end, seqs, n_seq: int,
     None), token and parent int32 [n_tok], u float32 [n_tok], u_end float32 [n_seq], path int32 [n_seq, cap]."""
     pp, ps = _probabilities(p, "p", vocab, n_tok)
     dp, ds = _probabilities(d, "d", vocab, n_tok)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise QSAError(QSA_ERR_INVALID_ARG, f"path must be an int32 tensor [n_seq, cap] (got {_what(path)})")
     cap = path.shape[1]
     _check(load().qsa_tree_verify(pp, ps, dp, ds, vocab, _array(token, "token", _I32, n_tok), _array(parent, "parent", _I32, n_tok),
                                   _array(u, "u", _F32, n_tok), _array(u_end, "u_end", _F32, n_seq),
@@ -383,7 +394,7 @@ def qsa_prefix_attention(q, kq, vq, ksc, vsc, n_pool: int, prefixes, n_prefix: i
                          max_prefix: int, max_n_kv: int, ids, out, ws=None, params=None, stream=None, gate=None):
     """Attention behind shared prefixes; prefixes int32 [n_prefix, 4] (or None), seqs int32 [n_seq, 4], tree int32 or uint32
     [n_tok, words] of mask bits, or None: a token sees the sequence's tokens up to itself."""
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    ws, ws_bytes = _scratch(ws)
     words = 0 if tree is None else tree.shape[1]
     topk = 2048 if params is None else params.topk if isinstance(params, qsa_params) else int(params[0])
     rows = n_tok * (N_HEADS * HEAD_DIM)
@@ -392,7 +403,7 @@ def qsa_prefix_attention(q, kq, vq, ksc, vsc, n_pool: int, prefixes, n_prefix: i
                                        _array(prefixes, "prefixes", _I32, 4 * n_prefix), n_prefix, _array(seqs, "seqs", _I32, 4 * n_seq),
                                        n_seq, n_tok, _array(tree, "tree", _I32, n_tok * words, True), words, max_prefix, max_n_kv,
                                        _array(ids, "ids", _I32, n_tok * N_GROUPS * topk, True), _array(gate, "gate", _F16, rows, True),
-                                       _array(out, "out", _F16, rows), _ptr(ws), ws_bytes, _params(params), _stream(stream)))
+                                       _array(out, "out", _F16, rows), ws, ws_bytes, _params(params), _stream(stream)))
 
 
 def qsa_cache_copy(kq, ksc, vq, vsc, n_pool: int, runs, n_run: int, max_cells: int, stream=None):
@@ -409,11 +420,11 @@ def qsa_cache_compact(kq, ksc, vq, vsc, n_pool: int, prefixes, n_prefix: int, se
                       stream=None):
     """The runs of a prefix and a sequence table (int32 [n, 4]) moved together to the front of the pool, in place; used
     is an int32 tensor of one element, or None."""
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    ws, ws_bytes = _scratch(ws)
     _check(load().qsa_cache_compact(*_pool(kq, ksc, vq, vsc, n_pool), n_pool, _array(prefixes, "prefixes", _I32, 4 * n_prefix),
                                     n_prefix, _array(seqs, "seqs", _I32, 4 * n_seq), n_seq,
                                     _array(prefixes_out, "prefixes_out", _I32, 4 * n_prefix),
-                                    _array(seqs_out, "seqs_out", _I32, 4 * n_seq), _array(used, "used", _I32, 1, True), _ptr(ws),
+                                    _array(seqs_out, "seqs_out", _I32, 4 * n_seq), _array(used, "used", _I32, 1, True), ws,
                                     ws_bytes, _stream(stream)))
 
 

@@ -311,6 +311,72 @@ def test_a_large_workspace_serves_smaller_calls():
         assert (np.abs(out.double().cpu().numpy() - want) <= bound).all()
 
 
+@pytest.mark.parametrize("params", [None, SMALL])
+def test_many_sequences_and_prefixes(params):
+    # more than the searches hold in shared memory, and prefixes than are planned one by one
+    rng = np.random.default_rng(71)
+    groups = [(int(rng.integers(0, 150)), [(int(x), 1) for x in rng.integers(0, 40, 4)]) for _ in range(300)]
+    rows = set(int(x) for x in rng.integers(0, 1200, 60)) | {0, 1199}
+    check(groups, seed=71, params=params, rows=rows, gate=True)
+
+
+def test_the_most_tokens():
+    n, shared = 65535, 70
+    rng = np.random.default_rng(72)
+    pool = shared_batch([(shared, [(n, 1)])], 72, gap=0, slack=0)[0]
+    first = int(pool["seqs"][0][0])
+    b = dict(pool, q=rng.standard_normal((n, 24, 256), np.float32).astype(np.float16), tree=None,
+             seqs=np.stack([first + np.arange(n), np.ones(n), np.zeros(n), np.arange(n)], 1).astype(np.int32))
+    ids, out = run_shared(b, with_ids=False, bounds=(shared, shared + 1))
+    qsa.qsa_check_device_status()
+    at = int(pool["prefixes"][0][0])
+    for t in (0, 1, 21, 32767, n - 2, n - 1):
+        cells = np.concatenate([at + np.arange(shared), [first + t]])
+        one = {k: pool[k][cells] for k in ("kq", "vq", "ksc", "vsc")} | {"q": b["q"][t:t + 1], "tree": np.array([[1]], np.uint32)}
+        w, _, bd = reference(one, np.array([(0, shared + 1, shared, 0)], np.int32))
+        assert (np.abs(out[t].double().cpu().numpy() - w[0]) <= bd[0]).all(), t
+
+
+def test_a_prefix_longer_than_the_other_calls_take():
+    check([(140000, [(40, 1), (3, 2)])], seed=73, params=(2048, 1 << 20, 1 / 16), with_ids=False)
+
+
+@pytest.mark.parametrize("gate", [False, True])
+def test_own_cells_alone(gate):
+    check([(0, [(20, 1), (300, 1), (0, 1)])], seed=74, gate=gate)          # one CTA has all of a token's cells
+    check([(0, [(20, 1), (1900, 1), (0, 1)])], seed=75, gate=gate)         # several share them
+    check([(0, [(20, 8), (300, 5)])], seed=76, gate=gate)                  # on the tensor-core kernel
+    check([(0, [(20, 1), (300, 1), (90, 2)])], seed=77, params=SMALL, gate=gate)
+
+
+def test_overlapping_rows_are_flagged_and_harm_nobody_elses_memory():
+    # first token rows that run back and forth: flagged; nothing is said of the rows, but what lies around the outputs stays
+    b, _, _ = shared_batch([(200, [(20, 1)] * 40), (90, [(10, 1)] * 40), (300, [(5, 1)] * 40)], 78)
+    rng = np.random.default_rng(78)
+    for how in range(4):
+        seqs = b["seqs"].copy()
+        seqs[1:, 3] = rng.permutation(seqs[1:, 3]) if how < 2 else rng.integers(-5, 130, len(seqs) - 1)
+        prefixes = b["prefixes"].copy()
+        if how == 3:
+            prefixes[1:, 2] = [80, 40]
+        d = on_gpu({k: v for k, v in b.items() if k in ("q", "kq", "vq", "ksc", "vsc")})
+        s, p = torch.from_numpy(seqs).cuda(), torch.from_numpy(prefixes).cuda()
+        tree = torch.from_numpy(b["tree"].view(np.int32)).cuda()
+        for params in (None, SMALL):
+            n, topk = 120, params[0] if params else 2048
+            out = torch.full((n + 2, 24, 256), 7.0, dtype=torch.float16, device="cuda")
+            ids = torch.full((n + 2, 2, topk), -7, dtype=torch.int32, device="cuda")
+            need = qsa.qsa_prefix_attention_workspace_bytes(3, n, n, 300, 330, params)
+            ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+            qsa.qsa_prefix_attention(d["q"], d["kq"], d["vq"], d["ksc"], d["vsc"], len(b["kq"]), p, 3, s, n, n, tree, 300, 330, ids[1:],
+                                     out[1:], ws[:need], params=params)
+            with pytest.raises(qsa.QSAError) as e:
+                qsa.qsa_check_device_status()
+            assert e.value.code == qsa.QSA_ERR_DEVICE
+            assert (out[0] == 7).all() and (out[-1] == 7).all() and (ids[0] == -7).all() and (ids[-1] == -7).all()
+            assert (ws[need:] == 0x5A).all()
+
+
 def test_tensors_of_the_wrong_kind_are_refused():
     b, _, _, d, call = device_batch([(20, [(3, 1)])], 51, None)
     for name, bad in (("q", d["q"].float()), ("q", d["q"][:, :, ::2]), ("kq", d["kq"][:-1]), ("vsc", d["vsc"].cpu()), ("seqs", d["seqs"].long()),

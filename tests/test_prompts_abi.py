@@ -174,9 +174,8 @@ def refused(fn, *args, **kw):
 
 @pytest.mark.parametrize("name,bad", [("p", torch.zeros(N, V)), ("d", torch.zeros(N, V)), ("token", ints(N)), ("seqs", ints(2, 4))])
 def test_tensors_that_are_not_on_the_gpu_are_refused(fake, name, bad):
-    args = dict(p=FAKE, d=None, vocab=V, token=FAKE, parent=FAKE, u=FAKE, u_end=FAKE, seqs=FAKE, n_seq=2, n_tok=N, path=ints(0, 4),
+    args = dict(p=FAKE, d=None, vocab=V, token=FAKE, parent=FAKE, u=FAKE, u_end=FAKE, seqs=FAKE, n_seq=2, n_tok=N, path=ints(2, 4),
                 n_path=FAKE, next=FAKE)
-    args["path"] = type("Path", (), {"shape": (2, 4)})()
     assert name in refused(qsa.qsa_tree_verify, **{**args, name: bad})
     assert fake == {}
 
@@ -193,3 +192,10 @@ def test_absent_arrays_and_raw_pointers_pass(fake):
     qsa.qsa_cache_compact(FAKE, FAKE, FAKE, FAKE, 9, None, 0, FAKE, 2, None, FAKE, None, None)
     assert fake["qsa_cache_compact"] == (FAKE, FAKE, FAKE, FAKE, 9, None, 0, FAKE, 2, None, FAKE, None, None, 0, 0)
     assert "prefixes" in refused(qsa.qsa_cache_compact, FAKE, FAKE, FAKE, FAKE, 9, None, 1, FAKE, 2, None, FAKE, None, None)
+
+
+def test_workspaces_on_the_cpu_are_refused(fake):
+    assert "ws" in refused(qsa.qsa_cache_compact, FAKE, FAKE, FAKE, FAKE, 9, None, 0, FAKE, 2, None, FAKE, None, torch.zeros(99))
+    assert "ws" in refused(qsa.qsa_prefix_attention, FAKE, FAKE, FAKE, FAKE, FAKE, 9, None, 0, FAKE, 2, 2, None, 0, 5, None, FAKE, torch.zeros(99))
+    assert "path" in refused(qsa.qsa_tree_verify, FAKE, None, V, FAKE, FAKE, FAKE, FAKE, FAKE, 2, N, ints(8), FAKE, FAKE)
+    assert fake == {}
