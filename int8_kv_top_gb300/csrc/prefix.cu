@@ -271,13 +271,16 @@ constexpr int kMaxOwn = 32, kMostOwn = 2048;  // CTAs that share a (token, group
 static_assert(2 * (kOwnSmem + 3 * 1024) <= 228 * 1024, "two CTAs on an SM");
 constexpr int kOPitch = kD + 4;                // floats of a warp's unmerged row, over the ring once the cells are attended to
 static_assert(kOwnWarps * kHPG * kOPitch * 4 <= kOwnWarps * kStages * kStageBytes, "the rows fit over the ring");
+static_assert((kNearSeqs + kNearPrefixes) * 4 <= kOwnWarps * kStages * kStageBytes, "and before them, the tables");
 static_assert(kOffRing % 16 == 0 && kStageBytes % 16 == 0, "16-byte copies");
 constexpr float kRescaleBy = 8.f, kPUp = 7.f;  // log2 units; as in tree.cu
 
 struct OwnArgs {
   TreeBatch b;
-  const TokMore* more;
+  TokMore* more;
   bool behind_dense;     // launched behind the prefixes' kernel
+  bool records;          // made here, and the tables checked (else by prefix_prep_kernel)
+  int* status;
   const __half* q;
   const int8_t* kq;
   const int8_t* vq;
@@ -320,9 +323,27 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   if (a.out == nullptr) pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % S, g = blockIdx.x / S % kGroups, t = blockIdx.x / S / kGroups;
-  const int4 ti = __ldcg(&a.b.tok[t]), e = __ldcg(&a.more[t].seq);
-  if (ti.x < 0) {
+  int4 ti, e;
+  if (a.records) {
+    const Finder find(a.b, reinterpret_cast<int*>(smem + kOffRing), tid, kOwnThreads);
+    TokMore more;
+    ti = find.record(t, &more);
+    e = more.seq;
+    if (g == 0 && rank == 0 && tid == 0) {
+      a.b.tok[t] = ti;
+      a.more[t] = more;
+    }
+    __syncthreads();  // the ring is free
+  } else {
+    ti = __ldcg(&a.b.tok[t]);
+    e = __ldcg(&a.more[t].seq);
+  }
+  auto last = [&] {  // off the path
+    if (a.records) check_tables(a.b, blockIdx.x * kOwnThreads + tid, gridDim.x * kOwnThreads, a.status);
     if (a.behind_dense && blockIdx.x == 0) pdl_begin();
+  };
+  if (ti.x < 0) {
+    last();
     return;
   }
   const int T = e.z, i_tok = t - e.w, pos0 = e.y;
@@ -561,7 +582,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
       *reinterpret_cast<uint4*>(a.out + at) = pack_out(v);
     }
   }
-  if (a.behind_dense && blockIdx.x == 0) pdl_begin();
+  last();
 }
 
 // ---------------------------------------------------------------- 3. the join
@@ -574,10 +595,11 @@ struct PartSet {  // parts of a token's rows, as the tensor-core kernel or prefi
   bool rows;      // of prefix_own_kernel: [n_tok][2][runs][kHPG]
 };
 struct JoinArgs {
-  const int4* tok;
+  TreeBatch b;
   const TokMore* more;
   PartSet prefix, own;  // runs 0: none
-  const int4* plan;     // of the prefixes' parts
+  const int4* plan;     // of the prefixes' parts; null: one prefix, and the launch before makes the records
+  int clusters;
   const __half* gate;
   __half* out;
 };
@@ -589,9 +611,20 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   __shared__ float s_inv[kHPG];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slice = blockIdx.x % kSlices, g = blockIdx.x / kSlices % kGroups, t = blockIdx.x / kSlices / kGroups;
-  // The launch before triggered this one when the one that makes the records was complete.
-  const int4 ti = __ldcg(&a.tok[t]), e = __ldcg(&a.more[t].seq);
-  const int4 pl = a.prefix.p.runs > 0 && ti.x >= 0 && ti.z > 0 ? __ldcg(&a.plan[ti.w]) : make_int4(0, 0, 0, 0);
+  // With a plan, the launch before triggered this one when the one that makes the records was complete.
+  const bool early = a.plan != nullptr;
+  if (!early) pdl_begin();
+  const int4 ti = __ldcg(&a.b.tok[t]), e = __ldcg(&a.more[t].seq);
+  int4 pl = make_int4(0, 0, 0, 0);
+  if (a.prefix.p.runs > 0 && ti.x >= 0 && ti.z > 0) {
+    if (early) {
+      pl = __ldcg(&a.plan[ti.w]);
+    } else {
+      int4 pe;
+      const int T = prefix_tokens(a.b, 0, &pe);
+      pl = only_prefix_plan(pe.w, T, pe.y, a.clusters);
+    }
+  }
   const int px_runs = pl.y;
   const int own_runs = a.own.rows ? a.own.p.runs : a.own.p.runs ? shared_runs((e.y + e.z + kTileCells - 1) / kTileCells, a.own.p.runs, a.own.p.run_tiles) : 0;
   const int n = px_runs + own_runs;
@@ -617,7 +650,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   uint4 gw = make_uint4(0u, 0u, 0u, 0u);
   if (mine && a.gate) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at));
   __syncthreads();
-  pdl_begin();
+  if (early) pdl_begin();
   if (ti.x < 0) return;
   // float4 between the dims of a row, float4 between parts, and (m, l) between parts
   constexpr int kDimStep = kTreeBlock / 2, kMlStep = kTreeBlock;
@@ -781,13 +814,19 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   int clusters = 0;
   cudaError_t e = dense ? prefix_clusters(b, own_dense ? 0 : own_cells, &clusters) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  const int prep = (select ? kGroups * b.n_tok + b.n_prefix * w.chunks_prefix + b.n_seq * own_chunks : 0) + (b.n_tok + 255) / 256 + dense;
-  e = launch_pdl(prefix_prep_kernel, dim3(prep), dim3(256), 0, stream, b, w, more, select, own_chunks, plan, clusters, q, ksc, status);
-  if (e != cudaSuccess) return e;
+  // One prefix, no selection and few tokens a sequence: the launches find their way without prefix_prep_kernel (3 us).
+  const bool records = !select && !own_dense && b.n_prefix <= 1;
+  if (records) {
+    plan = nullptr;
+  } else {
+    const int prep = (select ? kGroups * b.n_tok + b.n_prefix * w.chunks_prefix + b.n_seq * own_chunks : 0) + (b.n_tok + 255) / 256 + dense;
+    e = launch_pdl(prefix_prep_kernel, dim3(prep), dim3(256), 0, stream, b, w, more, select, own_chunks, plan, clusters, q, ksc, status);
+    if (e != cudaSuccess) return e;
+  }
   if (select && (e = launch_shared_select(b, w, own_cells, q, kq, ksc, ids, p, status, stream)) != cudaSuccess) return e;
   const uint32_t* bits = select ? w.bits : nullptr;
   const int pitch = w.pitch / 32;
-  JoinArgs j{b.tok, more, {}, {}, plan, gate, out};
+  JoinArgs j{b, more, {}, {}, plan, clusters, gate, out};
   if (dense && (e = launch_prefix_parts(b, clusters, plan, q, kq, vq, ksc, vsc, bits, pitch, base + l.prefix, p.sm_scale, &j.prefix.p,
                                         status, stream)) != cudaSuccess)
     return e;
@@ -804,7 +843,7 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     const bool last = !dense && S == 1;
     float* o = reinterpret_cast<float*>(base + l.own);
     float2* ml = reinterpret_cast<float2*>(o + (size_t)b.n_tok * kHeads * S * kD);
-    const OwnArgs a{b, more, dense, q, kq, vq, ksc, vsc, bits, pitch, p.sm_scale * kLog2e, gate, last ? out : nullptr, o, ml};
+    const OwnArgs a{b, more, dense, records, status, q, kq, vq, ksc, vsc, bits, pitch, p.sm_scale * kLog2e, gate, last ? out : nullptr, o, ml};
     e = launch_pdl(prefix_own_kernel, dim3((unsigned)(b.n_tok * kGroups * S)), dim3(kOwnThreads), kOwnSmem, stream, a, S);
     if (e != cudaSuccess || last) return e;
     j.own = PartSet{{reinterpret_cast<const float4*>(o), ml, S, 0}, true};

@@ -106,6 +106,7 @@ struct DenseTreeArgs {
   int runs;              // clusters that share a block: 1, or (with one pair a cluster) more and tree_join_kernel
   int run_tiles;         // shared calls: tiles of a run at most, so that a shorter prefix takes fewer of them
   bool behind_dense;     // own cells launched behind the prefixes'
+  int clusters;          // of the prefixes' launch; without a plan there is one prefix, and there are no records
   int* status;
 };
 
@@ -129,7 +130,8 @@ struct BlockAt {
   bool ours, sel;
 };
 template <CellsOf kOf>
-__device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4* plan, bool with_selected, int blk, int lane) {
+__device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4* plan, bool with_selected, int blk, int lane,
+                                                 int clusters = 0) {
   BlockAt x;
   bool here;
   if (kOf == kTreeCells && plan != nullptr) {
@@ -142,9 +144,20 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
     int sq;
     if constexpr (kOf == kPrefixCells) {
       // `blk` is the cluster's index and `plan` the prefixes' clusters
-      sq = warp_find_seq(b.n_prefix, blk, [&](int p) { return (long long)__ldg(&plan[p]).x; });
-      const int4 at = __ldg(&plan[sq]), pe = __ldg(&b.prefixes[sq]);
-      const int all = __ldg(&plan[b.n_prefix].x), i = blk - at.x, runs = max(at.y, 1);
+      int4 at, pe;
+      int all;
+      if (plan != nullptr) {
+        sq = warp_find_seq(b.n_prefix, blk, [&](int p) { return (long long)__ldg(&plan[p]).x; });
+        at = __ldg(&plan[sq]);
+        pe = __ldg(&b.prefixes[sq]);
+        all = __ldg(&plan[b.n_prefix].x);
+      } else {
+        sq = 0;
+        const int T = prefix_tokens(b, 0, &pe);
+        at = only_prefix_plan(pe.w, T, pe.y, clusters);
+        all = (at.w * kHPG + kTreeBlock - 1) / kTreeBlock * kGroups * at.y;
+      }
+      const int i = blk - at.x, runs = max(at.y, 1);
       x.T = blk < all && at.y > 0 ? at.w : 0;
       x.e = make_int4(pe.x, 0, pe.y, at.z);
       x.g = i / runs % kGroups;
@@ -169,6 +182,11 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
     if (kOf != kPrefixCells && live)
       x.m[w] = kOf == kTreeCells ? tree_mask_word(b, x.e.w + tok, w, x.T) : shared_mask_word(b, x.e.w + tok, tok, w, x.T);
     n_kv += __popc(x.m[w]);
+  }
+  if (kOf == kPrefixCells && plan == nullptr) {  // no records: rows that are nobody's are computed and not read
+    x.ours = live;
+    x.sel = false;
+    return x;
   }
   if constexpr (kOf != kTreeCells) {
     const int4 t = live ? __ldcg(&b.tok[x.e.w + tok]) : make_int4(-1, 0, 0, 0);
@@ -230,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     }
   }
   if (warp == 0) {
-    const BlockAt x = tree_block_at<kOf>(a.b, a.plan, a.bits != nullptr, blk, lane);
+    const BlockAt x = tree_block_at<kOf>(a.b, a.plan, a.bits != nullptr, blk, lane, a.clusters);
     const unsigned all_ours = __ballot_sync(0xffffffffu, x.ours), all_sel = __ballot_sync(0xffffffffu, x.sel);
 #pragma unroll
     for (int w = 0; w < kTreeWords; ++w) {
@@ -837,7 +855,7 @@ cudaError_t launch_tree_dense(const TreeBatch& b, const __half* q, const int8_t*
   const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, gate, out, plan,
                         static_cast<float*>(ws),
                         reinterpret_cast<float2*>(static_cast<float*>(ws) + part_rows(b.n_seq, b.n_tok, b.max_n_kv) * kD),
-                        d.runs, 0, false, status};
+                        d.runs, 0, false, 0, status};
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = tree_config(d.pairs, d.blocks * kGroups * d.runs, stream, attr);
   if ((e = cudaLaunchKernelEx(&cfg, tree_dense_kernel<kTreeCells>, a, d.pairs)) != cudaSuccess || d.runs == 1) return e;
@@ -869,7 +887,7 @@ cudaError_t launch_parts(const TreeBatch& b, int clusters, int runs, int run_til
   float2* ml = reinterpret_cast<float2*>(part + rows * kD);
   *parts = TreeParts{reinterpret_cast<const float4*>(part), ml, runs, run_tiles};
   const DenseTreeArgs a{b, q, kq, vq, ksc, vsc, bits, bits_pitch, sm_scale * kLog2e, nullptr, nullptr, plan, part, ml, runs, run_tiles,
-                        behind_dense, status};
+                        behind_dense, clusters, status};
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = tree_config(1, clusters, stream, attr);
   return cudaLaunchKernelEx(&cfg, tree_dense_kernel<kOf>, a, 1);

@@ -210,6 +210,15 @@ __device__ __forceinline__ int cta_rows(int T, int blk_row0, int half, int* x) {
   return half ? n - first : first;
 }
 
+// The clusters of a shared call's only prefix, of T tokens and `cells` cells, as plan_prefixes (prefix.cu) shares them out:
+// {first, runs a block and group, first token row, tokens}.
+__device__ __forceinline__ int4 only_prefix_plan(int row0, int T, int cells, int clusters) {
+  const int tiles = (cells + kTileCells - 1) / kTileCells, blocks = (T * kHPG + kTreeBlock - 1) / kTreeBlock * kGroups;
+  if (T <= 0 || tiles == 0) return make_int4(0, 0, row0, max(T, 0));
+  const int most = max(1, min(min(clusters / blocks, kMaxRuns), tiles)), L = (tiles + most - 1) / most;
+  return make_int4(0, (tiles + L - 1) / L, row0, T);
+}
+
 // Runs of a block and group of a shared call over n_tiles tiles: as many of run_tiles as it takes, `runs` at most.
 __device__ __forceinline__ int shared_runs(int n_tiles, int runs, int run_tiles) {
   return max(1, min(runs, (n_tiles + run_tiles - 1) / run_tiles));
