@@ -538,8 +538,10 @@ QSA_API size_t qsa_cache_compact_workspace_bytes(int64_t n_pool, int n_prefix, i
  * qsa_cache_compact - the runs of a server's tables moved together: the runs {first pool cell, n_cells} of all
  * prefixes and sequences, in the order in which they lie in the pool, are moved side by side to cells 0, 1, ...; in
  * place, every cell read before it is overwritten.  A run that a sequence has left free is one that no entry names.
- *   prefixes, seqs  DEVICE [n_prefix][4] and [n_seq][4] int32 {first pool cell, n_cells, -, -}, in any order; entries
- *          with n_cells 0 are left alone.  Either may be NULL where its count is 0
+ *   prefixes, seqs  DEVICE [n_prefix][4] and [n_seq][4] int32 {first pool cell, n_cells, -, -}, in any order.  An
+ *          entry with n_cells 0 moves with them: its new first cell is behind the cells of all entries with a lower first
+ *          cell, and of those with the same one that stand before it (prefixes, then seqs).  Either may be NULL where its
+ *          count is 0
  *   prefixes_out, seqs_out  DEVICE, the tables with their new first cells (written; may be the tables themselves)
  *   used   DEVICE int32 (written), or NULL: the number of cells in use, the first free cell
  *   ws     qsa_cache_compact_workspace_bytes(n_pool, n_prefix, n_seq) bytes, 16-byte aligned, clobbered.  Calls that

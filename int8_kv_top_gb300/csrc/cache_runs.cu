@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) compact_rank_kernel(const Tables t, 
       if (f.y <= 0) continue;  // an entry without cells; one with fewer is found by its own threads
       all += f.y;
       ++count;
-      if (f.x < e.x) {
+      if (f.x < e.x || (f.x == e.x && j0 + k < i)) {  // (of the same cell only where one of the two is empty)
         before += f.y;
         ++rank;
       }
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) compact_rank_kernel(const Tables t, 
     count += __shfl_xor_sync(0xffffffffu, count, o);
   }
   if (part == 0 && i < t.n) {
-    w.place[i] = e.y > 0 ? (int)before : e.x;
+    w.place[i] = (int)before;
     // sums of a broken table may be anything: what is stored is then not used
     if (e.y > 0) w.runs[rank] = make_int4(e.x, (int)before, e.y, 0);
     if (i == 0) {

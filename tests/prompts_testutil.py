@@ -32,17 +32,14 @@ def moved(pool, runs):
 
 
 def compacted(pool, tables):
-    """(pool, tables with their new first cells, cells in use)."""
-    at, runs, to = 0, [], {}
-    for a, n in sorted((int(r[0]), int(r[1])) for t in tables for r in t if r[1] > 0):
-        runs.append((a, at, n))
-        to[a] = at
-        at += n
+    """(pool, tables with their new first cells, cells in use): all entries in the order of their first cells, equal ones in
+    the tables' order; one without cells goes where a run in its place would."""
+    at, runs = 0, []
     out = [t.copy() for t in tables]
-    for t in out:
-        for r in t:
-            if r[1] > 0:
-                r[0] = to[int(r[0])]
+    for r in sorted((r for t in out for r in t), key=lambda r: int(r[0])):  # rows are views of `out`; the sort is stable
+        runs.append((int(r[0]), at, int(r[1])))
+        r[0] = at
+        at += int(r[1])
     return moved(pool, runs), out, at
 
 

@@ -129,6 +129,23 @@ def test_compact_random(seed):
     same_bytes(dev, want)
 
 
+def test_compact_entries_without_cells_in_both_tables():
+    # at the first cell of a run before and behind it in the tables, between runs, inside one, and behind all
+    rng = np.random.default_rng(12)
+    prefixes = table([(50, 0, 1, 2), (90, 7, 3, 4), (33, 0, 5, 6)])
+    seqs = table([(50, 20, 7, 8), (50, 0, 9, 10), (90, 0, 11, 12), (30, 10, 13, 14), (200, 0, 15, 16), (0, 0, 17, 18)])
+    pool = random_cache(200, rng)
+    for in_place in (False, True):
+        dev, a, b, used = run_compact(pool, prefixes, seqs, in_place)
+        qsa.qsa_check_device_status()
+        assert used == 37 and list(a[:, 0]) == [10, 30, 10] and list(b[:, 0]) == [10, 30, 37, 0, 37, 0]
+        want, (wa, wb), n = compacted(pool, (prefixes, seqs))
+        assert n == 37
+        np.testing.assert_array_equal(a, wa)
+        np.testing.assert_array_equal(b, wb)
+        same_bytes(dev, want)
+
+
 def test_compact_many_runs():
     rng = np.random.default_rng(9)
     prefixes, seqs, n_pool = holes([1] * 65535, [int(x) for x in rng.integers(0, 2, 65535)], rng, 35)
