@@ -325,13 +325,21 @@ def qsa_cache_commit(kq, ksc, vq, vsc, n_pool: int, seqs, n_seq: int, path, n_pa
 
 
 _device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device  # without its set-up
+_Tensor = torch.Tensor
 _F16, _I8, _I32, _F32 = (torch.float16, torch.uint16), (torch.int8,), (torch.int32, torch.uint32), (torch.float32,)
 
 
-def _array(t, name: str, dtypes: tuple, n: int, optional: bool = False):
-    """The pointer of a packed array of at least n elements on the current device."""
-    if isinstance(t, torch.Tensor):
-        if t.dtype in dtypes and t.numel() >= n and t.is_contiguous() and (t.is_cuda and t.get_device() == _device() or not t.numel()):
+def _here() -> int:
+    try:
+        return _device()
+    except RuntimeError:  # no GPU: every tensor with elements is refused
+        return -2
+
+
+def _array(t, name: str, dtypes: tuple, n: int, dev: int, optional: bool = False):
+    """The pointer of a packed array of at least n elements on device `dev`, the current one (a host tensor's is -1)."""
+    if isinstance(t, _Tensor):
+        if t.dtype in dtypes and t.numel() >= n and t.is_contiguous() and (t.get_device() == dev or not t.numel()):
             return t.data_ptr()
     elif isinstance(t, int) or t is None and (optional or n <= 0):
         return t
@@ -339,11 +347,11 @@ def _array(t, name: str, dtypes: tuple, n: int, optional: bool = False):
                                         f"device (got {_what(t)})")
 
 
-def _scratch(ws):
+def _scratch(ws, dev: int):
     """The pointer and bytes of a workspace on the current device."""
     if ws is None:
         return None, 0
-    if isinstance(ws, torch.Tensor) and ws.is_contiguous() and (ws.is_cuda and ws.get_device() == _device() or not ws.numel()):
+    if isinstance(ws, _Tensor) and ws.is_contiguous() and (ws.get_device() == dev or not ws.numel()):
         return ws.data_ptr(), ws.numel() * ws.element_size()
     raise QSAError(QSA_ERR_INVALID_ARG, f"ws must be a contiguous tensor on the current device (got {_what(ws)})")
 
@@ -354,19 +362,19 @@ def _what(t) -> str:
     return f"{t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, {t.device}"
 
 
-def _pool(kq, ksc, vq, vsc, n_pool: int):
+def _pool(kq, ksc, vq, vsc, n_pool: int, dev: int):
     codes, scales = n_pool * (N_GROUPS * HEAD_DIM), n_pool * (N_GROUPS * 4)
-    return (_array(kq, "kq", _I8, codes), _array(ksc, "ksc", _F16, scales), _array(vq, "vq", _I8, codes),
-            _array(vsc, "vsc", _F16, scales))
+    return (_array(kq, "kq", _I8, codes, dev), _array(ksc, "ksc", _F16, scales, dev), _array(vq, "vq", _I8, codes, dev),
+            _array(vsc, "vsc", _F16, scales, dev))
 
 
-def _probabilities(t, name: str, vocab: int, n_tok: int):
+def _probabilities(t, name: str, vocab: int, n_tok: int, dev: int):
     """The pointer and row stride of fp32 rows [n_tok, vocab or more]; entries of a row lie side by side."""
     if t is None or isinstance(t, int):
         return t, vocab
-    if (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.dim() == 2 and t.shape[0] >= n_tok and t.shape[1] >= vocab
+    if (isinstance(t, _Tensor) and t.dtype is torch.float32 and t.dim() == 2 and t.shape[0] >= n_tok and t.shape[1] >= vocab
             and (t.stride(1) == 1 or vocab == 1) and (n_tok <= 1 or t.stride(0) >= vocab)
-            and (t.is_cuda and t.get_device() == _device() or not t.numel())):
+            and (t.get_device() == dev or not t.numel())):
         return t.data_ptr(), max(t.stride(0), vocab)
     raise QSAError(QSA_ERR_INVALID_ARG, f"{name} must be a float32 tensor [{n_tok}, {vocab}] on the current device whose rows have "
                                         f"their elements side by side (got {_what(t)})")
@@ -375,15 +383,17 @@ def _probabilities(t, name: str, vocab: int, n_tok: int):
 def qsa_tree_verify(p, d, vocab: int, token, parent, u, u_end, seqs, n_seq: int, n_tok: int, path, n_path, next, stream=None):
     """The accepted path of each drafted tree and the token behind it.  p and d float32 [n_tok, vocab or more] (d may be
     None), token and parent int32 [n_tok], u float32 [n_tok], u_end float32 [n_seq], path int32 [n_seq, cap]."""
-    pp, ps = _probabilities(p, "p", vocab, n_tok)
-    dp, ds = _probabilities(d, "d", vocab, n_tok)
-    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+    dev = _here()
+    pp, ps = _probabilities(p, "p", vocab, n_tok, dev)
+    dp, ds = _probabilities(d, "d", vocab, n_tok, dev)
+    if not isinstance(path, _Tensor) or path.dim() != 2:
         raise QSAError(QSA_ERR_INVALID_ARG, f"path must be an int32 tensor [n_seq, cap] (got {_what(path)})")
     cap = path.shape[1]
-    _check(load().qsa_tree_verify(pp, ps, dp, ds, vocab, _array(token, "token", _I32, n_tok), _array(parent, "parent", _I32, n_tok),
-                                  _array(u, "u", _F32, n_tok), _array(u_end, "u_end", _F32, n_seq),
-                                  _array(seqs, "seqs", _I32, 4 * n_seq), n_seq, n_tok, _array(path, "path", _I32, n_seq * cap), cap,
-                                  _array(n_path, "n_path", _I32, n_seq), _array(next, "next", _I32, n_seq), _stream(stream)))
+    _check(load().qsa_tree_verify(pp, ps, dp, ds, vocab, _array(token, "token", _I32, n_tok, dev),
+                                  _array(parent, "parent", _I32, n_tok, dev), _array(u, "u", _F32, n_tok, dev),
+                                  _array(u_end, "u_end", _F32, n_seq, dev), _array(seqs, "seqs", _I32, 4 * n_seq, dev), n_seq, n_tok,
+                                  _array(path, "path", _I32, n_seq * cap, dev), cap, _array(n_path, "n_path", _I32, n_seq, dev),
+                                  _array(next, "next", _I32, n_seq, dev), _stream(stream)))
 
 
 def qsa_prefix_attention_workspace_bytes(n_prefix: int, n_seq: int, n_tok: int, max_prefix: int, max_n_kv: int, params=None) -> int:
@@ -394,22 +404,26 @@ def qsa_prefix_attention(q, kq, vq, ksc, vsc, n_pool: int, prefixes, n_prefix: i
                          max_prefix: int, max_n_kv: int, ids, out, ws=None, params=None, stream=None, gate=None):
     """Attention behind shared prefixes; prefixes int32 [n_prefix, 4] (or None), seqs int32 [n_seq, 4], tree int32 or uint32
     [n_tok, words] of mask bits, or None: a token sees the sequence's tokens up to itself."""
-    ws, ws_bytes = _scratch(ws)
+    dev = _here()
+    ws, ws_bytes = _scratch(ws, dev)
     words = 0 if tree is None else tree.shape[1]
     topk = 2048 if params is None else params.topk if isinstance(params, qsa_params) else int(params[0])
     rows = n_tok * (N_HEADS * HEAD_DIM)
-    kq, ksc, vq, vsc = _pool(kq, ksc, vq, vsc, n_pool)
-    _check(load().qsa_prefix_attention(_array(q, "q", _F16, rows), kq, vq, ksc, vsc, n_pool,
-                                       _array(prefixes, "prefixes", _I32, 4 * n_prefix), n_prefix, _array(seqs, "seqs", _I32, 4 * n_seq),
-                                       n_seq, n_tok, _array(tree, "tree", _I32, n_tok * words, True), words, max_prefix, max_n_kv,
-                                       _array(ids, "ids", _I32, n_tok * N_GROUPS * topk, True), _array(gate, "gate", _F16, rows, True),
-                                       _array(out, "out", _F16, rows), ws, ws_bytes, _params(params), _stream(stream)))
+    kq, ksc, vq, vsc = _pool(kq, ksc, vq, vsc, n_pool, dev)
+    _check(load().qsa_prefix_attention(_array(q, "q", _F16, rows, dev), kq, vq, ksc, vsc, n_pool,
+                                       _array(prefixes, "prefixes", _I32, 4 * n_prefix, dev), n_prefix,
+                                       _array(seqs, "seqs", _I32, 4 * n_seq, dev), n_seq, n_tok,
+                                       _array(tree, "tree", _I32, n_tok * words, dev, True), words, max_prefix, max_n_kv,
+                                       _array(ids, "ids", _I32, n_tok * N_GROUPS * topk, dev, True),
+                                       _array(gate, "gate", _F16, rows, dev, True), _array(out, "out", _F16, rows, dev), ws, ws_bytes,
+                                       _params(params), _stream(stream)))
 
 
 def qsa_cache_copy(kq, ksc, vq, vsc, n_pool: int, runs, n_run: int, max_cells: int, stream=None):
     """Runs of cells copied inside the pool; runs int32 [n_run, 4] {source, destination, cells, -} of at most max_cells."""
-    _check(load().qsa_cache_copy(*_pool(kq, ksc, vq, vsc, n_pool), n_pool, _array(runs, "runs", _I32, 4 * n_run), n_run, max_cells,
-                                 _stream(stream)))
+    dev = _here()
+    _check(load().qsa_cache_copy(*_pool(kq, ksc, vq, vsc, n_pool, dev), n_pool, _array(runs, "runs", _I32, 4 * n_run, dev), n_run,
+                                 max_cells, _stream(stream)))
 
 
 def qsa_cache_compact_workspace_bytes(n_pool: int, n_prefix: int, n_seq: int) -> int:
@@ -420,11 +434,13 @@ def qsa_cache_compact(kq, ksc, vq, vsc, n_pool: int, prefixes, n_prefix: int, se
                       stream=None):
     """The runs of a prefix and a sequence table (int32 [n, 4]) moved together to the front of the pool, in place; used
     is an int32 tensor of one element, or None."""
-    ws, ws_bytes = _scratch(ws)
-    _check(load().qsa_cache_compact(*_pool(kq, ksc, vq, vsc, n_pool), n_pool, _array(prefixes, "prefixes", _I32, 4 * n_prefix),
-                                    n_prefix, _array(seqs, "seqs", _I32, 4 * n_seq), n_seq,
-                                    _array(prefixes_out, "prefixes_out", _I32, 4 * n_prefix),
-                                    _array(seqs_out, "seqs_out", _I32, 4 * n_seq), _array(used, "used", _I32, 1, True), ws,
+    dev = _here()
+    ws, ws_bytes = _scratch(ws, dev)
+    _check(load().qsa_cache_compact(*_pool(kq, ksc, vq, vsc, n_pool, dev), n_pool,
+                                    _array(prefixes, "prefixes", _I32, 4 * n_prefix, dev), n_prefix,
+                                    _array(seqs, "seqs", _I32, 4 * n_seq, dev), n_seq,
+                                    _array(prefixes_out, "prefixes_out", _I32, 4 * n_prefix, dev),
+                                    _array(seqs_out, "seqs_out", _I32, 4 * n_seq, dev), _array(used, "used", _I32, 1, dev, True), ws,
                                     ws_bytes, _stream(stream)))
 
 
