@@ -517,9 +517,9 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
     l0 += __shfl_xor_sync(0xffffffffu, l0, d);
     l1 += __shfl_xor_sync(0xffffffffu, l1, d);
   }
-  if (i4 == 0) {
-    s_ml[warp][r] = make_float2(m0, l0);
-    s_ml[warp][r + 8] = make_float2(m1, l1);
+  if (i4 == 0) {  // NaN among a row's scores: a maximum that keeps its weight from being lost (fmaxf passes over NaN)
+    s_ml[warp][r] = make_float2(l0 != l0 ? INFINITY : m0, l0);
+    s_ml[warp][r + 8] = make_float2(l1 != l1 ? INFINITY : m1, l1);
   }
   __syncthreads();  // every warp is done with its ring
   // O: lane (r, i) has dims 128 hf + 32 i + {0, 16} + n of rows r and r + 8

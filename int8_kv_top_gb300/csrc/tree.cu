@@ -562,9 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
     const bool all_ok = !named_bar_any(1, 256, !ok);
     s_xm[wg][r] = l_run;
     named_bar_any(1, 256, false);
+    const float l = l_run + s_xm[wg ^ 1][r];
+    // NaN among the row's scores: a weight that the join cannot lose (the running maximum passes over NaN)
+    if (kOf != kTreeCells && l != l) m_run = INFINITY;
     if (!all_ok) m_run = -INFINITY;
     if (wg == 0) {
-      const float l = l_run + s_xm[1][r];
       if (!merges) a.part_ml[(size_t)blockIdx.x * kRows + r] = make_float2(m_run, l);
       const uint32_t at = smem_u32(smem + kOffML) + (uint32_t)(pair * kRows + r) * 8u;
       for (int c = 0; c < S; ++c)

@@ -157,6 +157,36 @@ def test_far_larger_logits_late_in_the_row():
     assert (np.abs(out.double().cpu().numpy() - want) <= bound).all()
 
 
+@pytest.mark.parametrize("groups", [[(300, [(50, 1), (60, 1)])], [(300, [(50, 5), (60, 5)])], [(0, [(50, 1), (2000, 1)])], [(0, [(50, 5), (60, 5)])],
+                                    [(900, [(9, 1)] * 30)]], ids=["one token", "drafts", "own cells", "own drafts", "a block"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nan_reaches_its_row_and_no_other(groups, value):
+    b, _, _ = shared_batch(groups, 41)
+    _, good = run_shared(b)
+    for h, d in ((3, 7), (14, 200)):
+        b["q"][1, h, d] = value
+    _, out = run_shared(b)
+    qsa.qsa_check_device_status()
+    hit = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+    hit[1, [3, 14]] = True
+    assert out[hit].isnan().all() and torch.equal(out[~hit], good[~hit])
+
+
+@pytest.mark.parametrize("tokens", [1, 5])
+@pytest.mark.parametrize("where", ["prefix", "own"])
+def test_a_cell_of_nan_among_far_larger_scores_reaches_every_row(tokens, where):
+    # the part with the NaN has a maximum far below the other part's: its weight is 0 but for the NaN
+    b, _, _ = shared_batch([(300, [(64, tokens)])], 42)
+    prefix, own = int(b["prefixes"][0, 0]), int(b["seqs"][0, 0])
+    big, nan = ((own, 64), prefix + 5) if where == "prefix" else ((prefix, 300), own + 5)
+    b["q"][:] = 4
+    b["kq"][big[0]:big[0] + big[1]] = 127
+    b["ksc"][nan] = np.nan
+    _, out = run_shared(b)
+    qsa.qsa_check_device_status()
+    assert out.isnan().all()
+
+
 @pytest.mark.parametrize("params", [None, SMALL])
 @pytest.mark.parametrize("tokens", [1, 6])
 def test_padding_and_rows_that_are_nobodys(params, tokens):
