@@ -10,7 +10,12 @@
 // have nothing to share, so prefix_own_kernel streams them past a 16-row mma.sync tile, a few CTAs a token and group.
 // It is launched behind the prefixes' kernel, but starts on the SMs that that one leaves and fills the others as they
 // fall idle.  Sequences of many tokens (drafted trees) take the tensor-core kernel for their own cells too.
-// prefix_join_kernel joins the parts.
+// prefix_join_kernel joins the parts.  Calls of few tokens behind short prefixes are one launch of prefix_own_kernel over
+// both sets of cells: its clusters join the parts themselves.
+//
+// Measured (GB300; replayed graphs over warm caches): 64 tokens behind 30,000 cells, all attended to, own cells 100-600: 65 us, of
+// which the tensor-core tiles' operations would take 24 at cuBLAS's rate; 48 tokens behind 16,000 that select 2,048 of
+// them each: 85 us; 40 sequences of 1-16 tokens behind three prompts of 900-12,000: 157 us; 8 tokens behind 1,800: 15 us.
 //
 // Selection (n_kv > identity_max) shares the prefix's codes in the same way: tree_select.cu scores them once for all
 // tokens behind the prefix and each sequence's own cells for its tokens, into rows of columns {prefix cells, gap up to a
@@ -269,8 +274,12 @@ constexpr int kOffRing = 16 * kQPitch;
 constexpr int kOwnSmem = kOffRing + kOwnWarps * kStages * kStageBytes;
 constexpr int kMaxOwn = 32, kMostOwn = 2048;  // CTAs that share a (token, group), and of a call and group where they do
 static_assert(2 * (kOwnSmem + 3 * 1024) <= 228 * 1024, "two CTAs on an SM");
+constexpr int kOwnSmemAlone = 116 * 1024;      // one: clusters otherwise put two of their CTAs on an SM while others have none
 constexpr int kOPitch = kD + 4;                // floats of a warp's unmerged row, over the ring once the cells are attended to
 static_assert(kOwnWarps * kHPG * kOPitch * 4 <= kOwnWarps * kStages * kStageBytes, "the rows fit over the ring");
+constexpr int kMaxMerge = 8;  // CTAs of a cluster that merges
+constexpr int kOffMerge = kOffRing + kOwnWarps * kHPG * kOPitch * 4;  // behind them, the parts of a cluster's CTAs: [CTA][item][8 dims]
+static_assert(kOffMerge + kHPG * kD * 4 <= kOwnSmem && kOffMerge % 16 == 0 && kHPG * (kD / 8) % kMaxMerge == 0, "fit over it too");
 static_assert((kNearSeqs + kNearPrefixes) * 4 <= kOwnWarps * kStages * kStageBytes, "and before them, the tables");
 static_assert(kOffRing % 16 == 0 && kStageBytes % 16 == 0, "16-byte copies");
 constexpr float kRescaleBy = 8.f, kPUp = 7.f;  // log2 units; as in tree.cu
@@ -279,6 +288,7 @@ struct OwnArgs {
   TreeBatch b;
   TokMore* more;
   bool behind_dense;     // launched behind the prefixes' kernel
+  bool shared;           // the prefixes' cells are attended to here too: no other kernel does
   bool records;          // made here, and the tables checked (else by prefix_prep_kernel)
   int* status;
   const __half* q;
@@ -289,7 +299,7 @@ struct OwnArgs {
   const uint32_t* bits;  // selected columns [2][n_tok][bits_pitch words], or null
   int bits_pitch;
   float scale_log2;
-  const __half* gate;    // gate and out: where these are all of a token's cells and one CTA has them
+  const __half* gate;    // gate and out: where these are all of a token's cells, and one cluster has them
   __half* out;
   float* o;              // else unmerged rows [n_tok][2][S][kHPG][kD], and their (m, l) [n_tok][2][S][kHPG]
   float2* ml;
@@ -307,6 +317,8 @@ __device__ __forceinline__ void part_row(long long first, int T, int g, int runs
 // S CTAs a (token, group), an S-th of its tiles of 16 cells each.  The warps take the tiles in turn, each through a ring of its own:
 //   S = Q K^T  (A = 16 rows of Q, 12 of them heads; B = K^, two n8 tiles), 16 k16 steps
 //   O += P V^  (A = P as it stands in S's registers, B = V^, 32 n8 tiles), one k16 step
+// Those 64 MMAs a tile bound it: an SM starts one in about 8.5 cycles (34 on each of its four tensor cores), so the 24,600 cells of
+// 48 tokens with 50-900 own cells take 10,100 cycles of MMAs in a kernel of 23.6 us (alone; 25.8 MB from DRAM).
 // Lanes take the k dims, and V's n dims, in an order of their own, the same for both operands, so that a lane's codes are 16
 // bytes side by side: of a k64 block lane (n, i) has dims 16 i .. 16 i + 15 of cell n, four k16 steps of four; of V lane
 // (n, i) has dims 16 n .. 16 n + 15 of a half of cells 2 i, 2 i + 1, 2 i + 8 and 2 i + 9, which sixteen n8 tiles take one by one.  The
@@ -317,6 +329,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   __shared__ float2 s_ml[kOwnWarps][16];   // (m, l) of the warps' rows
   __shared__ float s_wf[kOwnWarps][kHPG];  // what the warps' rows are multiplied by
   __shared__ float2 s_sum[kHPG];           // (m, l) of the CTA's
+  __shared__ float2 s_all[kMaxMerge][kHPG];  // and of the cluster's CTAs
   // Behind the prefixes' kernel nothing here needs what that one writes, and it triggered this launch when all launches
   // before it were complete: no wait.  One CTA waits for it at its end, so that this launch ends no earlier.
   if (!a.behind_dense) pdl_begin();
@@ -349,22 +362,25 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   const int T = e.z, i_tok = t - e.w, pos0 = e.y;
   const bool chosen = a.bits != nullptr && ti.y > a.b.identity_max;
   const size_t out_row = ((size_t)t * kHeads + g * kHPG) * kD;
-  const int n_own = pos0 + (a.b.tree ? T : i_tok + 1);
-  const int n_tiles = (n_own + kTile - 1) / kTile;
+  const int n_own = pos0 + (a.b.tree ? T : i_tok + 1), n_px = a.shared ? ti.z : 0;
+  const int px_tiles = (n_px + kTile - 1) / kTile, n_tiles = px_tiles + (n_own + kTile - 1) / kTile;  // the prefix's come first
   const int begin = (int)((long long)n_tiles * rank / S), end = (int)((long long)n_tiles * (rank + 1) / S);
   const int mine = max(0, (end - begin - warp + kOwnWarps - 1) / kOwnWarps);  // tiles begin + warp + 4 j
   const uint8_t* my_ring = smem + kOffRing + warp * (kStages * kStageBytes);
   const uint32_t ring = smem_u32(my_ring);
-  const size_t cell0 = (size_t)e.x;
+  const size_t own0 = (size_t)e.x, px0 = px_tiles > 0 ? (size_t)__ldg(&a.b.prefixes[ti.w].x) : 0;
   auto load = [&](int j) {
     if (j < mine) {
-      const int c0 = (begin + warp + kOwnWarps * j) * kTile;
+      const int tile = begin + warp + kOwnWarps * j;
+      const bool own = tile >= px_tiles;
+      const int c0 = (own ? tile - px_tiles : tile) * kTile, n = own ? n_own : n_px;
+      const size_t cell0 = own ? own0 : px0;
       const uint32_t st = ring + (j % kStages) * kStageBytes;
       const int chunk = lane & 15;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c = 2 * i + (lane >> 4);
-        const size_t row = ((cell0 + min(c0 + c, n_own - 1)) * kGroups + g) * kD + chunk * 16;
+        const size_t row = ((cell0 + min(c0 + c, n - 1)) * kGroups + g) * kD + chunk * 16;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(st + c * kD + ((chunk ^ ((c & 1) << 2)) << 4)),
                      "l"(reinterpret_cast<uint64_t>(a.kq + row))
                      : "memory");
@@ -372,17 +388,22 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
                      "l"(reinterpret_cast<uint64_t>(a.vq + row))
                      : "memory");
       }
-      const __half* sc = (lane < 16 ? a.ksc : a.vsc) + ((cell0 + min(c0 + (lane & 15), n_own - 1)) * kGroups + g) * kNB;
+      const __half* sc = (lane < 16 ? a.ksc : a.vsc) + ((cell0 + min(c0 + (lane & 15), n - 1)) * kGroups + g) * kNB;
       asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st + 2 * kTile * kD + lane * 8), "l"(reinterpret_cast<uint64_t>(sc))
                    : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  const uint32_t* bit_row =
-      chosen ? a.bits + (size_t)(g * a.b.n_tok + t) * a.bits_pitch + own_column(ti.z) / 32 : nullptr;
-  // the 16 cells from c0 on that are attended to, as bits
-  auto seen16 = [&](int c0) -> uint32_t {
-    if (chosen) return (__ldcg(bit_row + (c0 >> 5)) >> (c0 & 31)) & 0xffffu;
+  const uint32_t* bit_row = chosen ? a.bits + (size_t)(g * a.b.n_tok + t) * a.bits_pitch : nullptr;
+  // the 16 cells of a tile that are attended to, as bits
+  auto seen16 = [&](int tile) -> uint32_t {
+    const bool own = tile >= px_tiles;
+    const int c0 = (own ? tile - px_tiles : tile) * kTile;
+    if (chosen) {
+      const int column = c0 + (own ? own_column(ti.z) : 0);
+      return (__ldcg(bit_row + (column >> 5)) >> (column & 31)) & 0xffffu;
+    }
+    if (!own) return 0xffffu >> max(c0 + kTile - n_px, 0);
     if (c0 + kTile <= pos0) return 0xffffu;
     const int c = c0 + (lane & 15), dj = c - pos0;
     const bool s = dj < 0 || (dj < T && ((shared_mask_word(a.b, t, i_tok, min(dj >> 5, kTreeWords - 1), T) >> (dj & 31)) & 1u));
@@ -409,7 +430,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   auto at128 = [](const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); };
   for (int j = 0; j < mine; ++j) {
     load(j + 2);
-    const uint32_t seen = seen16((begin + warp + kOwnWarps * j) * kTile);
+    const uint32_t seen = seen16(begin + warp + kOwnWarps * j);
     asm volatile("cp.async.wait_group 2;" ::: "memory");
     __syncwarp();
     const uint8_t* st = my_ring + (j % kStages) * kStageBytes;
@@ -522,6 +543,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
     s_ml[warp][r + 8] = make_float2(l1 != l1 ? INFINITY : m1, l1);
   }
   __syncthreads();  // every warp is done with its ring
+  const bool merges = a.out != nullptr && S > 1;
+  if (merges) cluster_arrive_all();
   // O: lane (r, i) has dims 128 hf + 32 i + {0, 16} + n of rows r and r + 8
   float* rows = reinterpret_cast<float*>(smem + kOffRing) + warp * (kHPG * kOPitch);
 #pragma unroll
@@ -555,6 +578,15 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   static_assert(kGroups == 2, "blocks in the order of the rows");
   __syncthreads();
   const float* all = reinterpret_cast<const float*>(smem + kOffRing);
+  // A cluster's CTA owns an S-th of the items (8 dims of a row): each CTA's part of them is pushed to it.
+  const int per = kHPG * (kD / 8) / S;
+  if (merges) {
+    cluster_wait_all();  // every CTA's ring is free
+    if (tid < kHPG * S)
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(&s_all[rank][tid % kHPG]), tid / kHPG)),
+                   "f"(s_sum[tid % kHPG].x), "f"(s_sum[tid % kHPG].y)
+                   : "memory");
+  }
 #pragma unroll 1
   for (int i = tid; i < kHPG * (kD / 8); i += kOwnThreads) {
     const int h = i / (kD / 8), d = i % (kD / 8) * 8;
@@ -573,12 +605,46 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
       float4* to = reinterpret_cast<float4*>(a.o + ((size_t)blockIdx.x * kHPG + h) * kD + d);
       to[0] = make_float4(v[0], v[1], v[2], v[3]);
       to[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (merges) {
+      const uint32_t to = mapa_shared(smem_u32(smem + kOffMerge) + (uint32_t)(rank * per + i % per) * 32u, i / per);
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + 16u), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                   : "memory");
     } else {
       const float l = s_sum[h].y, inv = l > 0.f ? 1.f / l : 0.f;  // a token that sees nothing: zeros
       const size_t at = out_row + (size_t)h * kD + d;
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] *= inv;
       if (a.gate) apply_gate(v, __ldg(reinterpret_cast<const uint4*>(a.gate + at)));
+      *reinterpret_cast<uint4*>(a.out + at) = pack_out(v);
+    }
+  }
+  if (merges) {
+    cluster_arrive_all();
+    cluster_wait_all();  // the parts are here; no CTA touches another's memory after this
+#pragma unroll 1
+    for (int j = tid; j < per; j += kOwnThreads) {
+      const int i = rank * per + j, h = i / (kD / 8);
+      const size_t at = out_row + (size_t)h * kD + i % (kD / 8) * 8;
+      uint4 gw = make_uint4(0u, 0u, 0u, 0u);
+      if (a.gate) gw = __ldg(reinterpret_cast<const uint4*>(a.gate + at));
+      float M = -INFINITY, L = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < S; ++c) M = fmaxf(M, s_all[c][h].x);
+#pragma unroll 2
+      for (int c = 0; c < S; ++c) {
+        const float f = s_all[c][h].x == -INFINITY ? 0.f : fast_exp2(s_all[c][h].x - M);
+        const float4* z = reinterpret_cast<const float4*>(smem + kOffMerge + (size_t)(c * per + j) * 32);
+        const float4 x = z[0], y = z[1];
+        const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        if (f == 0.f) continue;  // a part that has nothing of the row
+        L = fmaf(s_all[c][h].y, f, L);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = fmaf(u[k], f, v[k]);
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;  // a token that sees nothing: zeros
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= inv;
+      if (a.gate) apply_gate(v, gw);
       *reinterpret_cast<uint4*>(a.out + at) = pack_out(v);
     }
   }
@@ -736,8 +802,15 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
 
 // ---------------------------------------------------------------- the call
 constexpr int kOwnInTopk = 2048;
-// From how many tokens a sequence (on average) their own cells go to the tensor-core kernel.
+// From how many tokens a sequence (on average) their own cells go to the tensor-core kernel.  40 sequences behind 6,000 cells with
+// 50, 300, 1,000, 2,000 own cells, us on prefix_own_kernel / the tensor cores: 3 tokens each 43/50, 54/55, 66/66, 112/102; 4 tokens
+// 53/58, 58/62, 111/73, 126/107; 6 tokens 71/71, 111/75, 115/88, 177/113.
 constexpr int kOwnTokens = 4;
+// Up to how many tokens times prefix cells prefix_own_kernel takes the prefixes' cells too: it reads and multiplies them
+// again for every token, but the tensor-core kernel takes 11 us for the first tile and a join of 5.  Own cells 50-150; us with
+// prefix_own_kernel alone / with both: 1 token behind 250 cells 10/16, behind 2,000 15/19, 16,000 24/28; 8 tokens behind 250 11/17, 2,000
+// 16/21, 4,000 24/33, 8,000 43/26; 16 tokens behind 2,000 19/24, 4,000 39/32; 64 tokens behind 500 20/20, 1,000 35/28.
+constexpr long long kFewCells = 1ll << 15;
 
 inline int own_rows(int n_tok) { return std::max(n_tok, std::min(kMaxOwn * n_tok, kMostOwn)); }  // tokens x CTAs that share one
 
@@ -768,16 +841,42 @@ Layout layout(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv, 
   return l;
 }
 
-cudaError_t own_setup() {
-  static std::atomic<int> ready[64];
+cudaLaunchConfig_t own_config(int ctas, int S, bool cluster, bool alone, cudaStream_t stream, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kOwnThreads);
+  cfg.dynamicSmemBytes = alone ? kOwnSmemAlone : kOwnSmem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cfg;
+}
+
+// fit[i]: how many clusters of kSplits[i] CTAs, each on an SM of its own, the device holds at once.
+constexpr int kNumSplits = 5, kSplits[kNumSplits + 1] = {8, 6, 4, 3, 2, 1};
+cudaError_t own_setup(int (&fit)[kNumSplits]) {
+  static std::atomic<int> ready[64], known[64][kNumSplits];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    if ((e = cudaFuncSetAttribute(prefix_own_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(prefix_own_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmemAlone)) != cudaSuccess) return e;
+    for (int i = 0; i < kNumSplits; ++i) {
+      cudaLaunchAttribute attr[2];
+      const cudaLaunchConfig_t cfg = own_config(kSplits[i], kSplits[i], true, true, nullptr, attr);
+      int n = 0;
+      if ((e = cudaOccupancyMaxActiveClusters(&n, prefix_own_kernel, &cfg)) != cudaSuccess) return e;
+      known[dev][i].store(n, std::memory_order_relaxed);
+    }
     ready[dev].store(1, std::memory_order_release);
   }
+  for (int i = 0; i < kNumSplits; ++i) fit[i] = known[dev][i].load(std::memory_order_relaxed);
   return cudaSuccess;
 }
 
@@ -798,7 +897,8 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   const bool select = b.max_n_kv > b.identity_max;
   // own cells of a sequence, for the shapes of launches (any number gives the same results): what the longest prefix leaves
   const int own_cells = std::max(std::min(b.max_n_kv, 128), b.max_n_kv - b.max_prefix);
-  const bool dense = b.n_prefix > 0 && b.max_prefix > 0, own_dense = (long long)b.n_tok >= (long long)kOwnTokens * b.n_seq;
+  const bool shared = b.n_prefix > 0 && b.max_prefix > 0, own_dense = (long long)b.n_tok >= (long long)kOwnTokens * b.n_seq;
+  const bool few = shared && !own_dense && (long long)b.n_tok * b.max_prefix <= kFewCells, dense = shared && !few;
   TreeSelect w{};
   int own_chunks = 1;
   if (select) {
@@ -814,8 +914,9 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   int clusters = 0;
   cudaError_t e = dense ? prefix_clusters(b, own_dense ? 0 : own_cells, &clusters) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  // One prefix, no selection and few tokens a sequence: the launches find their way without prefix_prep_kernel (3 us).
-  const bool records = !select && !own_dense && b.n_prefix <= 1;
+  // No selection, few tokens a sequence, and at most one prefix on the tensor-core kernel: the launches find their way
+  // without prefix_prep_kernel (3 us).
+  const bool records = !select && !own_dense && (b.n_prefix <= 1 || !dense);
   if (records) {
     plan = nullptr;
   } else {
@@ -834,17 +935,31 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     e = launch_own_parts(b, own_cells, dense, q, kq, vq, ksc, vsc, bits, pitch, base + l.own, p.sm_scale, &j.own.p, status, stream);
     if (e != cudaSuccess) return e;
   } else {
-    if ((e = own_setup()) != cudaSuccess) return e;
-    // CTAs that share a (token, group): one for every 512 cells of the longest, and more of them while the GPU has room
+    int fit[kNumSplits];
+    if ((e = own_setup(fit)) != cudaSuccess) return e;
+    // CTAs that share a (token, group).  Beside the prefixes' kernel: one for every 512 cells of the longest, and more of them
+    // while the GPU has room.  Alone: the largest cluster with an SM for every CTA of which as many fit (and whose warps have a
+    // tile each), or for every 512 cells, two on an SM.
+    const int cells = few ? b.max_n_kv : own_cells;
     int S = 1;
-    while (S < kMaxOwn && 2 * S * b.n_tok <= kMostOwn &&
-           (own_cells > 512 * S || (own_cells > 64 * S && b.n_tok * kGroups * S * 2 <= 152)))
+    bool alone = false;
+    for (int i = 0; !dense && !alone && i < kNumSplits; ++i)
+      if (cells > kOwnWarps * kTile * kSplits[i + 1] && b.n_tok * kGroups <= fit[i]) {
+        S = kSplits[i];
+        alone = true;
+      }
+    while (2 * S <= kMaxOwn && 2 * S * b.n_tok <= kMostOwn &&
+           (cells > 512 * S || (dense && cells > 64 * S && b.n_tok * kGroups * S * 2 <= 152))) {
       S *= 2;
-    const bool last = !dense && S == 1;
+      alone = false;
+    }
+    const bool last = !dense && kHPG * (kD / 8) % S == 0 && S <= kMaxMerge;  // its clusters merge
     float* o = reinterpret_cast<float*>(base + l.own);
     float2* ml = reinterpret_cast<float2*>(o + (size_t)b.n_tok * kHeads * S * kD);
-    const OwnArgs a{b, more, dense, records, status, q, kq, vq, ksc, vsc, bits, pitch, p.sm_scale * kLog2e, gate, last ? out : nullptr, o, ml};
-    e = launch_pdl(prefix_own_kernel, dim3((unsigned)(b.n_tok * kGroups * S)), dim3(kOwnThreads), kOwnSmem, stream, a, S);
+    const OwnArgs a{b, more, dense, few, records, status, q, kq, vq, ksc, vsc, bits, pitch, p.sm_scale * kLog2e, gate, last ? out : nullptr, o, ml};
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = own_config(b.n_tok * kGroups * S, S, last && S > 1, alone, stream, attr);
+    e = cudaLaunchKernelEx(&cfg, prefix_own_kernel, a, S);
     if (e != cudaSuccess || last) return e;
     j.own = PartSet{{reinterpret_cast<const float4*>(o), ml, S, 0}, true};
   }

@@ -13,10 +13,13 @@ pytestmark = pytest.mark.gpu
 SMALL = (40, 71, 1 / 16)  # topk, identity_max: selection over few cells
 
 
-def check(groups, seed=1, params=None, gate=False, causal=False, words=None, rows=None, with_ids=True):
+FAR = 40000  # as max_prefix: few tokens then take the kernels of many, whatever their prefixes are
+
+
+def check(groups, seed=1, params=None, gate=False, causal=False, words=None, rows=None, with_ids=True, max_prefix=None):
     b, ref, flat = shared_batch(groups, seed, words, causal)
     g = synth.gate_input(len(b["q"]), seed=seed + 50) if gate else None
-    ids, out = run_shared(b, params, g, with_ids)
+    ids, out = run_shared(b, params, g, with_ids, bounds=max_prefix and (max_prefix, bounds_of(b)[1]))
     qsa.qsa_check_device_status()
     p = params or (2048, 2051, 1 / 16)
     want, want_ids, bound = reference(ref, flat, *p, gate=g, rows=rows)
@@ -170,6 +173,96 @@ def test_nan_reaches_its_row_and_no_other(groups, value):
     hit = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
     hit[1, [3, 14]] = True
     assert out[hit].isnan().all() and torch.equal(out[~hit], good[~hit])
+
+
+@pytest.mark.parametrize("shared", [0, 1, 15, 127, 128, 129, 300])
+@pytest.mark.parametrize("own", [0, 17, 200])
+def test_decoding_identity_as_of_many(shared, own):
+    check([(shared, [(own, 1), (own + 3, 1), (0, 1)])], seed=shared + own, max_prefix=FAR)
+
+
+@pytest.mark.parametrize("n_seq", [1, 20, 21, 22, 43, 64, 170])
+def test_blocks_of_tokens_as_of_many(n_seq):
+    rng = np.random.default_rng(n_seq)
+    check([(200, [(int(x), 1) for x in rng.integers(0, 90, n_seq)])], seed=n_seq, causal=True, max_prefix=FAR)
+
+
+@pytest.mark.parametrize("groups", [
+    [(150, [(10, 1)] * 5), (0, [(300, 1)] * 3), (77, [(0, 1)] * 30)],
+    [(0, [(5, 2), (70, 1)]), (260, [(1, 3)])],
+    [(130, []), (40, [(9, 1)] * 2), (50, [])],
+    [(500, [(40, 1)] * 50)],
+    [(60, [(5, 1), (11, 1), (10, 1), (200, 1)])],
+], ids=range(5))
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("params", [None, SMALL])
+def test_prefixes_as_of_many(groups, gate, params):
+    check(groups, seed=7, gate=gate, params=params, max_prefix=FAR)
+
+
+@pytest.mark.parametrize("max_prefix", [None, FAR])
+@pytest.mark.parametrize("n_seq,shared,own", [(1, 1, 0), (1, 100, 30), (1, 300, 90), (1, 2000, 40), (1, 3000, 2000), (3, 900, 10), (5, 1900, 140), (8, 1500, 130),
+                                              (11, 40, 300), (20, 600, 50), (40, 100, 20)])
+def test_few_tokens_are_shared_out(n_seq, shared, own, max_prefix):
+    # one to many CTAs a token, whose parts a cluster or the last launch joins: the same result within its rounding
+    dense = (2048, 1 << 17, 1 / 16)
+    check([(shared, [(own + 7 * i, 1) for i in range(n_seq)])], seed=60 + n_seq, params=dense, with_ids=False, max_prefix=max_prefix)
+
+
+@pytest.mark.parametrize("max_prefix", [None, FAR])
+@pytest.mark.parametrize("how", ["cells", "n_kv", "prefix past the pool", "prefix cells<0"])
+def test_bad_tables_of_single_tokens(how, max_prefix):
+    b, ref, flat = shared_batch([(90, [(20, 1), (31, 1)]), (40, [(5, 1), (60, 1)]), (30, [(10, 1)])], 17)
+    bounds = (max_prefix or 90, bounds_of(b)[1])
+    if how == "cells":
+        b["seqs"][2][1] = 5
+    elif how == "n_kv":
+        b["seqs"][2][:3] = [0, 200, 150]
+    else:
+        b["prefixes"][1][:2] = [len(b["kq"]) - 39, 40] if how == "prefix past the pool" else [0, -1]
+    _, out = run_shared(b, fill=7.0, bounds=bounds)
+    with pytest.raises(qsa.QSAError) as e:
+        qsa.qsa_check_device_status()
+    assert e.value.code == qsa.QSA_ERR_DEVICE
+    want, _, bound = reference(ref, flat)
+    got = out.double().cpu().numpy()
+    gone = {2} if how in ("cells", "n_kv") else {2, 3}
+    for s in range(5):
+        assert (got[s] == 7).all() if s in gone else (np.abs(got[s] - want[s]) <= bound[s]).all(), s
+
+
+def test_nan_reaches_its_row_of_many():
+    b, _, _ = shared_batch([(900, [(9, 1)] * 30)], 43)
+    bounds = (FAR, bounds_of(b)[1])
+    _, good = run_shared(b, bounds=bounds)
+    b["q"][1, 3, 7] = np.nan
+    _, out = run_shared(b, bounds=bounds)
+    qsa.qsa_check_device_status()
+    hit = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+    hit[1, 3] = True
+    assert out[hit].isnan().all() and torch.equal(out[~hit], good[~hit])
+
+
+@pytest.mark.parametrize("params", [None, SMALL])
+def test_same_bits_of_many_in_graphs(params):
+    sets = [device_batch([(1200, [(50, 1)] * 30)], 21 + i, params) for i in range(2)]
+    for *_, call in sets:
+        call()
+    torch.cuda.synchronize()
+    want = [(s[3]["out"].clone(), s[3]["ids"].clone()) for s in sets]
+    for s in sets:
+        s[3]["out"].zero_()
+        s[3]["ids"].fill_(-7)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for *_, call in sets:
+            call()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    qsa.qsa_check_device_status()
+    for s, (out, ids) in zip(sets, want):
+        assert torch.equal(s[3]["out"], out) and torch.equal(s[3]["ids"], ids)
 
 
 @pytest.mark.parametrize("tokens", [1, 5])
