@@ -13,9 +13,9 @@
 // prefix_join_kernel joins the parts.  Calls of few tokens behind short prefixes are one launch of prefix_own_kernel over
 // both sets of cells: its clusters join the parts themselves.
 //
-// Measured (GB300; replayed graphs over warm caches): 64 tokens behind 30,000 cells, all attended to, own cells 100-600: 65 us, of
+// Measured (GB300; replayed graphs over warm caches): 64 tokens behind 30,000 cells, all attended to, own cells 100-600: 64 us, of
 // which the tensor-core tiles' operations would take 24 at cuBLAS's rate; 48 tokens behind 16,000 that select 2,048 of
-// them each: 85 us; 40 sequences of 1-16 tokens behind three prompts of 900-12,000: 157 us; 8 tokens behind 1,800: 15 us.
+// them each: 85 us; 40 sequences of 1-16 tokens behind three prompts of 900-12,000: 157 us; 8 tokens behind 1,800: 13 us.
 //
 // Selection (n_kv > identity_max) shares the prefix's codes in the same way: tree_select.cu scores them once for all
 // tokens behind the prefix and each sequence's own cells for its tokens, into rows of columns {prefix cells, gap up to a
@@ -275,7 +275,10 @@ constexpr int kOwnSmem = kOffRing + kOwnWarps * kStages * kStageBytes;
 constexpr int kMaxOwn = 32, kMostOwn = 2048;  // CTAs that share a (token, group), and of a call and group where they do
 static_assert(2 * (kOwnSmem + 3 * 1024) <= 228 * 1024, "two CTAs on an SM");
 constexpr int kOwnSmemAlone = 116 * 1024;      // one: clusters otherwise put two of their CTAs on an SM while others have none
-constexpr int kOPitch = kD + 4;                // floats of a warp's unmerged row, over the ring once the cells are attended to
+// A warp's unmerged rows, over the ring once the cells are attended to: 4 floats of padding every 32 dims and a pitch of 16 banks
+// more, so that the eight lanes of a store's phase (two rows, four runs of 32 dims) meet different banks.
+__device__ __forceinline__ constexpr int o_at(int dim) { return dim + dim / 32 * 4; }
+constexpr int kOPitch = kD + kD / 32 * 4 + 16;
 static_assert(kOwnWarps * kHPG * kOPitch * 4 <= kOwnWarps * kStages * kStageBytes, "the rows fit over the ring");
 constexpr int kMaxMerge = 8;  // CTAs of a cluster that merges
 constexpr int kOffMerge = kOffRing + kOwnWarps * kHPG * kOPitch * 4;  // behind them, the parts of a cluster's CTAs: [CTA][item][8 dims]
@@ -336,6 +339,20 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   if (a.out == nullptr) pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % S, g = blockIdx.x / S % kGroups, t = blockIdx.x / S / kGroups;
+  const size_t out_row = ((size_t)t * kHeads + g * kHPG) * kD;
+  // ---- the queries' rows; 12 .. 15 are zeros
+#pragma unroll 1
+  for (int i = tid; i < 16 * 32; i += kOwnThreads) {
+    const int r = i >> 5, c = i & 31;
+    uint8_t* to = smem + r * kQPitch + c * 16;
+    if (r < kHPG)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)),
+                   "l"(reinterpret_cast<uint64_t>(a.q + out_row + (size_t)r * kD + c * 8))
+                   : "memory");
+    else
+      *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
   int4 ti, e;
   if (a.records) {
     const Finder find(a.b, reinterpret_cast<int*>(smem + kOffRing), tid, kOwnThreads);
@@ -356,12 +373,12 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
     if (a.behind_dense && blockIdx.x == 0) pdl_begin();
   };
   if (ti.x < 0) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     last();
     return;
   }
   const int T = e.z, i_tok = t - e.w, pos0 = e.y;
   const bool chosen = a.bits != nullptr && ti.y > a.b.identity_max;
-  const size_t out_row = ((size_t)t * kHeads + g * kHPG) * kD;
   const int n_own = pos0 + (a.b.tree ? T : i_tok + 1), n_px = a.shared ? ti.z : 0;
   const int px_tiles = (n_px + kTile - 1) / kTile, n_tiles = px_tiles + (n_own + kTile - 1) / kTile;  // the prefix's come first
   const int begin = (int)((long long)n_tiles * rank / S), end = (int)((long long)n_tiles * (rank + 1) / S);
@@ -417,13 +434,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows lane / 4 and 8 above: running maximum (log2 units), lane's sum
   load(0);
   load(1);
-  // ---- the queries' rows; 12 .. 15 are zeros
-  for (int i = tid; i < 16 * 32; i += kOwnThreads) {
-    const int r = i >> 5, c = i & 31;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < kHPG) v = __ldg(reinterpret_cast<const uint4*>(a.q + out_row + (size_t)r * kD) + c);
-    *reinterpret_cast<uint4*>(smem + r * kQPitch + c * 16) = v;
-  }
+  asm volatile("cp.async.wait_group 2;" ::: "memory");
   __syncthreads();  // the queries are in shared memory
   const int r = lane >> 2, i4 = lane & 3;
   const uint8_t *q_lo = smem + r * kQPitch + i4 * 32, *q_hi = q_lo + 8 * kQPitch;
@@ -545,6 +556,23 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   __syncthreads();  // every warp is done with its ring
   const bool merges = a.out != nullptr && S > 1;
   if (merges) cluster_arrive_all();
+  if (tid < kHPG) {  // the warps' weights, and (m, l) of the CTA
+    float2 x[kOwnWarps];
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) {
+      x[w] = s_ml[w][tid];
+      m = fmaxf(m, x[w].x);
+    }
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) {
+      const float f = x[w].x == -INFINITY ? 0.f : fast_exp2(x[w].x - m);
+      s_wf[w][tid] = f;
+      l = fmaf(x[w].y, f, l);
+    }
+    s_sum[tid] = make_float2(m, l);
+    if (a.out == nullptr) a.ml[(size_t)blockIdx.x * kHPG + tid] = make_float2(m, l);
+  }
   // O: lane (r, i) has dims 128 hf + 32 i + {0, 16} + n of rows r and r + 8
   float* rows = reinterpret_cast<float*>(smem + kOffRing) + warp * (kHPG * kOPitch);
 #pragma unroll
@@ -555,25 +583,10 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
       if (row < kHPG) {
 #pragma unroll
         for (int n = 0; n < 16; n += 4)
-          *reinterpret_cast<float4*>(rows + row * kOPitch + dim + n) =
+          *reinterpret_cast<float4*>(rows + row * kOPitch + o_at(dim) + n) =
               make_float4(o[16 * hf + n][k], o[16 * hf + n + 1][k], o[16 * hf + n + 2][k], o[16 * hf + n + 3][k]);
       }
     }
-  // ---- the warps' rows in one
-  __syncthreads();
-  if (tid < kHPG) {
-    float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-    for (int w = 0; w < kOwnWarps; ++w) m = fmaxf(m, s_ml[w][tid].x);
-#pragma unroll 1
-    for (int w = 0; w < kOwnWarps; ++w) {
-      const float f = s_ml[w][tid].x == -INFINITY ? 0.f : fast_exp2(s_ml[w][tid].x - m);
-      s_wf[w][tid] = f;
-      l = fmaf(s_ml[w][tid].y, f, l);
-    }
-    s_sum[tid] = make_float2(m, l);
-    if (a.out == nullptr) a.ml[(size_t)blockIdx.x * kHPG + tid] = make_float2(m, l);
-  }
   // a CTA is (token, group, rank), as its rows are in `o`
   static_assert(kGroups == 2, "blocks in the order of the rows");
   __syncthreads();
@@ -595,7 +608,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
 #pragma unroll
     for (int w = 0; w < kOwnWarps; ++w) {
       const float f = s_wf[w][h];
-      const float4* z = reinterpret_cast<const float4*>(all + (w * kHPG + h) * kOPitch + d);
+      const float4* z = reinterpret_cast<const float4*>(all + (w * kHPG + h) * kOPitch + o_at(d));
       const float4 x = z[0], y = z[1];
       const float u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
