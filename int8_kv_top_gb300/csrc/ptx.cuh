@@ -172,13 +172,12 @@ __device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t nthreads, bo
 // pdl_begin() before its first access to global memory: the wait returns once the previous grid
 // has completed and its writes are visible, so stream order holds for every read and write after
 // it.  Only CTA-local setup (shared-memory barriers, TMEM allocation, tensor map prefetch from
-// kernel parameters) may come before it.  No kernel but two triggers its dependents early: CTAs of the
-// next kernel waiting beside running ones slowed the latency-bound kernels (the one-CTA decode
-// top-k most).
+// kernel parameters) may come before it.  No kernel but those of qsa_prefix_attention triggers its dependents early: CTAs
+// of the next kernel waiting beside running ones slowed the latency-bound kernels (the one-CTA decode top-k most).
 __device__ __forceinline__ void pdl_begin() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The exception, of two kernels of qsa_prefix_attention: the next launch may start once every CTA of this one has called this
-// (after pdl_begin, so that all launches before this one are complete by then) or has ended; its pdl_begin still waits for
-// all of this launch.
+// The exception, the attention kernels of qsa_prefix_attention: the next launch may start once every CTA of this one has
+// called this (after pdl_begin, so that all launches before this one are complete by then) or has ended; its pdl_begin
+// still waits for all of this launch.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------- fences

@@ -20,6 +20,8 @@
 // launched alone from a cold L2 (243 us as the call runs).  The score reads 88 MB; by a clock trace a tile takes
 // 2,400 cycles, 1,900 of them the issue of its MMAs, the rest between tiles; neither memory nor arithmetic (tensor 7%)
 // bounds it.  Two teams of producers and an epilogue that read each token's scale as it stored: 247 us.
+#include <algorithm>
+
 #include "select_math.cuh"
 #include "tree_common.cuh"
 
@@ -464,7 +466,7 @@ cudaError_t launch_shared_select(const TreeBatch& b, const TreeSelect& w, int ow
     return best;
   };
   const bool prefixes = b.n_prefix > 0 && b.max_prefix > 0;
-  const ScoreShape shape{0, prefixes ? shares(b.n_prefix, b.max_prefix) : 0, prefixes ? b.n_tok / kTokChunk + b.n_prefix : 0,
+  const ScoreShape shape{0, prefixes ? shares(b.n_prefix, std::min(b.max_prefix, b.max_n_kv)) : 0, prefixes ? b.n_tok / kTokChunk + b.n_prefix : 0,
                          w.own_in_topk ? 0 : shares(b.n_seq, own_cells)};
   const long long ctas = kGroups * ((long long)shape.prefix_x * shape.prefix_z + (long long)shape.own_x * (b.n_tok / kTokChunk + b.n_seq));
   if (ctas > 0) e = launch_pdl(tree_score_kernel<true>, dim3((unsigned)ctas), dim3(kScoreThreads), kScoreSmem, stream, b, w, kq, ksc, shape,
