@@ -2,7 +2,10 @@
 // server's tables put side by side at the front of the pool, in place).
 //
 // Both are copies bound by memory: a cell is 1,056 bytes (K and V codes, 512 bytes each, and their scales, 16 bytes
-// each), read once and written once.  A warp takes several cells, all loaded into registers before any is stored.
+// each), read once and written once.  A warp takes eight cells, all loaded into registers before any is stored: 17 loads of
+// 16 bytes a lane in flight.  Measured (GB300): 96 runs of 40-3,000 cells 45 us, 6.2 TB/s of the 278 MB read and written, 0.92 of a
+// plain copy's rate; 500 runs compacted, 461 MB, 87 us, 5.3 TB/s (flags and the look-up of runs cost the rest); 3 runs of 500 5 us
+// and 8 runs 7-8 us are the latency of one and two launches.
 #include <algorithm>
 
 #include "tree_common.cuh"

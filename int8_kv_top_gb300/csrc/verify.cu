@@ -14,6 +14,14 @@
 // Running sums over 100,000 entries have neighbours 1e-5 apart and less, and fp32 sums would land beside the border.  Sums are
 // whole numbers instead: a probability is taken in units of 2^-44 (fp32 holds 2^-24 of itself), so sums and
 // differences are exact, in any order, and only w = max(w - c d, 0) after a second refusal rounds (to a unit).
+//
+// Measured (GB300, rows from DRAM): 64 trees of 4-24 tokens over 131,071 entries 46 us for 84-92 MB of rows (13 us at a plain copy's
+// rate): the pass that every sequence has ends after 14 us, near the memory's rate; the second and third pass of the 21-27
+// sequences with several refusals take 8-18 us each, bound by their 64-bit arithmetic, since the hardware puts up to four CTAs of a
+// cluster on one SM while others are idle (a spreading preference of the launch changed nothing).  48 trees without drafts'
+// probabilities over 100,003 entries 11.7 us; one chain of 8 over 32,768 entries 6.6 us: start, gathers, a pass and the draw,
+// each a round trip to memory.  Tried without a gain: all blocks' loads ahead (spilled), prefetches into L2 (48.6 to 53 us), pairs
+// of floats for whole numbers, products of 32-bit halves written out (48.7 to 51).
 #include "tree_common.cuh"
 
 namespace qsa {
@@ -246,13 +254,13 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
       } else {
         uint32_t hs = 0u, ls = 0u;  // p - min(p, d): the biases cancel
         static_assert(kQuads == 4, "four of each row");
-        float4 v[4], z[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = load4(prow, j0 + 128 * i, a.vocab, a.vec_p);
-          z[i] = load4(drow, j0 + 128 * i, a.vocab, a.vec_d);
-        }
         if (refused == 1) {
+          float4 v[4], z[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = load4(prow, j0 + 128 * i, a.vocab, a.vec_p);
+            z[i] = load4(drow, j0 + 128 * i, a.vocab, a.vec_d);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, g[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
@@ -264,13 +272,20 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(const __grid_c
               ls += y.lo - m.lo;
             }
           }
-        } else {
+        } else {  // a quad ahead: all of them at once, as above, spilled (64 drafts 48.7 us against 46.2)
+          float4 x = load4(prow, j0, a.vocab, a.vec_p), y = load4(drow, j0, a.vocab, a.vec_d);
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const float4 x = i < 2 ? (i == 0 ? v[0] : v[1]) : i == 2 ? v[2] : v[3], y = i < 2 ? (i == 0 ? z[0] : z[1]) : i == 2 ? z[2] : z[3];
+          for (int i = 1; i <= 4; ++i) {
+            float4 nx = x, ny = y;
+            if (i < 4) {
+              nx = load4(prow, j0 + 128 * i, a.vocab, a.vec_p);
+              ny = load4(drow, j0 + 128 * i, a.vocab, a.vec_d);
+            }
             long long left[4];
             left_over<4>({x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}, s_mass, refused, left);
             sum += left[0] + left[1] + left[2] + left[3];
+            x = nx;
+            y = ny;
           }
         }
         sum += units(hs, ls);
