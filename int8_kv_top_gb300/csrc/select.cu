@@ -724,8 +724,9 @@ __device__ uint32_t first_key_warp(P pred) {
 // see are -inf, its selected cells go to a bitmap as well, and `ids` may be null.
 // kShared: the rows of a shared call (qsa_prefix_attention): columns are the prefix's cells, a gap of -inf up to a whole
 // tile, and the sequence's own cells.
-template <int V, bool kTree, bool kShared = false>
-__global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
+// kThr threads of V columns each.
+template <int V, bool kTree, bool kShared = false, int kThr = kTkThreads>
+__global__ void __launch_bounds__(kThr, (V <= 64 && kThr == kTkThreads ? 2 : 1))
     topk_kernel(const __half* __restrict__ scores, const __half* __restrict__ q, const int8_t* __restrict__ kq,
                 const __half* __restrict__ ksc, const float* __restrict__ eh, const float* __restrict__ kmax,
                 const unsigned* __restrict__ hist1, int32_t* __restrict__ ids, int t_sel, int T_sel, int n_pad,
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
   // are the ones most likely still in L2 when the first wave of this kernel starts
   const int r = gridDim.x - 1 - blockIdx.x, g = gridDim.y - 1 - blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int nwarps = kTkThreads / 32;
+  constexpr int nwarps = kThr / 32;
   const int t = t_sel + r;
   int n_kv = pos0 + t + 1;  // cells of the row
   const __half* row = scores + ((size_t)g * T_sel + r) * n_pad;
@@ -854,8 +855,8 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     for (int h = 0; h < kHPG; ++h) sq += half_int24(__half_as_ushort(qt[h * kD]));
     s_qsum[tid + (tid >> 5)] = sq;
   }
-  for (int i = tid; i < 512; i += kTkThreads) s_hist[i] = 0u;
-  for (int i = tid; i < (n_kv + 31) / 32; i += kTkThreads) s_bits[i] = 0u;
+  for (int i = tid; i < 512; i += kThr) s_hist[i] = 0u;
+  for (int i = tid; i < (n_kv + 31) / 32; i += kThr) s_bits[i] = 0u;
   if (tid == 0) {
     // |s~ - s| <= a + b |s~|: a covers the residual of Qsum after its fp16 hi + lo split
     // (E_b) and the fp32 accumulation of 128 exact products per block (128 * 2^-23 of the
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     __syncthreads();
     int ab_hi = 0, ab_lo = 0, b_hi = -1, b_lo = -1;
     find_bin_desc2(s_hist, r_hi, r_hi >= 1, s_hist, r_lo, r_lo <= n_samp, &b_hi, &ab_hi, &b_lo, &ab_lo, s_tmp);
-    for (int i = tid; i < 512; i += kTkThreads) s_hist[i] = 0u;
+    for (int i = tid; i < 512; i += kThr) s_hist[i] = 0u;
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < V / 8; ++m) {
@@ -981,20 +982,20 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
   const int Cn = s_cnt[0];
   const int need_c = K - A0;
   bracket = bracket && Cn <= kCandCap && need_c >= 1 && need_c <= Cn;
-  for (int i = tid; i < 512; i += kTkThreads) s_hist[i] = 0u;
+  for (int i = tid; i < 512; i += kThr) s_hist[i] = 0u;
   __syncthreads();
   // exact order key of the k-th largest score: among the candidates, or over the whole row
   uint32_t tau_key;
   {
     int ab1, ab2, b1, b2;
     if (bracket) {
-      for (int base = warp * 32; base < Cn; base += kTkThreads) {
+      for (int base = warp * 32; base < Cn; base += kThr) {
         const int i = base + lane;
         warp_hist_add(i < Cn, i < Cn ? (uint32_t)s_cand_key[i] >> 8 : 0u, s_hist);
       }
       __syncthreads();
       b1 = find_bin_desc(s_hist, need_c, &ab1, s_tmp);
-      for (int base = warp * 32; base < Cn; base += kTkThreads) {
+      for (int base = warp * 32; base < Cn; base += kThr) {
         const int i = base + lane;
         const uint32_t k = i < Cn ? (uint32_t)s_cand_key[i] : 0u;
         warp_hist_add(i < Cn && (int)(k >> 8) == b1, k & 0xFFu, s_hist + 256);
@@ -1017,10 +1018,10 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
       __syncthreads();
       b2 = find_bin_desc(s_hist + 256, K - ab1, &ab2, s_tmp);
     } else {
-      for (int c = tid; c < n_kv; c += kTkThreads) atomicAdd(&s_hist[fp16_order_key(__half_as_ushort(row[c])) >> 8], 1u);
+      for (int c = tid; c < n_kv; c += kThr) atomicAdd(&s_hist[fp16_order_key(__half_as_ushort(row[c])) >> 8], 1u);
       __syncthreads();
       b1 = find_bin_desc(s_hist, K, &ab1, s_tmp);
-      for (int c = tid; c < n_kv; c += kTkThreads) {
+      for (int c = tid; c < n_kv; c += kThr) {
         const uint32_t k = fp16_order_key(__half_as_ushort(row[c]));
         if ((int)(k >> 8) == b1) atomicAdd(&s_hist[256 + (k & 0xFFu)], 1u);
       }
@@ -1049,7 +1050,7 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
   bracket = bracket && k_def <= key_hi + 1u && k_band >= key_lo;
   int n_def = 0;
   if (bracket) {
-    for (int i = tid; i < Cn; i += kTkThreads) {
+    for (int i = tid; i < Cn; i += kThr) {
       const int c = s_cand_idx[i];
       const uint32_t k = s_cand_key[i];
       if (k >= k_def) {
@@ -1085,12 +1086,12 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     // codes of block lane / 8) forms the 64-bit block sums and the 128-bit key
     for (int i0 = 0; i0 < B; i0 += kStageRows) {
       const int nb = min(kStageRows, B - i0);
-      for (int x = tid; x < nb * 16; x += kTkThreads) {
+      for (int x = tid; x < nb * 16; x += kThr) {
         const int c = s_band_idx[i0 + (x >> 4)];
         cp_async16(s_stage + (x >> 4) * kStageStride + (x & 15) * 16,
                    kq + (pool_cell(c) * kGroups + g) * kD + (x & 15) * 16);
       }
-      for (int x = tid; x < nb; x += kTkThreads) {
+      for (int x = tid; x < nb; x += kThr) {
         const int c = s_band_idx[i0 + x];
         s_stage_sc[x] = *reinterpret_cast<const uint2*>(ksc + (pool_cell(c) * kGroups + g) * kNB);
       }
@@ -1165,10 +1166,10 @@ __global__ void __launch_bounds__(kTkThreads, (V <= 64 ? 2 : 1))
     unsigned __int128 pre = 0;
     int rem = need;
     for (int pass = 0; pass < 16; ++pass) {
-      for (int i = tid; i < 256; i += kTkThreads) s_hist[i] = 0u;
+      for (int i = tid; i < 256; i += kThr) s_hist[i] = 0u;
       __syncthreads();
       const int shift = 120 - 8 * pass;
-      for (int c = tid; c < n_kv; c += kTkThreads) {
+      for (int c = tid; c < n_kv; c += kThr) {
         if (!in_band(c)) continue;
         const unsigned __int128 kb = bkey(c);
         if (pass == 0 || (kb >> (shift + 8)) == (pre >> (shift + 8))) atomicAdd(&s_hist[(unsigned)(kb >> shift) & 0xFFu], 1u);
@@ -1374,15 +1375,20 @@ cudaError_t launch_select(const __half* q, const int8_t* kq, const __half* ksc, 
 
 cudaError_t launch_tree_topk(const TreeBatch& b, const TreeSelect& w, const __half* q, const int8_t* kq,
                              const __half* ksc, int32_t* ids, Params p, int* status, cudaStream_t stream) {
-  auto run = [&](auto kern) -> cudaError_t {
+  auto run = [&](auto kern, int threads = kTkThreads) -> cudaError_t {
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopkSmem);
     if (err != cudaSuccess) return err;
-    return launch_pdl(kern, dim3(b.n_tok, kGroups), dim3(kTkThreads), kTopkSmem, stream, w.scores, q, kq, ksc, w.eh,
+    return launch_pdl(kern, dim3(b.n_tok, kGroups), dim3(threads), kTopkSmem, stream, w.scores, q, kq, ksc, w.eh,
                       w.kmax, static_cast<const unsigned*>(nullptr), ids, 0, b.n_tok, w.pitch, 0, p.topk, p.sm_scale,
                       status, b, w);
   };
   if (b.tok != nullptr) {  // a shared call: up to a tile's gap between the prefix's cells and the own ones
     const int columns = b.max_n_kv + 127;
+    // an SM a row: twice the threads for its passes (48 tokens behind 16,000 cells, the whole call: 85.5 us against 80.4)
+    if (b.n_tok * kGroups <= 152) {
+      if (columns <= 16 * 1024) return run(topk_kernel<16, true, true, 1024>, 1024);
+      if (columns <= 32 * 1024) return run(topk_kernel<32, true, true, 1024>, 1024);
+    }
     if (columns <= 16 * kTkThreads) return run(topk_kernel<16, true, true>);
     if (columns <= 32 * kTkThreads) return run(topk_kernel<32, true, true>);
     if (columns <= 64 * kTkThreads) return run(topk_kernel<64, true, true>);

@@ -103,6 +103,13 @@ def test_long_prefix_many_tokens():
     check(groups, seed=8, params=(2048, 1 << 17, 1 / 16), rows=rows, causal=True)
 
 
+@pytest.mark.parametrize("n_seq", [3, 76, 77])
+@pytest.mark.parametrize("shared", [8000, 16200, 16300, 32500, 33000])
+def test_selection_at_the_borders_of_the_kernels(n_seq, shared):
+    # rows of scores on an SM of their own and two on an SM, of up to 8,192, 16,384, 32,768 and 65,536 columns
+    check([(shared, [(30 + i, 1) for i in range(n_seq)])], seed=n_seq, rows={0, n_seq - 1})
+
+
 def test_long_own_cells():
     check([(300, [(9000, 1), (40, 1)])], seed=9, rows={0, 1}, params=(2048, 1 << 17, 1 / 16))
     check([(300, [(9000, 1), (40, 1)])], seed=9, rows={0, 1})
