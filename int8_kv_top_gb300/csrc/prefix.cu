@@ -15,7 +15,7 @@
 //
 // Measured (GB300; replayed graphs over warm caches): 64 tokens behind 30,000 cells, all attended to, own cells 100-600: 64 us, of
 // which the tensor-core tiles' operations would take 24 at cuBLAS's rate; 48 tokens behind 16,000 that select 2,048 of
-// them each: 85 us; 40 sequences of 1-16 tokens behind three prompts of 900-12,000: 157 us; 8 tokens behind 1,800: 13 us.
+// them each: 80 us; 40 sequences of 1-16 tokens behind three prompts of 900-12,000: 157 us; 8 tokens behind 1,800: 13 us.
 //
 // Selection (n_kv > identity_max) shares the prefix's codes in the same way: tree_select.cu scores them once for all
 // tokens behind the prefix and each sequence's own cells for its tokens, into rows of columns {prefix cells, gap up to a
@@ -814,6 +814,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------- the call
+// Up to how many own cells (about) of a token or two a sequence the top-k kernel scores them itself.
 constexpr int kOwnInTopk = 2048;
 // From how many tokens a sequence (on average) their own cells go to the tensor-core kernel.  40 sequences behind 6,000 cells with
 // 50, 300, 1,000, 2,000 own cells, us on prefix_own_kernel / the tensor cores: 3 tokens each 43/50, 54/55, 66/66, 112/102; 4 tokens
