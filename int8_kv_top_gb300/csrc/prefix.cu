@@ -665,10 +665,16 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
 }
 
 // ---------------------------------------------------------------- 3. the join
-// A CTA a (token, group) and slice of 32 dims.  The parts' slices are fetched to shared memory at once (a part's rows
-// of a token lie side by side, 192 bytes a float4 of dims), while a warp a row makes the weights e^(m - M).  It has to be small:
-// its CTAs wait on the SMs beside those of the launch before.
-constexpr int kJoinThreads = 128, kSlices = 8, kQuads = kD / kSlices / 4, kFit = 16;  // runs fetched at a time
+// A CTA a (token, group) and slice of the dims.  The parts' slices are fetched to shared memory at once (a part's rows
+// of a token lie side by side, 192 bytes a float4 of dims), while a warp a row, or three, makes the weights e^(m - M).
+// Few tokens take eight slices, whose small CTAs wait on the SMs beside those of the launch before; of many tokens two, so that
+// less is looked up again.  The whole call behind 6,000 cells, us with 8 / 4 / 2 / 1 slices: 16 tokens 27/29/28/32, 64 31/32/34/35, 100 42/40/41/41,
+// 250 114/108/106/105; 40 sequences of 8 tokens 88/82/78/79.  kFit parts are fetched at a time.
+template <int kSlices>
+struct JoinShape {
+  static constexpr int kQuads = kD / kSlices / 4, kFit = 2 * kSlices;
+  static constexpr int kThreads = std::max(128, kHPG * kQuads / 2);
+};
 struct PartSet {  // parts of a token's rows, as the tensor-core kernel or prefix_own_kernel leaves them
   TreeParts p;
   bool rows;      // of prefix_own_kernel: [n_tok][2][runs][kHPG]
@@ -683,7 +689,11 @@ struct JoinArgs {
   __half* out;
 };
 constexpr int kMostParts = kMaxRuns + kMaxRuns;
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ JoinArgs a) {
+constexpr int kJoinMany = 88;  // tokens
+template <int kSlices>
+__global__ void __launch_bounds__(JoinShape<kSlices>::kThreads) prefix_join_kernel(const __grid_constant__ JoinArgs a) {
+  constexpr int kQuads = JoinShape<kSlices>::kQuads, kFit = JoinShape<kSlices>::kFit, kJoinThreads = JoinShape<kSlices>::kThreads;
+  static_assert(kJoinThreads % 32 == 0 && kHPG % (kJoinThreads / 32) == 0, "whole rows a warp");
   __shared__ __align__(16) float4 s_part[kFit * kQuads * kHPG];  // [part][quad][row]
   __shared__ float s_w[kMostParts][kHPG];                        // weights of the parts
   __shared__ size_t s_from[2][kHPG], s_ml[2][kHPG];              // a row of part 0 (prefix, own): its O, in float4, and its (m, l)
@@ -977,7 +987,11 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     if (e != cudaSuccess || last) return e;
     j.own = PartSet{{reinterpret_cast<const float4*>(o), ml, S, 0}, true};
   }
-  return launch_pdl(prefix_join_kernel, dim3((unsigned)(b.n_tok * kGroups * kSlices)), dim3(kJoinThreads), 0, stream, j);
+  auto join = [&](auto kernel, int slices, int threads) {
+    return launch_pdl(kernel, dim3((unsigned)(b.n_tok * kGroups * slices)), dim3(threads), 0, stream, j);
+  };
+  if (b.n_tok >= kJoinMany) return join(prefix_join_kernel<2>, 2, JoinShape<2>::kThreads);
+  return join(prefix_join_kernel<8>, 8, JoinShape<8>::kThreads);
 }
 
 }  // namespace qsa
