@@ -158,7 +158,7 @@ struct TreeParts {  // unmerged rows of blocks (tree.cu): O [CTA][64][128][4] an
   int run_tiles;  // own cells: a block of fewer tiles has as many of these runs as it takes (shared_runs)
 };
 size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells);
-cudaError_t prefix_clusters(const TreeBatch& b, int beside, int* clusters);
+cudaError_t prefix_clusters(const TreeBatch& b, int own_cells, int own_ctas, int* clusters);
 cudaError_t launch_prefix_parts(const TreeBatch& b, int clusters, const int4* plan, const __half* q, const int8_t* kq, const int8_t* vq,
                                 const __half* ksc, const __half* vsc, const uint32_t* bits, int bits_pitch, void* ws,
                                 float sm_scale, TreeParts* parts, int* status, cudaStream_t stream);

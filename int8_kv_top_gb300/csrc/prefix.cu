@@ -904,6 +904,28 @@ cudaError_t own_setup(int (&fit)[kNumSplits]) {
   return cudaSuccess;
 }
 
+// CTAs of prefix_own_kernel that share a (token, group), over about `cells` cells.  Beside the prefixes' kernel: one for every 512
+// cells of the longest, and more of them while the GPU has room.  Alone: the largest cluster with an SM for every CTA of which as
+// many fit (and whose warps have a tile each), or for every 512 cells, two on an SM.
+cudaError_t own_split(const TreeBatch& b, int cells, bool dense, int* split, bool* alone) {
+  int fit[kNumSplits], S = 1;
+  const cudaError_t e = own_setup(fit);
+  if (e != cudaSuccess) return e;
+  *alone = false;
+  for (int i = 0; !dense && !*alone && i < kNumSplits; ++i)
+    if (cells > kOwnWarps * kTile * kSplits[i + 1] && b.n_tok * kGroups <= fit[i]) {
+      S = kSplits[i];
+      *alone = true;
+    }
+  while (2 * S <= kMaxOwn && 2 * S * b.n_tok <= kMostOwn &&
+         (cells > 512 * S || (dense && cells > 64 * S && b.n_tok * kGroups * S * 2 <= 152))) {
+    S *= 2;
+    *alone = false;
+  }
+  *split = S;
+  return e;
+}
+
 }  // namespace
 
 size_t prefix_attention_workspace_bytes(int n_prefix, int n_seq, int n_tok, int max_prefix, int max_n_kv, int identity_max) {
@@ -936,8 +958,14 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   }
   int4* plan = reinterpret_cast<int4*>(base + l.plan);
   int clusters = 0;
-  cudaError_t e = dense ? prefix_clusters(b, own_dense ? 0 : own_cells, &clusters) : cudaSuccess;
+  int S = 1;
+  bool alone = false;
+  cudaError_t e = own_dense ? cudaSuccess : own_split(b, few ? b.max_n_kv : own_cells, dense, &S, &alone);
   if (e != cudaSuccess) return e;
+  if (dense) {
+    e = own_dense ? prefix_clusters(b, own_cells, 0, &clusters) : prefix_clusters(b, (own_cells + S - 1) / S, b.n_tok * kGroups * S, &clusters);
+    if (e != cudaSuccess) return e;
+  }
   // No selection, few tokens a sequence, and at most one prefix on the tensor-core kernel: the launches find their way
   // without prefix_prep_kernel (3 us).
   const bool records = !select && !own_dense && (b.n_prefix <= 1 || !dense);
@@ -959,24 +987,6 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
     e = launch_own_parts(b, own_cells, dense, q, kq, vq, ksc, vsc, bits, pitch, base + l.own, p.sm_scale, &j.own.p, status, stream);
     if (e != cudaSuccess) return e;
   } else {
-    int fit[kNumSplits];
-    if ((e = own_setup(fit)) != cudaSuccess) return e;
-    // CTAs that share a (token, group).  Beside the prefixes' kernel: one for every 512 cells of the longest, and more of them
-    // while the GPU has room.  Alone: the largest cluster with an SM for every CTA of which as many fit (and whose warps have a
-    // tile each), or for every 512 cells, two on an SM.
-    const int cells = few ? b.max_n_kv : own_cells;
-    int S = 1;
-    bool alone = false;
-    for (int i = 0; !dense && !alone && i < kNumSplits; ++i)
-      if (cells > kOwnWarps * kTile * kSplits[i + 1] && b.n_tok * kGroups <= fit[i]) {
-        S = kSplits[i];
-        alone = true;
-      }
-    while (2 * S <= kMaxOwn && 2 * S * b.n_tok <= kMostOwn &&
-           (cells > 512 * S || (dense && cells > 64 * S && b.n_tok * kGroups * S * 2 <= 152))) {
-      S *= 2;
-      alone = false;
-    }
     const bool last = !dense && kHPG * (kD / 8) % S == 0 && S <= kMaxMerge;  // its clusters merge
     float* o = reinterpret_cast<float*>(base + l.own);
     float2* ml = reinterpret_cast<float2*>(o + (size_t)b.n_tok * kHeads * S * kD);

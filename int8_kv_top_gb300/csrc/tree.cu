@@ -870,11 +870,20 @@ size_t tree_parts_workspace_bytes(int n, int n_tok, int max_cells) {
   return (size_t)shared_parts_most(n, n_tok, max_cells) * 2 * kRows * (kD * sizeof(float) + sizeof(float2));
 }
 
-cudaError_t prefix_clusters(const TreeBatch& b, int beside, int* clusters) {
+namespace {
+int own_part_runs(const PlanHeld& held, const TreeBatch& b, int cells) {
+  return shared_plan_runs(held.n[0], b.n_seq, b.n_tok, cells, shared_parts_most(b.n_seq, b.n_tok, b.max_n_kv));
+}
+}  // namespace
+
+// own_ctas: prefix_own_kernel's, each over own_cells cells; 0: the own cells go to launch_own_parts
+cudaError_t prefix_clusters(const TreeBatch& b, int own_cells, int own_ctas, int* clusters) {
   PlanHeld held;
   const cudaError_t e = tree_setup(&held);
-  if (e == cudaSuccess)
-    *clusters = shared_plan_clusters(held.n[0], b.n_prefix, b.n_tok, b.max_prefix, beside, shared_parts_most(b.n_prefix, b.n_tok, b.max_prefix));
+  if (e != cudaSuccess) return e;
+  const Beside o = own_ctas > 0 ? beside_own(own_ctas, own_cells)
+                                : beside_own_parts(b.n_seq, b.n_tok, own_cells, own_part_runs(held, b, own_cells));
+  *clusters = shared_plan_clusters(held.n[0], b.n_prefix, b.n_tok, b.max_prefix, o, shared_parts_most(b.n_prefix, b.n_tok, b.max_prefix));
   return e;
 }
 
@@ -909,7 +918,7 @@ cudaError_t launch_own_parts(const TreeBatch& b, int cells, bool behind_dense, c
   PlanHeld held;
   const cudaError_t e = tree_setup(&held);
   if (e != cudaSuccess) return e;
-  const int runs = shared_plan_runs(held.n[0], b.n_seq, b.n_tok, cells, shared_parts_most(b.n_seq, b.n_tok, b.max_n_kv));
+  const int runs = own_part_runs(held, b, cells);
   return launch_parts<kOwnCells>(b, tree_blocks_most(b.n_seq, b.n_tok) * kGroups * runs, runs, (plan_tiles(cells) + runs - 1) / runs,
                                  behind_dense, b.n_seq, b.max_n_kv, nullptr, q, kq, vq, ksc, vsc, bits, bits_pitch, ws, sm_scale, parts,
                                  status, stream);

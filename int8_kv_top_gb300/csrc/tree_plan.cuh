@@ -126,28 +126,58 @@ inline int shared_plan_runs(int held, int n, int n_tok, int cells, long long mos
   return best;
 }
 
-// Clusters over the prefixes' cells, `cells` of the longest.  The device, which knows how many each prefix has, shares them
-// out so that no run has more tiles than it must (prefix_prep_kernel).  At least two a block; whole fillings of the GPU at best.
-// `beside` own cells a sequence are attended to by a kernel that takes the SMs that this launch leaves, and all of them when it
-// ends: by SM, about 1.5 of a tile's time a CTA (512 cells of the longest sequence) and 0.0105 a cell and group, 0.6 of
-// the longest sequence's on average.
-inline int shared_plan_clusters(int held, int n, int n_tok, int cells, int beside, long long most) {
+// A launch that runs beside another: its CTAs, or pairs of CTAs; how many of them a pair of SMs that the other leaves holds at
+// once; and what they take then, on average and at most, in units of a tile's time.
+struct Beside {
+  long long ctas;
+  int held;
+  double each, longest;
+};
+
+// prefix_own_kernel's CTAs, `ctas` of them, two on an SM, each over `cells` own cells of the longest sequence and 0.6 of that on average
+// (fitted to what twelve calls of 16-250 tokens took with 5 to 19 numbers of clusters each: on average 2% over the best of them).
+inline Beside beside_own(long long ctas, int cells) {
+  return {ctas, 4, 2.0 * (0.8 + 0.0105 * 0.6 * cells), 2.0 * (0.8 + 0.0105 * cells)};
+}
+// The tensor-core kernel's pairs over the own cells.
+inline Beside beside_own_parts(int n_seq, int n_tok, int cells, int runs) {
+  const long long rows = (long long)n_tok * kPlanHeads;
+  const long long even = n_seq * ((rows + (long long)n_seq * kPlanRows - 1) / ((long long)n_seq * kPlanRows));
+  const double t = 5.0 + (plan_tiles(cells) + runs - 1) / runs;
+  return {even * kPlanGroups * runs, 1, t, t};
+}
+
+// Clusters over the prefixes' cells, `cells` of the longest, and of the SMs that they leave, which the own cells' launch `o` takes at
+// once (the others when this launch ends): with too many of them the own cells' last CTAs start late, and end late.
+// The device, which knows how many cells each prefix has, shares the clusters out so that no run has more tiles than it must
+// (prefix_prep_kernel).  us by the clusters that are used, one prefix of 6,000 cells, own cells 100-400: 64 tokens of a sequence each 36: 32,
+// 42: 31, 54: 32, 60: 39, 72: 41; 250 tokens 24: 105, 48: 70, 72: 76; 4 sequences of 8 tokens 36: 29, 48: 27, 60: 28, 64: 36, 80: 36.
+inline int shared_plan_clusters(int held, int n, int n_tok, int cells, const Beside& o, long long most) {
   const long long rows = (long long)n_tok * kPlanHeads, blocks = tree_blocks_most(n, n_tok);
   const long long even = std::min(blocks, (rows + kPlanRows - 1) / kPlanRows + (n - 1) / 2);
+  const long long least = blocks * kPlanGroups, a_run = n == 1 ? even * kPlanGroups : least;  // clusters that a run of every block takes
   const int tiles = plan_tiles(cells);
-  const double total = (double)(even * kPlanGroups) * tiles * (n == 1 ? 1.0 : 0.6);  // tiles of all blocks
-  const double other = (double)n_tok * kPlanGroups * (beside > 0 ? 1.5 * ((beside + 511) / 512) + 0.6 * 0.0105 * beside : 0.0);
-  const long long least = blocks * kPlanGroups;
-  const long long last = std::min<long long>(most, std::min<long long>(4LL * held, even * kPlanGroups * std::min(kMaxRuns, tiles)));
+  const double total = 0.6 * (double)(even * kPlanGroups) * tiles;  // tiles of several prefixes' blocks, and of the longest's 0.85 of the longest
+  const long long last = std::min<long long>(most, std::min<long long>(4LL * held, a_run * std::min(kMaxRuns, tiles)));
   long long best = least;
   double best_t = 0.0;
   for (long long c = least; c <= std::max(least, last); ++c) {
-    const double waves = std::ceil((double)c / held), run = std::ceil(total / (double)c);
-    double t = waves * (5.0 + run);
-    t += std::max(0.0, other - (waves * held - c) * 2.0 * t / waves) / (2.0 * held) + kJoinPart * c;
-    if (c == least || t < best_t) {
+    const long long runs = std::max(1LL, c / a_run);
+    const double used = n == 1 ? (double)(runs * a_run) : (double)c, waves = std::ceil(used / held);
+    const double run = n == 1 ? std::ceil((double)tiles / runs) : std::max(std::ceil(total / used), std::ceil(0.85 * tiles / runs));
+    const double t = waves * (5.0 + run), at_once = o.held * std::max(0.0, held - used);
+    double start = 0.0;  // of the own cells' last CTA
+    if (at_once < o.ctas) {
+      if (at_once > 0.0) start = (o.ctas / at_once - 1.0) * o.each;
+      if (at_once <= 0.0 || start > t) {
+        const double left = o.ctas - at_once * (1.0 + t / o.each);  // when this launch ends
+        start = t + std::max(0.0, left - o.held * std::min(used, (double)held)) / (o.held * held) * o.each;
+      }
+    }
+    const double all = std::max(t, o.ctas > 0 ? start + o.longest : 0.0) + kJoinPart * used;
+    if (c == least || all < best_t) {
       best = c;
-      best_t = t;
+      best_t = all;
     }
   }
   return (int)best;
