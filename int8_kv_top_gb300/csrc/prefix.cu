@@ -826,10 +826,10 @@ __global__ void __launch_bounds__(JoinShape<kSlices>::kThreads) prefix_join_kern
 // ---------------------------------------------------------------- the call
 // Up to how many own cells (about) of a token or two a sequence the top-k kernel scores them itself.
 constexpr int kOwnInTopk = 2048;
-// From how many tokens a sequence (on average) their own cells go to the tensor-core kernel.  40 sequences behind 6,000 cells with
-// 50, 300, 1,000, 2,000 own cells, us on prefix_own_kernel / the tensor cores: 3 tokens each 43/50, 54/55, 66/66, 112/102; 4 tokens
-// 53/58, 58/62, 111/73, 126/107; 6 tokens 71/71, 111/75, 115/88, 177/113.
-constexpr int kOwnTokens = 4;
+// From how many tokens a sequence (on average) their own cells go to the tensor-core kernel: five, or four with many own cells.  40
+// sequences behind 6,000 cells with 50, 300, 1,000, 2,000 own cells, all attended to, us on prefix_own_kernel / the tensor cores: 3 tokens
+// each 38/47, 47/53, 66/68, 98/95; 4 tokens 47/49, 49/58, 82/63, 119/94; 5 tokens 53/58, 61/62, 97/83, 140/97; 6 tokens 60/63, 75/64, 112/80, 165/103.
+constexpr int kOwnTokens = 4, kManyOwnCells = 512;
 // Up to how many tokens times prefix cells prefix_own_kernel takes the prefixes' cells too: it reads and multiplies them
 // again for every token, but the tensor-core kernel takes 11 us for the first tile and a join of 5.  Own cells 50-150; us with
 // prefix_own_kernel alone / with both: 1 token behind 250 cells 10/16, behind 2,000 15/19, 16,000 24/28; 8 tokens behind 250 11/17, 2,000
@@ -943,7 +943,7 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   const bool select = b.max_n_kv > b.identity_max;
   // own cells of a sequence, for the shapes of launches (any number gives the same results): what the longest prefix leaves
   const int own_cells = std::max(std::min(b.max_n_kv, 128), b.max_n_kv - b.max_prefix);
-  const bool shared = b.n_prefix > 0 && b.max_prefix > 0, own_dense = (long long)b.n_tok >= (long long)kOwnTokens * b.n_seq;
+  const bool shared = b.n_prefix > 0 && b.max_prefix > 0, own_dense = b.n_tok >= (long long)(own_cells > kManyOwnCells ? kOwnTokens : kOwnTokens + 1) * b.n_seq;
   const bool few = shared && !own_dense && (long long)b.n_tok * b.max_prefix <= kFewCells, dense = shared && !few;
   TreeSelect w{};
   int own_chunks = 1;
