@@ -15,7 +15,7 @@
 //
 // Measured (GB300; replayed graphs over warm caches): 64 tokens behind 30,000 cells, all attended to, own cells 100-600: 64 us, of
 // which the tensor-core tiles' operations would take 24 at cuBLAS's rate; 48 tokens behind 16,000 that select 2,048 of
-// them each: 80 us; 40 sequences of 1-16 tokens behind three prompts of 900-12,000: 157 us; 8 tokens behind 1,800: 13 us.
+// them each: 80 us; 40 sequences of 1-16 tokens behind three prompts of 900-12,000: 145 us; 8 tokens behind 1,800: 13 us.
 //
 // Selection (n_kv > identity_max) shares the prefix's codes in the same way: tree_select.cu scores them once for all
 // tokens behind the prefix and each sequence's own cells for its tokens, into rows of columns {prefix cells, gap up to a
@@ -943,7 +943,8 @@ cudaError_t launch_prefix_attention(const TreeBatch& batch, const __half* q, con
   const bool select = b.max_n_kv > b.identity_max;
   // own cells of a sequence, for the shapes of launches (any number gives the same results): what the longest prefix leaves
   const int own_cells = std::max(std::min(b.max_n_kv, 128), b.max_n_kv - b.max_prefix);
-  const bool shared = b.n_prefix > 0 && b.max_prefix > 0, own_dense = b.n_tok >= (long long)(own_cells > kManyOwnCells ? kOwnTokens : kOwnTokens + 1) * b.n_seq;
+  const bool shared = b.n_prefix > 0 && b.max_prefix > 0;
+  const bool own_dense = b.n_tok >= (long long)(own_cells > kManyOwnCells ? kOwnTokens : kOwnTokens + 1) * b.n_seq;
   const bool few = shared && !own_dense && (long long)b.n_tok * b.max_prefix <= kFewCells, dense = shared && !few;
   TreeSelect w{};
   int own_chunks = 1;
