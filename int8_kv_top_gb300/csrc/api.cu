@@ -776,6 +776,7 @@ int qsa_cache_copy(int8_t* kq, uint16_t* ksc, int8_t* vq, uint16_t* vsc, int64_t
   if (n_run < 0) return fail(QSA_ERR_INVALID_ARG, "n_run must be >= 0 (got %d)", n_run);
   if (n_run > kTreeMost) return fail(QSA_ERR_UNSUPPORTED, "n_run must be at most %d (got %d)", kTreeMost, n_run);
   if (max_cells < 0) return fail(QSA_ERR_INVALID_ARG, "max_cells must be >= 0 (got %d)", max_cells);
+  if (n_pool == 0 && max_cells == 0) return ok();  // nothing to copy, in a pool of no cells
   if (n_pool <= 0 || n_pool > 0x7fffffffLL)
     return fail(QSA_ERR_INVALID_ARG, "n_pool must be in [1, 2^31) (got %lld)", (long long)n_pool);
   if (n_run == 0 || max_cells == 0) return ok();

@@ -199,3 +199,8 @@ def test_workspaces_on_the_cpu_are_refused(fake):
     assert "ws" in refused(qsa.qsa_prefix_attention, FAKE, FAKE, FAKE, FAKE, FAKE, 9, None, 0, FAKE, 2, 2, None, 0, 5, None, FAKE, torch.zeros(99))
     assert "path" in refused(qsa.qsa_tree_verify, FAKE, None, V, FAKE, FAKE, FAKE, FAKE, FAKE, 2, N, ints(8), FAKE, FAKE)
     assert fake == {}
+
+
+def test_nothing_to_copy_in_a_pool_without_cells(lib):
+    assert call(lib.qsa_cache_copy, COPY, n_pool=0, max_cells=0, kq=None, ksc=None, vq=None, vsc=None) == 0
+    assert call(lib.qsa_cache_copy, COPY, n_pool=0) == qsa.QSA_ERR_INVALID_ARG
