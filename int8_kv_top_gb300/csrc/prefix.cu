@@ -29,28 +29,11 @@ namespace qsa {
 namespace {
 
 // ---------------------------------------------------------------- 1. records, queries' sums, maxima
-// What the later launches need of a token besides its record (TreeBatch::tok): its sequence's {first pool cell, committed own
-// cells, tokens, first token row}.
-struct TokMore {
-  int4 seq;
-};
-
 // The tables' first rows and first sequences, in shared memory where they are short, and what is looked up in them.
 constexpr int kNearSeqs = 1024, kNearPrefixes = 256;
 struct Finder {
   const TreeBatch& b;
   const int *row, *seq;  // shared memory, or null
-  // The last of n whose key is not above `at`.
-  template <class Key>
-  __device__ __forceinline__ static int last_at(int n, int at, Key key) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (key(mid) <= at) lo = mid;
-      else hi = mid - 1;
-    }
-    return lo;
-  }
   __device__ __forceinline__ Finder(const TreeBatch& batch, int* room, int tid, int threads) : b(batch) {
     row = b.n_seq <= kNearSeqs ? room : nullptr;
     seq = b.n_prefix <= kNearPrefixes ? room + kNearSeqs : nullptr;
@@ -65,13 +48,7 @@ struct Finder {
   // Token t's record; its `more` is written where the record is that of a valid sequence.
   __device__ __forceinline__ int4 record(int t, TokMore* more) const {
     const int s = row ? last_at(b.n_seq, t, [&](int i) { return row[i]; }) : last_at(b.n_seq, t, [&](int i) { return __ldg(&b.seqs[i].w); });
-    const int p = prefix_at(s);
-    const SharedSeq v = shared_seq(b, s, p);
-    if (v.T <= 0 || t < v.e.w || t >= v.e.w + v.T) return make_int4(-1, 0, 0, -1);
-    int seen = v.pe.y + v.e.z;
-    for (int i = 0; 32 * i < v.T; ++i) seen += __popc(shared_mask_word(b, t, t - v.e.w, i, v.T));
-    *more = TokMore{make_int4(v.e.x, v.e.z, v.T, v.e.w)};
-    return make_int4(s, seen, v.pe.y, p);
+    return shared_record(b, t, s, prefix_at(s), more);
   }
 };
 
@@ -307,15 +284,6 @@ struct OwnArgs {
   float* o;              // else unmerged rows [n_tok][2][S][kHPG][kD], and their (m, l) [n_tok][2][S][kHPG]
   float2* ml;
 };
-
-// Where row R of T tokens' (12 a token) lies among the parts: CTA of run 0, and row of that CTA.  first: their first pair.
-__device__ __forceinline__ void part_row(long long first, int T, int g, int runs, int R, size_t* cta, int* row) {
-  const int k = R / kTreeBlock, r = R % kTreeBlock;
-  const int n = min(kTreeBlock, T * kHPG - k * kTreeBlock), half_rows = (n + 1) / 2;
-  const int half = r >= half_rows;
-  *cta = ((size_t)first + (size_t)(k * kGroups + g) * runs) * 2 + half;
-  *row = half ? r - half_rows : r;
-}
 
 // S CTAs a (token, group), an S-th of its tiles of 16 cells each.  The warps take the tiles in turn, each through a ring of its own:
 //   S = Q K^T  (A = 16 rows of Q, 12 of them heads; B = K^, two n8 tiles), 16 k16 steps

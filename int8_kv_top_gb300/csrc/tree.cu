@@ -134,6 +134,7 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
                                                  int clusters = 0) {
   BlockAt x;
   bool here;
+  int sq = 0;
   if (kOf == kTreeCells && plan != nullptr) {
     const int4 head = __ldg(&plan[0]), at = __ldg(&plan[1 + 2 * blk]);
     x.row0 = __ldg(&plan[2 + 2 * blk].x);
@@ -141,7 +142,6 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
     x.e = make_int4(at.x, 0, at.y, at.w);
     x.T = at.z;
   } else {
-    int sq;
     if constexpr (kOf == kPrefixCells) {
       // `blk` is the cluster's index and `plan` the prefixes' clusters
       int4 at, pe;
@@ -152,7 +152,6 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
         pe = __ldg(&b.prefixes[sq]);
         all = __ldg(&plan[b.n_prefix].x);
       } else {
-        sq = 0;
         const int T = prefix_tokens(b, 0, &pe);
         at = only_prefix_plan(pe.w, T, pe.y, clusters);
         all = (at.w * kHPG + kTreeBlock - 1) / kTreeBlock * kGroups * at.y;
@@ -189,7 +188,7 @@ __device__ __forceinline__ BlockAt tree_block_at(const TreeBatch& b, const int4*
     return x;
   }
   if constexpr (kOf != kTreeCells) {
-    const int4 t = live ? __ldcg(&b.tok[x.e.w + tok]) : make_int4(-1, 0, 0, 0);
+    const int4 t = live ? record_in(b, kOf, sq, x.e.w + tok) : make_int4(-1, 0, 0, 0);
     x.ours = t.x >= 0;
     x.sel = x.ours && t.y > b.identity_max;
     return x;

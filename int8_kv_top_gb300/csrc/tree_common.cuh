@@ -3,112 +3,13 @@
 #pragma once
 #include "common.cuh"
 #include "tree_plan.cuh"
+#include "tree_tables.cuh"
 
 namespace qsa {
 
 // The two halves of a cluster barrier, executed by every thread of the cluster once per phase.
 __device__ __forceinline__ void cluster_arrive_all() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait_all() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
-struct TreeBatch {
-  const int4* seqs;  // per sequence {first pool cell, n_cells, pos0, first token row}
-  long long n_pool;
-  int n_seq, n_tok;
-  const uint32_t* tree;  // [n_tok][tree_words]; of a shared call null as well: causal
-  int tree_words, max_n_kv, identity_max;
-  // shared calls (qsa_prefix_attention) alone; max_n_kv then counts the prefix's cells too
-  const int4* prefixes = nullptr;  // per prefix {first pool cell, cells, first sequence, -}
-  int n_prefix = 0, max_prefix = 0;
-  int4* tok = nullptr;             // per token {sequence or -1, n_kv, prefix cells, prefix}: made by the call's first launch
-};
-
-// What a kernel that serves both kinds of calls works on: a tree call's sequences; the prefixes of a shared call, each
-// a sequence of committed cells whose tokens are those of all its sequences; the own cells of a shared call's sequences.
-enum CellsOf { kTreeCells, kPrefixCells, kOwnCells };
-
-// Sequence s's token count, or -1 when its entry breaks the contract; a padding sequence (no cells) has none.
-__device__ __forceinline__ int tree_seq_tokens(const TreeBatch& b, int s, int4* e_out) {
-  const int4 e = __ldg(&b.seqs[s]);
-  const int next = s + 1 < b.n_seq ? __ldg(&b.seqs[s + 1].w) : b.n_tok;
-  *e_out = e;
-  const bool rows_ok = (s == 0 ? e.w == 0 : e.w >= 0) && next >= e.w && next <= b.n_tok;
-  if (rows_ok && e.y == 0) return 0;
-  const long long T = (long long)next - e.w, end = (long long)e.z + T;
-  const bool ok = rows_ok && e.x >= 0 && e.y >= 1 && e.z >= 0 && end <= e.y && (long long)e.x + e.y <= b.n_pool &&
-                  end <= b.max_n_kv && T <= 32 * b.tree_words;
-  return ok ? (int)T : -1;
-}
-
-// Word w of token row's mask, with the bits past the sequence's T drafted tokens cleared.
-__device__ __forceinline__ uint32_t tree_mask_word(const TreeBatch& b, int row, int w, int T) {
-  const int left = T - 32 * w;
-  if (w >= b.tree_words || left <= 0) return 0u;
-  const uint32_t m = __ldg(b.tree + (size_t)row * b.tree_words + w);
-  return left >= 32 ? m : m & ((1u << left) - 1u);
-}
-
-// ---------------------------------------------------------------- shared calls
-// Prefix p: its tokens (rows of all its sequences), or -1 when its entry breaks the contract; *e_out = {first pool cell,
-// cells, first sequence, first token row}.
-__device__ __forceinline__ int prefix_tokens(const TreeBatch& b, int p, int4* e_out) {
-  int4 e = __ldg(&b.prefixes[p]);
-  const int next = p + 1 < b.n_prefix ? __ldg(&b.prefixes[p + 1].z) : b.n_seq;
-  const bool seqs_ok = (p == 0 ? e.z == 0 : e.z >= 0) && next >= e.z && next <= b.n_seq;
-  const int row0 = seqs_ok && e.z < b.n_seq ? __ldg(&b.seqs[e.z].w) : b.n_tok;
-  const int row1 = seqs_ok && next < b.n_seq ? __ldg(&b.seqs[next].w) : b.n_tok;
-  e.w = row0;
-  *e_out = e;
-  const bool ok = seqs_ok && row0 >= 0 && row1 >= row0 && row1 <= b.n_tok && e.x >= 0 && e.y >= 0 && e.y <= b.max_prefix &&
-                  (long long)e.x + e.y <= b.n_pool;
-  return ok ? row1 - row0 : -1;
-}
-
-// The prefix of sequence s (the last whose first sequence is not behind s); -1 without prefixes.
-__device__ __forceinline__ int prefix_of(const TreeBatch& b, int s) {
-  if (b.n_prefix == 0) return -1;
-  int lo = 0, hi = b.n_prefix - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(&b.prefixes[mid].z) <= s) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
-// A shared call's sequence, behind prefix p (-1: none): its entry, tokens as in tree_seq_tokens, and the prefix's tokens
-// and {first pool cell, cells, first sequence, first token row}.
-struct SharedSeq {
-  int4 e, pe;
-  int T, pT;
-};
-__device__ __forceinline__ SharedSeq shared_seq(const TreeBatch& b, int s, int p) {
-  SharedSeq x;
-  x.e = __ldg(&b.seqs[s]);
-  const int next = s + 1 < b.n_seq ? __ldg(&b.seqs[s + 1].w) : b.n_tok;
-  x.pe = make_int4(0, 0, 0, 0);
-  x.pT = p < 0 ? 0 : prefix_tokens(b, p, &x.pe);
-  const bool rows_ok = (s == 0 ? x.e.w == 0 : x.e.w >= 0) && next >= x.e.w && next <= b.n_tok;
-  const long long T = (long long)next - x.e.w, end = (long long)x.e.z + T;
-  const bool ok = x.pT >= 0 && rows_ok && x.e.x >= 0 && x.e.y >= 1 && x.e.z >= 0 && end <= x.e.y &&
-                  (long long)x.e.x + x.e.y <= b.n_pool && x.pe.y + end <= b.max_n_kv && T <= 32 * (b.tree ? b.tree_words : kTreeWords);
-  x.T = rows_ok && x.e.y == 0 ? 0 : ok ? (int)T : -1;
-  return x;
-}
-__device__ __forceinline__ int shared_seq_tokens(const TreeBatch& b, int s, int4* e_out) {
-  const SharedSeq x = shared_seq(b, s, prefix_of(b, s));
-  *e_out = x.e;
-  return x.T;
-}
-
-// Word w of the mask of token i (row `row`) of a shared call's sequence of T tokens.
-__device__ __forceinline__ uint32_t shared_mask_word(const TreeBatch& b, int row, int i, int w, int T) {
-  if (b.tree != nullptr) return tree_mask_word(b, row, w, T);
-  const int n = i + 1 - 32 * w;  // causal
-  return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
-}
-
-// Columns of a shared call's rows of scores and selected cells: the prefix's cells, a gap up to a whole tile, the own cells.
-__device__ __forceinline__ int own_column(int prefix_cells) { return (prefix_cells + 127) & ~127; }
 
 // The last sequence whose key(s) is not above `at`, by a whole warp (32 probes a step); key is increasing and
 // key(0) is at most `at` in a valid table (else some sequence, whose entry the caller checks).
@@ -197,37 +98,8 @@ __device__ __forceinline__ float tree_row_scale(const float* eh, const float (&k
 }
 
 // ---------------------------------------------------------------- blocks of an attention launch
-constexpr int kTileCells = 128;    // cells of a tile
-constexpr int kTreeBlock = 256;    // (token, head) rows of a block: a CTA pair's UMMA M
 constexpr int kPlanSeqs = 8;       // sequences from which on a launch takes its blocks from a list, longest first
 constexpr int kPlanThreads = 256;
-
-// Rows of a block that exist are shared out evenly: its CTA `half` of each pair has rows [x, x + n) of the tree, so
-// that the loads of Q and the stores of O, 1 KB a row, are halved where a block is not full.
-__device__ __forceinline__ int cta_rows(int T, int blk_row0, int half, int* x) {
-  const int n = min(kTreeBlock, T * kHPG - blk_row0), first = (n + 1) / 2;
-  *x = blk_row0 + half * first;
-  return half ? n - first : first;
-}
-
-// The clusters of a shared call's only prefix, of T tokens and `cells` cells, as plan_prefixes (prefix.cu) shares them out:
-// {first, runs a block and group, first token row, tokens}.
-__device__ __forceinline__ int4 only_prefix_plan(int row0, int T, int cells, int clusters) {
-  const int tiles = (cells + kTileCells - 1) / kTileCells, blocks = (T * kHPG + kTreeBlock - 1) / kTreeBlock * kGroups;
-  if (T <= 0 || tiles == 0) return make_int4(0, 0, row0, max(T, 0));
-  const int most = max(1, min(min(clusters / blocks, kMaxRuns), tiles)), L = (tiles + most - 1) / most;
-  return make_int4(0, (tiles + L - 1) / L, row0, T);
-}
-
-// Runs of a block and group of a shared call over n_tiles tiles: as many of run_tiles as it takes, `runs` at most.
-__device__ __forceinline__ int shared_runs(int n_tiles, int runs, int run_tiles) {
-  return max(1, min(runs, (n_tiles + run_tiles - 1) / run_tiles));
-}
-
-// Index of a sequence's first block in the grid: block k of sequence s has index first_block(s) + k.
-// The sequences' ranges never meet, since floor((a + b) / 256) + 1 >= floor(a / 256) + ceil(b / 256), so
-// a block finds its sequence by a search over the table, without a prefix sum; some indices stay unused.
-__device__ __forceinline__ long long first_block(long long first_row, int s) { return first_row * kHPG / kTreeBlock + s; }
 
 // The list, by one CTA of kPlanThreads: plan[0].x blocks, then for block i plan[1 + 2 i] = {first pool cell,
 // committed cells, drafted tokens, first token row} of its sequence and plan[2 + 2 i].x = its first row, in decreasing

@@ -28,8 +28,6 @@
 namespace qsa {
 namespace {
 
-constexpr int kTokChunk = 32;  // tokens per score CTA: UMMA N is at most twice that
-
 // ---------------------------------------------------------------- 1. prep
 // Blocks [0, 2 n_tok): (token row, group), thread = dim.  Blocks behind them: (sequence, chunk of cells); then, where
 // a plan is wanted, one that lists the attention's blocks.
@@ -137,9 +135,6 @@ struct __align__(8) TreeScoreBars {
   uint64_t full[kTileStages], empty[kTileStages], acc_full[2], acc_empty[2], b_full, tmem_ready, drain;
 };
 
-// First token chunk of a sequence: as first_block in tree.cu, for chunks of 32 tokens.
-__device__ __forceinline__ long long first_chunk(long long first_row, int s) { return first_row / kTokChunk + s; }
-
 // Of a shared call: CTAs over the prefixes' cells, for the tokens of all their sequences, and behind them CTAs over each
 // sequence's own cells, in one launch (two launches of few CTAs each took 30 us, 48 chats of 475 own cells behind 16,000).  How
 // many cells there are the host does not know, so a chunk's CTAs share its tiles evenly.
@@ -201,9 +196,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   }
   if (T <= 0 || kc < 0 || kc * kTokChunk >= T || J <= 0) return;  // uniform
   if (!kShared && n_scan <= b.identity_max) return;
+  const CellsOf of = !kShared ? kTreeCells : prefix ? kPrefixCells : kOwnCells;
   if constexpr (kShared) {  // no token of the chunk selects
     const int i = (int)kc * kTokChunk + lane;
-    const int4 ti = i < T ? __ldg(&b.tok[e4.w + i]) : make_int4(-1, 0, 0, 0);
+    const int4 ti = i < T ? record_in(b, of, sq, e4.w + i) : make_int4(-1, 0, 0, 0);
     if (!__any_sync(0xffffffffu, ti.x >= 0 && ti.y > b.identity_max)) return;  // the same in every warp
   }
   const int t0 = e4.w + (int)kc * kTokChunk;  // first token row
@@ -301,7 +297,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       } else {
         // km: the prefix's maxima, the same for all tokens here, and each token's own sequence's
         float km[kNB] = {0.f, 0.f, 0.f, 0.f};
-        const int4 ti = lane < n_here ? __ldg(&b.tok[t0 + lane]) : make_int4(-1, 0, 0, -1);
+        const int4 ti = lane < n_here ? record_in(b, of, sq, t0 + lane) : make_int4(-1, 0, 0, -1);
         const int one = max(__ffs(__ballot_sync(0xffffffffu, ti.x >= 0)) - 1, 0);
         const int p = __shfl_sync(0xffffffffu, ti.w, one), cells = __shfl_sync(0xffffffffu, ti.z, one);
         if (p >= 0) {
@@ -333,7 +329,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     };
     uint2 sw_next = scales_of(0);
     __half* dst0 = w.scores + (size_t)(g * b.n_tok + t0 + n0) * w.pitch;
-    if (kShared && !prefix) dst0 += own_column(__ldg(&b.tok[t0]).z);
+    if (kShared) dst0 += score_column(b, of, sq, t0);
     for (int j = 0; t_ok && j < J; ++j) {
       const int buf = j & 1, cell = (j_begin + j) * kTileCells + quarter * 32 + lane, dj = cell - pos0;
       const uint2 sw = sw_next;
