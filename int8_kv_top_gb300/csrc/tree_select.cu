@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     z = i / xs / kGroups;
   }
   int sq, T, drafted;  // of the sequence, or of the prefix: tokens; cells behind the committed ones
+  int behind = 0;      // cells of the sequence's prefix
   int4 e4;
   if (kShared && prefix) {
     int4 pe;
@@ -181,7 +182,14 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     drafted = 0;
   } else {
     sq = warp_find_seq(b.n_seq, z, [&](int i) { return first_chunk(__ldg(&b.seqs[i].w), i); });
-    T = kShared ? shared_seq_tokens(b, sq, &e4) : tree_seq_tokens(b, sq, &e4);
+    if constexpr (kShared) {
+      const SharedSeq v = shared_seq(b, sq, prefix_of(b, sq));
+      T = v.T;
+      e4 = v.e;
+      behind = v.pe.y;
+    } else {
+      T = tree_seq_tokens(b, sq, &e4);
+    }
     drafted = T;
   }
   const long long kc = (long long)z - first_chunk(e4.w, sq);
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     };
     uint2 sw_next = scales_of(0);
     __half* dst0 = w.scores + (size_t)(g * b.n_tok + t0 + n0) * w.pitch;
-    if (kShared) dst0 += score_column(b, of, sq, t0);
+    if (kShared) dst0 += score_column(of, behind);
     for (int j = 0; t_ok && j < J; ++j) {
       const int buf = j & 1, cell = (j_begin + j) * kTileCells + quarter * 32 + lane, dj = cell - pos0;
       const uint2 sw = sw_next;

@@ -127,13 +127,16 @@ __device__ __forceinline__ int4 shared_record(const TreeBatch& b, int t, int s, 
   return make_int4(s, seen, v.pe.y, p);
 }
 
-// Token row's record, as a launch over the cells of prefix or sequence i (kOwnCells) takes it.
-__device__ __forceinline__ int4 record_in(const TreeBatch& b, CellsOf of, int i, int row) { return __ldcg(&b.tok[row]); }
-
-// The column of a row of scores at which the cells of prefix or sequence i begin, i's first token here being row t0.
-__device__ __forceinline__ int score_column(const TreeBatch& b, CellsOf of, int i, int t0) {
-  return of == kPrefixCells ? 0 : own_column(__ldcg(&b.tok[t0]).z);
+// Token row's record, as a launch over the cells of prefix or sequence i (kOwnCells) takes it: none where the token is
+// another's.  First rows that run backwards give a row to several sequences, of which its record names one, and the others'
+// cells and columns are not those that its rows of scores and selected cells are made for.
+__device__ __forceinline__ int4 record_in(const TreeBatch& b, CellsOf of, int i, int row) {
+  const int4 ti = __ldcg(&b.tok[row]);
+  return (of == kPrefixCells ? ti.w : ti.x) == i ? ti : make_int4(-1, 0, 0, -1);
 }
+
+// The column of a row of scores at which the cells of a prefix, or a sequence's own ones behind prefix_cells, begin.
+__device__ __forceinline__ int score_column(CellsOf of, int prefix_cells) { return of == kPrefixCells ? 0 : own_column(prefix_cells); }
 
 // ---------------------------------------------------------------- blocks of an attention launch
 constexpr int kTileCells = 128;    // cells of a tile
