@@ -117,10 +117,11 @@ struct TokMore {
   int4 seq;
 };
 
-// Token t's record (TreeBatch::tok), of sequence s behind prefix p; `more` is written where it is a valid sequence's.
+// Token t's record (TreeBatch::tok), of sequence s behind prefix p; `more` is written where it is a valid sequence's.  Where
+// rows or first sequences run backwards, a sequence's rows may lie outside its prefix's, where the prefix's parts have none for it.
 __device__ __forceinline__ int4 shared_record(const TreeBatch& b, int t, int s, int p, TokMore* more) {
   const SharedSeq v = shared_seq(b, s, p);
-  if (v.T <= 0 || t < v.e.w || t >= v.e.w + v.T) return make_int4(-1, 0, 0, -1);
+  if (v.T <= 0 || t < v.e.w || t >= v.e.w + v.T || (p >= 0 && (t < v.pe.w || t >= v.pe.w + v.pT))) return make_int4(-1, 0, 0, -1);
   int seen = v.pe.y + v.e.z;
   for (int i = 0; 32 * i < v.T; ++i) seen += __popc(shared_mask_word(b, t, t - v.e.w, i, v.T));
   *more = TokMore{make_int4(v.e.x, v.e.z, v.T, v.e.w)};

@@ -151,6 +151,11 @@ def test_broken_tables_store_and_read_rows_inside(outside, how):
     assert not broken(outside, how) & {1, 2, 3, 4, 7}
 
 
+@pytest.mark.parametrize("how", ["rows in any order", "rows of any value", "first sequences too", "entries of any value"])
+def test_broken_tables_join_parts_that_are_there(outside, how):
+    assert broken(outside, how) == {0}
+
+
 def broken(outside, how):
     """What is outside, over tables that break the contract."""
     rng = np.random.default_rng(7)
