@@ -755,9 +755,16 @@ __global__ void __launch_bounds__(kThr, (V <= 64 && kThr == kTkThreads ? 2 : 1))
   constexpr int nwarps = kThr / 32;
   const int t = t_sel + r;
   int n_kv = pos0 + t + 1;  // cells of the row
-  const __half* row = scores + ((size_t)g * T_sel + r) * n_pad;
+  // of a shared call this CTA may write the row itself, so it is read through the pointer that is written
+  const __half* row = (kShared ? ts.scores : scores) + ((size_t)g * T_sel + r) * n_pad;
   float row_scale = 1.f;    // of the stored scores
   float km[kNB];
+  auto score_bits = [&](int c) -> uint16_t {
+    uint16_t x;
+    if constexpr (kShared) asm volatile("ld.global.b16 %0, [%1];" : "=h"(x) : "l"(row + c) : "memory");  // coherent
+    else x = __half_as_ushort(row[c]);
+    return x;
+  };
   int shared = 0, gap = 0;        // kShared: the prefix's cells, and the columns between them and the own ones
   long long cell0 = 0, own0 = 0;  // pool cells of column 0 and, of the own columns, of column 0 continued backwards
   auto pool_cell = [&](int c) -> size_t { return kShared ? (size_t)(c + (c < shared ? cell0 : own0)) : (size_t)c; };
@@ -1018,11 +1025,11 @@ __global__ void __launch_bounds__(kThr, (V <= 64 && kThr == kTkThreads ? 2 : 1))
       __syncthreads();
       b2 = find_bin_desc(s_hist + 256, K - ab1, &ab2, s_tmp);
     } else {
-      for (int c = tid; c < n_kv; c += kThr) atomicAdd(&s_hist[fp16_order_key(__half_as_ushort(row[c])) >> 8], 1u);
+      for (int c = tid; c < n_kv; c += kThr) atomicAdd(&s_hist[fp16_order_key(score_bits(c)) >> 8], 1u);
       __syncthreads();
       b1 = find_bin_desc(s_hist, K, &ab1, s_tmp);
       for (int c = tid; c < n_kv; c += kThr) {
-        const uint32_t k = fp16_order_key(__half_as_ushort(row[c]));
+        const uint32_t k = fp16_order_key(score_bits(c));
         if ((int)(k >> 8) == b1) atomicAdd(&s_hist[256 + (k & 0xFFu)], 1u);
       }
       __syncthreads();
@@ -1155,7 +1162,7 @@ __global__ void __launch_bounds__(kThr, (V <= 64 && kThr == kTkThreads ? 2 : 1))
     // large band (many near-ties): exact radix select over the band, keys recomputed per
     // pass, 16 passes of 8 bits over the biased 128-bit key (cells read from the score row)
     auto in_band = [&](int c) -> bool {
-      const uint32_t k = fp16_order_key(__half_as_ushort(row[c]));
+      const uint32_t k = fp16_order_key(score_bits(c));
       return k >= k_band && k < k_def;
     };
     auto bkey = [&](int c) -> unsigned __int128 {
