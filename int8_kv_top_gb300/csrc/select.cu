@@ -722,8 +722,8 @@ __device__ uint32_t first_key_warp(P pred) {
 //
 // kTree: rows are the drafted tokens of a tree batch (row, group); the scores of cells that a token does not
 // see are -inf, its selected cells go to a bitmap as well, and `ids` may be null.
-// kShared: the rows of a shared call (qsa_prefix_attention): columns are the prefix's cells, a gap of -inf up to a whole
-// tile, and the sequence's own cells.
+// kShared: the rows of a shared call (qsa_prefix_attention): columns are the prefix's cells, a gap up to a whole tile, and the
+// sequence's own cells.  The gap, which no launch writes, reads as -inf.
 // kThr threads of V columns each.
 template <int V, bool kTree, bool kShared = false, int kThr = kTkThreads>
 __global__ void __launch_bounds__(kThr, (V <= 64 && kThr == kTkThreads ? 2 : 1))
@@ -759,14 +759,16 @@ __global__ void __launch_bounds__(kThr, (V <= 64 && kThr == kTkThreads ? 2 : 1))
   const __half* row = (kShared ? ts.scores : scores) + ((size_t)g * T_sel + r) * n_pad;
   float row_scale = 1.f;    // of the stored scores
   float km[kNB];
+  int shared = 0, gap = 0;        // kShared: the prefix's cells, and the columns between them and the own ones
+  long long cell0 = 0, own0 = 0;  // pool cells of column 0 and, of the own columns, of column 0 continued backwards
+  auto in_gap = [&](int c) { return kShared && c >= shared && c < shared + gap; };
   auto score_bits = [&](int c) -> uint16_t {
-    uint16_t x;
+    uint16_t x = 0xFC00u;
+    if (in_gap(c)) return x;
     if constexpr (kShared) asm volatile("ld.global.b16 %0, [%1];" : "=h"(x) : "l"(row + c) : "memory");  // coherent
     else x = __half_as_ushort(row[c]);
     return x;
   };
-  int shared = 0, gap = 0;        // kShared: the prefix's cells, and the columns between them and the own ones
-  long long cell0 = 0, own0 = 0;  // pool cells of column 0 and, of the own columns, of column 0 continued backwards
   auto pool_cell = [&](int c) -> size_t { return kShared ? (size_t)(c + (c < shared ? cell0 : own0)) : (size_t)c; };
   if constexpr (kShared) {
     const int4 ti = __ldg(&tb.tok[t]);
@@ -893,10 +895,10 @@ __global__ void __launch_bounds__(kThr, (V <= 64 && kThr == kTkThreads ? 2 : 1))
                      : "memory");
       else
         x = __ldg(reinterpret_cast<const uint4*>(row + c));
-      if (c + 8 > n_kv) {
+      if (c + 8 > n_kv || (kShared && c + 8 > shared && c < shared + gap)) {
         uint16_t* hh = reinterpret_cast<uint16_t*>(&x);
         for (int j = 0; j < 8; ++j)
-          if (c + j >= n_kv) hh[j] = 0xFC00u;
+          if (c + j >= n_kv || in_gap(c + j)) hh[j] = 0xFC00u;
       }
     }
     w[m] = x;

@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       tc_fence_before();  // the accumulators are in registers
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-      if (n0 >= n16 || (!(kShared && prefix) && cell >= n_scan)) continue;
+      if (n0 >= n16 || cell >= n_scan) continue;
       __half* dst = dst0 + cell;
       const bool tail = (j_begin + j + 1) * kTileCells > pos0;
       const float4* sc4 = reinterpret_cast<const float4*>(s_scale + n0);
@@ -381,10 +381,6 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[i] *= sc[i];
-      if (kShared && prefix && cell >= n_scan) {  // the gap before the own cells' columns
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = -INFINITY;
-      }
       if (!(kShared && prefix) && tail && dj >= 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)

@@ -108,7 +108,8 @@ __device__ __forceinline__ uint32_t shared_mask_word(const TreeBatch& b, int row
   return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1u : 0u;
 }
 
-// Columns of a shared call's rows of scores and selected cells: the prefix's cells, a gap up to a whole tile, the own cells.
+// Columns of a shared call's rows of scores and selected cells: the prefix's cells, a gap up to a whole tile, which holds anything
+// (its cells, counted on from either side, may be outside the pool) and is never read as a score, the own cells.
 __device__ __forceinline__ int own_column(int prefix_cells) { return (prefix_cells + 127) & ~127; }
 
 // What the later launches need of a token besides its record (TreeBatch::tok): its sequence's {first pool cell, committed own

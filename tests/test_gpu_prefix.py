@@ -507,6 +507,43 @@ def test_overlapping_rows_are_flagged_and_harm_nobody_elses_memory():
             assert (ws[need:] == 0x5A).all()
 
 
+@pytest.mark.parametrize("own", [10, 3000])
+def test_broken_orders_leave_ids_that_are_cells(own):
+    # first sequences and first rows that run backwards, over a workspace of large scores: what is selected is among the cells,
+    # once each, and nothing is written around the outputs
+    n, shared = 64, 200
+    b, _, _ = shared_batch([(shared, [(own, 1)] * 2), (90, [(own, 1)] * 10), (300, [(own, 1)] * 52)], 79)
+    rows = 0
+    for how in range(6):
+        seqs, prefixes = b["seqs"].copy(), b["prefixes"].copy()
+        if how < 3:
+            prefixes[1, 2] = (-1, 70, 1)[how]
+            prefixes[2, 2] = (2, 12, 0)[how]
+        elif how < 5:
+            seqs[10:14, 3], seqs[40:45, 3] = ([13, 12, 11, 10], [44, 41, 43, 40, 45]) if how == 3 else ([11, 10, 13, 12], [42] * 5)
+        else:
+            seqs[20, 3] = 1 << 20
+        d = on_gpu({k: v for k, v in b.items() if k in ("q", "kq", "vq", "ksc", "vsc")})
+        s, p = torch.from_numpy(seqs).cuda(), torch.from_numpy(prefixes).cuda()
+        out = torch.full((n + 2, 24, 256), 7.0, dtype=torch.float16, device="cuda")
+        ids = torch.full((n + 2, 2, 40), -7, dtype=torch.int32, device="cuda")
+        most = 300 + own + 1
+        need = qsa.qsa_prefix_attention_workspace_bytes(3, n, n, 300, most, SMALL)
+        ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        qsa.qsa_prefix_attention(d["q"], d["kq"], d["vq"], d["ksc"], d["vsc"], len(b["kq"]), p, 3, s, n, n, None, 300, most, ids[1:], out[1:],
+                                 ws[:need], params=SMALL)
+        with pytest.raises(qsa.QSAError) as e:
+            qsa.qsa_check_device_status()
+        assert e.value.code == qsa.QSA_ERR_DEVICE
+        assert (out[0] == 7).all() and (out[-1] == 7).all() and (ids[0] == -7).all() and (ids[-1] == -7).all()
+        assert (ws[need:] == 0x5A).all()
+        got = ids[1:-1].cpu().numpy()
+        got = got[(got != -7).any(-1)]
+        rows += len(got)
+        assert (got >= 0).all() and (got < most).all() and (np.diff(got, axis=-1) > 0).all(), how
+    assert rows > 100
+
+
 def test_tensors_of_the_wrong_kind_are_refused():
     b, _, _, d, call = device_batch([(20, [(3, 1)])], 51, None)
     for name, bad in (("q", d["q"].float()), ("q", d["q"][:, :, ::2]), ("kq", d["kq"][:-1]), ("vsc", d["vsc"].cpu()), ("seqs", d["seqs"].long()),

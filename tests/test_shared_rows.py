@@ -15,3 +15,13 @@ def test_a_row_that_the_kernel_writes_is_read_through_the_pointer_that_it_writes
     wide = [m.start() for m in re.finditer(r"\(row \+ c\)", plain)]
     assert len(wide) == 2  # eight at once: by ld.global, and by __ldg in calls whose rows another launch has written
     assert "if constexpr (kShared)" in plain[:wide[0]] and "ld.global" in plain[:wide[0]] and "__ldg" in plain[wide[0]:wide[1]]
+
+
+def test_columns_between_the_prefix_and_the_own_cells_are_no_cells():
+    # nobody writes them where a broken table keeps the score kernel from a prefix, and their cells may lie before the pool
+    kernel = body("select.cu", "topk_kernel(const __half* __restrict__ scores")
+    one = kernel[kernel.index("auto score_bits"):]
+    one = one[:one.index("};")]
+    assert one.index("if (in_gap(c)) return") < one.index("ld.global")
+    wide = kernel[kernel.index("uint4 w[V / 8]"):kernel.index("w[m] = x;")]
+    assert "in_gap(c + j)" in wide and "c + 8 > shared && c < shared + gap" in wide
