@@ -126,6 +126,34 @@ def test_equal_scores_go_to_the_lower_cell():
     assert (ids.cpu().numpy() == np.arange(40)).all()
 
 
+@pytest.mark.parametrize("n_seq", [3, 80])  # 1,024 threads a row, and 512
+@pytest.mark.parametrize("shared,own", [(700, 900), (1, 1500), (1280, 300), (1100, 2600)])
+@pytest.mark.parametrize("far", [0, 25])
+def test_many_equal_scores_go_to_the_lower_cells(n_seq, shared, own, far):
+    # one key in every cell, more of them than are ranked one by one: the first topk cells, from the prefix over the gap
+    # into the own ones.  With `far`, that many of the last own cells have a key twice as large, or small: chosen, or not
+    topk = 1200
+    if n_seq > 3:
+        own = own // 3 + 200 if shared > 800 else own
+    b, _, _ = shared_batch([(shared, [(own, 1)] * n_seq)], 14, causal=True)
+    b["kq"][:] = 3
+    b["ksc"][:] = np.where(np.isnan(b["ksc"]), b["ksc"], np.float16(0.01))
+    for first, _, held, _ in b["seqs"]:
+        b["kq"][first + held - far:first + held] = 6
+    ids, _ = run_shared(b, (topk, topk + 50, 1 / 16))
+    qsa.qsa_check_device_status()
+    got = ids.cpu().numpy()
+    n_kv = shared + own + 1
+    up = b["q"].astype(np.float64).reshape(n_seq, 2, 12 * 256).sum(-1) > 0  # the sign of a row's scores
+    lows = np.concatenate([np.arange(shared + own - far), [n_kv - 1]])
+    highs = np.arange(shared + own - far, shared + own)
+    assert n_kv > topk + 50 and len(lows) > topk
+    for t in range(n_seq):
+        for g in range(2):
+            want = np.sort(np.concatenate([highs, lows[:topk - far]])) if up[t, g] else lows[:topk]
+            np.testing.assert_array_equal(got[t, g], want)
+
+
 def test_a_token_that_sees_nothing_gets_zeros():
     b, _, _ = shared_batch([(0, [(0, 2), (0, 1)])], 13)
     b["tree"][:] = [[0], [2], [0]]
