@@ -4,7 +4,7 @@
 // Both are copies bound by memory: a cell is 1,056 bytes (K and V codes, 512 bytes each, and their scales, 16 bytes
 // each), read once and written once.  A warp takes eight cells, all loaded into registers before any is stored: 17 loads of
 // 16 bytes a lane in flight.  Measured (GB300): 96 runs of 40-3,000 cells 45 us, 6.2 TB/s of the 278 MB read and written, 0.92 of a
-// plain copy's rate; 500 runs compacted, 461 MB, 87 us, 5.3 TB/s (flags and the look-up of runs cost the rest); 3 runs of 500 5 us
+// plain copy's rate; 500 runs compacted, 461 MB, 89 us, 5.2 TB/s (flags and the look-up of runs cost the rest); 3 runs of 500 5 us
 // and 8 runs 7-8 us are the latency of one and two launches.
 #include <algorithm>
 
@@ -41,18 +41,6 @@ __device__ __forceinline__ void load_cells(const Pool& p, int64_t from, int lane
   }
   const int64_t y = __shfl_sync(0xffffffffu, from, (lane >> 1) & (N - 1));
   if (lane < 2 * N && y >= 0) c.s = reinterpret_cast<const uint4*>(lane & 1 ? p.vsc : p.ksc)[y];
-}
-// A word that depends on all of them: who has it has them all.
-template <int N>
-__device__ __forceinline__ uint32_t folded(int64_t from, int lane, const Cells<N>& c) {
-  uint32_t x = 0u;
-#pragma unroll
-  for (int u = 0; u < N; ++u)
-    if (__shfl_sync(0xffffffffu, from, u) >= 0)
-      x ^= c.k[u].x ^ c.k[u].y ^ c.k[u].z ^ c.k[u].w ^ c.v[u].x ^ c.v[u].y ^ c.v[u].z ^ c.v[u].w;
-  const int64_t y = __shfl_sync(0xffffffffu, from, (lane >> 1) & (N - 1));
-  if (lane < 2 * N && y >= 0) x ^= c.s.x ^ c.s.y ^ c.s.z ^ c.s.w;
-  return x;
 }
 template <int N>
 __device__ __forceinline__ void store_cells(const Pool& p, int64_t to, int lane, const Cells<N>& c) {
@@ -243,14 +231,13 @@ __device__ __forceinline__ bool wait_loaded(const uint32_t* flag, int* status) {
 }
 
 constexpr int kNearRuns = 1024;  // a table up to so long is looked up in shared memory
-// on an SM (500 runs 84 us; 3 of them, spilled, 105; with four cells a warp 4 CTAs 92, 5 97)
+// on an SM (measured with a relaxed flag, 500 runs: 84 us; 3 of them, spilled, 105; with four cells a warp 4 CTAs 92, 5 97)
 constexpr int kMoveCtas = 2;
 __global__ void __launch_bounds__(kThreads, kMoveCtas)
     compact_move_kernel(const Pool pool, const Tables t, const CompactWs w, int rank_ctas, int4* prefixes_out, int4* seqs_out,
                         int* used_out, int* status) {
   __shared__ int4 s_runs[kNearRuns];
   __shared__ int s_next, s_wait[2];
-  __shared__ volatile uint32_t s_sink[kThreads];
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_next = atomicAdd(&w.head[0], 1);
@@ -321,11 +308,11 @@ __global__ void __launch_bounds__(kThreads, kMoveCtas)
         s_wait[1] = xb < 0 ? -1 : xb / kMoveChunk;
       }
     }
-    // This thread's cells are in its registers, every thread's behind the barrier, and then the flag says so.  It says nothing
-    // of earlier stores, so nothing waits for those (a fence here did: 500 runs 97 us against 90).
-    if (moves) s_sink[tid] = folded(from, lane, x);
+    // The flag says that every thread's loads are behind it.  Only a release orders a load before a store of another SM: it
+    // waits for this CTA's earlier stores as well (500 runs 89 us; with a relaxed flag behind a use of every loaded word 86, and
+    // nothing in the memory model that keeps the loads before it).
     __syncthreads();
-    if (tid == 0) asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(w.loaded + chunk), "r"(1u) : "memory");
+    if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(w.loaded + chunk), "r"(1u) : "memory");
     if (moves) {
       bool ok = true;
       const int j = s_wait[0] + tid;
