@@ -406,6 +406,8 @@ def qsa_prefix_attention(q, kq, vq, ksc, vsc, n_pool: int, prefixes, n_prefix: i
     [n_tok, words] of mask bits, or None: a token sees the sequence's tokens up to itself."""
     dev = _here()
     ws, ws_bytes = _scratch(ws, dev)
+    if tree is not None and not (isinstance(tree, _Tensor) and tree.dim() == 2):
+        raise QSAError(QSA_ERR_INVALID_ARG, f"tree must be an int32 or uint32 tensor [n_tok, words] or None (got {_what(tree)})")
     words = 0 if tree is None else tree.shape[1]
     topk = 2048 if params is None else params.topk if isinstance(params, qsa_params) else int(params[0])
     rows = n_tok * (N_HEADS * HEAD_DIM)

@@ -204,3 +204,9 @@ def test_workspaces_on_the_cpu_are_refused(fake):
 def test_nothing_to_copy_in_a_pool_without_cells(lib):
     assert call(lib.qsa_cache_copy, COPY, n_pool=0, max_cells=0, kq=None, ksc=None, vq=None, vsc=None) == 0
     assert call(lib.qsa_cache_copy, COPY, n_pool=0) == qsa.QSA_ERR_INVALID_ARG
+
+
+def test_masks_that_are_no_rows_of_words_are_refused(fake):
+    for tree in (ints(2), ints(2, 1, 1), FAKE, [[1], [3]]):
+        assert "tree" in refused(qsa.qsa_prefix_attention, FAKE, FAKE, FAKE, FAKE, FAKE, 9, None, 0, FAKE, 2, 2, tree, 0, 5, None, FAKE)
+    assert fake == {}
