@@ -220,3 +220,53 @@ def test_verify_feeds_the_commit():
         way, _ = verified(b["p"][r0:], b["d"][r0:], b["token"][r0:r0 + counts[s]], b["parent"][r0:r0 + counts[s]], b["u"][r0:], b["u_end"][s], 9)
         for i, k in enumerate(way):
             np.testing.assert_array_equal(kq[c0 + pos0 + i].cpu().numpy(), before[c0 + pos0 + k])
+
+
+UNIT = 2.0 ** -44
+
+
+def plainly(b, r0, t, points, u_end):
+    """(path, left-over row, its sum, refusals of it, least margin of a decision over its bound) in 64-bit floating point."""
+    p, d = b["p"][r0:r0 + t].astype(np.float64), b["d"][r0:r0 + t].astype(np.float64)
+    u, parent, token, vocab = b["u"][r0:r0 + t].astype(np.float64), b["parent"][r0:r0 + t], b["token"][r0:r0 + t], p.shape[1]
+    way, w, c, r, margin = [0], p[0], 1.0, 0, np.inf
+    for k in range(1, t):
+        if parent[k] != way[-1]:
+            continue
+        x = token[k]
+        base = np.eye(1, vocab, x)[0] if points else d[way[-1]]
+        # an entry is rounded to a unit (half a unit each for p and d at the first refusal, one for each later product), and what
+        # is left of c is the sum of vocab of them, times d at the next refusal
+        off = (2 * r + 2) * UNIT * (1 + vocab * base[x]) + 2.0 ** -50
+        margin = min(margin, abs(u[k] * c * base[x] - w[x]) / off)
+        if u[k] * c * base[x] < w[x]:
+            way, w, c, r = way + [k], p[k], 1.0, 0
+            continue
+        if points:
+            c, w = c - w[x], np.where(np.arange(vocab) == x, 0.0, w)
+        else:
+            w = np.maximum(w - c * base, 0.0)
+            c = w.sum()
+        r += 1
+    return way, w, r, margin
+
+
+@pytest.mark.parametrize("points", [False, True])
+@pytest.mark.parametrize("counts,vocab,bush,near", [([9] * 12, 131071, 3, 0.4), ([30, 2, 11] * 3, 100003, 6, 1.0), ([20] * 4, 262144, 12, 2.0)])
+def test_large_vocabularies_against_plain_arithmetic_in_64_bits(points, counts, vocab, bush, near):
+    b = batch(counts, vocab, 11, bush, near)
+    path, n_path, after = run(b, len(counts), vocab, max(counts), points)
+    qsa.qsa_check_device_status()
+    close = 0
+    for s, (r0, t) in enumerate(zip(b["first"], counts)):
+        way, w, r, margin = plainly(b, r0, t, points, b["u_end"][s])
+        if margin <= 1:  # a decision that the rounding may turn
+            close += 1
+            continue
+        assert path[s, :n_path[s]].tolist() == way, s
+        up = np.cumsum(w)
+        at, x = float(b["u_end"][s]) * up[-1], after[s]
+        off = 2 * vocab * (2 * r + 2) * UNIT  # of the running sum, and of the total
+        assert up[x] > at - off and (x == 0 or up[x - 1] <= at + off), (s, x)
+        assert w[x] > 0
+    assert close <= 1
