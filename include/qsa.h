@@ -510,7 +510,9 @@ QSA_API size_t qsa_prefix_attention_workspace_bytes(int n_prefix, int n_seq, int
  *   ws    qsa_prefix_attention_workspace_bytes(...) bytes, 16-byte aligned, clobbered.  Calls that overlap on the GPU (two
  *         streams, two captured graphs) need a workspace each.
  * A sequence whose entry or prefix breaks these rules is skipped (its rows are not written) and flagged in the status
- * word (QSA_ERR_DEVICE).  n_prefix, n_tok and n_seq at most 65535; n_tok or n_seq 0 does nothing.
+ * word (QSA_ERR_DEVICE).  First token rows and first sequences do not decrease over the whole of their tables: where they do,
+ * that is flagged too, and rows of any sequence may be skipped or hold anything; nothing else is read or written.
+ * n_prefix, n_tok and n_seq at most 65535; n_tok or n_seq 0 does nothing.
  */
 QSA_API int qsa_prefix_attention(const uint16_t* q, const int8_t* kq, const int8_t* vq, const uint16_t* ksc, const uint16_t* vsc,
                                  int64_t n_pool, const int32_t* prefixes, int n_prefix, const int32_t* seqs, int n_seq, int n_tok,

@@ -288,8 +288,10 @@ struct OwnArgs {
 // S CTAs a (token, group), an S-th of its tiles of 16 cells each.  The warps take the tiles in turn, each through a ring of its own:
 //   S = Q K^T  (A = 16 rows of Q, 12 of them heads; B = K^, two n8 tiles), 16 k16 steps
 //   O += P V^  (A = P as it stands in S's registers, B = V^, 32 n8 tiles), one k16 step
-// Those 64 MMAs a tile bound it: an SM starts one in about 8.5 cycles (34 on each of its four tensor cores), so the 24,600 cells of
-// 48 tokens with 50-900 own cells take 10,100 cycles of MMAs in a kernel of 23.6 us (alone; 25.8 MB from DRAM).
+// 64 MMAs a tile, of which an SM starts one in about 8.5 cycles (34 on each of its four tensor cores): the 24,600 cells of 48 tokens
+// with 50-900 own cells take 10,100 cycles of its matrix pipe out of 30,600 active ones in a kernel of 23.6 us (alone; 25.8 MB from
+// DRAM, issue slots 24-33% in use).  So no unit is full: what bounds it is a warp's tiles in line (loads, the MMAs, the
+// softmax between the two products), in the CTA of the longest sequence, which has seven rounds where the shortest has one.
 // Lanes take the k dims, and V's n dims, in an order of their own, the same for both operands, so that a lane's codes are 16
 // bytes side by side: of a k64 block lane (n, i) has dims 16 i .. 16 i + 15 of cell n, four k16 steps of four; of V lane
 // (n, i) has dims 16 n .. 16 n + 15 of a half of cells 2 i, 2 i + 1, 2 i + 8 and 2 i + 9, which sixteen n8 tiles take one by one.  The
@@ -302,7 +304,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2) prefix_own_kernel(const __grid
   __shared__ float2 s_sum[kHPG];           // (m, l) of the CTA's
   __shared__ float2 s_all[kMaxMerge][kHPG];  // and of the cluster's CTAs
   // Behind the prefixes' kernel nothing here needs what that one writes, and it triggered this launch when all launches
-  // before it were complete: no wait.  One CTA waits for it at its end, so that this launch ends no earlier.
+  // before it were complete: no wait (launch O of ptx.cuh, pdl_trigger).  One CTA waits for it at its end, so that this launch
+  // ends no earlier.
   if (!a.behind_dense) pdl_begin();
   if (a.out == nullptr) pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(JoinShape<kSlices>::kThreads) prefix_join_kern
   __shared__ float s_inv[kHPG];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slice = blockIdx.x % kSlices, g = blockIdx.x / kSlices % kGroups, t = blockIdx.x / kSlices / kGroups;
-  // With a plan, the launch before triggered this one when the one that makes the records was complete.
+  // With a plan, the launch before triggered this one when the one that makes the records was complete (ptx.cuh, pdl_trigger).
   const bool early = a.plan != nullptr;
   if (!early) pdl_begin();
   const int4 ti = __ldcg(&a.b.tok[t]), e = __ldcg(&a.more[t].seq);

@@ -176,8 +176,18 @@ __device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t nthreads, bo
 // of the next kernel waiting beside running ones slowed the latency-bound kernels (the one-CTA decode top-k most).
 __device__ __forceinline__ void pdl_begin() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The exception, the attention kernels of qsa_prefix_attention: the next launch may start once every CTA of this one has
-// called this (after pdl_begin, so that all launches before this one are complete by then) or has ended; its pdl_begin
-// still waits for all of this launch.
+// called this or has ended; its pdl_begin still waits for all of this launch.  Some of them read before their pdl_begin, or
+// without one.  The launches of a call, and what makes that right:
+//   makers  prep, scores, top-k (those that the call takes), each behind its pdl_begin; none triggers
+//   D       the prefixes' cells: triggers behind its pdl_begin, so every maker, and every launch before the call, is complete
+//           when the next launch starts
+//   O       the own cells: behind D without pdl_begin.  It reads what the caller gave and what makers wrote, and nothing of
+//           D's; its CTAs trigger at once, and its first CTA waits for D at its end, so that O complete means D complete.
+//           Without D before it, it has a pdl_begin in front like any other
+//   J       the join: before its pdl_begin it reads what makers wrote (records, plan) and the caller's gate; behind it the
+//           parts of D and O.  Where O makes the records there is no plan, and J has its pdl_begin in front
+// So no launch may come between D and J that writes what O or J reads early, or that ends without having waited for those
+// before it; a kernel of the chain that triggers does so behind its pdl_begin, or is O behind D.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------- fences

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_dense_kernel(const __grid_co
   }
   cluster_arrive_all();  // #0, waited for before the first remote access: every CTA's barriers are set up
   // Own cells need nothing of the prefixes' launch before them, which triggered this one when all launches before it were
-  // complete: one CTA waits for it at its end, so that this launch ends no earlier.
+  // complete: one CTA waits for it at its end, so that this launch ends no earlier (ptx.cuh, pdl_trigger: launches D and O).
   const bool late = kOf == kOwnCells && a.behind_dense;
   if (!late) pdl_begin();
   if constexpr (kOf != kTreeCells) pdl_trigger();  // the next launch's CTAs may start, or wait, beside these

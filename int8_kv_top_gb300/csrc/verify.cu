@@ -15,7 +15,7 @@
 // whole numbers instead: a probability is taken in units of 2^-44 (fp32 holds 2^-24 of itself), so sums and
 // differences are exact, in any order, and only w = max(w - c d, 0) after a second refusal rounds (to a unit).
 //
-// Measured (GB300, rows from DRAM): 64 trees of 4-24 tokens over 131,071 entries 46 us for 84-92 MB of rows (13 us at a plain copy's
+// Measured (GB300, rows from DRAM): 64 trees of 4-24 tokens over 131,071 entries 40-53 us over runs for 84-92 MB of rows (13 us at a plain copy's
 // rate): the pass that every sequence has ends after 14 us, near the memory's rate; the second and third pass of the 21-27
 // sequences with several refusals take 8-18 us each, bound by their 64-bit arithmetic, since the hardware puts up to four CTAs of a
 // cluster on one SM while others are idle (a spreading preference of the launch changed nothing).  48 trees without drafts'
